@@ -71,13 +71,15 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.dera_relpos_fused_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f,
                                                    i, i, i, vp, sz, vp]
         lib.dera_relpos_fused_backward.restype = i
+        from . import train   # imports this module
+        train.declare(lib)
         _lib = lib
         return lib
 
 
-def declared_entry_points() -> list[str]:
-    """Function names declared in include/dera_relpos.h."""
-    with open(HEADER) as fh:
+def declared_entry_points(header: str = HEADER) -> list[str]:
+    """Function names declared in include/dera_relpos.h (or another header of the library)."""
+    with open(header) as fh:
         text = fh.read()
     pat = r"^\s*DERA_API\s+(?:const\s+char\s*\*|dera_status|int)\s+(dera_\w+)\s*\("
     return sorted(set(re.findall(pat, text, re.M)))

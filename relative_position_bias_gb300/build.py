@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdera_relpos.so")
 SOURCES = ["dera_relpos.cu", "attention_w16.cu", "attention_w32.cu", "attention_w40.cu", "attention_w64.cu",
-           "backward.cu"]
+           "backward.cu", "train.cu", "qk_norm_rope.cu", "compact_backward_d64.cu", "compact_backward_d128.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
                 "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -32,7 +32,8 @@ def nvcc() -> str:
 
 def _inputs() -> list[str]:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh"))]
-    return files + [os.path.join(ROOT, "include", "dera_relpos.h"), os.path.abspath(__file__)]
+    include = os.path.join(ROOT, "include")
+    return files + [os.path.join(include, f) for f in os.listdir(include)] + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:

@@ -943,7 +943,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // again at the end of the CTA's work with no overshoot (cap 0, l >= 1).
       const int n_keys = (min(sg.j1 * KHT, H) - sg.j0 * KHT) * W;
       volatile int* bad = bad_flag + 2 * wg + (seg & 1);
-      if (row_valid && !(l >= ldexpf(static_cast<float>(n_keys), kMinRowSumLog2))) *bad = 1;
+      // A row whose every key so far is masked (a bias of -inf) still has the
+      // starting maximum -FLT_MAX: its O and l are exactly 0, and no replay helps.
+      if (row_valid && m_used != -FLT_MAX && !(l >= ldexpf(static_cast<float>(n_keys), kMinRowSumLog2))) *bad = 1;
       if (!wg_sync()) return false;
       const bool tile_bad = *bad != 0;
       if (r == 0) bad_flag[2 * wg + ((seg + 1) & 1)] = 0;   // every thread has read this segment's flag
@@ -1005,7 +1007,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
       };
       if (sg.full(n_kv)) {
-        const float inv_l = 1.0f / l;
+        const float inv_l = l == 0.f ? 0.f : 1.0f / l;   // a masked row gives zeros, and lse = -inf
         if (args.lse != nullptr && row_valid) args.lse[static_cast<size_t>(bh) * N + n] = m_used + log2f(l);
         #pragma unroll
         for (int h = 0; h < Dm::kAtoms; ++h) {
@@ -1058,9 +1060,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         auto merge_store = [&](int h, const float4 (&xa)[16], float2 ma, const float4 (&xb)[16], float2 mb) {
           const float mstar = fmaxf(ma.x, mb.x);
           const float fa = ex2_approx(ma.x - mstar), fb = ex2_approx(mb.x - mstar);
-          const float inv_l = 1.0f / (fa * ma.y + fb * mb.y);
+          const float l_ab = fa * ma.y + fb * mb.y;
+          const float inv_l = l_ab == 0.f ? 0.f : 1.0f / l_ab;
           if (h == 0 && args.lse != nullptr && row_valid)
-            args.lse[static_cast<size_t>(bh) * N + n] = mstar + log2f(fa * ma.y + fb * mb.y);
+            args.lse[static_cast<size_t>(bh) * N + n] = mstar + log2f(l_ab);
           #pragma unroll
           for (int cc = 0; cc < 4; ++cc) {
             float v[16];

@@ -105,6 +105,27 @@ __device__ __forceinline__ float load_elem(const void* p, size_t i, int fmt) {
   return __half2float(__ushort_as_half(raw));
 }
 
+// The two 16-bit values of a packed pair, low half first.
+__device__ __forceinline__ float2 unpack_in(uint32_t u, int fmt) {
+  if (fmt == kBF16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+  return make_float2(__half2float(__ushort_as_half(static_cast<unsigned short>(u & 0xFFFFu))),
+                     __half2float(__ushort_as_half(static_cast<unsigned short>(u >> 16))));
+}
+
+__device__ __forceinline__ uint32_t pack_in(float lo, float hi, int fmt) {
+  return fmt == kBF16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+}
+
+// Stores 4 consecutive gradient values of a row in the gradient dtype.
+__device__ __forceinline__ void st_grad4(void* base, size_t i, float a, float b, float c, float d, int fmt) {
+  if (fmt == kF32) {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + i) = make_float4(a, b, c, d);
+  } else {
+    const uint2 w = make_uint2(pack_in(a, b, fmt), pack_in(c, d, fmt));
+    *reinterpret_cast<uint2*>(reinterpret_cast<unsigned short*>(base) + i) = w;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // On-chip skew of the tensor-core products G = Q_tile . [T_h ; T_w]^T.
 //

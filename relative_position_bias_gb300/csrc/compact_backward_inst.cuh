@@ -1,0 +1,65 @@
+// Launch of the compact-bias backward for one head dimension; included by one .cu for each, so that
+// the build compiles them side by side.
+#pragma once
+#include "compact_backward.cuh"
+
+namespace dera {
+
+template <class K>
+static cudaError_t cb_smem(K kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int WP, bool BF16, int D>
+static cudaError_t launch_cb_rows(const CbMaps& m, const CbArgs& a, unsigned grid, cudaStream_t s) {
+  auto kernel = relpos_cb_rows_kernel<WP, BF16, D>;
+  using SM = CbRowsSmem<WP, D>;
+  const cudaError_t e = cb_smem(kernel, SM::kAlloc);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, kCbThreads, SM::kAlloc, s>>>(m.q, m.dout, m.kg, m.vg, a);
+  return cudaGetLastError();
+}
+
+template <bool BF16, int D>
+static cudaError_t launch_cb(const CbMaps& m, const CbArgs& a, cudaStream_t s) {
+  const int units = a.BH * a.n_tiles;
+  const CbSplit rs = {a.rows_full, a.rows_split}, cs = {a.cols_full, a.cols_split};
+  // heads in y: at most 65535 a launch
+  cudaError_t e = cudaSuccess;
+  for (int b0 = 0; b0 < a.BH && e == cudaSuccess; b0 += 65535) {
+    CbArgs p = a;
+    const int nb = a.BH - b0 < 65535 ? a.BH - b0 : 65535;
+    const size_t rows = static_cast<size_t>(b0) * a.N, blocks = static_cast<size_t>(b0) * a.n_blocks;
+    const size_t bias = a.bias_fmt == kF32 ? 4 : 2, out = a.out_fmt == kF32 ? 4 : 2;
+    p.rel_h = static_cast<const char*>(a.rel_h) + rows * a.H * bias;
+    p.rel_w = static_cast<const char*>(a.rel_w) + rows * a.W * bias;
+    p.lse = a.lse + rows;
+    p.out = static_cast<const char*>(a.out) + rows * D * out;
+    p.dout = static_cast<const char*>(a.dout) + rows * D * 2;
+    p.hl = a.hl + blocks * a.H * kCbRow;
+    p.rw = a.rw + blocks * a.W * kCbRow;
+    p.nD = a.nD + blocks * 64;
+    relpos_cb_prep_kernel<BF16, D><<<dim3(a.n_tiles, nb), kCbPrepThreads, 0, s>>>(p);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
+  const unsigned rgrid = static_cast<unsigned>(rs.blocks(units)), cgrid = static_cast<unsigned>(cs.blocks(units));
+  switch (cb_width(a.W)) {
+    case 16: e = launch_cb_rows<16, BF16, D>(m, a, rgrid, s); break;
+    case 32: e = launch_cb_rows<32, BF16, D>(m, a, rgrid, s); break;
+    case 48: e = launch_cb_rows<48, BF16, D>(m, a, rgrid, s); break;
+    default: e = launch_cb_rows<64, BF16, D>(m, a, rgrid, s); break;
+  }
+  if (e != cudaSuccess) return e;
+  auto cols = relpos_cb_cols_kernel<BF16, D>;
+  e = cb_smem(cols, CbColsSmem<D>::kAlloc);
+  if (e != cudaSuccess) return e;
+  cols<<<cgrid, kCbThreads, CbColsSmem<D>::kAlloc, s>>>(m.q64, m.dout64, m.k, m.v, a);
+  e = cudaGetLastError();
+  const int joins = rs.tail(units) + cs.tail(units);
+  if (e != cudaSuccess || joins == 0) return e;
+  relpos_cb_join_kernel<D><<<joins, 512, 0, s>>>(a, rs.tail(units));
+  return cudaGetLastError();
+}
+
+}  // namespace dera

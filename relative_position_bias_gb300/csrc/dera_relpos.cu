@@ -15,6 +15,7 @@
 #include <mutex>
 
 #include "../../include/dera_relpos.h"
+#include "host.cuh"
 #include "launch.cuh"
 #include "project.cuh"
 
@@ -81,7 +82,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Device address of the status word on the current device (looked up once per device).
+}  // namespace
+
+namespace dera {
+
 int* status_ptr(int dev) {
   static int* ptrs[kMaxDevices] = {};
   static std::mutex mu;
@@ -108,7 +112,6 @@ dera_status check_shape(int BH, int H, int W, int head_dim) {
   return DERA_OK;
 }
 
-// Host-only checks: non-null and 16-byte aligned (TMA operands).
 dera_status check_host(std::initializer_list<const void*> ptrs) {
   for (const void* p : ptrs)
     if (!p) return DERA_ERR_NULL;
@@ -117,7 +120,6 @@ dera_status check_host(std::initializer_list<const void*> ptrs) {
   return DERA_OK;
 }
 
-// Device memory of device `dev` (the launcher's same-device rule).
 dera_status check_ptr(const void* p, int dev) {
   cudaPointerAttributes a;
   if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
@@ -129,7 +131,7 @@ dera_status check_ptr(const void* p, int dev) {
   return DERA_OK;
 }
 
-bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, const cuuint64_t* dims,
+static bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, const cuuint64_t* dims,
               const cuuint64_t* strides_bytes, const cuuint32_t* box) {
   auto fn = encode_fn();
   if (!fn) return false;
@@ -140,23 +142,18 @@ bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-CUtensorMapDataType tma_type(dera_dtype t) {
+static CUtensorMapDataType tma_type(dera_dtype t) {
   return t == DERA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
-// Every box is 64 elements (128 bytes, one swizzle atom) wide; a row of
-// head_dim d is d / 64 boxes, loaded at element offsets 0 and 64.
-
-// q / out-like tensor [BH, N, d] read in 128-row tiles
-bool map_rows(CUtensorMap* m, const void* p, dera_dtype t, int BH, int N, int d) {
+bool map_rows(CUtensorMap* m, const void* p, dera_dtype t, int BH, int N, int d, int rows) {
   const cuuint64_t row = 2 * static_cast<cuuint64_t>(d);
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(BH)};
   const cuuint64_t strides[2] = {row, static_cast<cuuint64_t>(N) * row};
-  const cuuint32_t box[3] = {64, 128, 1};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(rows), 1};
   return make_map(m, p, tma_type(t), 3, dims, strides, box);
 }
 
-// k / v viewed as [BH, H, W, d], read in tiles of KHT grid rows x WP columns
 bool map_keys(CUtensorMap* m, const void* p, dera_dtype t, int BH, int H, int W, int d, int WP, int KHT) {
   const cuuint64_t row = 2 * static_cast<cuuint64_t>(d);
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(W), static_cast<cuuint64_t>(H),
@@ -167,23 +164,22 @@ bool map_keys(CUtensorMap* m, const void* p, dera_dtype t, int BH, int H, int W,
 }
 
 // table [2L-1, d], one 128-row box per 64 columns (rows past 2L-1 read as zero)
-bool map_table(CUtensorMap* m, const void* p, dera_dtype t, int L, int d) {
+static bool map_table(CUtensorMap* m, const void* p, dera_dtype t, int L, int d) {
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(2 * L - 1)};
   const cuuint64_t strides[1] = {2 * static_cast<cuuint64_t>(d)};
   const cuuint32_t box[2] = {64, 128};
   return make_map(m, p, tma_type(t), 2, dims, strides, box);
 }
 
-int padded_width(int W) { return W <= 16 ? 16 : (W <= 32 ? 32 : (W <= 40 ? 40 : 64)); }
+static int padded_width(int W) { return W <= 16 ? 16 : (W <= 32 ? 32 : (W <= 40 ? 40 : 64)); }
 // grid rows per key tile (KeyTile<WP, d>::KHT), and the forward's
 // (FwdKeyTile<WP, d>::KHT: three for a 40-column grid with head_dim 64)
-int rows_per_tile(int WP, int d) {
+static int rows_per_tile(int WP, int d) {
   if (d == 64) return WP <= 16 ? 8 : (WP <= 32 ? 4 : 2);
   return WP <= 16 ? 4 : (WP <= 40 ? 2 : 1);
 }
-int fwd_rows_per_tile(int WP, int d) { return (d == 64 && WP == 40) ? 3 : rows_per_tile(WP, d); }
+static int fwd_rows_per_tile(int WP, int d) { return (d == 64 && WP == 40) ? 3 : rows_per_tile(WP, d); }
 
-// Streaming-multiprocessor count of a device (cached; 0 if the query fails).
 int sm_count(int dev) {
   static int counts[kMaxDevices] = {};
   static std::mutex mu;
@@ -205,7 +201,7 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 // Arrival tags of the split schedule's per-unit counters: a 64-bit sequence
 // from a random start, so no two launches of this process share a tag and
 // counters left by any earlier launch (finished or stopped) never match.
-unsigned long long next_launch_tag() {
+static unsigned long long next_launch_tag() {
   static std::atomic<unsigned long long> next{[] {
     unsigned long long seed = 0x9e3779b97f4a7c15ull ^ static_cast<unsigned long long>(
         std::chrono::steady_clock::now().time_since_epoch().count());
@@ -231,9 +227,9 @@ struct Plan {
 // CTAs of a schedule without cuts: one per SM, taking whole units
 // round-robin, or one per unit when there are fewer units (or the SM count
 // is unknown).
-int uncut_ctas(int n_units, int sms) { return sms > 0 && n_units > sms ? sms : n_units; }
+static int uncut_ctas(int n_units, int sms) { return sms > 0 && n_units > sms ? sms : n_units; }
 
-Plan make_plan(int BH, int H, int W, int d, int sms) {
+static Plan make_plan(int BH, int H, int W, int d, int sms) {
   Plan p;
   const int N = H * W;
   const int KHT = fwd_rows_per_tile(padded_width(W), d);
@@ -255,7 +251,7 @@ Plan make_plan(int BH, int H, int W, int d, int sms) {
   return p;
 }
 
-size_t workspace_bytes_for(const Plan& p) { return p.split ? p.counters_bytes + p.partial_bytes : 0; }
+static size_t workspace_bytes_for(const Plan& p) { return p.split ? p.counters_bytes + p.partial_bytes : 0; }
 dera_status current_device(int* dev) {
   if (cudaGetDevice(dev) != cudaSuccess) {
     cudaGetLastError();
@@ -263,12 +259,6 @@ dera_status current_device(int* dev) {
   }
   return DERA_OK;
 }
-
-#define DERA_TRY(expr)              \
-  do {                              \
-    const dera_status s_ = (expr);  \
-    if (s_ != DERA_OK) return s_;   \
-  } while (0)
 
 // Workspace of the backward: fp32 regions, each 256-byte aligned.
 struct BwdLayout {
@@ -295,7 +285,7 @@ struct BwdLayout {
 dera_status run_attention(const void* q, const void* k, const void* v, const void* a, const void* b, void* out,
                           int BH, int H, int W, int d, float scale, dera_dtype in_dtype, dera_dtype bias_dtype,
                           dera_dtype out_dtype, bool fused, void* workspace, size_t workspace_bytes,
-                          void* stream, float* lse = nullptr) {
+                          void* stream, float* lse) {
   int dev = 0;
   DERA_TRY(current_device(&dev));
   const int N = H * W;
@@ -352,6 +342,10 @@ dera_status run_attention(const void* q, const void* k, const void* v, const voi
   }
   return e == cudaSuccess ? DERA_OK : DERA_ERR_CUDA;
 }
+
+}  // namespace dera
+
+namespace {
 
 // Scratch of dera_relpos_fused_noalloc: a buffer compiled into the library,
 // for callers that cannot allocate device memory.  In host code the array's

@@ -1,0 +1,73 @@
+// Launchers of the kernels in qk_norm_rope.cuh.
+#include "qk_norm_rope.cuh"
+
+#include <algorithm>
+
+namespace dera {
+
+namespace {
+
+template <bool BF16, int D, bool NORM>
+cudaError_t fwd(const QkArgs& a, int mode, dim3 grid, cudaStream_t s) {
+  switch (mode) {
+    case kRotNone: qk_norm_rope_kernel<BF16, D, kRotNone, NORM><<<grid, kQkThreads, 0, s>>>(a); break;
+    case kRotHalf: qk_norm_rope_kernel<BF16, D, kRotHalf, NORM><<<grid, kQkThreads, 0, s>>>(a); break;
+    default: qk_norm_rope_kernel<BF16, D, kRotPairs, NORM><<<grid, kQkThreads, 0, s>>>(a); break;
+  }
+  return cudaGetLastError();
+}
+
+template <bool BF16, int D, bool NORM>
+cudaError_t bwd(const QkArgs& a, int mode, dim3 grid, cudaStream_t s) {
+  switch (mode) {
+    case kRotNone: qk_norm_rope_bwd_kernel<BF16, D, kRotNone, NORM><<<grid, kQkThreads, 0, s>>>(a); break;
+    case kRotHalf: qk_norm_rope_bwd_kernel<BF16, D, kRotHalf, NORM><<<grid, kQkThreads, 0, s>>>(a); break;
+    default: qk_norm_rope_bwd_kernel<BF16, D, kRotPairs, NORM><<<grid, kQkThreads, 0, s>>>(a); break;
+  }
+  return cudaGetLastError();
+}
+
+template <bool BF16, int D>
+cudaError_t pick(const QkArgs& a, int mode, bool norm, bool backward, dim3 grid, cudaStream_t s) {
+  if (backward) return norm ? bwd<BF16, D, true>(a, mode, grid, s) : bwd<BF16, D, false>(a, mode, grid, s);
+  return norm ? fwd<BF16, D, true>(a, mode, grid, s) : fwd<BF16, D, false>(a, mode, grid, s);
+}
+
+int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
+
+}  // namespace
+
+QkPlan qk_plan(long long tokens, const int (&heads)[3], int head_dim, bool backward, int sms) {
+  QkPlan p;
+  const int blocks = ceil_div(tokens, kQkThreads / (head_dim / 8));   // runs of tokens
+  const int total = heads[0] + heads[1] + heads[2];
+  // Heads per block: as many as leave eight blocks for every SM (each block
+  // loads its tokens' angles once), at least one.
+  const long long want = 8ll * std::max(sms, 1);
+  p.per = static_cast<int>(std::max<long long>(1, std::min<long long>(8, static_cast<long long>(blocks) * total / want)));
+  for (int i = 0; i < 3; ++i) p.groups[i] = ceil_div(heads[i], p.per);
+  const int gy = p.groups[0] + p.groups[1] + p.groups[2];
+  // backward: few enough blocks that the partial weight gradients stay small
+  p.grid_x = backward ? std::min(blocks, std::max(1, ceil_div(want, gy))) : blocks;
+  p.part_rows_q = p.groups[0] * p.grid_x;
+  p.part_rows_k = p.groups[1] * p.grid_x;
+  return p;
+}
+
+cudaError_t launch_qk(QkArgs& a, const QkPlan& p, int head_dim, int mode, bool bf16, bool norm, bool backward,
+                      float* dqw, float* dkw, cudaStream_t s) {
+  a.per = p.per;
+  for (int i = 0; i < 3; ++i) a.groups[i] = p.groups[i];
+  const dim3 grid(p.grid_x, p.groups[0] + p.groups[1] + p.groups[2]);
+  cudaError_t e;
+  if (head_dim == 128)
+    e = bf16 ? pick<true, 128>(a, mode, norm, backward, grid, s) : pick<false, 128>(a, mode, norm, backward, grid, s);
+  else
+    e = bf16 ? pick<true, 64>(a, mode, norm, backward, grid, s) : pick<false, 64>(a, mode, norm, backward, grid, s);
+  if (e != cudaSuccess || !backward || !norm) return e;
+  qk_weight_grad_kernel<<<dim3(head_dim / 32, 2), dim3(32, 32), 0, s>>>(a.parts, p.part_rows_q, p.part_rows_k, head_dim,
+                                                                       dqw, dkw);
+  return cudaGetLastError();
+}
+
+}  // namespace dera

@@ -1,0 +1,99 @@
+// Launch arguments and launchers behind the entry points of dera_train.h.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+
+namespace dera {
+
+constexpr int kQkThreads = 256;
+
+struct HeadsPtr {
+  char* data;
+  long long sb, st, sh;   // strides in elements
+};
+
+struct QkArgs {
+  HeadsPtr x[3];        // q, k, v in token order (forward: read; backward: q, k read)
+  HeadsPtr dx[3];       // backward: dq, dk, dv in token order
+  const void* z[3];     // backward: dq_out, dk_out, dv_out
+  void* zo[3];          // forward: q_out, k_out, v_out
+  const void* w[2];     // q_weight, k_weight
+  const float* cos;
+  const float* sin;
+  const int* positions;
+  float* parts;         // backward: [2][part_rows][D] partial weight gradients
+  int heads[3];         // q, k, v heads (v: 0 if absent)
+  int groups[3];        // blocks in y for each, each of `per` heads
+  int per;
+  int N, table_rows, half;   // half = rotary_dim / 2
+  long long tokens;     // B * N
+  float eps;
+  int w_fmt, z_fmt, dx_fmt;
+};
+
+// Rotation: none, pairs (i, i + half), pairs (2i, 2i + 1).
+enum : int { kRotNone = 0, kRotHalf = 1, kRotPairs = 2 };
+
+// How qk_norm_rope's grid is cut for a size.
+struct QkPlan {
+  int per;             // heads per block
+  int groups[3];       // blocks in y of q, k, v
+  int grid_x;          // blocks over tokens
+  int part_rows_q, part_rows_k;   // backward: partial rows of the weight gradients
+};
+QkPlan qk_plan(long long tokens, const int (&heads)[3], int head_dim, bool backward, int sms);
+cudaError_t launch_qk(QkArgs& a, const QkPlan& p, int head_dim, int mode, bool bf16, bool norm, bool backward,
+                      float* dqw, float* dkw, cudaStream_t s);
+
+// Compact-bias backward (compact_backward.cuh).
+constexpr int kCbRow = 68;   // floats of a 64-query row of hl or rw (272 bytes: rows start in different
+                             // banks and stay 16-byte aligned)
+
+struct CbArgs {
+  const void* rel_h;    // [BH, N, H] bias dtype
+  const void* rel_w;    // [BH, N, W]
+  const float* lse;     // [BH, N] base 2
+  const void* out;      // [BH, N, D]
+  const void* dout;     // [BH, N, D]
+  float* hl;            // [BH][n_blocks][H][kCbRow] log2(e) rel_h - lse of 64 queries (-inf: P = 0)
+  float* rw;            // [BH][n_blocks][W][kCbRow] log2(e) rel_w
+  float* nD;            // [BH][64 n_blocks] -D
+  void* dq;
+  void* dk;
+  void* dv;
+  float* drel_h;
+  float* drel_w;
+  float* parts_rows;    // [piece][128 (D + W)] of the split units
+  float* parts_cols;    // [piece][128 (2 D)]
+  int* status;
+  int BH, H, W, N;
+  int n_tiles;          // ceil(N / 128)
+  int n_blocks;         // 2 n_tiles: 64-query blocks
+  int rows_full, rows_split, cols_full, cols_split;   // units that are whole, pieces of each other unit
+  float scale, scale_log2;
+  int out_fmt, grad_fmt, bias_fmt;
+};
+
+// Whole units and pieces per remaining unit, of `units` tiles that take `steps` steps each.
+struct CbSplit {
+  int full, split;
+  int tail(int units) const { return split > 1 ? units - full : 0; }
+  int blocks(int units) const { return full + (units - full) * split; }
+};
+CbSplit cb_split(int units, int steps, int sms);
+// Padded width of the rows kernel's key steps, and its steps for H grid rows.
+int cb_width(int W);
+int cb_rows_steps(int H, int W);
+
+struct CbMaps {
+  CUtensorMap q, dout;          // 128-row tiles (rows kernel)
+  CUtensorMap q64, dout64;      // 64-row tiles (cols kernel)
+  CUtensorMap kg, vg;           // by grid rows (rows kernel)
+  CUtensorMap k, v;             // 128-row tiles (cols kernel)
+};
+cudaError_t launch_cb_d64(const CbMaps& maps, const CbArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_cb_d128(const CbMaps& maps, const CbArgs& a, bool bf16, cudaStream_t s);
+
+}  // namespace dera

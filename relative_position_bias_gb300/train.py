@@ -1,0 +1,266 @@
+"""ctypes binding of the entry points in ``include/dera_train.h`` (argument marshalling only).
+
+What a training step needs around :func:`~relative_position_bias_gb300.attention`: the heads of a
+packed projection normed, rotated and laid out (:func:`qk_norm_rope`), the compact-bias attention
+with its log-sum-exp (:func:`attention_lse`), and the backward of each (:func:`attention_backward`,
+:func:`qk_norm_rope_backward`).  As in
+``api``: shapes are checked, pointers and the stream are passed on, and error codes become
+exceptions; there is no fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+
+import torch
+
+from . import api
+from .api import _check, _code, _expect, _ptr, _stream, _workspace
+
+HEADER = os.path.join(os.path.dirname(api.HEADER), "dera_train.h")
+
+
+class _Heads(ctypes.Structure):
+    """``dera_heads``: a [B, N, heads, d] tensor by its strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_longlong), ("stride_token", ctypes.c_longlong),
+                ("stride_head", ctypes.c_longlong)]
+
+
+def declare(lib: ctypes.CDLL) -> None:
+    """Signatures of the entry points (called by ``api.load_library``)."""
+    vp, i, f, sz, hp = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(_Heads)
+    szp = ctypes.POINTER(sz)
+    for name, args in {
+        "dera_qk_norm_rope": [hp] * 3 + [vp] * 8 + [i] * 8 + [f, i, i, vp],
+        "dera_qk_norm_rope_backward_workspace_size": [i] * 5 + [szp],
+        "dera_qk_norm_rope_backward": [hp] * 2 + [vp] * 8 + [hp] * 3 + [vp] * 2 + [i] * 8 + [f] + [i] * 4 + [vp, sz, vp],
+        "dera_relpos_attention_lse": [vp] * 7 + [i] * 4 + [f] + [i] * 3 + [vp, sz, vp],
+        "dera_relpos_attention_backward_workspace_size": [i] * 4 + [szp],
+        "dera_relpos_attention_backward": [vp] * 13 + [i] * 4 + [f] + [i] * 4 + [vp, sz, vp],
+    }.items():
+        fn = getattr(lib, name)
+        fn.argtypes = args
+        fn.restype = i
+
+
+def _scratch(need: int, device: torch.device, stream, workspace: torch.Tensor | None) -> tuple:
+    """(tensor to keep alive, pointer, bytes) of one call's scratch: the caller's, or a new buffer
+    that the allocator keeps until the work on `stream` is done."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if int(stream or 0) != torch.cuda.current_stream(device).cuda_stream:
+            workspace.record_stream(torch.cuda.ExternalStream(int(stream or 0), device=device))
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+# ------------------------------------------------------------------------ norms, rotation, layout
+def _heads(t: torch.Tensor, name: str, B: int, N: int, heads: int, d: int) -> _Heads:
+    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != N or t.shape[2] != heads or t.shape[3] != d:
+        raise ValueError(f"{name}: expected shape {(B, N, heads, d)}, got {tuple(t.shape)}")
+    sb, st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return _Heads(t.data_ptr(), sb, st, sh)
+
+
+def _same(t: torch.Tensor | None, shape: tuple, dtype, name: str) -> None:
+    if t is None:
+        return
+    _expect(t, shape, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _qk_common(q, k, v, q_weight, k_weight, cos, sin, positions):
+    """Sizes and the checks that forward and backward share:
+    (B, N, q heads, kv heads, d, rotary_dim, table rows, weight dtype code)."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [B, N, heads, d]")
+    B, N, hq, d = q.shape
+    hk = k.shape[2]
+    if k.dtype != q.dtype or (v is not None and v.dtype != q.dtype):
+        raise TypeError("q, k and v must share a dtype")
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    wcode = api.DERA_F32
+    if q_weight is not None:
+        if q_weight.dtype not in (q.dtype, torch.float32):
+            raise TypeError("the weights must be float32 or of q's dtype")
+        _same(q_weight, (d,), q_weight.dtype, "q_weight")
+        _same(k_weight, (d,), q_weight.dtype, "k_weight")
+        wcode = _code(q_weight.dtype)
+    rot = rows = 0
+    if cos is not None:
+        if cos.dim() != 2:
+            raise ValueError("cos and sin must be [rows, rotary_dim / 2]")
+        rows, rot = cos.shape[0], 2 * cos.shape[1]
+        _same(cos, (rows, rot // 2), torch.float32, "cos")
+        _same(sin, (rows, rot // 2), torch.float32, "sin")
+        _same(positions, (B, N), torch.int32, "positions")
+    elif positions is not None:
+        raise ValueError("positions need cos and sin")
+    return B, N, hq, hk, d, rot, rows, wcode
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None = None, *,
+                 q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                 cos: torch.Tensor | None = None, sin: torch.Tensor | None = None,
+                 positions: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """Per-head norms of q and k and their rotation by position, via ``dera_qk_norm_rope``.
+
+    q ``[B, N, q_heads, d]``, k and v ``[B, N, kv_heads, d]`` in token order with any strides that keep
+    rows whole (slices of a packed projection as they lie).  Returns ``(q_out, k_out)``, or
+    ``(q_out, k_out, v_out)`` with v, as ``[B * heads, N, d]``: what ``project``, ``attention`` and
+    ``fused`` take.  ``q_weight``, ``k_weight`` ``[d]``: weights of the root-mean-square norm (None:
+    no norm).  ``cos``, ``sin`` ``[rows, rotary_dim / 2]`` fp32 (None: no rotation), row ``positions[b, n]``
+    (int32) or ``n``; pairs ``(i, i + rotary_dim / 2)``, or ``(2i, 2i + 1)`` if ``interleaved``."""
+    B, N, hq, hk, d, rot, rows, wcode = _qk_common(q, k, v, q_weight, k_weight, cos, sin, positions)
+    hqs, hks = _heads(q, "q", B, N, hq, d), _heads(k, "k", B, N, hk, d)
+    hvs = None if v is None else _heads(v, "v", B, N, hk, d)
+    q_out = torch.empty((B * hq, N, d), dtype=q.dtype, device=q.device)
+    k_out = torch.empty((B * hk, N, d), dtype=q.dtype, device=q.device)
+    v_out = None if v is None else torch.empty((B * hk, N, d), dtype=q.dtype, device=q.device)
+    _check(api.load_library().dera_qk_norm_rope(
+        hqs, hks, hvs, _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions), q_out.data_ptr(),
+        k_out.data_ptr(), _ptr(v_out), B, N, hq, hk, d, rot, rows, interleaved, eps, _code(q.dtype), wcode,
+        _stream(q.device, stream)))
+    return (q_out, k_out) if v is None else (q_out, k_out, v_out)
+
+
+def qk_norm_rope_backward_workspace_size(B: int, N: int, q_heads: int, kv_heads: int, head_dim: int = 64) -> int:
+    """Scratch bytes of :func:`qk_norm_rope_backward` on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(api.load_library().dera_qk_norm_rope_backward_workspace_size(B, N, q_heads, kv_heads, head_dim,
+                                                                        ctypes.byref(n)))
+    return n.value
+
+
+def qk_norm_rope_backward(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_out: torch.Tensor,
+                          dv_out: torch.Tensor | None = None, *, q_weight: torch.Tensor | None = None,
+                          k_weight: torch.Tensor | None = None, cos: torch.Tensor | None = None,
+                          sin: torch.Tensor | None = None, positions: torch.Tensor | None = None, eps: float = 1e-6,
+                          interleaved: bool = False, grad_dtype: torch.dtype | None = None,
+                          dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                          dv: torch.Tensor | None = None, stream=None, workspace: torch.Tensor | None = None):
+    """Gradients of :func:`qk_norm_rope` via ``dera_qk_norm_rope_backward``:
+    ``(dq, dk, dv, dq_weight, dk_weight)``.
+
+    q and k are the forward's; ``dq_out``, ``dk_out``, ``dv_out`` the gradients of its outputs, fp32 or
+    of q's dtype.  dq, dk and dv (None without ``dv_out``) come back in token order in ``grad_dtype``
+    (default fp32), or are written to the tensors given, which may be slices of one packed
+    gradient; the weights' gradients are fp32 (None without weights)."""
+    B, N, hq, hk, d, rot, rows, wcode = _qk_common(q, k, None, q_weight, k_weight, cos, sin, positions)
+    norm = q_weight is not None
+    given = [t for t in (dq, dk, dv) if t is not None]
+    gd = grad_dtype or (given[0].dtype if given else torch.float32)
+    if any(t.dtype != gd for t in given):
+        raise TypeError(f"dq, dk and dv must be {gd}")
+    if dv is not None and dv_out is None:
+        raise ValueError("dv needs dv_out")
+    if dk_out.dtype != dq_out.dtype or (dv_out is not None and dv_out.dtype != dq_out.dtype):
+        raise TypeError("dq_out, dk_out and dv_out must share a dtype")
+    _expect(dq_out, (B * hq, N, d), "dq_out")
+    _expect(dk_out, (B * hk, N, d), "dk_out")
+    if dv_out is not None:
+        _expect(dv_out, (B * hk, N, d), "dv_out")
+    dev = q.device
+    dq = torch.empty((B, N, hq, d), dtype=gd, device=dev) if dq is None else dq
+    dk = torch.empty((B, N, hk, d), dtype=gd, device=dev) if dk is None else dk
+    if dv is None and dv_out is not None:
+        dv = torch.empty((B, N, hk, d), dtype=gd, device=dev)
+    hdq, hdk = _heads(dq, "dq", B, N, hq, d), _heads(dk, "dk", B, N, hk, d)
+    hdv = None if dv is None else _heads(dv, "dv", B, N, hk, d)
+    hqs, hks = _heads(q, "q", B, N, hq, d), _heads(k, "k", B, N, hk, d)
+    dqw = torch.empty(d, dtype=torch.float32, device=dev) if norm else None
+    dkw = torch.empty(d, dtype=torch.float32, device=dev) if norm else None
+    st = _stream(dev, stream)
+    keep, ws, ws_bytes = None, None, 0
+    if norm and dev.type == "cuda":
+        need = 0
+        if workspace is None:
+            with torch.cuda.device(dev):
+                need = qk_norm_rope_backward_workspace_size(B, N, hq, hk, d)
+        keep, ws, ws_bytes = _scratch(need, dev, st, workspace)
+    _check(api.load_library().dera_qk_norm_rope_backward(
+        hqs, hks, _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions), dq_out.data_ptr(),
+        dk_out.data_ptr(), _ptr(dv_out), hdq, hdk, hdv, _ptr(dqw), _ptr(dkw), B, N, hq, hk, d, rot, rows, interleaved,
+        eps, _code(q.dtype), wcode, _code(dq_out.dtype), _code(gd), ws, ws_bytes, st))
+    return dq, dk, dv, dqw, dkw
+
+
+# ------------------------------------------------------------------------------------- attention
+def attention_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h: torch.Tensor, rel_w: torch.Tensor,
+                  H: int, W: int, scale: float | None = None, out_dtype: torch.dtype | None = None, stream=None,
+                  workspace=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Training forward of the two-step form via ``dera_relpos_attention_lse``: ``(out, lse)``, lse
+    ``[BH, N]`` fp32 (base 2).  A bias of -inf masks its keys; a row with every key masked gives
+    out = 0 and lse = -inf.  ``workspace`` as in :func:`~relative_position_bias_gb300.attention`."""
+    BH, N, d = q.shape
+    scale = d ** -0.5 if scale is None else scale
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _expect(t, (BH, H * W, d), name)
+    _expect(rel_h, (BH, N, H), "rel_h")
+    _expect(rel_w, (BH, N, W), "rel_w")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k, v must share a dtype")
+    if rel_h.dtype != rel_w.dtype:
+        raise TypeError("rel_h and rel_w must share a dtype")
+    out = torch.empty((BH, N, d), dtype=out_dtype or q.dtype, device=q.device)
+    lse = torch.empty((BH, N), dtype=torch.float32, device=q.device)
+    st = _stream(q.device, stream)
+    ws, ws_bytes = _workspace(q.device, BH, H, W, d, workspace, st)
+    _check(api.load_library().dera_relpos_attention_lse(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(rel_h), _ptr(rel_w), _ptr(out), _ptr(lse), BH, H, W, d, float(scale),
+        _code(q.dtype), _code(rel_h.dtype), _code(out.dtype), ws, ws_bytes, st))
+    return out, lse
+
+
+def attention_backward_workspace_size(BH: int, H: int, W: int, head_dim: int = 64) -> int:
+    """Scratch bytes of :func:`attention_backward` for this size on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(api.load_library().dera_relpos_attention_backward_workspace_size(BH, H, W, head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h: torch.Tensor, rel_w: torch.Tensor,
+                       out: torch.Tensor, lse: torch.Tensor, dout: torch.Tensor, H: int, W: int,
+                       scale: float | None = None, grad_dtype: torch.dtype | None = None, stream=None,
+                       workspace: torch.Tensor | None = None):
+    """Gradients of :func:`attention_lse` via ``dera_relpos_attention_backward``:
+    ``(dq, dk, dv, drel_h, drel_w)``; dq, dk, dv in ``grad_dtype`` (default fp32), the bias's fp32.
+    ``out`` and ``lse`` come from :func:`attention_lse`.  ``workspace``: a caller-owned uint8 tensor that
+    no other call in flight uses, or None for a buffer of this call."""
+    BH, N, d = q.shape
+    scale = d ** -0.5 if scale is None else scale
+    gd = grad_dtype or torch.float32
+    for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out"), (dout, "dout")):
+        _expect(t, (BH, H * W, d), name)
+    _expect(lse, (BH, N), "lse")
+    _expect(rel_h, (BH, N, H), "rel_h")
+    _expect(rel_w, (BH, N, W), "rel_w")
+    if k.dtype != q.dtype or v.dtype != q.dtype or dout.dtype != q.dtype:
+        raise TypeError("q, k, v and dout must share a dtype")
+    if rel_h.dtype != rel_w.dtype:
+        raise TypeError("rel_h and rel_w must share a dtype")
+    if lse.dtype != torch.float32:
+        raise TypeError("lse must be float32")
+    dev = q.device
+    dq = torch.empty((BH, N, d), dtype=gd, device=dev)
+    dk, dv = torch.empty_like(dq), torch.empty_like(dq)
+    drel_h = torch.empty((BH, N, H), dtype=torch.float32, device=dev)
+    drel_w = torch.empty((BH, N, W), dtype=torch.float32, device=dev)
+    st = _stream(dev, stream)
+    need = 0
+    if workspace is None and dev.type == "cuda":
+        with torch.cuda.device(dev):
+            need = attention_backward_workspace_size(BH, H, W, d)
+    keep, ws, ws_bytes = _scratch(need, dev, st, workspace)
+    _check(api.load_library().dera_relpos_attention_backward(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(rel_h), _ptr(rel_w), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
+        _ptr(dv), _ptr(drel_h), _ptr(drel_w), BH, H, W, d, float(scale), _code(q.dtype), _code(rel_h.dtype),
+        _code(out.dtype), _code(gd), ws, ws_bytes, st))
+    return dq, dk, dv, drel_h, drel_w

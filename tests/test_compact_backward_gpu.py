@@ -1,0 +1,239 @@
+"""attention_lse and attention_backward (compact bias, head_dim 64 and 128) against the CPU float64 oracle.
+
+Tolerances.  The backward gets the same out and lse as the oracle.  dq, dk and dv sum products of a
+rounded P or dZ (relative 2^-8 for bf16, 2^-11 for fp16; half of that on average and of either sign, so an
+element is off by far less than the bound): an element may differ by u = 2^-8 (2^-11) times the sum of its
+terms' sizes, plus the output's own rounding.  The terms' sizes are sums the oracle forms with
+absolute values.  With fp16 a P or dZ below 2^-14 is subnormal and off by up to 2^-25: the sum of the
+other factors' sizes times 2^-25 more.  drel_h and drel_w are fp32 sums of the unrounded dZ: the exponent is a sum of terms
+of up to 2^7 in fp32, each rounded to 2^-24 relative, so P is off by less than 2^-14 relative
+in the worst case (4 roundings of 2^7 2^-24, times ln 2), and every sum by that times the sum of |P| (|dP| + |D|).
+The forward's P is rounded to fp16: out may be off by (2^-11 + 2^-9) max|v| (the bound that the forward
+keeps) plus its own rounding; lse is an fp32 sum: 2^-13 absolute.
+"""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import relative_position_bias_gb300 as rpb
+from relative_position_bias_gb300 import build as rbuild
+
+pytestmark = pytest.mark.gpu
+
+BF, HF, FL = torch.bfloat16, torch.float16, torch.float32
+U = {BF: 2.0 ** -8, HF: 2.0 ** -11}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    rbuild.build()
+    rpb.load_library()
+    yield
+    assert rpb.device_status() == 0, "a kernel hit its bounded-wait budget"
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def make(BH, H, W, d, dtype, bias=FL, mask="none", seed=0, sigma=1.0):
+    g = torch.Generator().manual_seed(seed)
+    N = H * W
+    x = {n: (sigma * torch.randn(BH, N, d, generator=g)).to(dtype) for n in ("q", "k", "v")}
+    x["dout"] = torch.randn(BH, N, d, generator=g).to(dtype)
+    x["rel_h"], x["rel_w"] = 2 * torch.randn(BH, N, H, generator=g), 2 * torch.randn(BH, N, W, generator=g)
+    x["rel_h"], x["rel_w"] = x["rel_h"].to(bias), x["rel_w"].to(bias)
+    low = {"inf": -math.inf, "low": torch.finfo(bias).min, "rows": -math.inf, "all": -math.inf}.get(mask)
+    if low is not None:
+        for b in range(BH):   # its own valid area for every problem; the last has none masked
+            vh, vw = max(1, H - b % 3 * (H // 3)), max(1, W - b % 2 * (W // 2))
+            x["rel_h"][b, :, vh:] = low
+            x["rel_w"][b, :, vw:] = low
+    if mask == "rows":        # rows without keys, by either bias
+        x["rel_h"][:, ::3] = -math.inf
+        x["rel_w"][:, 1::5] = -math.inf
+    if mask == "all":
+        x["rel_h"][:] = -math.inf
+    return x
+
+
+def run(x, H, W, scale, out_dtype=None, grad_dtype=FL, **more):
+    d = {n: t.cuda() for n, t in x.items()}
+    out, lse = rpb.attention_lse(d["q"], d["k"], d["v"], d["rel_h"], d["rel_w"], H, W, scale, out_dtype=out_dtype)
+    grads = rpb.attention_backward(d["q"], d["k"], d["v"], d["rel_h"], d["rel_w"], out, lse, d["dout"], H, W, scale,
+                                   grad_dtype=grad_dtype, **more)
+    torch.cuda.synchronize()
+    return out, lse, grads
+
+
+def masks_for_oracle(x):
+    """A bias of the type's lowest value masks like -inf."""
+    return [np.where(f64(x[n]) <= -1e38, -np.inf, f64(x[n])) for n in ("rel_h", "rel_w")]
+
+
+def check(x, H, W, scale, out, lse, grads, dtype, what):
+    f = {n: f64(t) for n, t in x.items()}
+    rh, rw = masks_for_oracle(x)
+    want_o, want_l = oracle.masked_attention(f["q"], f["k"], f["v"], rh, rw, H, W, scale)
+    vmax = np.abs(f["v"]).max(initial=0)
+    tol = (2.0 ** -11 + 2.0 ** -9) * vmax + (torch.finfo(out.dtype).eps / 2) * np.abs(want_o)
+    assert np.all(np.abs(f64(out) - want_o) <= tol), f"{what} out"
+    empty = ~np.isfinite(want_l)
+    assert np.array_equal(empty, np.isneginf(f64(lse))) and np.all(f64(out)[empty] == 0), what
+    assert np.all(np.abs(f64(lse)[~empty] - want_l[~empty]) <= 2.0 ** -13), f"{what} lse"
+    check_backward(x, H, W, scale, out, lse, grads, dtype, what)
+
+
+def check_backward(x, H, W, scale, out, lse, grads, dtype, what):
+    f = {n: f64(t) for n, t in x.items()}
+    rh, rw = masks_for_oracle(x)
+    o, l = f64(out), f64(lse)
+    want = oracle.attention_backward_from(f["q"], f["k"], f["v"], rh, rw, o, l, f["dout"], H, W, scale)
+    u, sub = U[dtype], (2.0 ** -25 if dtype == HF else 0.0)
+    for b in range(f["q"].shape[0]):
+        q, k, v, do = (f[n][b] for n in ("q", "k", "v", "dout"))
+        z = scale * (q @ k.T) + oracle.dense_bias(rh[b], rw[b], H, W)
+        some = np.isfinite(l[b])
+        p = np.exp(z - np.where(some, l[b], 0.0)[:, None] * np.log(2.0)) * some[:, None]
+        dp, dd = do @ v.T, (do * o[b]).sum(-1, keepdims=True)
+        dz = np.abs(p * (dp - dd))
+        size = p * (np.abs(do) @ np.abs(v).T + (np.abs(do) * np.abs(o[b])).sum(-1, keepdims=True))
+        g32 = 2.0 ** -14 * size
+        grid = g32.reshape(-1, H, W)
+        # sizes of terms, so the scale's size too (a negative scale would make a tolerance negative)
+        tols = [abs(scale) * ((u * dz + g32 + sub) @ np.abs(k)), abs(scale) * ((u * dz + g32 + sub).T @ np.abs(q)),
+                (u * p + 2.0 ** -14 * p + sub).T @ np.abs(do), grid.sum(2), grid.sum(1)]
+        for name, got, ref, tol in zip(("dq", "dk", "dv", "drel_h", "drel_w"), grads, want, tols):
+            g = f64(got[b])
+            tol = tol + torch.finfo(got.dtype).eps / 2 * np.abs(ref[b]) + (2.0 ** -25 if got.dtype == HF else 1e-37)
+            assert np.isfinite(g).all(), f"{what} {name}"
+            over = (np.abs(g - ref[b]) - tol).max(initial=0)
+            assert over <= 0, f"{what} {name}[{b}]: {over:.3e} over its tolerance of up to {tol.max():.3e}"
+        assert np.all(f64(grads[0][b])[~some] == 0) and np.all(f64(grads[3][b])[~some] == 0), what
+
+
+SIZES = [(2, 16, 16), (3, 14, 14), (1, 1, 1), (4, 1, 7), (4, 7, 1), (1, 64, 1), (1, 1, 64), (2, 2, 64), (2, 64, 2), (2, 9, 33),
+         (1, 40, 40), (2, 13, 48), (2, 5, 49), (3, 17, 32), (2, 6, 63), (2, 11, 17), (1, 64, 64)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("BH,H,W", SIZES)
+def test_sizes(BH, H, W, d):
+    dtype = BF if (H + W) % 2 == 0 else HF
+    x = make(BH, H, W, d, dtype, seed=H * 64 + W)
+    out, lse, grads = run(x, H, W, d ** -0.5, out_dtype=FL)
+    check(x, H, W, d ** -0.5, out, lse, grads, dtype, f"{BH}x{H}x{W} d{d}")
+
+
+@pytest.mark.parametrize("mask", ["inf", "low", "rows", "all"])
+@pytest.mark.parametrize("bias", [FL, BF, HF])
+@pytest.mark.parametrize("dtype,d,H,W", [(BF, 64, 14, 14), (HF, 128, 10, 20), (HF, 64, 6, 40), (BF, 128, 5, 64)])
+def test_masks(dtype, d, H, W, bias, mask):
+    x = make(7, H, W, d, dtype, bias, mask, seed=5)
+    out, lse, grads = run(x, H, W, d ** -0.5, grad_dtype=dtype)
+    check(x, H, W, d ** -0.5, out, lse, grads, dtype, f"{mask} {bias}")
+    if mask == "all":
+        assert all(torch.count_nonzero(g) == 0 for g in grads)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_split_units(d):
+    """More tiles than fill whole waves of CTAs: the rest is cut into pieces and joined."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    H, W = 32, 33                               # 9 tiles a problem
+    BH = sms // 9 + 3                           # just past one wave
+    x = make(BH, H, W, d, BF, seed=6)
+    out, lse, grads = run(x, H, W, d ** -0.5)
+    check(x, H, W, d ** -0.5, out, lse, grads, BF, "split")
+    few = make(1, 40, 40, d, HF, seed=7)        # fewer tiles than SMs: every one is cut
+    out, lse, grads = run(few, 40, 40, d ** -0.5, out_dtype=FL, grad_dtype=HF)
+    check(few, 40, 40, d ** -0.5, out, lse, grads, HF, "few")
+
+
+def test_wide_logits():
+    """Logits spread over tens of powers of two, of either sign of scale."""
+    for scale in (0.125, -0.2):
+        x = make(2, 12, 20, 64, HF, seed=8, sigma=3.0)
+        out, lse, grads = run(x, 12, 20, scale, out_dtype=FL)
+        check(x, 12, 20, scale, out, lse, grads, HF, f"wide {scale}")
+
+
+def test_against_the_fused_backward():
+    """The chain project, attention_lse, attention_backward gives the fused backward's dk and dv."""
+    H, W, BH = 24, 30, 3
+    x = make(BH, H, W, 64, BF, seed=9)
+    g = torch.Generator().manual_seed(1)
+    th, tw = (0.3 * torch.randn(2 * L - 1, 64, generator=g) for L in (H, W))
+    th, tw = th.to(BF).cuda(), tw.to(BF).cuda()
+    d = {n: t.cuda() for n, t in x.items()}
+    rh, rw = rpb.project(d["q"], th, tw, H, W)
+    out, lse = rpb.attention_lse(d["q"], d["k"], d["v"], rh, rw, H, W, 0.125, out_dtype=FL)
+    out2, lse2 = rpb.fused_lse(d["q"], d["k"], d["v"], th, tw, H, W, 0.125, out_dtype=FL)
+    assert (lse - lse2).abs().max() <= 2.0 ** -13
+    a = rpb.attention_backward(d["q"], d["k"], d["v"], rh, rw, out, lse, d["dout"], H, W, 0.125)
+    b = rpb.fused_backward(d["q"], d["k"], d["v"], th, tw, out2, lse2, d["dout"], H, W, 0.125)
+    for i in (1, 2):
+        assert (a[i] - b[i]).norm() <= 2 * 2.0 ** -8 * b[i].norm()
+
+
+def test_types_streams_and_repeats():
+    """16-bit gradients are the fp32 ones rounded; the same bits every time and on another stream."""
+    x = make(5, 20, 21, 64, BF, seed=10)
+    out, lse, want = run(x, 20, 21, 0.125)
+    _, _, g16 = run(x, 20, 21, 0.125, grad_dtype=BF)
+    for a, b in zip(g16[:3], want[:3]):
+        assert torch.equal(a, b.to(BF))
+    d = {n: t.cuda() for n, t in x.items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = rpb.attention_backward(d["q"], d["k"], d["v"], d["rel_h"], d["rel_w"], out, lse, d["dout"], 20, 21, 0.125,
+                                 stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_graph_and_guarded_outputs():
+    """Captured and replayed on new inputs, with the caller's workspace full of NaN before each run."""
+    H, W, BH = 9, 18, 4
+    x = make(BH, H, W, 128, HF, seed=11)
+    d = {n: t.cuda() for n, t in x.items()}
+    ws = torch.full((rpb.attention_backward_workspace_size(BH, H, W, 128) // 4,), float("nan"), device="cuda")
+
+    def step():
+        o, l = rpb.attention_lse(d["q"], d["k"], d["v"], d["rel_h"], d["rel_w"], H, W, 0.1)
+        return (o, l, *rpb.attention_backward(d["q"], d["k"], d["v"], d["rel_h"], d["rel_w"], o, l, d["dout"], H, W, 0.1,
+                                              workspace=ws))
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = step()
+    for n in ("q", "k", "v", "dout", "rel_h", "rel_w"):
+        d[n].mul_(-0.75)
+    ws.fill_(float("nan"))
+    graph.replay()
+    got = [t.clone() for t in res]
+    ws.fill_(float("nan"))
+    for a, b in zip(got, step()):
+        assert torch.equal(a, b)
+
+
+def test_empty_batch_and_scratch():
+    e = torch.empty(0, 6, 64, dtype=BF, device="cuda")
+    out, lse = rpb.attention_lse(e, e, e, torch.empty(0, 6, 2, device="cuda"), torch.empty(0, 6, 3, device="cuda"), 2, 3)
+    grads = rpb.attention_backward(e, e, e, torch.empty(0, 6, 2, device="cuda"), torch.empty(0, 6, 3, device="cuda"), out,
+                                   lse, e, 2, 3)
+    assert [tuple(g.shape) for g in grads] == [(0, 6, 64)] * 3 + [(0, 6, 2), (0, 6, 3)]
+    x = {n: t.cuda() for n, t in make(1, 2, 3, 64, BF).items()}
+    out, lse = rpb.attention_lse(x["q"], x["k"], x["v"], x["rel_h"], x["rel_w"], 2, 3)
+    with pytest.raises(rpb.DeraError) as ei:
+        rpb.attention_backward(x["q"], x["k"], x["v"], x["rel_h"], x["rel_w"], out, lse, x["dout"], 2, 3,
+                               workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert ei.value.status == 9
