@@ -4,7 +4,11 @@
  *   - dera_qk_norm_rope: the heads of the packed projection, normed, rotated and
  *     laid out as the attention takes them, and its backward;
  *   - dera_relpos_attention_lse: the compact-bias attention that also writes its
- *     log-sum-exp, and dera_relpos_attention_backward (head_dim 64 or 128).
+ *     log-sum-exp, and dera_relpos_attention_backward (head_dim 64 or 128);
+ *   - dera_relpos_project_backward: from the compact bias's gradient to the
+ *     tables' and q's.
+ * One step of the two-step form, in order:
+ *   qk_norm_rope, project, attention_lse | attention_backward, project_backward, qk_norm_rope_backward.
  *
  * The conventions of dera_relpos.h hold: device pointers of the current device,
  * 16-byte aligned; row-major contiguous layouts unless strides are given; the
@@ -130,6 +134,28 @@ DERA_API dera_status dera_relpos_attention_backward(const void* q, const void* k
                               const void* rel_w, const void* out, const float* lse, const void* dout, void* dq,
                               void* dk, void* dv, float* drel_h, float* drel_w, int BH, int H, int W, int head_dim,
                               float scale, dera_dtype in_dtype, dera_dtype bias_dtype, dera_dtype out_dtype,
+                              dera_dtype grad_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Scratch of dera_relpos_project_backward on the current device (partial table gradients). */
+DERA_API dera_status dera_relpos_project_backward_workspace_size(int BH, int H, int W, int head_dim, size_t* bytes);
+
+/*
+ * Backward of dera_relpos_project.  With the gradient of the compact bias, drel_h [BH,N,H] and
+ * drel_w [BH,N,W] in fp32:
+ *   dq[b, n] = dq_in[b, n] + sum_kh drel_h[b, n, kh] rel_pos_h[qh - kh + H - 1]
+ *                          + sum_kw drel_w[b, n, kw] rel_pos_w[qw - kw + W - 1],
+ *   drel_pos_h[i] = sum over (b, n, kh) with qh - kh + H - 1 = i of drel_h[b, n, kh] q[b, n]  (same for w).
+ * in:  q [BH,N,head_dim] and the tables in in_dtype; dq_in [BH,N,head_dim] in grad_dtype (the
+ *      attention's own part of dq), or NULL for none; it may be dq itself.
+ * out: dq [BH,N,head_dim] in grad_dtype (DERA_F32 or in_dtype); drel_pos_h [2H-1,head_dim], drel_pos_w
+ *      [2W-1,head_dim] fp32, summed over every batch and head.
+ * Precision: fp32 sums; drel_h and drel_w enter the products as two bf16 terms each (what is
+ *      left out is 2^-16 of a value at most), and with fp16 q and the tables as two bf16 terms, exactly.
+ * Errors: as for dera_relpos_project; DERA_ERR_SCRATCH as above.  BH = 0 writes zero table gradients.
+ */
+DERA_API dera_status dera_relpos_project_backward(const void* q, const void* rel_pos_h, const void* rel_pos_w,
+                              const float* drel_h, const float* drel_w, const void* dq_in, void* dq, float* drel_pos_h,
+                              float* drel_pos_w, int BH, int H, int W, int head_dim, dera_dtype in_dtype,
                               dera_dtype grad_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus

@@ -10,11 +10,12 @@ this package is its thin Python binding.  Entry points: :func:`project`,
 from .api import (DERA_BF16, DERA_F16, DERA_F32, DeraError, attention, backward_workspace_size, declared_entry_points,
                   device_status, fused, fused_backward, fused_lse, load_library, project, selftest_wait_timeout,
                   workspace_size)
-from .train import (attention_backward, attention_backward_workspace_size, attention_lse, qk_norm_rope,
-                    qk_norm_rope_backward, qk_norm_rope_backward_workspace_size)
+from .train import (attention_backward, attention_backward_workspace_size, attention_lse, project_backward,
+                    project_backward_workspace_size, qk_norm_rope, qk_norm_rope_backward,
+                    qk_norm_rope_backward_workspace_size)
 
 __all__ = ["DERA_BF16", "DERA_F16", "DERA_F32", "DeraError", "attention", "attention_backward",
-           "attention_backward_workspace_size", "attention_lse", "backward_workspace_size",
-           "declared_entry_points", "device_status", "fused", "fused_backward", "fused_lse", "load_library", "project",
-           "qk_norm_rope", "qk_norm_rope_backward", "qk_norm_rope_backward_workspace_size", "selftest_wait_timeout",
-           "workspace_size"]
+           "attention_backward_workspace_size", "attention_lse", "backward_workspace_size", "declared_entry_points",
+           "device_status", "fused", "fused_backward", "fused_lse", "load_library", "project", "project_backward",
+           "project_backward_workspace_size", "qk_norm_rope", "qk_norm_rope_backward",
+           "qk_norm_rope_backward_workspace_size", "selftest_wait_timeout", "workspace_size"]

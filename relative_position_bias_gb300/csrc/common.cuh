@@ -126,6 +126,42 @@ __device__ __forceinline__ void st_grad4(void* base, size_t i, float a, float b,
   }
 }
 
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8], int fmt) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack_in(w[i], fmt);
+    x[2 * i] = p.x;
+    x[2 * i + 1] = p.y;
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8], int fmt) {
+  return make_uint4(pack_in(x[0], x[1], fmt), pack_in(x[2], x[3], fmt), pack_in(x[4], x[5], fmt),
+                    pack_in(x[6], x[7], fmt));
+}
+
+// Eight consecutive values, fp32 or 16-bit (i a multiple of 8, p 16-byte aligned).
+__device__ __forceinline__ void load8(const void* p, size_t i, float (&x)[8], int fmt) {
+  if (fmt == kF32) {
+    const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
+    const float4 lo = f[0], hi = f[1];
+    x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w;
+    x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+  } else {
+    unpack8(*reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i), x, fmt);
+  }
+}
+__device__ __forceinline__ void store8(void* p, size_t i, const float (&x)[8], int fmt) {
+  if (fmt == kF32) {
+    float4* f = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i);
+    f[0] = make_float4(x[0], x[1], x[2], x[3]);
+    f[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) = pack8(x, fmt);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // On-chip skew of the tensor-core products G = Q_tile . [T_h ; T_w]^T.
 //

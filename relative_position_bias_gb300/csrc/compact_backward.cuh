@@ -87,14 +87,6 @@ struct CbColsSmem {
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
-// Contiguous global -> shared copy; addresses and size are multiples of 16 bytes.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 struct CbCta {
   uint8_t* smem;
   uint64_t* bars;

@@ -20,21 +20,6 @@
 
 namespace dera {
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8], int fmt) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 p = unpack_in(w[i], fmt);
-    x[2 * i] = p.x;
-    x[2 * i + 1] = p.y;
-  }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&x)[8], int fmt) {
-  return make_uint4(pack_in(x[0], x[1], fmt), pack_in(x[2], x[3], fmt), pack_in(x[4], x[5], fmt),
-                    pack_in(x[6], x[7], fmt));
-}
-
 // Sum over the D / 8 lanes of a row (in a fixed order, so every lane gets the same bits).
 template <int LANES>
 __device__ __forceinline__ float row_sum(float v) {
@@ -180,29 +165,6 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkArgs a
   }
 }
 
-// Eight consecutive values of a gradient in fp32 or in the input type.
-template <int FMT>
-__device__ __forceinline__ void load_grad8(const void* p, size_t i, float (&x)[8], int fmt) {
-  if (fmt == kF32) {
-    const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + i);
-    const float4 lo = __ldg(f), hi = __ldg(f + 1);
-    x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w;
-    x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
-  } else {
-    unpack8(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + i)), x, FMT);
-  }
-}
-template <int FMT>
-__device__ __forceinline__ void store_grad8(void* p, size_t i, const float (&x)[8], int fmt) {
-  if (fmt == kF32) {
-    float4* f = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i);
-    f[0] = make_float4(x[0], x[1], x[2], x[3]);
-    f[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i) = pack8(x, FMT);
-  }
-}
-
 // The weights' gradients are sums over every row of every token: a block takes
 // every gridDim.x-th run of tokens and keeps its slots' sums in registers, one partial row
 // per block, which qk_weight_grad_kernel adds in a fixed order.
@@ -234,8 +196,8 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_bwd_kernel(const QkAr
     if (blk.kind == 2) {
       for (int h = blk.h0; h < blk.h1; ++h) {
         float g[8];
-        load_grad8<fmt>(a.z[2], zrow + h * hstep, g, a.z_fmt);
-        if (valid) store_grad8<fmt>(dx.data, dxrow + h * dx.sh, g, a.dx_fmt);
+        load8(a.z[2], zrow + h * hstep, g, a.z_fmt);
+        if (valid) store8(dx.data, dxrow + h * dx.sh, g, a.dx_fmt);
       }
       continue;
     }
@@ -244,7 +206,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_bwd_kernel(const QkAr
     #pragma unroll 2
     for (int h = blk.h0; h < blk.h1; ++h) {
       float g[8];
-      load_grad8<fmt>(a.z[blk.kind], zrow + h * hstep, g, a.z_fmt);
+      load8(a.z[blk.kind], zrow + h * hstep, g, a.z_fmt);
       float v[8];
       if (NORM)
         unpack8(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(x.data) + xrow + h * x.sh)), v, fmt);
@@ -261,7 +223,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_bwd_kernel(const QkAr
           g[e] = r * fmaf(-m, v[e], g[e] * w[e]);
         }
       }
-      if (valid) store_grad8<fmt>(dx.data, dxrow + h * dx.sh, g, a.dx_fmt);
+      if (valid) store8(dx.data, dxrow + h * dx.sh, g, a.dx_fmt);
     }
   }
   if (!NORM || blk.kind == 2) return;

@@ -173,6 +173,17 @@ dera_status check_cb(int BH, int H, int W, int head_dim) {
   return tiles * BH > (1ll << 30) ? DERA_ERR_SHAPE : DERA_OK;
 }
 
+// CTAs of the projection's backward for one 64-column slice: one an SM over all slices, no more
+// than there are tiles.
+int pb_ctas(int BH, int H, int W, int d, int sms) {
+  const long long tiles = (static_cast<long long>(BH) * H * W + 127) / 128;
+  const long long most = sms >= d / 64 ? sms / (d / 64) : 1;
+  return static_cast<int>(tiles < most ? tiles : most);
+}
+size_t pb_workspace(int BH, int H, int W, int d, int sms) {
+  return align256(static_cast<size_t>(pb_ctas(BH, H, W, d, sms)) * (2 * H - 1 + 2 * W - 1) * d * sizeof(float));
+}
+
 }  // namespace
 
 extern "C" {
@@ -389,6 +400,71 @@ dera_status dera_relpos_attention_backward(const void* q, const void* k, const v
   const bool bf16 = in_dtype == DERA_BF16;
   return (head_dim == 128 ? launch_cb_d128(m, a, bf16, s) : launch_cb_d64(m, a, bf16, s)) == cudaSuccess ? DERA_OK
                                                                                                        : DERA_ERR_CUDA;
+}
+
+dera_status dera_relpos_project_backward_workspace_size(int BH, int H, int W, int head_dim, size_t* bytes) {
+  if (!bytes) return DERA_ERR_NULL;
+  DERA_TRY(check_shape(BH, H, W, head_dim));
+  *bytes = 0;
+  if (BH == 0) return DERA_OK;
+  int dev = 0;
+  DERA_TRY(current_device(&dev));
+  *bytes = pb_workspace(BH, H, W, head_dim, sm_count(dev));
+  return DERA_OK;
+}
+
+dera_status dera_relpos_project_backward(const void* q, const void* rel_pos_h, const void* rel_pos_w,
+                                         const float* drel_h, const float* drel_w, const void* dq_in, void* dq,
+                                         float* drel_pos_h, float* drel_pos_w, int BH, int H, int W, int head_dim,
+                                         dera_dtype in_dtype, dera_dtype grad_dtype, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+  DERA_TRY(check_shape(BH, H, W, head_dim));
+  if (!is16(in_dtype) || !(grad_dtype == DERA_F32 || grad_dtype == in_dtype)) return DERA_ERR_DTYPE;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int dev = 0;
+  if (BH == 0) {   // no rows: only the tables' gradients are written, as zeros
+    DERA_TRY(check_host({drel_pos_h, drel_pos_w}));
+    DERA_TRY(current_device(&dev));
+    DERA_TRY(check_ptr(drel_pos_h, dev));
+    DERA_TRY(check_ptr(drel_pos_w, dev));
+    const size_t row = static_cast<size_t>(head_dim) * sizeof(float);
+    if (cudaMemsetAsync(drel_pos_h, 0, (2 * H - 1) * row, s) != cudaSuccess ||
+        cudaMemsetAsync(drel_pos_w, 0, (2 * W - 1) * row, s) != cudaSuccess)
+      return DERA_ERR_CUDA;
+    return DERA_OK;
+  }
+  DERA_TRY(check_host({q, rel_pos_h, rel_pos_w, drel_h, drel_w, dq, drel_pos_h, drel_pos_w}));
+  if (dq_in) DERA_TRY(check_host({dq_in}));
+  DERA_TRY(current_device(&dev));
+  for (const void* p : {q, rel_pos_h, rel_pos_w, static_cast<const void*>(drel_h), static_cast<const void*>(drel_w),
+                        dq_in, static_cast<const void*>(dq), static_cast<const void*>(drel_pos_h),
+                        static_cast<const void*>(drel_pos_w)})
+    if (p) DERA_TRY(check_ptr(p, dev));
+  const int sms = sm_count(dev);
+  DERA_TRY(check_workspace(workspace, workspace_bytes, pb_workspace(BH, H, W, head_dim, sms), dev));
+  PbArgs a = {};
+  a.q = q;
+  a.th = rel_pos_h;
+  a.tw = rel_pos_w;
+  a.drel_h = drel_h;
+  a.drel_w = drel_w;
+  a.dq_in = dq_in;
+  a.dq = dq;
+  a.parts = static_cast<float*>(workspace);
+  a.dth = drel_pos_h;
+  a.dtw = drel_pos_w;
+  a.status = status_ptr(dev);
+  if (!a.status) return DERA_ERR_CUDA;
+  a.H = H;
+  a.W = W;
+  a.N = H * W;
+  a.D = head_dim;
+  a.tokens = static_cast<long long>(BH) * a.N;
+  a.n_tiles = (a.tokens + 127) / 128;
+  a.grad_fmt = fmt_of(grad_dtype);
+  return launch_project_backward(a, pb_ctas(BH, H, W, head_dim, sms), in_dtype == DERA_BF16, s) == cudaSuccess
+             ? DERA_OK
+             : DERA_ERR_CUDA;
 }
 
 }  // extern "C"

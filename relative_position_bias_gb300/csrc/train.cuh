@@ -96,4 +96,24 @@ struct CbMaps {
 cudaError_t launch_cb_d64(const CbMaps& maps, const CbArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_cb_d128(const CbMaps& maps, const CbArgs& a, bool bf16, cudaStream_t s);
 
+// Backward of the projection (project_backward.cuh).
+struct PbArgs {
+  const void* q;         // [tokens, D]
+  const void* th;        // [2H-1, D]
+  const void* tw;        // [2W-1, D]
+  const float* drel_h;   // [tokens, H]
+  const float* drel_w;   // [tokens, W]
+  const void* dq_in;     // [tokens, D] grad dtype, or null
+  void* dq;
+  float* parts;          // [CTA][(2H-1) + (2W-1)][D]
+  float* dth;
+  float* dtw;
+  int* status;
+  int H, W, N, D;
+  long long tokens;      // BH * N
+  long long n_tiles;     // ceil(tokens / 128)
+  int grad_fmt;
+};
+cudaError_t launch_project_backward(const PbArgs& a, int ctas, bool bf16, cudaStream_t s);
+
 }  // namespace dera

@@ -2,8 +2,8 @@
 
 What a training step needs around :func:`~relative_position_bias_gb300.attention`: the heads of a
 packed projection normed, rotated and laid out (:func:`qk_norm_rope`), the compact-bias attention
-with its log-sum-exp (:func:`attention_lse`), and the backward of each (:func:`attention_backward`,
-:func:`qk_norm_rope_backward`).  As in
+with its log-sum-exp (:func:`attention_lse`), and the backward of each step
+(:func:`attention_backward`, :func:`project_backward`, :func:`qk_norm_rope_backward`).  As in
 ``api``: shapes are checked, pointers and the stream are passed on, and error codes become
 exceptions; there is no fallback.
 """
@@ -37,6 +37,8 @@ def declare(lib: ctypes.CDLL) -> None:
         "dera_relpos_attention_lse": [vp] * 7 + [i] * 4 + [f] + [i] * 3 + [vp, sz, vp],
         "dera_relpos_attention_backward_workspace_size": [i] * 4 + [szp],
         "dera_relpos_attention_backward": [vp] * 13 + [i] * 4 + [f] + [i] * 4 + [vp, sz, vp],
+        "dera_relpos_project_backward_workspace_size": [i] * 4 + [szp],
+        "dera_relpos_project_backward": [vp] * 9 + [i] * 6 + [vp, sz, vp],
     }.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -264,3 +266,46 @@ def attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h:
         _ptr(dv), _ptr(drel_h), _ptr(drel_w), BH, H, W, d, float(scale), _code(q.dtype), _code(rel_h.dtype),
         _code(out.dtype), _code(gd), ws, ws_bytes, st))
     return dq, dk, dv, drel_h, drel_w
+
+
+# ------------------------------------------------------------------------------------ projection
+def project_backward_workspace_size(BH: int, H: int, W: int, head_dim: int = 64) -> int:
+    """Scratch bytes of :func:`project_backward` for this size on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(api.load_library().dera_relpos_project_backward_workspace_size(BH, H, W, head_dim, ctypes.byref(n)))
+    return n.value
+
+
+def project_backward(q: torch.Tensor, rel_pos_h: torch.Tensor, rel_pos_w: torch.Tensor, drel_h: torch.Tensor,
+                     drel_w: torch.Tensor, H: int, W: int, dq: torch.Tensor | None = None,
+                     grad_dtype: torch.dtype | None = None, stream=None, workspace: torch.Tensor | None = None):
+    """Gradients of :func:`~relative_position_bias_gb300.project` via ``dera_relpos_project_backward``:
+    ``(dq, drel_pos_h, drel_pos_w)``.
+
+    ``drel_h``, ``drel_w``: the compact bias's gradient, fp32.  ``dq``, if given, is the attention's part
+    of dq, to which the projection's is added (in a new tensor of the same dtype); else dq comes in
+    ``grad_dtype`` (default fp32).  The tables' gradients are fp32."""
+    BH, N, d = q.shape
+    gd = grad_dtype or (torch.float32 if dq is None else dq.dtype)
+    _expect(q, (BH, H * W, d), "q")
+    _expect(rel_pos_h, (2 * H - 1, d), "rel_pos_h")
+    _expect(rel_pos_w, (2 * W - 1, d), "rel_pos_w")
+    if rel_pos_h.dtype != q.dtype or rel_pos_w.dtype != q.dtype:
+        raise TypeError("q and the tables must share a dtype")
+    _same(drel_h, (BH, N, H), torch.float32, "drel_h")
+    _same(drel_w, (BH, N, W), torch.float32, "drel_w")
+    _same(dq, (BH, N, d), gd, "dq")
+    dev = q.device
+    out = torch.empty((BH, N, d), dtype=gd, device=dev)
+    dth = torch.empty((2 * H - 1, d), dtype=torch.float32, device=dev)
+    dtw = torch.empty((2 * W - 1, d), dtype=torch.float32, device=dev)
+    st = _stream(dev, stream)
+    need = 0
+    if workspace is None and dev.type == "cuda":
+        with torch.cuda.device(dev):
+            need = project_backward_workspace_size(BH, H, W, d)
+    keep, ws, ws_bytes = _scratch(need, dev, st, workspace)
+    _check(api.load_library().dera_relpos_project_backward(
+        _ptr(q), _ptr(rel_pos_h), _ptr(rel_pos_w), _ptr(drel_h), _ptr(drel_w), _ptr(dq), _ptr(out), _ptr(dth), _ptr(dtw),
+        BH, H, W, d, _code(q.dtype), _code(gd), ws, ws_bytes, st))
+    return out, dth, dtw

@@ -28,7 +28,8 @@ def test_header_and_exports(lib):
     names = set(rpb.declared_entry_points(train.HEADER))
     assert names == {"dera_qk_norm_rope", "dera_qk_norm_rope_backward", "dera_qk_norm_rope_backward_workspace_size",
                      "dera_relpos_attention_lse", "dera_relpos_attention_backward",
-                     "dera_relpos_attention_backward_workspace_size"}
+                     "dera_relpos_attention_backward_workspace_size", "dera_relpos_project_backward",
+                     "dera_relpos_project_backward_workspace_size"}
     out = subprocess.run(["nm", "-D", "--defined-only", rbuild.LIB], capture_output=True, text=True, check=True)
     exported = {line.split()[-1] for line in out.stdout.splitlines() if " T " in line}
     assert names <= exported
@@ -178,3 +179,36 @@ def test_attention_binding_checks():
         rpb.attention_backward(q, q, q, rh, rw, q, lse, q.float(), 2, 3)
     with pytest.raises(ValueError):
         rpb.attention_backward(q, q, q, rh, rw, q, lse[:1], q, 2, 3)
+
+
+def _pb(lib, *, ptrs=(FAKE,) * 5 + (None,) + (FAKE,) * 3, BH=1, H=4, W=4, d=64, in_dt=BF16, grad_dt=F32):
+    return lib.dera_relpos_project_backward(*ptrs, BH, H, W, d, in_dt, grad_dt, FAKE, 1 << 30, None)
+
+
+def test_project_backward_refusals(lib):
+    assert _pb(lib, d=96) == CODES["DERA_ERR_HEAD_DIM"]
+    for bad in (dict(H=65), dict(W=0), dict(BH=-1)):
+        assert _pb(lib, **bad) == CODES["DERA_ERR_SHAPE"], bad
+    for bad in (dict(in_dt=F32), dict(grad_dt=F16)):
+        assert _pb(lib, **bad) == CODES["DERA_ERR_DTYPE"], bad
+    for i in range(9):
+        ptrs = [FAKE] * 9
+        ptrs[i] = None
+        if i != 5:    # dq_in is optional
+            assert _pb(lib, ptrs=tuple(ptrs)) == CODES["DERA_ERR_NULL"]
+        ptrs[i] = FAKE_MISALIGNED
+        assert _pb(lib, ptrs=tuple(ptrs)) == CODES["DERA_ERR_ALIGN"]
+    assert _pb(lib, BH=0, ptrs=(None,) * 9) == CODES["DERA_ERR_NULL"]    # the tables' gradients are still written
+
+
+def test_project_backward_binding_checks():
+    q, th, tw = torch.zeros(2, 6, 64).half(), torch.zeros(3, 64).half(), torch.zeros(5, 64).half()
+    gh, gw = torch.zeros(2, 6, 2), torch.zeros(2, 6, 3)
+    with pytest.raises(ValueError):
+        rpb.project_backward(q, tw, th, gh, gw, 2, 3)
+    with pytest.raises(TypeError):
+        rpb.project_backward(q, th, tw, gh.half(), gw.half(), 2, 3)
+    with pytest.raises(TypeError):
+        rpb.project_backward(q, th, tw, gh, gw, 2, 3, dq=q.float(), grad_dtype=torch.float16)
+    with pytest.raises(TypeError):
+        rpb.project_backward(q, th.float(), tw, gh, gw, 2, 3)
