@@ -19,10 +19,9 @@
 // S and dP are formed twice, so that dq, dk and dv are each complete in one CTA: no atomics, and
 // the same result on every run.
 //
-// In rows and cols two softmax warpgroups take the steps in turn, each with its own S and dP in
-// TMEM: while one exponentiates step i the tensor core forms S and dP of step i + 1 for the
-// other and adds step i - 1 to the accumulators.  With one group (one warp a scheduler)
-// every wait of the chain TMEM load, exponent, TMEM store, product stood in the open.
+// In rows and cols two or three softmax warpgroups (in cols two pairs of them) take the steps in turn,
+// each with its own S and dP in TMEM: while one exponentiates step i the tensor core forms S and dP
+// of the next steps for the others and adds step i - 1 to the accumulators.
 #pragma once
 #include <cfloat>
 
@@ -31,7 +30,8 @@
 
 namespace dera {
 
-constexpr int kCbThreads = 64 + 256;   // TMA warp, MMA warp, two softmax warpgroups
+constexpr int kCbColsThreads = 64 + 512;   // TMA warp, MMA warp, two pairs of softmax warpgroups
+
 // Key steps of the rows kernel: KHT whole grid rows of WP >= W columns, so that a column's kw
 // is known at compile time and a thread's rel_w row and drel_w sums stay in registers.
 template <int WP>
@@ -43,38 +43,57 @@ struct CbKeys {
 
 // Barriers of both kernels.
 enum : int {
-  kCbAFull = 0,                    // the CTA's own tiles landed
-  kCbRingFull = 1,                 // [4]
-  kCbRingEmpty = kCbRingFull + 4,  // [4]
-  kCbSFull = kCbRingEmpty + 4,     // [2] S and dP of a step are in TMEM
-  kCbPFull = kCbSFull + 2,         // [2] the warpgroup has read S and dP and written dZ (and P)
-  kCbAccDone = kCbPFull + 2,       // [2] the products that read dZ (and P) are complete
-  kCbAllDone = kCbAccDone + 2,     // every product is complete
-  kCbJoin = kCbAllDone + 1,        // the softmax threads, at the end (count 256)
+  kCbAFull = 0,                    // the CTA's own tiles are where the products read them
+  kCbRingFull = 1,                 // [8]
+  kCbRingEmpty = kCbRingFull + 8,  // [8]
+  kCbSFull = kCbRingEmpty + 8,     // [3] S and dP of a step are in TMEM
+  kCbPFull = kCbSFull + 3,         // [3] the softmax threads have read S and dP and written dZ (and P)
+  kCbAccDone = kCbPFull + 3,       // [3] the products that read dZ (and P) are complete
+  kCbAllDone = kCbAccDone + 3,     // every product is complete
+  kCbJoin = kCbAllDone + 1,        // the softmax threads among themselves
   kCbBars = kCbJoin + 1
 };
 
 constexpr int cb_align(int x) { return (x + 1023) / 1024 * 1024; }
 
+// rows: NB steps in flight, one softmax warpgroup each.  Registers: the block launches with what
+// its threads get, then the control warps give most of theirs to the softmax warpgroups (a split larger
+// than the launch pool would block, so the host checks the compiled count).
+template <int D>
+struct CbRowsDims {
+  static constexpr int NB = D == 64 ? 3 : 2;
+  static constexpr int kThreads = 128 * (NB + 1);   // warp 0 TMA, warp 1 MMA, warps 2 and 3 idle, then the softmax threads
+  static constexpr int kLaunchRegs = NB == 3 ? 128 : 168, kRegsCtl = 56, kRegsSmx = NB == 3 ? 152 : 224;
+  static_assert(kRegsCtl + NB * kRegsSmx <= (NB + 1) * kLaunchRegs, "register split exceeds the launch pool");
+  // TMEM columns: S_b [128 b, 128 b + 64) (dZ_b over it), dP_b 64 further, dq, then q and dO as packed pairs
+  static constexpr uint32_t tmDQ = 128 * NB, tmQ = tmDQ + D, tmDO = tmQ + D / 2;
+  static_assert(tmDO + D / 2 <= 512, "TMEM");
+};
+
 template <int WP, int D>
 struct CbRowsSmem {
-  static constexpr int AT = atoms_of<D>(), BN = CbKeys<WP>::BN, KHT = CbKeys<WP>::KHT, KS = 4;
-  static constexpr int kQ = 0, kDO = AT * kTileBytes, kRing = 2 * AT * kTileBytes;
+  static constexpr int AT = atoms_of<D>(), BN = CbKeys<WP>::BN, KHT = CbKeys<WP>::KHT, NB = CbRowsDims<D>::NB;
+  static constexpr int KS = D == 64 ? 8 : 4;
+  static constexpr int kRing = 0;
   static constexpr int kKV = AT * BN * kRowBytes;              // K or V of a step
   static constexpr int kHl = 2 * kKV;                          // within a stage: hl of the step, by 64 queries
   static constexpr int kHlBlock = KHT * kCbRow * 4;
   static constexpr int kStage = kHl + cb_align(2 * kHlBlock);
-  static constexpr int kBars = kRing + KS * kStage;
+  static constexpr int kBwStride = WP + 4;                     // floats: rows 16-byte aligned, in different banks
+  static constexpr int kBw = kRing + KS * kStage;              // [128] rw rows
+  static constexpr int kDh = kBw + kBlockM * kBwStride * 4;    // [128][65] drel_h
+  static constexpr int kBars = kDh + kBlockM * 65 * 4;
   static constexpr int kMisc = kBars + kCbBars * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory");
-  static_assert(KS * kStage >= kBlockM * (WP + 1) * 4, "the drel_w sums are joined in the ring");
+  static_assert(KS * kStage >= NB * kBlockM * (WP + 1) * 4, "the drel_w sums are joined in the ring");
 };
 
 template <int D>
 struct CbColsSmem {
-  static constexpr int AT = atoms_of<D>(), KS = D == 64 ? 4 : 3;
-  static constexpr int kK = 0, kV = AT * kTileBytes, kRing = 2 * AT * kTileBytes;
+  static constexpr int AT = atoms_of<D>(), KS = D == 64 ? 6 : 3;
+  static constexpr bool kTmemA = D == 64;                      // k and v are read from TMEM, else from here
+  static constexpr int kK = 0, kV = AT * kTileBytes, kRing = kTmemA ? 0 : 2 * AT * kTileBytes;
   static constexpr int kQ = AT * 64 * kRowBytes;               // Q or dO of a step
   static constexpr int kBias = 2 * kQ;                         // within a stage: W rows of rw, then the key tile's
   // grid rows of hl (128 consecutive keys touch at most 127 / W + 2 of them, and at most H), then -D
@@ -94,8 +113,9 @@ struct CbCta {
   uint32_t tbase;
 };
 
+// `on_a`, `on_step`, `all`: threads that arrive on kCbAFull, on a step's kCbPFull, on kCbJoin.
 template <class SM>
-__device__ __forceinline__ CbCta cb_setup(uint8_t* smem_raw, int warp) {
+__device__ __forceinline__ CbCta cb_setup(uint8_t* smem_raw, int warp, int on_a, int on_step, int all) {
   CbCta c;
   const uint32_t raw = smem_u32(smem_raw);
   c.smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -105,7 +125,7 @@ __device__ __forceinline__ CbCta cb_setup(uint8_t* smem_raw, int warp) {
   if (threadIdx.x == 0) {
     *c.abort_flag = 0;
     for (int i = 0; i < kCbBars; ++i) {
-      const int n = (i >= kCbPFull && i < kCbPFull + 2) ? kBlockM : (i == kCbJoin ? 2 * kBlockM : 1);
+      const int n = i == kCbAFull ? on_a : ((i >= kCbPFull && i < kCbPFull + 3) ? on_step : (i == kCbJoin ? all : 1));
       mbar_init(&c.bars[i], n);
     }
     fence_mbar_init();
@@ -128,6 +148,25 @@ __device__ __forceinline__ void cb_teardown(uint32_t tbase, int warp) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
+}
+
+// Row `row` of a [BH, N, D] tensor (zeros if !valid) into TMEM as an A operand: this thread's lane, D / 2
+// columns of packed pairs.  Reading A from TMEM leaves shared memory, which a 128 x 64 product
+// would keep busy for 48 cycles a step of 16 (4 KB of A, 2 KB of B; the product takes 32), to B.
+template <int D>
+__device__ __forceinline__ void cb_row_to_tmem(const void* src, size_t row, bool valid, uint32_t taddr) {
+  #pragma unroll
+  for (int h = 0; h < D / 64; ++h) {
+    uint32_t u[32];
+    #pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (valid) v = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(src) + row * D + 64 * h + 8 * c));
+      u[4 * c] = v.x, u[4 * c + 1] = v.y, u[4 * c + 2] = v.z, u[4 * c + 3] = v.w;
+    }
+    tmem_st32(taddr + 32 * h, u);
+  }
+  tmem_wait_st();
 }
 
 // What a CTA computes: a whole unit (a 128-row tile of a head), or a piece of one of the
@@ -153,93 +192,90 @@ struct CbUnit {
 
 // ---------------------------------------------------------------------------
 // prep: one CTA per (128 queries, head).  Reads 4 (H + W) bytes (fp32 bias) and
-// 4 D of out and dO per query and writes 4.25 (H + W): bound by memory.
-constexpr int kCbPrepThreads = 256;
+// 4 D of out and dO per query and writes 4 (H + W): bound by memory.  Half of the threads take rel_h, half
+// rel_w, a query's row each: all of its loads are in flight at once, and every store is a run of queries.
+constexpr int kCbPrepThreads = 2 * kBlockM;
+
+// A row of L <= 64 bias values in base 2, in fp32 (unused entries are left alone).
+__device__ __forceinline__ void cb_load_row(const void* src, size_t at, int L, int fmt, float (&x)[64]) {
+  if (fmt == kF32 && L % 4 == 0) {
+    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(src) + at);
+    #pragma unroll
+    for (int c = 0; c < 16; ++c)
+      if (4 * c < L) {
+        const float4 v = __ldg(p + c);
+        x[4 * c] = kLog2e * v.x, x[4 * c + 1] = kLog2e * v.y, x[4 * c + 2] = kLog2e * v.z, x[4 * c + 3] = kLog2e * v.w;
+      }
+  } else if (fmt != kF32 && L % 8 == 0) {
+    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(src) + at);
+    #pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (8 * c < L) {
+        float v[8];
+        unpack8(__ldg(p + c), v, fmt);
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) x[8 * c + e] = kLog2e * v[e];
+      }
+  } else {
+    #pragma unroll
+    for (int c = 0; c < 64; ++c)
+      if (c < L) x[c] = kLog2e * load_elem(src, at + c, fmt);
+  }
+}
 
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kCbPrepThreads) relpos_cb_prep_kernel(const CbArgs a) {
-  constexpr int fmt = BF16 ? kBF16 : kF16, LANES = D / 8, WARPS = kCbPrepThreads / 32;
-  __shared__ float tr[64][kBlockM + 1];
-  __shared__ float s_lse[kBlockM];
+  constexpr int fmt = BF16 ? kBF16 : kF16, LANES = D / 8;
   const int bh = blockIdx.y, n0 = blockIdx.x * kBlockM;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = min(kBlockM, a.N - n0);
-  const float inf = __int_as_float(0x7f800000);
   const size_t row0 = static_cast<size_t>(bh) * a.N + n0;
-  if (threadIdx.x < kBlockM) {
-    // a row without keys (lse = -inf) takes +inf, so that its P is exactly 0, and so does a row past N
-    const float l = threadIdx.x < rows ? a.lse[row0 + threadIdx.x] : inf;
-    s_lse[threadIdx.x] = l == -inf ? inf : l;
-  }
-  #pragma unroll 2
-  for (int r = threadIdx.x / LANES; r < kBlockM; r += kCbPrepThreads / LANES) {
-    const int c = threadIdx.x % LANES;
+  const float inf = __int_as_float(0x7f800000);
+  #pragma unroll
+  for (int i = 0; i < kBlockM * LANES / kCbPrepThreads; ++i) {
+    const int r = threadIdx.x / LANES + i * (kCbPrepThreads / LANES), c = threadIdx.x % LANES;
     float s = 0.f;
     if (r < rows) {
       const size_t at = (row0 + r) * D + 8 * c;
-      const uint4 g = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.dout) + at));
-      const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
-      float o[8];
-      if (a.out_fmt == kF32) {
-        const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.out) + at);
-        const float4 lo = __ldg(p), hi = __ldg(p + 1);
-        o[0] = lo.x, o[1] = lo.y, o[2] = lo.z, o[3] = lo.w, o[4] = hi.x, o[5] = hi.y, o[6] = hi.z, o[7] = hi.w;
-      } else {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.out) + at));
-        const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 t = unpack_in(uw[i], fmt);
-          o[2 * i] = t.x;
-          o[2 * i + 1] = t.y;
-        }
-      }
+      float g[8], o[8];
+      load8(a.dout, at, g, fmt);
+      load8(a.out, at, o, a.out_fmt);
       #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 t = unpack_in(gw[i], fmt);
-        s = fmaf(t.x, o[2 * i], s);
-        s = fmaf(t.y, o[2 * i + 1], s);
-      }
+      for (int e = 0; e < 8; ++e) s = fmaf(g[e], o[e], s);
     }
     #pragma unroll
     for (int o = 1; o < LANES; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (c == 0) a.nD[static_cast<size_t>(bh) * a.n_blocks * 64 + n0 + r] = -s;
   }
-  #pragma unroll 1
-  for (int part = 0; part < 2; ++part) {
-    const int L = part == 0 ? a.H : a.W;
-    const void* src = part == 0 ? a.rel_h : a.rel_w;
-    float* dst = (part == 0 ? a.hl : a.rw) + (static_cast<size_t>(bh) * a.n_blocks + 2 * blockIdx.x) * L * kCbRow;
-    __syncthreads();   // s_lse is written; the other part's rows are read
-    #pragma unroll 4
-    for (int r = warp; r < rows; r += WARPS)
-      for (int c = lane; c < L; c += 32) tr[c][r] = load_elem(src, (row0 + r) * L + c, a.bias_fmt);
-    __syncthreads();
-    for (int c = warp; c < L; c += WARPS)
-      #pragma unroll
-      for (int r = lane; r < kBlockM; r += 32) {
-        float v;
-        if (part == 0) v = r < rows ? kLog2e * tr[c][r] - s_lse[r] : -inf;
-        else v = r < rows ? kLog2e * tr[c][r] : 0.f;
-        dst[(static_cast<size_t>(r >> 6) * L + c) * kCbRow + (r & 63)] = v;
-      }
+  const bool is_w = threadIdx.x >= kBlockM;
+  const int r = threadIdx.x & (kBlockM - 1), L = is_w ? a.W : a.H;
+  float x[64];
+  // rows past N take rw = 0 and hl = -inf, and so does a row without keys (lse = -inf)
+  float off = 0.f;
+  if (r < rows) {
+    if (!is_w) off = a.lse[row0 + r];
+    cb_load_row(is_w ? a.rel_w : a.rel_h, (row0 + r) * L, L, a.bias_fmt, x);
   }
+  const bool none = !is_w && (r >= rows || off == -inf);
+  float* dst = (is_w ? a.rw : a.hl) + (static_cast<size_t>(bh) * a.n_blocks + 2 * blockIdx.x + (r >> 6)) * L * kCbRow;
+  #pragma unroll
+  for (int c = 0; c < 64; ++c)
+    if (c < L) dst[cb_at(c, r & 63)] = none ? -inf : (r < rows ? x[c] - off : 0.f);
 }
 
 // ---------------------------------------------------------------------------
-// rows.  TMEM columns: S_b [128 b, 128 b + 64), dP_b 64 further, dZ_b [256 + 32 b, ...) as packed
-// pairs, dq [320, 320 + D).
+// rows.  What a step of 64 keys costs an SM: the products 384 cycles (head_dim 64), the exponents 256
+// and the packed fp32 arithmetic about 400 on each scheduler.
 template <int WP, bool BF16, int D>
-__global__ void __launch_bounds__(kCbThreads, 1)
-relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                      const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+__global__ void __launch_bounds__(CbRowsDims<D>::kThreads, 1)
+relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const CbArgs a) {
   using SM = CbRowsSmem<WP, D>;
-  constexpr int KHT = SM::KHT, BN = SM::BN, KS = SM::KS, AT = SM::AT;
+  using DM = CbRowsDims<D>;
+  constexpr int KHT = SM::KHT, BN = SM::BN, KS = SM::KS, AT = SM::AT, NB = DM::NB;
   constexpr int fmt = BF16 ? kBF16 : kF16;
   extern __shared__ uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const CbCta cta = cb_setup<SM>(smem_raw, warp);
+  const CbCta cta = cb_setup<SM>(smem_raw, warp, 2 * kBlockM, kBlockM, NB * kBlockM);
   uint8_t* smem = cta.smem;
   uint64_t* bars = cta.bars;
   volatile int* abort_flag = cta.abort_flag;
@@ -250,17 +286,12 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   const int bh = unit.bh, steps = unit.i1 - unit.i0;
   auto stage = [&](int i) { return smem + SM::kRing + (i % KS) * SM::kStage; };
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- TMA
-    if (lane == 0) {
+  if (warp < 4) {
+    regs_release<DM::kRegsCtl>();
+    if (warp == 0 && lane == 0) {
+      // -------------------------------------------------------------- TMA
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
-      mbar_arrive_expect_tx(&bars[kCbAFull], 2 * AT * kTileBytes);
-      #pragma unroll
-      for (int t = 0; t < AT; ++t) {
-        tma_load_3d(smem + SM::kQ + t * kTileBytes, &tm_q, &bars[kCbAFull], 64 * t, unit.tile * kBlockM, bh);
-        tma_load_3d(smem + SM::kDO + t * kTileBytes, &tm_do, &bars[kCbAFull], 64 * t, unit.tile * kBlockM, bh);
-      }
       const float* hl = a.hl + (static_cast<size_t>(bh) * a.n_blocks + 2 * unit.tile) * a.H * kCbRow;
       for (int i = 0; i < steps; ++i) {
         if (!mbar_wait(&bars[kCbRingEmpty + i % KS], ((i / KS) & 1) ^ 1, abort_flag, status)) break;
@@ -277,90 +308,98 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         for (int b = 0; b < 2; ++b)
           bulk_load(stage(i) + SM::kHl + b * SM::kHlBlock, hl + (static_cast<size_t>(b) * a.H + kh0) * kCbRow, hb, full);
       }
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    constexpr uint32_t id_s = idesc_f16(kBlockM, BN, fmt, fmt, 0, 0);   // S, dP: both K-major
-    constexpr uint32_t id_n = idesc_f16(kBlockM, 64, fmt, fmt, 0, 1);   // dZ k: k N-major, 64 columns at a time
-    const uint64_t d_q = sdesc_sw128(smem_u32(smem + SM::kQ), 16, 1024);
-    const uint64_t d_do = sdesc_sw128(smem_u32(smem + SM::kDO), 16, 1024);
-    const uint64_t d_ring = sdesc_sw128(smem_u32(smem + SM::kRing), 16, 1024);
-    constexpr uint32_t kStep = SM::kStage >> 4, kV = SM::kKV >> 4, kA = kTileBytes >> 4, kB = (BN * kRowBytes) >> 4;
-    auto issue_s = [&](int i) {
-      const uint64_t k = d_ring + (i % KS) * kStep;
-      const uint32_t t = tbase + 128u * (i & 1);
-      #pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-        umma_ss_w(t, d_q + (c / 4) * kA + 2 * (c % 4), k + (c / 4) * kB + 2 * (c % 4), id_s, c > 0);
-      #pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-        umma_ss_w(t + 64, d_do + (c / 4) * kA + 2 * (c % 4), k + kV + (c / 4) * kB + 2 * (c % 4), id_s, c > 0);
-      umma_commit_w(&bars[kCbSFull + (i & 1)]);
-    };
-    bool ok = warp_all(mbar_wait(&bars[kCbAFull], 0, abort_flag, status));
-    for (int i = 0; ok && i < min(2, steps); ++i) {
-      ok = warp_all(mbar_wait(&bars[kCbRingFull + i % KS], 0, abort_flag, status));
-      if (!ok) break;
-      tc_fence_after();
-      issue_s(i);
-    }
-    for (int i = 0; ok && i < steps; ++i) {
-      ok = warp_all(mbar_wait(&bars[kCbPFull + (i & 1)], (i >> 1) & 1, abort_flag, status));
-      if (!ok) break;
-      if (i + 2 < steps) {   // first what the warpgroup that has just finished waits for next
-        ok = warp_all(mbar_wait(&bars[kCbRingFull + (i + 2) % KS], ((i + 2) / KS) & 1, abort_flag, status));
+    } else if (warp == 1) {
+      // -------------------------------------------------------------- MMA issuer
+      constexpr uint32_t id_s = idesc_f16(kBlockM, BN, fmt, fmt, 0, 0);   // S, dP: both K-major
+      constexpr uint32_t id_n = idesc_f16(kBlockM, 64, fmt, fmt, 0, 1);   // dZ k: k N-major, 64 columns at a time
+      const uint64_t d_ring = sdesc_sw128(smem_u32(smem + SM::kRing), 16, 1024);
+      constexpr uint32_t kStep = SM::kStage >> 4, kV = SM::kKV >> 4, kB = (BN * kRowBytes) >> 4;
+      // S and dP of step i: its buffer is free once the products of step i - NB are complete
+      auto next_s = [&](int i) -> bool {
+        if (i >= NB && !warp_all(mbar_wait(&bars[kCbAccDone + i % NB], (i / NB - 1) & 1, abort_flag, status))) return false;
+        if (!warp_all(mbar_wait(&bars[kCbRingFull + i % KS], (i / KS) & 1, abort_flag, status))) return false;
+        tc_fence_after();
+        const uint64_t k = d_ring + (i % KS) * kStep;
+        const uint32_t t = tbase + 128u * (i % NB);
+        #pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+          umma_ts_w(t, tbase + DM::tmQ + 8 * c, k + (c / 4) * kB + 2 * (c % 4), id_s, c > 0);
+        #pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+          umma_ts_w(t + 64, tbase + DM::tmDO + 8 * c, k + kV + (c / 4) * kB + 2 * (c % 4), id_s, c > 0);
+        umma_commit_w(&bars[kCbSFull + i % NB]);
+        return true;
+      };
+      bool ok = warp_all(mbar_wait(&bars[kCbAFull], 0, abort_flag, status));
+      if (ok) tc_fence_after();
+      for (int i = 0; ok && i < min(NB - 1, steps); ++i) ok = next_s(i);
+      for (int i = 0; ok && i < steps; ++i) {
+        if (i + NB - 1 < steps && !(ok = next_s(i + NB - 1))) break;
+        ok = warp_all(mbar_wait(&bars[kCbPFull + i % NB], (i / NB) & 1, abort_flag, status));
         if (!ok) break;
         tc_fence_after();
-        issue_s(i + 2);
-      }
-      tc_fence_after();
-      #pragma unroll
-      for (int t = 0; t < AT; ++t)
         #pragma unroll
-        for (int c = 0; c < BN / 16; ++c)
-          umma_ts_w(tbase + 320 + 64 * t, tbase + 256 + 32 * (i & 1) + 8 * c, d_ring + (i % KS) * kStep + t * kB + 128 * c,
-                    id_n, (i > 0 || c > 0) ? 1u : 0u);
-      umma_commit_w(&bars[kCbAccDone + (i & 1)]);
-      umma_commit_w(&bars[kCbRingEmpty + i % KS]);
+        for (int t = 0; t < AT; ++t)
+          #pragma unroll
+          for (int c = 0; c < BN / 16; ++c)
+            umma_ts_w(tbase + DM::tmDQ + 64 * t, tbase + 128 * (i % NB) + 8 * c,
+                      d_ring + (i % KS) * kStep + t * kB + 128 * c, id_n, (i > 0 || c > 0) ? 1u : 0u);
+        umma_commit_w(&bars[kCbAccDone + i % NB]);
+        umma_commit_w(&bars[kCbRingEmpty + i % KS]);
+      }
+      // every product issued above completes before TMEM is read at the end or released
+      umma_commit_w(&bars[kCbAllDone]);
+      mbar_wait_budget(&bars[kCbAllDone], 0, kWaitBudgetCycles);
+      __syncwarp();
     }
-    // every product issued above completes before TMEM is read at the end or released
-    umma_commit_w(&bars[kCbAllDone]);
-    mbar_wait_budget(&bars[kCbAllDone], 0, kWaitBudgetCycles);
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax threads
+    regs_claim<DM::kRegsSmx>();
     const int H = a.H, W = a.W, N = a.N;
-    const int wg = (warp - 2) >> 2, wq = warp & 3, r = wq * 32 + lane;
+    const int wg = (warp >> 2) - 1, wq = warp & 3, r = wq * 32 + lane;
     const int n = unit.tile * kBlockM + r;
     const bool row_valid = n < N;
     const size_t row = static_cast<size_t>(bh) * N + n;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t tS = tbase + lanes + 128 * wg, tdP = tS + 64, tdZ = tbase + lanes + 256 + 32 * wg;
+    const uint32_t tS = tbase + lanes + 128 * wg, tdP = tS + 64;
     const float NEG_INF = -__int_as_float(0x7f800000);
     const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
-    float bw[WP], dRW[WP];
+    if (wg < 2) {
+      cb_row_to_tmem<D>(wg == 0 ? a.q : a.dout, row, row_valid, tbase + lanes + (wg == 0 ? DM::tmQ : DM::tmDO));
+      tc_fence_before();
+      mbar_arrive(&bars[kCbAFull]);
+    }
+    float* bw_row = reinterpret_cast<float*>(smem + SM::kBw) + r * SM::kBwStride;
+    float* dh_row = reinterpret_cast<float*>(smem + SM::kDh) + r * 65;
     {
-      const float* src = a.rw + (static_cast<size_t>(bh) * a.n_blocks + 2 * unit.tile + (r >> 6)) * W * kCbRow + (r & 63);
-      #pragma unroll
-      for (int kw = 0; kw < WP; ++kw) {
-        bw[kw] = kw < W ? __ldg(src + kw * kCbRow) : NEG_INF;
-        dRW[kw] = 0.f;
-      }
+      // this thread's rw row, a part by each group
+      const float* src = a.rw + (static_cast<size_t>(bh) * a.n_blocks + 2 * unit.tile + (r >> 6)) * W * kCbRow;
+      #pragma unroll 8
+      for (int kw = wg; kw < WP; kw += NB) bw_row[kw] = kw < W ? __ldg(src + cb_at(kw, r & 63)) : NEG_INF;
     }
     const float nDn = __ldg(a.nD + static_cast<size_t>(bh) * a.n_blocks * 64 + n);
     const float2 nD = make_float2(nDn, nDn);
-    bool ok = true;
-    for (int i = wg; ok && i < steps; i += 2) {
+    float dRW[WP];
+    #pragma unroll
+    for (int kw = 0; kw < WP; ++kw) dRW[kw] = 0.f;
+    auto join = [&](int phase) {
+      mbar_arrive(&bars[kCbJoin]);
+      return warp_all(mbar_wait(&bars[kCbJoin], phase, abort_flag, status));
+    };
+    bool ok = join(0);   // bw_row is complete
+    for (int i = wg; ok && i < steps; i += NB) {
       const int kh0 = (unit.i0 + i) * KHT;
       ok = warp_all(mbar_wait(&bars[kCbRingFull + i % KS], (i / KS) & 1, abort_flag, status));
       if (!ok) break;
       float bh_[KHT];
       {
-        const float* hl = reinterpret_cast<const float*>(stage(i) + SM::kHl + (r >> 6) * SM::kHlBlock) + (r & 63);
+        // row g of the stage is grid row kh0 + g, whose chunks are permuted by its own number
+        const float* hl = reinterpret_cast<const float*>(stage(i) + SM::kHl + (r >> 6) * SM::kHlBlock);
         #pragma unroll
-        for (int g = 0; g < KHT; ++g) bh_[g] = (KHT == 1 || kh0 + g < H) ? hl[g * kCbRow] : NEG_INF;
+        for (int g = 0; g < KHT; ++g)
+          bh_[g] = (KHT == 1 || kh0 + g < H) ? hl[cb_at(kh0 + g, r & 63) - kh0 * kCbRow] : NEG_INF;
       }
-      ok = warp_all(mbar_wait(&bars[kCbSFull + wg], (i >> 1) & 1, abort_flag, status));
+      ok = warp_all(mbar_wait(&bars[kCbSFull + wg], (i / NB) & 1, abort_flag, status));
       if (!ok) break;
       tc_fence_after();
       float2 dRH[KHT];   // even and odd columns apart
@@ -379,69 +418,63 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
         }
         uint32_t pk[8];
         #pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-          const int col = cb + k, g = col / WP, kw = col % WP;
-          const float2 s2 = make_float2(__uint_as_float(us[cur][k]), __uint_as_float(us[cur][k + 1]));
-          const float2 dp = make_float2(__uint_as_float(up[cur][k]), __uint_as_float(up[cur][k + 1]));
-          const float2 b2 = fadd2(make_float2(bw[kw], bw[kw + 1]), make_float2(bh_[g], bh_[g]));
-          const float2 x = ffma2(s2, sl2, b2);
-          const float2 d = __fmul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), fadd2(dp, nD));
-          const float2 acc = fadd2(make_float2(dRW[kw], dRW[kw + 1]), d);
-          dRW[kw] = acc.x;
-          dRW[kw + 1] = acc.y;
-          dRH[g] = fadd2(dRH[g], d);
-          pk[k / 2] = pack_in(d.x, d.y, fmt);
-        }
-        if (bb == 0 && i >= 2) {   // this group's last dZ has been read before it is overwritten
-          ok = warp_all(mbar_wait(&bars[kCbAccDone + wg], ((i >> 1) - 1) & 1, abort_flag, status));
-          if (!ok) {
-            tmem_wait_ld();
-            break;
+        for (int k4 = 0; k4 < 16; k4 += 4) {
+          const int g = (cb + k4) / WP, kw = (cb + k4) % WP;
+          const float4 w4 = *reinterpret_cast<const float4*>(bw_row + kw);
+          #pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            const int k = k4 + e;
+            const float2 w2 = e == 0 ? make_float2(w4.x, w4.y) : make_float2(w4.z, w4.w);
+            const float2 s2 = make_float2(__uint_as_float(us[cur][k]), __uint_as_float(us[cur][k + 1]));
+            const float2 dp = make_float2(__uint_as_float(up[cur][k]), __uint_as_float(up[cur][k + 1]));
+            const float2 x = ffma2(s2, sl2, fadd2(w2, make_float2(bh_[g], bh_[g])));
+            const float2 d = __fmul2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), fadd2(dp, nD));
+            const float2 acc = fadd2(make_float2(dRW[kw + e], dRW[kw + e + 1]), d);
+            dRW[kw + e] = acc.x;
+            dRW[kw + e + 1] = acc.y;
+            dRH[g] = fadd2(dRH[g], d);
+            pk[k / 2] = pack_in(d.x, d.y, fmt);
           }
-          tc_fence_after();
         }
-        tmem_st8(tdZ + cb / 2, pk);
+        tmem_st8(tS + cb / 2, pk);   // dZ over columns of S that this thread has read
       }
-      if (!ok) break;
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&bars[kCbPFull + wg]);
-      if (row_valid) {
-        #pragma unroll
-        for (int g = 0; g < KHT; ++g)
-          if (KHT == 1 || kh0 + g < H) a.drel_h[row * H + kh0 + g] = dRH[g].x + dRH[g].y;
-      }
+      #pragma unroll
+      for (int g = 0; g < KHT; ++g)
+        if (KHT == 1 || kh0 + g < H) dh_row[i * KHT + g] = dRH[g].x + dRH[g].y;
     }
     if (ok) ok = warp_all(mbar_wait(&bars[kCbAllDone], 0, abort_flag, status));
-    // drel_w: the two groups' sums, added in the (now idle) ring and stored row by row
+    // drel_w: the groups' sums, side by side in the (now idle) ring, added as they are stored
     float* sum = reinterpret_cast<float*>(smem + SM::kRing);
-    auto join = [&](int phase) {
-      mbar_arrive(&bars[kCbJoin]);
-      return warp_all(mbar_wait(&bars[kCbJoin], phase, abort_flag, status));
-    };
-    if (ok && wg == 1) {
+    constexpr int kSum = kBlockM * (WP + 1);
+    if (ok) {
       #pragma unroll
-      for (int kw = 0; kw < WP; ++kw) sum[r * (WP + 1) + kw] = dRW[kw];
+      for (int kw = 0; kw < WP; ++kw) sum[wg * kSum + r * (WP + 1) + kw] = dRW[kw];
+      ok = join(1);
     }
-    if (ok) ok = join(0);
-    if (ok && wg == 0) {
-      #pragma unroll
-      for (int kw = 0; kw < WP; ++kw) sum[r * (WP + 1) + kw] += dRW[kw];
-    }
-    if (ok) ok = join(1);
     if (ok) {
       const int n0 = unit.tile * kBlockM, rows = min(kBlockM, N - n0);
+      const size_t row0 = static_cast<size_t>(bh) * N + n0;
       float* part = unit.piece < 0 ? nullptr : a.parts_rows + static_cast<size_t>(unit.piece) * kBlockM * (D + W);
-      float* dst = part ? part + kBlockM * D : a.drel_w + (static_cast<size_t>(bh) * N + n0) * W;
-      for (int rr = warp - 2; rr < rows; rr += 8)
-        for (int c = lane; c < W; c += 32) dst[rr * W + c] = sum[rr * (WP + 1) + c];
-      // dq: each group half of the columns
+      float* dw = part ? part + kBlockM * D : a.drel_w + row0 * W;
+      const float* dh = reinterpret_cast<const float*>(smem + SM::kDh);
+      const int h0 = unit.i0 * KHT, hn = min(H, unit.i1 * KHT) - h0;
+      for (int rr = warp - 4; rr < rows; rr += 4 * NB) {
+        for (int c = lane; c < W; c += 32) {
+          float v = sum[rr * (WP + 1) + c];
+          #pragma unroll
+          for (int b = 1; b < NB; ++b) v += sum[b * kSum + rr * (WP + 1) + c];
+          dw[rr * W + c] = v;
+        }
+        for (int c = lane; c < hn; c += 32) a.drel_h[(row0 + rr) * H + h0 + c] = dh[rr * 65 + c];
+      }
+      // dq, 32 columns at a time
       tc_fence_after();
-      #pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-        const int c0 = wg * (D / 2) + 32 * h;
+      for (int c0 = 32 * wg; c0 < D; c0 += 32 * NB) {
         uint32_t u[32];
-        tmem_ld32(tbase + lanes + 320 + c0, u);
+        tmem_ld32(tbase + lanes + DM::tmDQ + c0, u);
         tmem_wait_ld();
         if (part) {   // column chunks of four, chunk by chunk: a warp's rows lie together
           #pragma unroll
@@ -451,10 +484,12 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                             __uint_as_float(u[4 * c + 3]));
         } else if (row_valid) {
           #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            st_grad4(a.dq, row * D + c0 + 4 * c, a.scale * __uint_as_float(u[4 * c]),
-                     a.scale * __uint_as_float(u[4 * c + 1]), a.scale * __uint_as_float(u[4 * c + 2]),
-                     a.scale * __uint_as_float(u[4 * c + 3]), a.grad_fmt);
+          for (int c = 0; c < 32; c += 8) {
+            float v[8];
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = a.scale * __uint_as_float(u[c + e]);
+            store8(a.dq, row * D + c0 + c, v, a.grad_fmt);
+          }
         }
       }
     }
@@ -464,24 +499,26 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 
 // ---------------------------------------------------------------------------
 // cols.  128 consecutive keys of a head, whatever its grid, one per TMEM lane.  TMEM columns:
-// S^T_b [128 b, 128 b + 64), dP^T_b 64 further.  head_dim 64: P^T_b [256 + 64 b, ...), dZ^T_b 32
-// further, dv [384, 448), dk [448, 512).  head_dim 128: dv [256, 384), dk [384, 512), and P^T_b and
-// dZ^T_b lie over the columns of S^T_b and dP^T_b that the threads have read, so the next step of
-// a buffer waits until its products are complete.
+// S^T_b [128 b, 128 b + 64), dP^T_b 64 further, dv [256, 256 + D), dk, then (head_dim 64) k and v
+// as packed pairs.  P^T_b and dZ^T_b lie over S^T_b and dP^T_b, each thread's over columns that it has
+// read.  Shared memory bounds it: a step's operands, bias and their reads keep it busy for about
+// 900 cycles (head_dim 64; 1800 with 128, where TMEM has no room for k and v).
 template <bool BF16, int D>
-__global__ void __launch_bounds__(kCbThreads, 1)
+__global__ void __launch_bounds__(kCbColsThreads, 1)
 relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const CbArgs a) {
   using SM = CbColsSmem<D>;
   constexpr int KS = SM::KS, AT = SM::AT;
-  constexpr bool kOver = D == 128;   // P^T and dZ^T over S^T and dP^T
-  constexpr uint32_t tmP = kOver ? 0 : 256, tmZ = kOver ? 64 : 288, kPStep = kOver ? 128 : 64;
-  constexpr uint32_t tmDV = kOver ? 256 : 384, tmDK = tmDV + D;
+  constexpr bool kTmemA = SM::kTmemA;
+  constexpr uint32_t tmDV = 256, tmDK = tmDV + D, tmK = tmDK + D, tmV = tmK + D / 2;
+  static_assert((kTmemA ? tmV + D / 2 : tmDK + D) <= 512, "TMEM");
+  // the 16 queries c of P^T and dZ^T: each half of a step over its own columns
+  auto at_step = [](int c) { return static_cast<uint32_t>(32 * (c >> 1) + 8 * (c & 1)); };
   constexpr int fmt = BF16 ? kBF16 : kF16;
   extern __shared__ uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const CbCta cta = cb_setup<SM>(smem_raw, warp);
+  const CbCta cta = cb_setup<SM>(smem_raw, warp, kTmemA ? 2 * kBlockM : 1, 2 * kBlockM, 1);
   uint8_t* smem = cta.smem;
   uint64_t* bars = cta.bars;
   volatile int* abort_flag = cta.abort_flag;
@@ -500,11 +537,13 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     if (lane == 0) {
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_do);
-      mbar_arrive_expect_tx(&bars[kCbAFull], 2 * AT * kTileBytes);
-      #pragma unroll
-      for (int t = 0; t < AT; ++t) {
-        tma_load_3d(smem + SM::kK + t * kTileBytes, &tm_k, &bars[kCbAFull], 64 * t, m0, bh);
-        tma_load_3d(smem + SM::kV + t * kTileBytes, &tm_v, &bars[kCbAFull], 64 * t, m0, bh);
+      if (!kTmemA) {
+        mbar_arrive_expect_tx(&bars[kCbAFull], 2 * AT * kTileBytes);
+        #pragma unroll
+        for (int t = 0; t < AT; ++t) {
+          tma_load_3d(smem + SM::kK + t * kTileBytes, &tm_k, &bars[kCbAFull], 64 * t, m0, bh);
+          tma_load_3d(smem + SM::kV + t * kTileBytes, &tm_v, &bars[kCbAFull], 64 * t, m0, bh);
+        }
       }
       const uint32_t wb = static_cast<uint32_t>(a.W) * kCbRow * 4, hb = static_cast<uint32_t>(kh_count) * kCbRow * 4;
       for (int i = 0; i < steps; ++i) {
@@ -531,60 +570,71 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     const uint64_t d_v = sdesc_sw128(smem_u32(smem + SM::kV), 16, 1024);
     const uint64_t d_ring = sdesc_sw128(smem_u32(smem + SM::kRing), 16, 1024);
     constexpr uint32_t kStep = SM::kStage >> 4, kDO = SM::kQ >> 4, kA = kTileBytes >> 4, kB = (64 * kRowBytes) >> 4;
-    auto issue_s = [&](int i) {
+    // S^T and dP^T of step i: its buffer is free once the products of step i - 2 are complete
+    auto next_s = [&](int i) -> bool {
+      if (i >= 2 && !warp_all(mbar_wait(&bars[kCbAccDone + (i & 1)], (i / 2 - 1) & 1, abort_flag, status))) return false;
+      if (!warp_all(mbar_wait(&bars[kCbRingFull + i % KS], (i / KS) & 1, abort_flag, status))) return false;
+      tc_fence_after();
       const uint64_t q = d_ring + (i % KS) * kStep;
       const uint32_t t = tbase + 128u * (i & 1);
       #pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-        umma_ss_w(t, d_k + (c / 4) * kA + 2 * (c % 4), q + (c / 4) * kB + 2 * (c % 4), id_s, c > 0);
+      for (int c = 0; c < D / 16; ++c) {
+        const uint64_t b = q + (c / 4) * kB + 2 * (c % 4);
+        if (kTmemA) umma_ts_w(t, tbase + tmK + 8 * c, b, id_s, c > 0);
+        else umma_ss_w(t, d_k + (c / 4) * kA + 2 * (c % 4), b, id_s, c > 0);
+      }
       #pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-        umma_ss_w(t + 64, d_v + (c / 4) * kA + 2 * (c % 4), q + kDO + (c / 4) * kB + 2 * (c % 4), id_s, c > 0);
+      for (int c = 0; c < D / 16; ++c) {
+        const uint64_t b = q + kDO + (c / 4) * kB + 2 * (c % 4);
+        if (kTmemA) umma_ts_w(t + 64, tbase + tmV + 8 * c, b, id_s, c > 0);
+        else umma_ss_w(t + 64, d_v + (c / 4) * kA + 2 * (c % 4), b, id_s, c > 0);
+      }
       umma_commit_w(&bars[kCbSFull + (i & 1)]);
-    };
-    auto next_s = [&](int i) -> bool {
-      if (!warp_all(mbar_wait(&bars[kCbRingFull + i % KS], (i / KS) & 1, abort_flag, status))) return false;
-      tc_fence_after();
-      issue_s(i);
       return true;
     };
     bool ok = warp_all(mbar_wait(&bars[kCbAFull], 0, abort_flag, status));
-    for (int i = 0; ok && i < min(2, steps); ++i) ok = next_s(i);
+    if (ok) {
+      tc_fence_after();
+      ok = next_s(0);
+    }
     for (int i = 0; ok && i < steps; ++i) {
+      if (i + 1 < steps && !(ok = next_s(i + 1))) break;
       ok = warp_all(mbar_wait(&bars[kCbPFull + (i & 1)], (i >> 1) & 1, abort_flag, status));
       if (!ok) break;
-      if (!kOver && i + 2 < steps && !(ok = next_s(i + 2))) break;
       tc_fence_after();
       const uint64_t q = d_ring + (i % KS) * kStep;
-      const uint32_t p = tbase + tmP + kPStep * (i & 1), z = tbase + tmZ + kPStep * (i & 1);
+      const uint32_t p = tbase + 128u * (i & 1), z = p + 64;
       #pragma unroll
       for (int t = 0; t < AT; ++t)
         #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const uint32_t acc = (i > 0 || c > 0) ? 1u : 0u;
-          umma_ts_w(tbase + tmDV + 64 * t, p + 8 * c, q + kDO + t * kB + 128 * c, id_n, acc);
-          umma_ts_w(tbase + tmDK + 64 * t, z + 8 * c, q + t * kB + 128 * c, id_n, acc);
+          umma_ts_w(tbase + tmDV + 64 * t, p + at_step(c), q + kDO + t * kB + 128 * c, id_n, acc);
+          umma_ts_w(tbase + tmDK + 64 * t, z + at_step(c), q + t * kB + 128 * c, id_n, acc);
         }
       umma_commit_w(&bars[kCbAccDone + (i & 1)]);
       umma_commit_w(&bars[kCbRingEmpty + i % KS]);
-      if (kOver && i + 2 < steps) {
-        ok = warp_all(mbar_wait(&bars[kCbAccDone + (i & 1)], (i >> 1) & 1, abort_flag, status)) && next_s(i + 2);
-      }
     }
     umma_commit_w(&bars[kCbAllDone]);
     mbar_wait_budget(&bars[kCbAllDone], 0, kWaitBudgetCycles);
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax threads
-    const int wg = (warp - 2) >> 2, wq = warp & 3, m = wq * 32 + lane;
+    // groups 0 and 2 take the even steps, 1 and 3 the odd ones, each 32 of a step's 64 queries
+    const int wg = ((warp - 2) >> 2) & 1, half = (warp - 2) >> 3, wq = warp & 3, m = wq * 32 + lane;
     const bool key_valid = m0 + m < a.N;
     const int key = min(m0 + m, a.N - 1);   // lanes without a key compute what nobody stores
     const int kh = key / a.W, kw = key - kh * a.W;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tbase + lanes + 128 * wg, tdP = tS + 64;
-    const uint32_t tP = tbase + lanes + tmP + kPStep * wg, tZ = tbase + lanes + tmZ + kPStep * wg;
-    const int rw_at = kw * kCbRow, hl_at = (a.W + kh - kh_first) * kCbRow;
+    const int rw_at = kw * kCbRow, rw_x = kw & 7, hl_at = (a.W + kh - kh_first) * kCbRow, hl_x = kh & 7;
     const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
+    if (kTmemA && half == 0) {
+      cb_row_to_tmem<D>(wg == 0 ? a.k : a.v, static_cast<size_t>(bh) * a.N + m0 + m, key_valid,
+                        tbase + lanes + (wg == 0 ? tmK : tmV));
+      tc_fence_before();
+      mbar_arrive(&bars[kCbAFull]);
+    }
     bool ok = true;
     for (int i = wg; ok && i < steps; i += 2) {
       ok = warp_all(mbar_wait(&bars[kCbRingFull + i % KS], (i / KS) & 1, abort_flag, status));
@@ -595,21 +645,21 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       if (!ok) break;
       tc_fence_after();
       uint32_t us[2][16], up[2][16];
-      tmem_ld16(tS, us[0]);
-      tmem_ld16(tdP, up[0]);
+      tmem_ld16(tS + 32 * half, us[0]);
+      tmem_ld16(tdP + 32 * half, up[0]);
       #pragma unroll
-      for (int bb = 0; bb < 4; ++bb) {
-        const int cb = 16 * bb, cur = bb & 1;
+      for (int bb = 0; bb < 2; ++bb) {
+        const int cb = 32 * half + 16 * bb, cur = bb & 1;
         tmem_wait_ld();
-        if (bb < 3) {
+        if (bb < 1) {
           tmem_ld16(tS + cb + 16, us[cur ^ 1]);
           tmem_ld16(tdP + cb + 16, up[cur ^ 1]);
         }
         uint32_t pp[8], pz[8];
         #pragma unroll
         for (int k = 0; k < 16; k += 4) {
-          const float4 w4 = *reinterpret_cast<const float4*>(bias + rw_at + cb + k);
-          const float4 h4 = *reinterpret_cast<const float4*>(bias + hl_at + cb + k);
+          const float4 w4 = *reinterpret_cast<const float4*>(bias + rw_at + ((((cb + k) >> 2) ^ rw_x) << 2));
+          const float4 h4 = *reinterpret_cast<const float4*>(bias + hl_at + ((((cb + k) >> 2) ^ hl_x) << 2));
           const float4 d4 = *reinterpret_cast<const float4*>(nDs + cb + k);
           #pragma unroll
           for (int e = 0; e < 4; e += 2) {
@@ -625,32 +675,25 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             pz[(k + e) / 2] = pack_in(z.x, z.y, fmt);
           }
         }
-        if (!kOver && bb == 0 && i >= 2) {   // this group's last P^T and dZ^T have been read
-          ok = warp_all(mbar_wait(&bars[kCbAccDone + wg], ((i >> 1) - 1) & 1, abort_flag, status));
-          if (!ok) {
-            tmem_wait_ld();
-            break;
-          }
-          tc_fence_after();
-        }
-        tmem_st8(tP + cb / 2, pp);
-        tmem_st8(tZ + cb / 2, pz);
+        tmem_st8(tS + at_step(2 * half + bb), pp);
+        tmem_st8(tdP + at_step(2 * half + bb), pz);
       }
-      if (!ok) break;
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&bars[kCbPFull + wg]);
     }
     if (ok) ok = warp_all(mbar_wait(&bars[kCbAllDone], 0, abort_flag, status));
     if (ok) {
-      // group 0 stores dv, group 1 dk (tcgen05.ld is warp-collective: every lane loads)
+      // the even steps' groups store dv, the odd ones' dk, half of the columns each (tcgen05.ld is
+      // warp-collective: every lane loads)
       tc_fence_after();
       const size_t row = static_cast<size_t>(bh) * a.N + m0 + m;
       float* part = unit.piece < 0 ? nullptr : a.parts_cols + static_cast<size_t>(unit.piece) * kBlockM * 2 * D + wg * kBlockM * D;
       void* dst = wg == 0 ? a.dv : a.dk;
       const float mul = wg == 0 ? 1.f : a.scale;
       #pragma unroll
-      for (int h = 0; h < D / 32; ++h) {
+      for (int hh = 0; hh < D / 64; ++hh) {
+        const int h = half * (D / 64) + hh;
         uint32_t u[32];
         tmem_ld32(tbase + lanes + (wg == 0 ? tmDV : tmDK) + 32 * h, u);
         tmem_wait_ld();
@@ -662,9 +705,12 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
                             __uint_as_float(u[4 * c + 3]));
         } else if (key_valid) {
           #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            st_grad4(dst, row * D + 32 * h + 4 * c, mul * __uint_as_float(u[4 * c]), mul * __uint_as_float(u[4 * c + 1]),
-                     mul * __uint_as_float(u[4 * c + 2]), mul * __uint_as_float(u[4 * c + 3]), a.grad_fmt);
+          for (int c = 0; c < 32; c += 8) {
+            float v[8];
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = mul * __uint_as_float(u[c + e]);
+            store8(dst, row * D + 32 * h + c, v, a.grad_fmt);
+          }
         }
       }
     }
@@ -673,11 +719,13 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
 }
 
 // ---------------------------------------------------------------------------
-// join: the pieces of a split unit added in order.  Blocks [0, rows_tail) take the rows kernel's
-// units, the rest the cols kernel's; thread (r, y) takes the chunks y, y + 4, ... of row r.
+// join: the pieces of a split unit added in order.  Blocks [0, rows_tail) in x take the rows kernel's
+// units, the rest the cols kernel's; thread (r, y) of block y takes chunk 2 blockIdx.y + y of row r.
+constexpr int kCbJoinThreads = 256;
+
 template <int D>
-__global__ void __launch_bounds__(512) relpos_cb_join_kernel(const CbArgs a, int rows_tail) {
-  const int r = threadIdx.x & 127, y = threadIdx.x >> 7;
+__global__ void __launch_bounds__(kCbJoinThreads) relpos_cb_join_kernel(const CbArgs a, int rows_tail) {
+  const int r = threadIdx.x & 127, c = 2 * blockIdx.y + (threadIdx.x >> 7);
   const bool rows = static_cast<int>(blockIdx.x) < rows_tail;
   const int t = rows ? blockIdx.x : blockIdx.x - rows_tail;
   const int split = rows ? a.rows_split : a.cols_split;
@@ -686,10 +734,9 @@ __global__ void __launch_bounds__(512) relpos_cb_join_kernel(const CbArgs a, int
   const int per = kBlockM * (rows ? D + a.W : 2 * D);
   const float* part = (rows ? a.parts_rows : a.parts_cols) + static_cast<size_t>(t) * split * per;
   const size_t row0 = static_cast<size_t>(bh) * a.N + n0;
-  const bool valid = n0 + r < a.N;
-  const int chunks = rows ? D / 4 : D / 2;
-  for (int c = y; c < chunks; c += 4) {
+  if (c < (rows ? D / 4 : D / 2)) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    #pragma unroll 4
     for (int p = 0; p < split; ++p) {
       const float4 v = reinterpret_cast<const float4*>(part + static_cast<size_t>(p) * per)[c * kBlockM + r];
       s.x += v.x;
@@ -700,12 +747,14 @@ __global__ void __launch_bounds__(512) relpos_cb_join_kernel(const CbArgs a, int
     const bool first = c < D / 4;   // dq or dv, else dk
     const float mul = rows || !first ? a.scale : 1.f;
     void* dst = rows ? a.dq : (first ? a.dv : a.dk);
-    if (valid) st_grad4(dst, (row0 + r) * D + 4 * (first ? c : c - D / 4), mul * s.x, mul * s.y, mul * s.z, mul * s.w, a.grad_fmt);
+    if (n0 + r < a.N)
+      st_grad4(dst, (row0 + r) * D + 4 * (first ? c : c - D / 4), mul * s.x, mul * s.y, mul * s.z, mul * s.w, a.grad_fmt);
   }
   if (!rows) return;
   const int n = min(kBlockM, a.N - n0) * a.W;
-  for (int e = threadIdx.x; e < n; e += 512) {
+  for (int e = blockIdx.y * kCbJoinThreads + threadIdx.x; e < n; e += gridDim.y * kCbJoinThreads) {
     float s = 0.f;
+    #pragma unroll 4
     for (int p = 0; p < split; ++p) s += part[static_cast<size_t>(p) * per + kBlockM * D + e];
     a.drel_w[row0 * a.W + e] = s;
   }

@@ -1,6 +1,8 @@
 // Launch of the compact-bias backward for one head dimension; included by one .cu for each, so that
 // the build compiles them side by side.
 #pragma once
+#include <atomic>
+
 #include "compact_backward.cuh"
 
 namespace dera {
@@ -14,9 +16,20 @@ template <int WP, bool BF16, int D>
 static cudaError_t launch_cb_rows(const CbMaps& m, const CbArgs& a, unsigned grid, cudaStream_t s) {
   auto kernel = relpos_cb_rows_kernel<WP, BF16, D>;
   using SM = CbRowsSmem<WP, D>;
-  const cudaError_t e = cb_smem(kernel, SM::kAlloc);
+  using DM = CbRowsDims<D>;
+  cudaError_t e = cb_smem(kernel, SM::kAlloc);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kCbThreads, SM::kAlloc, s>>>(m.q, m.dout, m.kg, m.vg, a);
+  // The register split needs the launch pool it was computed for; a build that compiled to fewer
+  // registers is refused rather than launched into a wait that never ends.
+  static std::atomic<int> fits{0};   // 0 unknown, 1 fits, -1 refused
+  if (fits.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    fits.store(fa.numRegs * (DM::NB + 1) >= DM::kRegsCtl + DM::NB * DM::kRegsSmx ? 1 : -1, std::memory_order_relaxed);
+  }
+  if (fits.load(std::memory_order_relaxed) < 0) return cudaErrorInvalidKernelImage;
+  kernel<<<grid, DM::kThreads, SM::kAlloc, s>>>(m.kg, m.vg, a);
   return cudaGetLastError();
 }
 
@@ -54,11 +67,11 @@ static cudaError_t launch_cb(const CbMaps& m, const CbArgs& a, cudaStream_t s) {
   auto cols = relpos_cb_cols_kernel<BF16, D>;
   e = cb_smem(cols, CbColsSmem<D>::kAlloc);
   if (e != cudaSuccess) return e;
-  cols<<<cgrid, kCbThreads, CbColsSmem<D>::kAlloc, s>>>(m.q64, m.dout64, m.k, m.v, a);
+  cols<<<cgrid, kCbColsThreads, CbColsSmem<D>::kAlloc, s>>>(m.q64, m.dout64, m.k, m.v, a);
   e = cudaGetLastError();
   const int joins = rs.tail(units) + cs.tail(units);
   if (e != cudaSuccess || joins == 0) return e;
-  relpos_cb_join_kernel<D><<<joins, 512, 0, s>>>(a, rs.tail(units));
+  relpos_cb_join_kernel<D><<<dim3(joins, D / 4), kCbJoinThreads, 0, s>>>(a, rs.tail(units));
   return cudaGetLastError();
 }
 

@@ -355,8 +355,7 @@ dera_status dera_relpos_attention_backward(const void* q, const void* k, const v
   DERA_TRY(check_workspace(workspace, workspace_bytes, L.total, dev));
   const int N = H * W, WP = cb_width(W), KHT = WP <= 16 ? 4 : (WP <= 32 ? 2 : 1);
   CbMaps m;
-  if (!map_rows(&m.q, q, in_dtype, BH, N, head_dim) || !map_rows(&m.dout, dout, in_dtype, BH, N, head_dim) ||
-      !map_rows(&m.q64, q, in_dtype, BH, N, head_dim, 64) || !map_rows(&m.dout64, dout, in_dtype, BH, N, head_dim, 64) ||
+  if (!map_rows(&m.q64, q, in_dtype, BH, N, head_dim, 64) || !map_rows(&m.dout64, dout, in_dtype, BH, N, head_dim, 64) ||
       !map_keys(&m.kg, k, in_dtype, BH, H, W, head_dim, WP, KHT) ||
       !map_keys(&m.vg, v, in_dtype, BH, H, W, head_dim, WP, KHT) ||
       !map_rows(&m.k, k, in_dtype, BH, N, head_dim) || !map_rows(&m.v, v, in_dtype, BH, N, head_dim))
@@ -364,6 +363,9 @@ dera_status dera_relpos_attention_backward(const void* q, const void* k, const v
   char* ws = static_cast<char*>(workspace);
   auto at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
   CbArgs a = {};
+  a.q = q;
+  a.k = k;
+  a.v = v;
   a.rel_h = rel_h;
   a.rel_w = rel_w;
   a.lse = lse;

@@ -48,10 +48,18 @@ cudaError_t launch_qk(QkArgs& a, const QkPlan& p, int head_dim, int mode, bool b
                       float* dqw, float* dkw, cudaStream_t s);
 
 // Compact-bias backward (compact_backward.cuh).
-constexpr int kCbRow = 68;   // floats of a 64-query row of hl or rw (272 bytes: rows start in different
-                             // banks and stay 16-byte aligned)
+// hl and rw are kept by blocks of 64 queries, a row of 64 floats for each grid row (column), so that
+// what a step needs is one run of whole 256-byte rows.  The 16-byte chunks of row i are permuted by
+// i % 8: threads that read the same queries of neighbouring rows then hit different banks.
+constexpr int kCbRow = 64;
+__host__ __device__ constexpr int cb_at(int row, int query) {
+  return row * kCbRow + ((((query >> 2) ^ (row & 7))) << 2) + (query & 3);
+}
 
 struct CbArgs {
+  const void* q;        // [BH, N, D]
+  const void* k;
+  const void* v;
   const void* rel_h;    // [BH, N, H] bias dtype
   const void* rel_w;    // [BH, N, W]
   const float* lse;     // [BH, N] base 2
@@ -88,7 +96,6 @@ int cb_width(int W);
 int cb_rows_steps(int H, int W);
 
 struct CbMaps {
-  CUtensorMap q, dout;          // 128-row tiles (rows kernel)
   CUtensorMap q64, dout64;      // 64-row tiles (cols kernel)
   CUtensorMap kg, vg;           // by grid rows (rows kernel)
   CUtensorMap k, v;             // 128-row tiles (cols kernel)
