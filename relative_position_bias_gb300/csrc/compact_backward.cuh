@@ -30,7 +30,10 @@
 
 namespace dera {
 
-constexpr int kCbColsThreads = 64 + 512;   // TMA warp, MMA warp, two pairs of softmax warpgroups
+constexpr int kCbColsThreads = 128 + 512;   // TMA, S and dP, accumulators, idle; two pairs of softmax warpgroups
+// registers at launch (the most that 640 threads get), and what the two kinds of warps make of them
+constexpr int kCbColsLaunchRegs = 96, kCbColsRegsCtl = 40, kCbColsRegsSmx = 104;
+static_assert(kCbColsRegsCtl + 4 * kCbColsRegsSmx <= 5 * kCbColsLaunchRegs, "register split exceeds the launch pool");
 
 // Key steps of the rows kernel: KHT whole grid rows of WP >= W columns, so that a column's kw
 // is known at compile time and a thread's rel_w row and drel_w sums stay in registers.
@@ -49,8 +52,10 @@ enum : int {
   kCbSFull = kCbRingEmpty + 8,     // [3] S and dP of a step are in TMEM
   kCbPFull = kCbSFull + 3,         // [3] the softmax threads have read S and dP and written dZ (and P)
   kCbAccDone = kCbPFull + 3,       // [3] the products that read dZ (and P) are complete
-  kCbAllDone = kCbAccDone + 3,     // every product is complete
-  kCbJoin = kCbAllDone + 1,        // the softmax threads among themselves
+  kCbAllDone = kCbAccDone + 3,     // every product of the accumulators is complete
+  kCbSDone = kCbAllDone + 1,       // and every S and dP
+  kCbSFree = kCbSDone + 1,         // [2] cols: S^T and dP^T of a step are in registers
+  kCbJoin = kCbSFree + 2,        // the softmax threads among themselves
   kCbBars = kCbJoin + 1
 };
 
@@ -62,7 +67,7 @@ constexpr int cb_align(int x) { return (x + 1023) / 1024 * 1024; }
 template <int D>
 struct CbRowsDims {
   static constexpr int NB = D == 64 ? 3 : 2;
-  static constexpr int kThreads = 128 * (NB + 1);   // warp 0 TMA, warp 1 MMA, warps 2 and 3 idle, then the softmax threads
+  static constexpr int kThreads = 128 * (NB + 1);   // TMA, S and dP, accumulators, idle; then the softmax threads
   static constexpr int kLaunchRegs = NB == 3 ? 128 : 168, kRegsCtl = 56, kRegsSmx = NB == 3 ? 152 : 224;
   static_assert(kRegsCtl + NB * kRegsSmx <= (NB + 1) * kLaunchRegs, "register split exceeds the launch pool");
   // TMEM columns: S_b [128 b, 128 b + 64) (dZ_b over it), dP_b 64 further, dq, then q and dO as packed pairs
@@ -125,7 +130,7 @@ __device__ __forceinline__ CbCta cb_setup(uint8_t* smem_raw, int warp, int on_a,
   if (threadIdx.x == 0) {
     *c.abort_flag = 0;
     for (int i = 0; i < kCbBars; ++i) {
-      const int n = i == kCbAFull ? on_a : ((i >= kCbPFull && i < kCbPFull + 3) ? on_step : (i == kCbJoin ? all : 1));
+      const int n = i == kCbAFull ? on_a : (((i >= kCbPFull && i < kCbPFull + 3) || i == kCbSFree || i == kCbSFree + 1) ? on_step : (i == kCbJoin ? all : 1));
       mbar_init(&c.bars[i], n);
     }
     fence_mbar_init();
@@ -275,6 +280,7 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
   constexpr int fmt = BF16 ? kBF16 : kF16;
   extern __shared__ uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_launch_dependents();   // cols reads nothing of this kernel: its blocks fill the SMs that run out of these
   const CbCta cta = cb_setup<SM>(smem_raw, warp, 2 * kBlockM, kBlockM, NB * kBlockM);
   uint8_t* smem = cta.smem;
   uint64_t* bars = cta.bars;
@@ -309,15 +315,17 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
           bulk_load(stage(i) + SM::kHl + b * SM::kHlBlock, hl + (static_cast<size_t>(b) * a.H + kh0) * kCbRow, hb, full);
       }
     } else if (warp == 1) {
-      // -------------------------------------------------------------- MMA issuer
-      constexpr uint32_t id_s = idesc_f16(kBlockM, BN, fmt, fmt, 0, 0);   // S, dP: both K-major
-      constexpr uint32_t id_n = idesc_f16(kBlockM, 64, fmt, fmt, 0, 1);   // dZ k: k N-major, 64 columns at a time
+      // -------------------------------------------------------------- S and dP
+      constexpr uint32_t id_s = idesc_f16(kBlockM, BN, fmt, fmt, 0, 0);   // both K-major
       const uint64_t d_ring = sdesc_sw128(smem_u32(smem + SM::kRing), 16, 1024);
       constexpr uint32_t kStep = SM::kStage >> 4, kV = SM::kKV >> 4, kB = (BN * kRowBytes) >> 4;
-      // S and dP of step i: its buffer is free once the products of step i - NB are complete
-      auto next_s = [&](int i) -> bool {
-        if (i >= NB && !warp_all(mbar_wait(&bars[kCbAccDone + i % NB], (i / NB - 1) & 1, abort_flag, status))) return false;
-        if (!warp_all(mbar_wait(&bars[kCbRingFull + i % KS], (i / KS) & 1, abort_flag, status))) return false;
+      bool ok = warp_all(mbar_wait(&bars[kCbAFull], 0, abort_flag, status));
+      for (int i = 0; ok && i < steps; ++i) {
+        // the buffer is free once the products of step i - NB are complete
+        ok = (i < NB || mbar_wait(&bars[kCbAccDone + i % NB], (i / NB - 1) & 1, abort_flag, status)) &&
+             mbar_wait(&bars[kCbRingFull + i % KS], (i / KS) & 1, abort_flag, status);
+        ok = warp_all(ok);
+        if (!ok) break;
         tc_fence_after();
         const uint64_t k = d_ring + (i % KS) * kStep;
         const uint32_t t = tbase + 128u * (i % NB);
@@ -328,15 +336,18 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         for (int c = 0; c < D / 16; ++c)
           umma_ts_w(t + 64, tbase + DM::tmDO + 8 * c, k + kV + (c / 4) * kB + 2 * (c % 4), id_s, c > 0);
         umma_commit_w(&bars[kCbSFull + i % NB]);
-        return true;
-      };
-      bool ok = warp_all(mbar_wait(&bars[kCbAFull], 0, abort_flag, status));
-      if (ok) tc_fence_after();
-      for (int i = 0; ok && i < min(NB - 1, steps); ++i) ok = next_s(i);
-      for (int i = 0; ok && i < steps; ++i) {
-        if (i + NB - 1 < steps && !(ok = next_s(i + NB - 1))) break;
-        ok = warp_all(mbar_wait(&bars[kCbPFull + i % NB], (i / NB) & 1, abort_flag, status));
-        if (!ok) break;
+      }
+      // every product issued here completes before TMEM is released
+      umma_commit_w(&bars[kCbSDone]);
+      mbar_wait_budget(&bars[kCbSDone], 0, kWaitBudgetCycles);
+      __syncwarp();
+    } else if (warp == 2) {
+      // -------------------------------------------------------------- dq += dZ k
+      constexpr uint32_t id_n = idesc_f16(kBlockM, 64, fmt, fmt, 0, 1);   // k N-major, 64 columns at a time
+      const uint64_t d_ring = sdesc_sw128(smem_u32(smem + SM::kRing), 16, 1024);
+      constexpr uint32_t kStep = SM::kStage >> 4, kB = (BN * kRowBytes) >> 4;
+      for (int i = 0; i < steps; ++i) {
+        if (!warp_all(mbar_wait(&bars[kCbPFull + i % NB], (i / NB) & 1, abort_flag, status))) break;
         tc_fence_after();
         #pragma unroll
         for (int t = 0; t < AT; ++t)
@@ -347,7 +358,7 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         umma_commit_w(&bars[kCbAccDone + i % NB]);
         umma_commit_w(&bars[kCbRingEmpty + i % KS]);
       }
-      // every product issued above completes before TMEM is read at the end or released
+      // every product issued here completes before TMEM is read at the end or released
       umma_commit_w(&bars[kCbAllDone]);
       mbar_wait_budget(&bars[kCbAllDone], 0, kWaitBudgetCycles);
       __syncwarp();
@@ -364,20 +375,28 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     const uint32_t tS = tbase + lanes + 128 * wg, tdP = tS + 64;
     const float NEG_INF = -__int_as_float(0x7f800000);
     const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
-    if (wg < 2) {
-      cb_row_to_tmem<D>(wg == 0 ? a.q : a.dout, row, row_valid, tbase + lanes + (wg == 0 ? DM::tmQ : DM::tmDO));
-      tc_fence_before();
-      mbar_arrive(&bars[kCbAFull]);
-    }
     float* bw_row = reinterpret_cast<float*>(smem + SM::kBw) + r * SM::kBwStride;
     float* dh_row = reinterpret_cast<float*>(smem + SM::kDh) + r * 65;
-    {
-      // this thread's rw row, a part by each group
-      const float* src = a.rw + (static_cast<size_t>(bh) * a.n_blocks + 2 * unit.tile + (r >> 6)) * W * kCbRow;
-      #pragma unroll 8
-      for (int kw = wg; kw < WP; kw += NB) bw_row[kw] = kw < W ? __ldg(src + cb_at(kw, r & 63)) : NEG_INF;
-    }
     const float nDn = __ldg(a.nD + static_cast<size_t>(bh) * a.n_blocks * 64 + n);
+    {
+      // this thread's rw row, a part by each group, and q or dO's, all loads in flight at once
+      const float* src = a.rw + (static_cast<size_t>(bh) * a.n_blocks + 2 * unit.tile + (r >> 6)) * W * kCbRow;
+      constexpr int kPart = (WP + NB - 1) / NB;
+      float w[kPart];
+      #pragma unroll
+      for (int e = 0; e < kPart; ++e) {
+        const int kw = wg * kPart + e;
+        w[e] = kw < W ? __ldg(src + cb_at(kw, r & 63)) : NEG_INF;
+      }
+      if (wg < 2) {
+        cb_row_to_tmem<D>(wg == 0 ? a.q : a.dout, row, row_valid, tbase + lanes + (wg == 0 ? DM::tmQ : DM::tmDO));
+        tc_fence_before();
+        mbar_arrive(&bars[kCbAFull]);
+      }
+      #pragma unroll
+      for (int e = 0; e < kPart; ++e)
+        if (wg * kPart + e < WP) bw_row[wg * kPart + e] = w[e];
+    }
     const float2 nD = make_float2(nDn, nDn);
     float dRW[WP];
     #pragma unroll
@@ -461,14 +480,21 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
       float* dw = part ? part + kBlockM * D : a.drel_w + row0 * W;
       const float* dh = reinterpret_cast<const float*>(smem + SM::kDh);
       const int h0 = unit.i0 * KHT, hn = min(H, unit.i1 * KHT) - h0;
+      #pragma unroll 4
       for (int rr = warp - 4; rr < rows; rr += 4 * NB) {
-        for (int c = lane; c < W; c += 32) {
-          float v = sum[rr * (WP + 1) + c];
-          #pragma unroll
-          for (int b = 1; b < NB; ++b) v += sum[b * kSum + rr * (WP + 1) + c];
-          dw[rr * W + c] = v;
+        #pragma unroll
+        for (int cc = 0; cc < WP; cc += 32) {
+          const int c = cc + lane;
+          if (c < W) {
+            float v = sum[rr * (WP + 1) + c];
+            #pragma unroll
+            for (int b = 1; b < NB; ++b) v += sum[b * kSum + rr * (WP + 1) + c];
+            dw[rr * W + c] = v;
+          }
         }
-        for (int c = lane; c < hn; c += 32) a.drel_h[(row0 + rr) * H + h0 + c] = dh[rr * 65 + c];
+        #pragma unroll
+        for (int cc = 0; cc < 64; cc += 32)
+          if (cc + lane < hn) a.drel_h[(row0 + rr) * H + h0 + cc + lane] = dh[rr * 65 + cc + lane];
       }
       // dq, 32 columns at a time
       tc_fence_after();
@@ -500,8 +526,9 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
 // ---------------------------------------------------------------------------
 // cols.  128 consecutive keys of a head, whatever its grid, one per TMEM lane.  TMEM columns:
 // S^T_b [128 b, 128 b + 64), dP^T_b 64 further, dv [256, 256 + D), dk, then (head_dim 64) k and v
-// as packed pairs.  P^T_b and dZ^T_b lie over S^T_b and dP^T_b, each thread's over columns that it has
-// read.  Shared memory bounds it: a step's operands, bias and their reads keep it busy for about
+// as packed pairs, and one P^T and dZ^T, which the threads hold in registers until the last step's have been
+// read.  With 128 there is no room for either: k and v are read from shared memory, and P^T_b and dZ^T_b lie
+// over S^T_b and dP^T_b, each thread's over columns that it has read.  Shared memory bounds it: a step's operands, bias and their reads keep it busy for about
 // 900 cycles (head_dim 64; 1800 with 128, where TMEM has no room for k and v).
 template <bool BF16, int D>
 __global__ void __launch_bounds__(kCbColsThreads, 1)
@@ -511,10 +538,13 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   using SM = CbColsSmem<D>;
   constexpr int KS = SM::KS, AT = SM::AT;
   constexpr bool kTmemA = SM::kTmemA;
-  constexpr uint32_t tmDV = 256, tmDK = tmDV + D, tmK = tmDK + D, tmV = tmK + D / 2;
-  static_assert((kTmemA ? tmV + D / 2 : tmDK + D) <= 512, "TMEM");
-  // the 16 queries c of P^T and dZ^T: each half of a step over its own columns
-  auto at_step = [](int c) { return static_cast<uint32_t>(32 * (c >> 1) + 8 * (c & 1)); };
+  constexpr bool kOver = D == 128;   // P^T and dZ^T over S^T and dP^T
+  constexpr uint32_t tmDV = 256, tmDK = tmDV + D, tmK = tmDK + D, tmV = tmK + D / 2, tmP = tmV + D / 2;
+  static_assert((kOver ? tmDK + D : tmP + 64) <= 512, "TMEM");
+  // P^T of a buffer, dZ^T's distance from it, and the 16 queries c of both
+  auto tm_p = [](int buf) { return kOver ? 128u * buf : tmP; };
+  constexpr uint32_t kZ = kOver ? 64 : 32;
+  auto at_step = [](int c) { return static_cast<uint32_t>(kOver ? 32 * (c >> 1) + 8 * (c & 1) : 8 * c); };
   constexpr int fmt = BF16 ? kBF16 : kF16;
   extern __shared__ uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -532,96 +562,102 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   const int m0 = unit.tile * kBlockM, kh_first = m0 / a.W;
   const int kh_count = (min(m0 + kBlockM, a.N) - 1) / a.W - kh_first + 1;
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- TMA
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_do);
-      if (!kTmemA) {
-        mbar_arrive_expect_tx(&bars[kCbAFull], 2 * AT * kTileBytes);
-        #pragma unroll
-        for (int t = 0; t < AT; ++t) {
-          tma_load_3d(smem + SM::kK + t * kTileBytes, &tm_k, &bars[kCbAFull], 64 * t, m0, bh);
-          tma_load_3d(smem + SM::kV + t * kTileBytes, &tm_v, &bars[kCbAFull], 64 * t, m0, bh);
+  if (warp < 4) {
+    regs_release<kCbColsRegsCtl>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------- TMA
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_do);
+        if (!kTmemA) {
+          mbar_arrive_expect_tx(&bars[kCbAFull], 2 * AT * kTileBytes);
+          #pragma unroll
+          for (int t = 0; t < AT; ++t) {
+            tma_load_3d(smem + SM::kK + t * kTileBytes, &tm_k, &bars[kCbAFull], 64 * t, m0, bh);
+            tma_load_3d(smem + SM::kV + t * kTileBytes, &tm_v, &bars[kCbAFull], 64 * t, m0, bh);
+          }
+        }
+        const uint32_t wb = static_cast<uint32_t>(a.W) * kCbRow * 4, hb = static_cast<uint32_t>(kh_count) * kCbRow * 4;
+        for (int i = 0; i < steps; ++i) {
+          if (!mbar_wait(&bars[kCbRingEmpty + i % KS], ((i / KS) & 1) ^ 1, abort_flag, status)) break;
+          uint64_t* full = &bars[kCbRingFull + i % KS];
+          const int blk = unit.i0 + i;
+          const size_t at = static_cast<size_t>(bh) * a.n_blocks + blk;
+          mbar_arrive_expect_tx(full, 2 * SM::kQ + wb + hb + 256);
+          #pragma unroll
+          for (int t = 0; t < AT; ++t) {
+            tma_load_3d(stage(i) + t * 64 * kRowBytes, &tm_q, full, 64 * t, blk * 64, bh);
+            tma_load_3d(stage(i) + SM::kQ + t * 64 * kRowBytes, &tm_do, full, 64 * t, blk * 64, bh);
+          }
+          bulk_load(stage(i) + SM::kBias, a.rw + at * a.W * kCbRow, wb, full);
+          bulk_load(stage(i) + SM::kBias + wb, a.hl + (at * a.H + kh_first) * kCbRow, hb, full);
+          bulk_load(stage(i) + SM::kND, a.nD + at * 64, 256, full);
         }
       }
-      const uint32_t wb = static_cast<uint32_t>(a.W) * kCbRow * 4, hb = static_cast<uint32_t>(kh_count) * kCbRow * 4;
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- S^T and dP^T
+      constexpr uint32_t id_s = idesc_f16(kBlockM, 64, fmt, fmt, 0, 0);   // both K-major
+      const uint64_t d_k = sdesc_sw128(smem_u32(smem + SM::kK), 16, 1024);
+      const uint64_t d_v = sdesc_sw128(smem_u32(smem + SM::kV), 16, 1024);
+      const uint64_t d_ring = sdesc_sw128(smem_u32(smem + SM::kRing), 16, 1024);
+      constexpr uint32_t kStep = SM::kStage >> 4, kDO = SM::kQ >> 4, kA = kTileBytes >> 4, kB = (64 * kRowBytes) >> 4;
+      bool ok = warp_all(mbar_wait(&bars[kCbAFull], 0, abort_flag, status));
+      for (int i = 0; ok && i < steps; ++i) {
+        // the buffer is free once the products of step i - 2 are complete (kOver), or the threads have read it
+        ok = (i < 2 || mbar_wait(&bars[(kOver ? kCbAccDone : kCbSFree) + (i & 1)], (i / 2 - 1) & 1, abort_flag, status)) &&
+             mbar_wait(&bars[kCbRingFull + i % KS], (i / KS) & 1, abort_flag, status);
+        ok = warp_all(ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t q = d_ring + (i % KS) * kStep;
+        const uint32_t t = tbase + 128u * (i & 1);
+        #pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint64_t b = q + (c / 4) * kB + 2 * (c % 4);
+          if (kTmemA) umma_ts_w(t, tbase + tmK + 8 * c, b, id_s, c > 0);
+          else umma_ss_w(t, d_k + (c / 4) * kA + 2 * (c % 4), b, id_s, c > 0);
+        }
+        #pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint64_t b = q + kDO + (c / 4) * kB + 2 * (c % 4);
+          if (kTmemA) umma_ts_w(t + 64, tbase + tmV + 8 * c, b, id_s, c > 0);
+          else umma_ss_w(t + 64, d_v + (c / 4) * kA + 2 * (c % 4), b, id_s, c > 0);
+        }
+        umma_commit_w(&bars[kCbSFull + (i & 1)]);
+      }
+      umma_commit_w(&bars[kCbSDone]);
+      mbar_wait_budget(&bars[kCbSDone], 0, kWaitBudgetCycles);
+      __syncwarp();
+    } else if (warp == 2) {
+      // ---------------------------------------------------------------- dv += P^T dO, dk += dZ^T q
+      constexpr uint32_t id_n = idesc_f16(kBlockM, 64, fmt, fmt, 0, 1);   // q, dO N-major, 64 columns at a time
+      const uint64_t d_ring = sdesc_sw128(smem_u32(smem + SM::kRing), 16, 1024);
+      constexpr uint32_t kStep = SM::kStage >> 4, kDO = SM::kQ >> 4, kB = (64 * kRowBytes) >> 4;
       for (int i = 0; i < steps; ++i) {
-        if (!mbar_wait(&bars[kCbRingEmpty + i % KS], ((i / KS) & 1) ^ 1, abort_flag, status)) break;
-        uint64_t* full = &bars[kCbRingFull + i % KS];
-        const int blk = unit.i0 + i;
-        const size_t at = static_cast<size_t>(bh) * a.n_blocks + blk;
-        mbar_arrive_expect_tx(full, 2 * SM::kQ + wb + hb + 256);
+        if (!warp_all(mbar_wait(&bars[kCbPFull + (i & 1)], (i >> 1) & 1, abort_flag, status))) break;
+        tc_fence_after();
+        const uint64_t q = d_ring + (i % KS) * kStep;
+        const uint32_t p = tbase + tm_p(i & 1), z = p + kZ;
         #pragma unroll
-        for (int t = 0; t < AT; ++t) {
-          tma_load_3d(stage(i) + t * 64 * kRowBytes, &tm_q, full, 64 * t, blk * 64, bh);
-          tma_load_3d(stage(i) + SM::kQ + t * 64 * kRowBytes, &tm_do, full, 64 * t, blk * 64, bh);
-        }
-        bulk_load(stage(i) + SM::kBias, a.rw + at * a.W * kCbRow, wb, full);
-        bulk_load(stage(i) + SM::kBias + wb, a.hl + (at * a.H + kh_first) * kCbRow, hb, full);
-        bulk_load(stage(i) + SM::kND, a.nD + at * 64, 256, full);
+        for (int t = 0; t < AT; ++t)
+          #pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t acc = (i > 0 || c > 0) ? 1u : 0u;
+            umma_ts_w(tbase + tmDV + 64 * t, p + at_step(c), q + kDO + t * kB + 128 * c, id_n, acc);
+            umma_ts_w(tbase + tmDK + 64 * t, z + at_step(c), q + t * kB + 128 * c, id_n, acc);
+          }
+        umma_commit_w(&bars[kCbAccDone + (i & 1)]);
+        umma_commit_w(&bars[kCbRingEmpty + i % KS]);
       }
+      umma_commit_w(&bars[kCbAllDone]);
+      mbar_wait_budget(&bars[kCbAllDone], 0, kWaitBudgetCycles);
+      __syncwarp();
     }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    constexpr uint32_t id_s = idesc_f16(kBlockM, 64, fmt, fmt, 0, 0);   // S^T, dP^T: both K-major
-    constexpr uint32_t id_n = idesc_f16(kBlockM, 64, fmt, fmt, 0, 1);   // q, dO N-major, 64 columns at a time
-    const uint64_t d_k = sdesc_sw128(smem_u32(smem + SM::kK), 16, 1024);
-    const uint64_t d_v = sdesc_sw128(smem_u32(smem + SM::kV), 16, 1024);
-    const uint64_t d_ring = sdesc_sw128(smem_u32(smem + SM::kRing), 16, 1024);
-    constexpr uint32_t kStep = SM::kStage >> 4, kDO = SM::kQ >> 4, kA = kTileBytes >> 4, kB = (64 * kRowBytes) >> 4;
-    // S^T and dP^T of step i: its buffer is free once the products of step i - 2 are complete
-    auto next_s = [&](int i) -> bool {
-      if (i >= 2 && !warp_all(mbar_wait(&bars[kCbAccDone + (i & 1)], (i / 2 - 1) & 1, abort_flag, status))) return false;
-      if (!warp_all(mbar_wait(&bars[kCbRingFull + i % KS], (i / KS) & 1, abort_flag, status))) return false;
-      tc_fence_after();
-      const uint64_t q = d_ring + (i % KS) * kStep;
-      const uint32_t t = tbase + 128u * (i & 1);
-      #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const uint64_t b = q + (c / 4) * kB + 2 * (c % 4);
-        if (kTmemA) umma_ts_w(t, tbase + tmK + 8 * c, b, id_s, c > 0);
-        else umma_ss_w(t, d_k + (c / 4) * kA + 2 * (c % 4), b, id_s, c > 0);
-      }
-      #pragma unroll
-      for (int c = 0; c < D / 16; ++c) {
-        const uint64_t b = q + kDO + (c / 4) * kB + 2 * (c % 4);
-        if (kTmemA) umma_ts_w(t + 64, tbase + tmV + 8 * c, b, id_s, c > 0);
-        else umma_ss_w(t + 64, d_v + (c / 4) * kA + 2 * (c % 4), b, id_s, c > 0);
-      }
-      umma_commit_w(&bars[kCbSFull + (i & 1)]);
-      return true;
-    };
-    bool ok = warp_all(mbar_wait(&bars[kCbAFull], 0, abort_flag, status));
-    if (ok) {
-      tc_fence_after();
-      ok = next_s(0);
-    }
-    for (int i = 0; ok && i < steps; ++i) {
-      if (i + 1 < steps && !(ok = next_s(i + 1))) break;
-      ok = warp_all(mbar_wait(&bars[kCbPFull + (i & 1)], (i >> 1) & 1, abort_flag, status));
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t q = d_ring + (i % KS) * kStep;
-      const uint32_t p = tbase + 128u * (i & 1), z = p + 64;
-      #pragma unroll
-      for (int t = 0; t < AT; ++t)
-        #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t acc = (i > 0 || c > 0) ? 1u : 0u;
-          umma_ts_w(tbase + tmDV + 64 * t, p + at_step(c), q + kDO + t * kB + 128 * c, id_n, acc);
-          umma_ts_w(tbase + tmDK + 64 * t, z + at_step(c), q + t * kB + 128 * c, id_n, acc);
-        }
-      umma_commit_w(&bars[kCbAccDone + (i & 1)]);
-      umma_commit_w(&bars[kCbRingEmpty + i % KS]);
-    }
-    umma_commit_w(&bars[kCbAllDone]);
-    mbar_wait_budget(&bars[kCbAllDone], 0, kWaitBudgetCycles);
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax threads
+    regs_claim<kCbColsRegsSmx>();
     // groups 0 and 2 take the even steps, 1 and 3 the odd ones, each 32 of a step's 64 queries
-    const int wg = ((warp - 2) >> 2) & 1, half = (warp - 2) >> 3, wq = warp & 3, m = wq * 32 + lane;
+    const int wg = ((warp - 4) >> 2) & 1, half = (warp - 4) >> 3, wq = warp & 3, m = wq * 32 + lane;
     const bool key_valid = m0 + m < a.N;
     const int key = min(m0 + m, a.N - 1);   // lanes without a key compute what nobody stores
     const int kh = key / a.W, kw = key - kh * a.W;
@@ -645,17 +681,20 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
       if (!ok) break;
       tc_fence_after();
       uint32_t us[2][16], up[2][16];
-      tmem_ld16(tS + 32 * half, us[0]);
-      tmem_ld16(tdP + 32 * half, up[0]);
       #pragma unroll
       for (int bb = 0; bb < 2; ++bb) {
-        const int cb = 32 * half + 16 * bb, cur = bb & 1;
-        tmem_wait_ld();
-        if (bb < 1) {
-          tmem_ld16(tS + cb + 16, us[cur ^ 1]);
-          tmem_ld16(tdP + cb + 16, up[cur ^ 1]);
-        }
-        uint32_t pp[8], pz[8];
+        tmem_ld16(tS + 32 * half + 16 * bb, us[bb]);
+        tmem_ld16(tdP + 32 * half + 16 * bb, up[bb]);
+      }
+      tmem_wait_ld();
+      if (!kOver) {   // S^T and dP^T of step i + 2 may go ahead
+        tc_fence_before();
+        mbar_arrive(&bars[kCbSFree + wg]);
+      }
+      uint32_t pp[2][8], pz[2][8];
+      #pragma unroll
+      for (int bb = 0; bb < 2; ++bb) {
+        const int cb = 32 * half + 16 * bb;
         #pragma unroll
         for (int k = 0; k < 16; k += 4) {
           const float4 w4 = *reinterpret_cast<const float4*>(bias + rw_at + ((((cb + k) >> 2) ^ rw_x) << 2));
@@ -666,17 +705,25 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
             const float2 w2 = e == 0 ? make_float2(w4.x, w4.y) : make_float2(w4.z, w4.w);
             const float2 h2 = e == 0 ? make_float2(h4.x, h4.y) : make_float2(h4.z, h4.w);
             const float2 d2 = e == 0 ? make_float2(d4.x, d4.y) : make_float2(d4.z, d4.w);
-            const float2 s2 = make_float2(__uint_as_float(us[cur][k + e]), __uint_as_float(us[cur][k + e + 1]));
-            const float2 dp = make_float2(__uint_as_float(up[cur][k + e]), __uint_as_float(up[cur][k + e + 1]));
+            const float2 s2 = make_float2(__uint_as_float(us[bb][k + e]), __uint_as_float(us[bb][k + e + 1]));
+            const float2 dp = make_float2(__uint_as_float(up[bb][k + e]), __uint_as_float(up[bb][k + e + 1]));
             const float2 x = ffma2(s2, sl2, fadd2(w2, h2));
             const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
             const float2 z = __fmul2_rn(p, fadd2(dp, d2));
-            pp[(k + e) / 2] = pack_in(p.x, p.y, fmt);
-            pz[(k + e) / 2] = pack_in(z.x, z.y, fmt);
+            pp[bb][(k + e) / 2] = pack_in(p.x, p.y, fmt);
+            pz[bb][(k + e) / 2] = pack_in(z.x, z.y, fmt);
           }
         }
-        tmem_st8(tS + at_step(2 * half + bb), pp);
-        tmem_st8(tdP + at_step(2 * half + bb), pz);
+      }
+      if (!kOver && i > 0) {   // the last step's P^T and dZ^T have been read
+        ok = warp_all(mbar_wait(&bars[kCbAccDone + (wg ^ 1)], ((i - 1) >> 1) & 1, abort_flag, status));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      #pragma unroll
+      for (int bb = 0; bb < 2; ++bb) {
+        tmem_st8(tbase + lanes + tm_p(wg) + at_step(2 * half + bb), pp[bb]);
+        tmem_st8(tbase + lanes + tm_p(wg) + kZ + at_step(2 * half + bb), pz[bb]);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -716,6 +763,9 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     }
   }
   cb_teardown(tbase, warp);
+  // rows may still run: this kernel must not be complete before it is, since what follows in the
+  // stream waits for this one
+  grid_wait_prerequisites();
 }
 
 // ---------------------------------------------------------------------------

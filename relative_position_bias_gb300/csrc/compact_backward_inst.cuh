@@ -7,30 +7,50 @@
 
 namespace dera {
 
+// Sets up a kernel whose warps split their registers: the split needs the launch pool it was computed
+// for, and a build that compiled to fewer registers is refused rather than launched into a wait that
+// never ends.
 template <class K>
-static cudaError_t cb_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+static cudaError_t cb_prepare(K kernel, int smem, int launch_regs, std::atomic<int>& fits) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  if (fits.load(std::memory_order_relaxed) == 0) {   // 0 unknown, 1 fits, -1 refused
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    fits.store(fa.numRegs >= launch_regs ? 1 : -1, std::memory_order_relaxed);
+  }
+  return fits.load(std::memory_order_relaxed) > 0 ? cudaSuccess : cudaErrorInvalidKernelImage;
 }
 
 template <int WP, bool BF16, int D>
 static cudaError_t launch_cb_rows(const CbMaps& m, const CbArgs& a, unsigned grid, cudaStream_t s) {
   auto kernel = relpos_cb_rows_kernel<WP, BF16, D>;
   using SM = CbRowsSmem<WP, D>;
-  using DM = CbRowsDims<D>;
-  cudaError_t e = cb_smem(kernel, SM::kAlloc);
+  static std::atomic<int> fits{0};
+  const cudaError_t e = cb_prepare(kernel, SM::kAlloc, CbRowsDims<D>::kLaunchRegs, fits);
   if (e != cudaSuccess) return e;
-  // The register split needs the launch pool it was computed for; a build that compiled to fewer
-  // registers is refused rather than launched into a wait that never ends.
-  static std::atomic<int> fits{0};   // 0 unknown, 1 fits, -1 refused
-  if (fits.load(std::memory_order_relaxed) == 0) {
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, kernel);
-    if (e != cudaSuccess) return e;
-    fits.store(fa.numRegs * (DM::NB + 1) >= DM::kRegsCtl + DM::NB * DM::kRegsSmx ? 1 : -1, std::memory_order_relaxed);
-  }
-  if (fits.load(std::memory_order_relaxed) < 0) return cudaErrorInvalidKernelImage;
-  kernel<<<grid, DM::kThreads, SM::kAlloc, s>>>(m.kg, m.vg, a);
+  kernel<<<grid, CbRowsDims<D>::kThreads, SM::kAlloc, s>>>(m.kg, m.vg, a);
   return cudaGetLastError();
+}
+
+template <bool BF16, int D>
+static cudaError_t launch_cb_cols(const CbMaps& m, const CbArgs& a, unsigned grid, cudaStream_t s) {
+  auto kernel = relpos_cb_cols_kernel<BF16, D>;
+  static std::atomic<int> fits{0};
+  const cudaError_t e = cb_prepare(kernel, CbColsSmem<D>::kAlloc, kCbColsLaunchRegs, fits);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kCbColsThreads);
+  cfg.dynamicSmemBytes = CbColsSmem<D>::kAlloc;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, m.q64, m.dout64, m.k, m.v, a);
 }
 
 template <bool BF16, int D>
@@ -64,11 +84,7 @@ static cudaError_t launch_cb(const CbMaps& m, const CbArgs& a, cudaStream_t s) {
     default: e = launch_cb_rows<64, BF16, D>(m, a, rgrid, s); break;
   }
   if (e != cudaSuccess) return e;
-  auto cols = relpos_cb_cols_kernel<BF16, D>;
-  e = cb_smem(cols, CbColsSmem<D>::kAlloc);
-  if (e != cudaSuccess) return e;
-  cols<<<cgrid, kCbColsThreads, CbColsSmem<D>::kAlloc, s>>>(m.q64, m.dout64, m.k, m.v, a);
-  e = cudaGetLastError();
+  e = launch_cb_cols<BF16, D>(m, a, cgrid, s);
   const int joins = rs.tail(units) + cs.tail(units);
   if (e != cudaSuccess || joins == 0) return e;
   relpos_cb_join_kernel<D><<<dim3(joins, D / 4), kCbJoinThreads, 0, s>>>(a, rs.tail(units));

@@ -18,24 +18,34 @@ int cb_rows_steps(int H, int W) {
   return (H + per - 1) / per;
 }
 
-CbSplit cb_split(int units, int steps, int sms) {
-  // One CTA an SM, so `units` of equal length leave a last wave that is only partly filled.  Its
-  // units are cut into as many pieces as finish them soonest; a piece costs kStart steps
-  // more than the steps it takes (its tiles, the pieces' partial results and the join).
-  constexpr int kStart = 6, kMinSteps = 4;
-  CbSplit s = {units, 1};
-  if (sms <= 0 || units % sms == 0) return s;
-  const int tail = units % sms;
+void cb_split(int units, int rows_steps, int cols_steps, int sms, CbSplit* rows, CbSplit* cols) {
+  // One CTA an SM, first the rows kernel's units, then the cols kernel's, whose CTAs start where the
+  // rows kernel's run out: the 2 * units CTAs leave one last wave that is only partly filled.
+  // Its units, all of them cols' unless there are fewer CTAs than SMs, are cut into as many pieces as
+  // finish them soonest; a piece costs kStart steps more than the steps it takes (its tiles, the
+  // pieces' partial results and the join).
+  constexpr int kStart = 10, kMinSteps = 4;
+  *rows = {units, 1};
+  *cols = {units, 1};
+  if (sms <= 0) return;
+  const long long all = 2ll * units;
+  const int tail = static_cast<int>(all % sms);
+  if (tail == 0) return;
+  const bool few = all < sms;   // every unit is of the last wave
+  const int steps = few ? (rows_steps < cols_steps ? rows_steps : cols_steps) : cols_steps;
+  int pieces = 1;
   long long best = steps + kStart;
   for (int p = 2; p <= steps / kMinSteps; ++p) {
     const long long waves = (static_cast<long long>(tail) * p + sms - 1) / sms;
     const long long cost = waves * ((steps + p - 1) / p + kStart);
     if (cost < best) {
       best = cost;
-      s = {units - tail, p};
+      pieces = p;
     }
   }
-  return s;
+  if (pieces == 1) return;
+  if (few) *rows = {0, pieces};
+  *cols = {few ? 0 : units - (tail < units ? tail : units), pieces};
 }
 
 }  // namespace dera
@@ -149,8 +159,7 @@ struct CbLayout {
     const int N = H * W;
     n_tiles = (N + 127) / 128;
     units = BH * n_tiles;
-    rows = cb_split(units, cb_rows_steps(H, W), sms);
-    cols = cb_split(units, (N + 63) / 64, sms);
+    cb_split(units, cb_rows_steps(H, W), (N + 63) / 64, sms, &rows, &cols);
     const size_t blocks = static_cast<size_t>(BH) * 2 * n_tiles;
     size_t o = 0;
     auto take = [&](size_t floats) {

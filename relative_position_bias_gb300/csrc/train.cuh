@@ -90,7 +90,7 @@ struct CbSplit {
   int tail(int units) const { return split > 1 ? units - full : 0; }
   int blocks(int units) const { return full + (units - full) * split; }
 };
-CbSplit cb_split(int units, int steps, int sms);
+void cb_split(int units, int rows_steps, int cols_steps, int sms, CbSplit* rows, CbSplit* cols);
 // Padded width of the rows kernel's key steps, and its steps for H grid rows.
 int cb_width(int W);
 int cb_rows_steps(int H, int W);
