@@ -165,22 +165,43 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const QkArgs a
   }
 }
 
+// Eight values of a gradient as they lie: 16 bytes, or 32 in fp32.
+template <bool F32>
+struct Grad8 {
+  uint4 u[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, size_t i) {
+    const uint4* at = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * (F32 ? 4 : 2));
+    u[0] = __ldg(at);
+    if (F32) u[F32 ? 1 : 0] = __ldg(at + 1);
+  }
+  __device__ __forceinline__ void get(float (&x)[8], int fmt) const {
+    if (F32) {
+      const uint4 lo = u[0], hi = u[F32 ? 1 : 0];
+      x[0] = __uint_as_float(lo.x), x[1] = __uint_as_float(lo.y), x[2] = __uint_as_float(lo.z), x[3] = __uint_as_float(lo.w);
+      x[4] = __uint_as_float(hi.x), x[5] = __uint_as_float(hi.y), x[6] = __uint_as_float(hi.z), x[7] = __uint_as_float(hi.w);
+    } else {
+      unpack8(u[0], x, fmt);
+    }
+  }
+};
+
 // The weights' gradients are sums over every row of every token: a block takes
 // every gridDim.x-th run of tokens and keeps its slots' sums in registers, one partial row
 // per block, which qk_weight_grad_kernel adds in a fixed order.
-template <bool BF16, int D, int MODE, bool NORM>
-__global__ void __launch_bounds__(kQkThreads) qk_norm_rope_bwd_kernel(const QkArgs a) {
-  constexpr int LANES = D / 8, TOK = kQkThreads / LANES, WARPS = kQkThreads / 32;
+template <bool BF16, int D, int MODE, bool NORM, bool ZF32>
+__global__ void __launch_bounds__(kQkThreads, 3) qk_norm_rope_bwd_kernel(const QkArgs a) {
+  constexpr int LANES = D / 8, TOK = kQkThreads / LANES, WARPS = kQkThreads / 32, U = 4;
   constexpr int fmt = BF16 ? kBF16 : kF16;
   __shared__ float red[WARPS][D];
   const QkBlock blk(a, blockIdx.y);
   const int lane = threadIdx.x & 31, slot = threadIdx.x % LANES;
   const HeadsPtr x = a.x[blk.kind], dx = a.dx[blk.kind];
   const int heads = a.heads[blk.kind];
+  const bool v_rows = blk.kind == 2;   // v's gradient is moved as it is
   float w[8], dw[8];
   #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    w[i] = (NORM && blk.kind < 2) ? load_elem(a.w[blk.kind], 8 * slot + i, a.w_fmt) : 1.f;
+    w[i] = (NORM && !v_rows) ? load_elem(a.w[blk.kind], 8 * slot + i, a.w_fmt) : 1.f;
     dw[i] = 0.f;
   }
   const long long step = static_cast<long long>(gridDim.x) * TOK;
@@ -192,41 +213,46 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_bwd_kernel(const QkAr
     const int n = static_cast<int>(t - b * a.N);
     const size_t zrow = (static_cast<size_t>(b) * heads * a.N + n) * D + 8 * slot;
     const size_t hstep = static_cast<size_t>(a.N) * D;
-    const long long xrow = b * x.sb + n * x.st + 8 * slot, dxrow = b * dx.sb + n * dx.st + 8 * slot;
-    if (blk.kind == 2) {
-      for (int h = blk.h0; h < blk.h1; ++h) {
-        float g[8];
-        load8(a.z[2], zrow + h * hstep, g, a.z_fmt);
-        if (valid) store8(dx.data, dxrow + h * dx.sh, g, a.dx_fmt);
-      }
-      continue;
-    }
+    const uint16_t* xrow = reinterpret_cast<const uint16_t*>(x.data) + b * x.sb + n * x.st + 8 * slot;
+    const long long dxrow = b * dx.sb + n * dx.st + 8 * slot;
     Angles<D, MODE> ang;
-    ang.load(a, t, n, slot, lane);
-    #pragma unroll 2
-    for (int h = blk.h0; h < blk.h1; ++h) {
-      float g[8];
-      load8(a.z[blk.kind], zrow + h * hstep, g, a.z_fmt);
-      float v[8];
-      if (NORM)
-        unpack8(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(x.data) + xrow + h * x.sh)), v, fmt);
-      ang.turn(g, -1.f);
-      if (NORM) {
-        float gx = 0.f;
-        #pragma unroll
-        for (int e = 0; e < 8; ++e) gx = fmaf(g[e] * w[e], v[e], gx);
-        const float r = rsqrtf(mean_square<D>(v) + a.eps);
-        const float m = row_sum<LANES>(gx) * (1.f / D) * r * r;
-        #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (valid) dw[e] = fmaf(g[e], v[e] * r, dw[e]);
-          g[e] = r * fmaf(-m, v[e], g[e] * w[e]);
-        }
+    if (!v_rows) ang.load(a, t, n, slot, lane);
+    for (int h = blk.h0; h < blk.h1; h += U) {
+      Grad8<ZF32> z[U];
+      uint4 xv[U];
+      #pragma unroll
+      for (int i = 0; i < U; ++i) {   // U rows in flight; one past the group reads the last row again
+        const int hh = min(h + i, blk.h1 - 1);
+        z[i].load(a.z[blk.kind], zrow + hh * hstep);
+        if (NORM && !v_rows) xv[i] = __ldg(reinterpret_cast<const uint4*>(xrow + hh * x.sh));
       }
-      if (valid) store8(dx.data, dxrow + h * dx.sh, g, a.dx_fmt);
+      #pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (h + i >= blk.h1) break;
+        float g[8];
+        z[i].get(g, fmt);
+        if (!v_rows) {
+          ang.turn(g, -1.f);
+          if (NORM) {
+            float v[8];
+            unpack8(xv[i], v, fmt);
+            float gx = 0.f;
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) gx = fmaf(g[e] * w[e], v[e], gx);
+            const float r = rsqrtf(mean_square<D>(v) + a.eps);
+            const float m = row_sum<LANES>(gx) * (1.f / D) * r * r;
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              if (valid) dw[e] = fmaf(g[e], v[e] * r, dw[e]);
+              g[e] = r * fmaf(-m, v[e], g[e] * w[e]);
+            }
+          }
+        }
+        if (valid) store8(dx.data, dxrow + (h + i) * dx.sh, g, a.dx_fmt == kF32 ? kF32 : fmt);
+      }
     }
   }
-  if (!NORM || blk.kind == 2) return;
+  if (!NORM || v_rows) return;
   #pragma unroll
   for (int e = 0; e < 8; ++e) {
     #pragma unroll
@@ -238,7 +264,8 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_bwd_kernel(const QkAr
     float v = 0.f;
     #pragma unroll
     for (int i = 0; i < WARPS; ++i) v += red[i][threadIdx.x];
-    const size_t row = static_cast<size_t>(blk.kind) * a.groups[0] * gridDim.x + static_cast<size_t>(blk.y) * gridDim.x + blockIdx.x;
+    const size_t row = (blk.kind == 1 ? static_cast<size_t>(a.groups[0]) * gridDim.x : 0) +
+                       static_cast<size_t>(blk.y) * gridDim.x + blockIdx.x;
     a.parts[row * D + threadIdx.x] = v;
   }
 }

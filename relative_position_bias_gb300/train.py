@@ -10,14 +10,16 @@ exceptions; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
 
 from . import api
-from .api import _check, _code, _expect, _ptr, _stream, _workspace
+from .api import DERA_F32, _check, _expect, _ptr, _workspace
 
 HEADER = os.path.join(os.path.dirname(api.HEADER), "dera_train.h")
+_CODE = api._DTYPE_CODE
 
 
 class _Heads(ctypes.Structure):
@@ -28,12 +30,12 @@ class _Heads(ctypes.Structure):
 
 def declare(lib: ctypes.CDLL) -> None:
     """Signatures of the entry points (called by ``api.load_library``)."""
-    vp, i, f, sz, hp = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(_Heads)
+    vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     szp = ctypes.POINTER(sz)
     for name, args in {
-        "dera_qk_norm_rope": [hp] * 3 + [vp] * 8 + [i] * 8 + [f, i, i, vp],
+        "dera_qk_norm_rope": [vp] * 11 + [i] * 8 + [f, i, i, vp],
         "dera_qk_norm_rope_backward_workspace_size": [i] * 5 + [szp],
-        "dera_qk_norm_rope_backward": [hp] * 2 + [vp] * 8 + [hp] * 3 + [vp] * 2 + [i] * 8 + [f] + [i] * 4 + [vp, sz, vp],
+        "dera_qk_norm_rope_backward": [vp] * 15 + [i] * 8 + [f] + [i] * 4 + [vp, sz, vp],
         "dera_relpos_attention_lse": [vp] * 7 + [i] * 4 + [f] + [i] * 3 + [vp, sz, vp],
         "dera_relpos_attention_backward_workspace_size": [i] * 4 + [szp],
         "dera_relpos_attention_backward": [vp] * 13 + [i] * 4 + [f] + [i] * 4 + [vp, sz, vp],
@@ -45,32 +47,82 @@ def declare(lib: ctypes.CDLL) -> None:
         fn.restype = i
 
 
-def _scratch(need: int, device: torch.device, stream, workspace: torch.Tensor | None) -> tuple:
+# A call of the smallest sizes is bound by what happens before its kernels start, so these helpers
+# ask PyTorch for as little as they can.
+def _dtype(t: torch.dtype) -> int:
+    code = _CODE.get(t)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t}")
+    return code
+
+
+def _want(t: torch.Tensor, shape, name: str) -> None:
+    if t.shape != shape or not t.is_contiguous():
+        _expect(t, shape, name)   # says what is wrong
+
+
+def _launch_stream(device: torch.device, stream) -> int | None:
+    """Handle of the stream to launch on (the current one of `device` unless given)."""
+    if stream is None and device.type == "cuda":
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return api._stream(device, stream)
+
+
+@functools.lru_cache(maxsize=256)
+def _size_on(device_index: int, entry: str, *sizes: int) -> int:
+    """What a workspace-size entry says on a device (a function of the sizes and the device alone)."""
+    n = ctypes.c_size_t(0)
+    with torch.cuda.device(device_index):
+        _check(getattr(api.load_library(), entry)(*sizes, ctypes.byref(n)))
+    return n.value
+
+
+def _size(entry: str, *sizes: int) -> int:
+    """The same on the current device, if there is one."""
+    n = ctypes.c_size_t(0)
+    _check(getattr(api.load_library(), entry)(*sizes, ctypes.byref(n)))
+    return n.value
+
+
+def _scratch(device: torch.device, stream, handle, workspace: torch.Tensor | None, entry: str, *sizes: int) -> tuple:
     """(tensor to keep alive, pointer, bytes) of one call's scratch: the caller's, or a new buffer
-    that the allocator keeps until the work on `stream` is done."""
+    that the allocator keeps until the work on the launching stream is done."""
     if workspace is None:
+        if device.type != "cuda":
+            return None, None, 0
+        need = _size_on(device.index, entry, *sizes)
         if need == 0:
             return None, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if int(stream or 0) != torch.cuda.current_stream(device).cuda_stream:
-            workspace.record_stream(torch.cuda.ExternalStream(int(stream or 0), device=device))
+        if stream is not None and int(handle or 0) != torch.cuda.current_stream(device).cuda_stream:
+            workspace.record_stream(torch.cuda.ExternalStream(int(handle or 0), device=device))
+        return workspace, workspace.data_ptr(), need
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 # ------------------------------------------------------------------------ norms, rotation, layout
-def _heads(t: torch.Tensor, name: str, B: int, N: int, heads: int, d: int) -> _Heads:
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != N or t.shape[2] != heads or t.shape[3] != d:
-        raise ValueError(f"{name}: expected shape {(B, N, heads, d)}, got {tuple(t.shape)}")
-    sb, st, sh, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return _Heads(t.data_ptr(), sb, st, sh)
+def _heads(tensors, shapes, names):
+    """The ``dera_heads`` of some tensors (None: none), one after another, and their addresses."""
+    flat = []
+    for t, shape, name in zip(tensors, shapes, names):
+        if t is None:
+            flat += (0, 0, 0, 0)
+            continue
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        sb, st, sh, sd = t.stride()
+        if sd != 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+        flat += (t.data_ptr(), sb, st, sh)
+    views = (ctypes.c_int64 * len(flat))(*flat)
+    at = ctypes.addressof(views)
+    return views, [None if t is None else at + 32 * k for k, t in enumerate(tensors)]
 
 
 def _same(t: torch.Tensor | None, shape: tuple, dtype, name: str) -> None:
     if t is None:
         return
-    _expect(t, shape, name)
+    _want(t, shape, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
@@ -88,13 +140,13 @@ def _qk_common(q, k, v, q_weight, k_weight, cos, sin, positions):
         raise ValueError("q_weight and k_weight go together")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
-    wcode = api.DERA_F32
+    wcode = DERA_F32
     if q_weight is not None:
         if q_weight.dtype not in (q.dtype, torch.float32):
             raise TypeError("the weights must be float32 or of q's dtype")
         _same(q_weight, (d,), q_weight.dtype, "q_weight")
         _same(k_weight, (d,), q_weight.dtype, "k_weight")
-        wcode = _code(q_weight.dtype)
+        wcode = _dtype(q_weight.dtype)
     rot = rows = 0
     if cos is not None:
         if cos.dim() != 2:
@@ -121,24 +173,21 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None = None
     no norm).  ``cos``, ``sin`` ``[rows, rotary_dim / 2]`` fp32 (None: no rotation), row ``positions[b, n]``
     (int32) or ``n``; pairs ``(i, i + rotary_dim / 2)``, or ``(2i, 2i + 1)`` if ``interleaved``."""
     B, N, hq, hk, d, rot, rows, wcode = _qk_common(q, k, v, q_weight, k_weight, cos, sin, positions)
-    hqs, hks = _heads(q, "q", B, N, hq, d), _heads(k, "k", B, N, hk, d)
-    hvs = None if v is None else _heads(v, "v", B, N, hk, d)
-    q_out = torch.empty((B * hq, N, d), dtype=q.dtype, device=q.device)
-    k_out = torch.empty((B * hk, N, d), dtype=q.dtype, device=q.device)
-    v_out = None if v is None else torch.empty((B * hk, N, d), dtype=q.dtype, device=q.device)
+    views, (hqs, hks, hvs) = _heads((q, k, v), (q.shape, (B, N, hk, d), (B, N, hk, d)), ("q", "k", "v"))
+    dt, dev = q.dtype, q.device
+    q_out = torch.empty((B * hq, N, d), dtype=dt, device=dev)
+    k_out = torch.empty((B * hk, N, d), dtype=dt, device=dev)
+    v_out = None if v is None else torch.empty((B * hk, N, d), dtype=dt, device=dev)
     _check(api.load_library().dera_qk_norm_rope(
         hqs, hks, hvs, _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions), q_out.data_ptr(),
-        k_out.data_ptr(), _ptr(v_out), B, N, hq, hk, d, rot, rows, interleaved, eps, _code(q.dtype), wcode,
-        _stream(q.device, stream)))
+        k_out.data_ptr(), _ptr(v_out), B, N, hq, hk, d, rot, rows, interleaved, eps, _dtype(dt), wcode,
+        _launch_stream(dev, stream)))
     return (q_out, k_out) if v is None else (q_out, k_out, v_out)
 
 
 def qk_norm_rope_backward_workspace_size(B: int, N: int, q_heads: int, kv_heads: int, head_dim: int = 64) -> int:
     """Scratch bytes of :func:`qk_norm_rope_backward` on the current device."""
-    n = ctypes.c_size_t(0)
-    _check(api.load_library().dera_qk_norm_rope_backward_workspace_size(B, N, q_heads, kv_heads, head_dim,
-                                                                        ctypes.byref(n)))
-    return n.value
+    return _size("dera_qk_norm_rope_backward_workspace_size", B, N, q_heads, kv_heads, head_dim)
 
 
 def qk_norm_rope_backward(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor, dk_out: torch.Tensor,
@@ -165,32 +214,29 @@ def qk_norm_rope_backward(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor
         raise ValueError("dv needs dv_out")
     if dk_out.dtype != dq_out.dtype or (dv_out is not None and dv_out.dtype != dq_out.dtype):
         raise TypeError("dq_out, dk_out and dv_out must share a dtype")
-    _expect(dq_out, (B * hq, N, d), "dq_out")
-    _expect(dk_out, (B * hk, N, d), "dk_out")
+    _want(dq_out, (B * hq, N, d), "dq_out")
+    _want(dk_out, (B * hk, N, d), "dk_out")
     if dv_out is not None:
-        _expect(dv_out, (B * hk, N, d), "dv_out")
+        _want(dv_out, (B * hk, N, d), "dv_out")
     dev = q.device
     dq = torch.empty((B, N, hq, d), dtype=gd, device=dev) if dq is None else dq
     dk = torch.empty((B, N, hk, d), dtype=gd, device=dev) if dk is None else dk
     if dv is None and dv_out is not None:
         dv = torch.empty((B, N, hk, d), dtype=gd, device=dev)
-    hdq, hdk = _heads(dq, "dq", B, N, hq, d), _heads(dk, "dk", B, N, hk, d)
-    hdv = None if dv is None else _heads(dv, "dv", B, N, hk, d)
-    hqs, hks = _heads(q, "q", B, N, hq, d), _heads(k, "k", B, N, hk, d)
+    kv = (B, N, hk, d)
+    views, (hqs, hks, hdq, hdk, hdv) = _heads((q, k, dq, dk, dv), (q.shape, kv, q.shape, kv, kv),
+                                              ("q", "k", "dq", "dk", "dv"))
     dqw = torch.empty(d, dtype=torch.float32, device=dev) if norm else None
     dkw = torch.empty(d, dtype=torch.float32, device=dev) if norm else None
-    st = _stream(dev, stream)
+    st = _launch_stream(dev, stream)
     keep, ws, ws_bytes = None, None, 0
-    if norm and dev.type == "cuda":
-        need = 0
-        if workspace is None:
-            with torch.cuda.device(dev):
-                need = qk_norm_rope_backward_workspace_size(B, N, hq, hk, d)
-        keep, ws, ws_bytes = _scratch(need, dev, st, workspace)
+    if norm:
+        keep, ws, ws_bytes = _scratch(dev, stream, st, workspace, "dera_qk_norm_rope_backward_workspace_size", B, N, hq,
+                                      hk, d)
     _check(api.load_library().dera_qk_norm_rope_backward(
         hqs, hks, _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin), _ptr(positions), dq_out.data_ptr(),
         dk_out.data_ptr(), _ptr(dv_out), hdq, hdk, hdv, _ptr(dqw), _ptr(dkw), B, N, hq, hk, d, rot, rows, interleaved,
-        eps, _code(q.dtype), wcode, _code(dq_out.dtype), _code(gd), ws, ws_bytes, st))
+        eps, _dtype(q.dtype), wcode, _dtype(dq_out.dtype), _dtype(gd), ws, ws_bytes, st))
     return dq, dk, dv, dqw, dkw
 
 
@@ -203,29 +249,28 @@ def attention_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h: torc
     out = 0 and lse = -inf.  ``workspace`` as in :func:`~relative_position_bias_gb300.attention`."""
     BH, N, d = q.shape
     scale = d ** -0.5 if scale is None else scale
+    size = (BH, H * W, d)
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _expect(t, (BH, H * W, d), name)
-    _expect(rel_h, (BH, N, H), "rel_h")
-    _expect(rel_w, (BH, N, W), "rel_w")
+        _want(t, size, name)
+    _want(rel_h, (BH, N, H), "rel_h")
+    _want(rel_w, (BH, N, W), "rel_w")
     if k.dtype != q.dtype or v.dtype != q.dtype:
         raise TypeError("q, k, v must share a dtype")
     if rel_h.dtype != rel_w.dtype:
         raise TypeError("rel_h and rel_w must share a dtype")
     out = torch.empty((BH, N, d), dtype=out_dtype or q.dtype, device=q.device)
     lse = torch.empty((BH, N), dtype=torch.float32, device=q.device)
-    st = _stream(q.device, stream)
+    st = _launch_stream(q.device, stream)
     ws, ws_bytes = _workspace(q.device, BH, H, W, d, workspace, st)
     _check(api.load_library().dera_relpos_attention_lse(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(rel_h), _ptr(rel_w), _ptr(out), _ptr(lse), BH, H, W, d, float(scale),
-        _code(q.dtype), _code(rel_h.dtype), _code(out.dtype), ws, ws_bytes, st))
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), rel_h.data_ptr(), rel_w.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        BH, H, W, d, scale, _dtype(q.dtype), _dtype(rel_h.dtype), _dtype(out.dtype), ws, ws_bytes, st))
     return out, lse
 
 
 def attention_backward_workspace_size(BH: int, H: int, W: int, head_dim: int = 64) -> int:
     """Scratch bytes of :func:`attention_backward` for this size on the current device."""
-    n = ctypes.c_size_t(0)
-    _check(api.load_library().dera_relpos_attention_backward_workspace_size(BH, H, W, head_dim, ctypes.byref(n)))
-    return n.value
+    return _size("dera_relpos_attention_backward_workspace_size", BH, H, W, head_dim)
 
 
 def attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h: torch.Tensor, rel_w: torch.Tensor,
@@ -239,11 +284,12 @@ def attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h:
     BH, N, d = q.shape
     scale = d ** -0.5 if scale is None else scale
     gd = grad_dtype or torch.float32
+    size, size_h, size_w = (BH, H * W, d), (BH, N, H), (BH, N, W)
     for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out"), (dout, "dout")):
-        _expect(t, (BH, H * W, d), name)
-    _expect(lse, (BH, N), "lse")
-    _expect(rel_h, (BH, N, H), "rel_h")
-    _expect(rel_w, (BH, N, W), "rel_w")
+        _want(t, size, name)
+    _want(lse, (BH, N), "lse")
+    _want(rel_h, size_h, "rel_h")
+    _want(rel_w, size_w, "rel_w")
     if k.dtype != q.dtype or v.dtype != q.dtype or dout.dtype != q.dtype:
         raise TypeError("q, k, v and dout must share a dtype")
     if rel_h.dtype != rel_w.dtype:
@@ -251,29 +297,24 @@ def attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h:
     if lse.dtype != torch.float32:
         raise TypeError("lse must be float32")
     dev = q.device
-    dq = torch.empty((BH, N, d), dtype=gd, device=dev)
-    dk, dv = torch.empty_like(dq), torch.empty_like(dq)
-    drel_h = torch.empty((BH, N, H), dtype=torch.float32, device=dev)
-    drel_w = torch.empty((BH, N, W), dtype=torch.float32, device=dev)
-    st = _stream(dev, stream)
-    need = 0
-    if workspace is None and dev.type == "cuda":
-        with torch.cuda.device(dev):
-            need = attention_backward_workspace_size(BH, H, W, d)
-    keep, ws, ws_bytes = _scratch(need, dev, st, workspace)
+    dq = torch.empty(size, dtype=gd, device=dev)
+    dk = torch.empty(size, dtype=gd, device=dev)
+    dv = torch.empty(size, dtype=gd, device=dev)
+    drel_h = torch.empty(size_h, dtype=torch.float32, device=dev)
+    drel_w = torch.empty(size_w, dtype=torch.float32, device=dev)
+    st = _launch_stream(dev, stream)
+    keep, ws, ws_bytes = _scratch(dev, stream, st, workspace, "dera_relpos_attention_backward_workspace_size", BH, H, W, d)
     _check(api.load_library().dera_relpos_attention_backward(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(rel_h), _ptr(rel_w), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk),
-        _ptr(dv), _ptr(drel_h), _ptr(drel_w), BH, H, W, d, float(scale), _code(q.dtype), _code(rel_h.dtype),
-        _code(out.dtype), _code(gd), ws, ws_bytes, st))
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), rel_h.data_ptr(), rel_w.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), drel_h.data_ptr(), drel_w.data_ptr(), BH, H, W, d,
+        scale, _dtype(q.dtype), _dtype(rel_h.dtype), _dtype(out.dtype), _dtype(gd), ws, ws_bytes, st))
     return dq, dk, dv, drel_h, drel_w
 
 
 # ------------------------------------------------------------------------------------ projection
 def project_backward_workspace_size(BH: int, H: int, W: int, head_dim: int = 64) -> int:
     """Scratch bytes of :func:`project_backward` for this size on the current device."""
-    n = ctypes.c_size_t(0)
-    _check(api.load_library().dera_relpos_project_backward_workspace_size(BH, H, W, head_dim, ctypes.byref(n)))
-    return n.value
+    return _size("dera_relpos_project_backward_workspace_size", BH, H, W, head_dim)
 
 
 def project_backward(q: torch.Tensor, rel_pos_h: torch.Tensor, rel_pos_w: torch.Tensor, drel_h: torch.Tensor,
@@ -287,25 +328,22 @@ def project_backward(q: torch.Tensor, rel_pos_h: torch.Tensor, rel_pos_w: torch.
     ``grad_dtype`` (default fp32).  The tables' gradients are fp32."""
     BH, N, d = q.shape
     gd = grad_dtype or (torch.float32 if dq is None else dq.dtype)
-    _expect(q, (BH, H * W, d), "q")
-    _expect(rel_pos_h, (2 * H - 1, d), "rel_pos_h")
-    _expect(rel_pos_w, (2 * W - 1, d), "rel_pos_w")
+    size, size_h, size_w = (BH, H * W, d), (2 * H - 1, d), (2 * W - 1, d)
+    _want(q, size, "q")
+    _want(rel_pos_h, size_h, "rel_pos_h")
+    _want(rel_pos_w, size_w, "rel_pos_w")
     if rel_pos_h.dtype != q.dtype or rel_pos_w.dtype != q.dtype:
         raise TypeError("q and the tables must share a dtype")
     _same(drel_h, (BH, N, H), torch.float32, "drel_h")
     _same(drel_w, (BH, N, W), torch.float32, "drel_w")
     _same(dq, (BH, N, d), gd, "dq")
     dev = q.device
-    out = torch.empty((BH, N, d), dtype=gd, device=dev)
-    dth = torch.empty((2 * H - 1, d), dtype=torch.float32, device=dev)
-    dtw = torch.empty((2 * W - 1, d), dtype=torch.float32, device=dev)
-    st = _stream(dev, stream)
-    need = 0
-    if workspace is None and dev.type == "cuda":
-        with torch.cuda.device(dev):
-            need = project_backward_workspace_size(BH, H, W, d)
-    keep, ws, ws_bytes = _scratch(need, dev, st, workspace)
+    out = torch.empty(size, dtype=gd, device=dev)
+    dth = torch.empty(size_h, dtype=torch.float32, device=dev)
+    dtw = torch.empty(size_w, dtype=torch.float32, device=dev)
+    st = _launch_stream(dev, stream)
+    keep, ws, ws_bytes = _scratch(dev, stream, st, workspace, "dera_relpos_project_backward_workspace_size", BH, H, W, d)
     _check(api.load_library().dera_relpos_project_backward(
-        _ptr(q), _ptr(rel_pos_h), _ptr(rel_pos_w), _ptr(drel_h), _ptr(drel_w), _ptr(dq), _ptr(out), _ptr(dth), _ptr(dtw),
-        BH, H, W, d, _code(q.dtype), _code(gd), ws, ws_bytes, st))
+        q.data_ptr(), rel_pos_h.data_ptr(), rel_pos_w.data_ptr(), drel_h.data_ptr(), drel_w.data_ptr(), _ptr(dq),
+        out.data_ptr(), dth.data_ptr(), dtw.data_ptr(), BH, H, W, d, _dtype(q.dtype), _dtype(gd), ws, ws_bytes, st))
     return out, dth, dtw

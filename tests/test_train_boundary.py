@@ -41,19 +41,22 @@ def _h(p=FAKE, sb=64 * 12, st=64 * 4, sh=64):
     return train._Heads(p, sb, st, sh)
 
 
+def _at(h):
+    return None if h is None else ctypes.byref(h)
+
+
 def _qk(lib, *, q=None, k=None, v=None, qw=FAKE, kw=FAKE, cos=FAKE, sin=FAKE, pos=None, qo=FAKE, ko=FAKE, vo=None, B=2,
         N=3, hq=2, hk=1, d=64, rot=64, rows=3, eps=1e-6, in_dt=BF16, w_dt=BF16):
-    return lib.dera_qk_norm_rope(_h() if q is None else q, _h() if k is None else k, v, qw, kw, cos, sin, pos, qo, ko,
-                                 vo, B, N, hq, hk, d, rot, rows, 0, eps, in_dt, w_dt, None)
+    return lib.dera_qk_norm_rope(_at(q or _h()), _at(k or _h()), _at(v), qw, kw, cos, sin, pos, qo, ko, vo, B, N, hq, hk,
+                                 d, rot, rows, 0, eps, in_dt, w_dt, None)
 
 
 def _qk_bwd(lib, *, q=None, k=None, qw=FAKE, kw=FAKE, cos=FAKE, sin=FAKE, pos=None, zq=FAKE, zk=FAKE, zv=None, dq=None,
             dk=None, dv=None, dqw=FAKE, dkw=FAKE, B=2, N=3, hq=2, hk=1, d=64, rot=64, rows=3, eps=1e-6, in_dt=BF16,
             w_dt=BF16, z_dt=BF16, g_dt=F32):
-    return lib.dera_qk_norm_rope_backward(_h() if q is None else q, _h() if k is None else k, qw, kw, cos, sin, pos, zq,
-                                          zk, zv, _h() if dq is None else dq, _h() if dk is None else dk, dv, dqw, dkw,
-                                          B, N, hq, hk, d, rot, rows, 0, eps, in_dt, w_dt, z_dt, g_dt, FAKE, 1 << 30,
-                                          None)
+    return lib.dera_qk_norm_rope_backward(_at(q or _h()), _at(k or _h()), qw, kw, cos, sin, pos, zq, zk, zv,
+                                          _at(dq or _h()), _at(dk or _h()), _at(dv), dqw, dkw, B, N, hq, hk, d, rot,
+                                          rows, 0, eps, in_dt, w_dt, z_dt, g_dt, FAKE, 1 << 30, None)
 
 
 @pytest.mark.parametrize("call", [_qk, _qk_bwd])
