@@ -7,48 +7,58 @@
 // bytes of drel, and q, dq_in and dq, per token); the products take half as long.
 //
 // A CTA takes every gridDim.x-th tile of 128 tokens (of any heads: a token's coordinates are
-// all that matters) and 64 columns of head_dim.  drel comes by bulk copies one tile ahead;
-// eight warps form G in shared memory; one set of G serves both products, K-major (tokens by table rows) for dq
-// and M-major for dT.  dT stays in TMEM over all of the CTA's tiles and leaves once, as a partial
-// that relpos_pb_tables_kernel adds in a fixed order.
+// all that matters) and 64 columns of head_dim.  drel comes by bulk copies, half a tile of one table at a
+// time and ahead of its use; eight warps form G in shared memory, K-major (tokens by table rows); the same G,
+// read M-major, serves dT.  Two G buffers (bf16 inputs; one fits with fp16, whose operands take twice the
+// room), so that the next table's G is formed while the products of this one run.
 //
 // Precision: tensor-core operands have 16 bits, drel has 32.  G is split into two bf16 terms,
 // G = G1 + G2 to 2^-16 (a single one would leave 2^-8 in the tables' gradients, which
 // are fp32 sums over all tokens).  bf16 and not fp16, because a gradient may have any size; fp16
 // q and tables are split into two bf16 terms as well, exactly (11 bits = 8 + 3), and the product
-// of the two small terms, 2^-16 of the whole, is left out.
+// of the two small terms, 2^-16 of the whole, is left out.  The tensor core adds to its accumulator with
+// truncation, 2^-24 a step and always towards zero: over all of a CTA's tiles that left 1e-4 of the tables'
+// gradients, so dT leaves TMEM after every tile and is summed in fp32 registers; the CTAs' partial sums are
+// added in a fixed order by relpos_pb_tables_kernel.
 #pragma once
 #include "common.cuh"
 #include "train.cuh"
 
 namespace dera {
 
-constexpr int kPbBuilders = 256, kPbThreads = 64 + kPbBuilders + 128;
+// warpgroups: control (warp 0 copies, warp 1 products), two that form G, two that take dq and dT
+constexpr int kPbThreads = 640, kPbBuilders = 256;
+constexpr int kPbLaunchRegs = 96, kPbRegsCtl = 40, kPbRegsBuild = 80, kPbRegsOut = 136;
+static_assert(kPbRegsCtl + 2 * kPbRegsBuild + 2 * kPbRegsOut <= 5 * kPbLaunchRegs, "register split exceeds the launch pool");
 constexpr int kPbAtoms = 2 * kTileBytes;   // a 128 x 128 operand of 16-bit values: two atoms of 64 columns
 
 template <bool BF16>
 struct PbSmem {
   static constexpr int kTerms = BF16 ? 1 : 2;                 // bf16 terms of q and the tables
+  static constexpr int NG = BF16 ? 2 : 1;                     // buffers of G
+  static constexpr int NS = BF16 ? 3 : 4;                     // staged halves of drel
   static constexpr int kT = 0;                                // [term][table] 128 rows x 64 columns
   static constexpr int kQ = kT + 2 * kTerms * kTileBytes;     // [term]
-  static constexpr int kG = kQ + kTerms * kTileBytes;         // [term of G] two atoms
-  static constexpr int kStg = kG + 2 * kPbAtoms;              // [table] drel of a tile, fp32
-  static constexpr int kStgBytes = kBlockM * 64 * 4;
-  static constexpr int kBars = kStg + 2 * kStgBytes;
-  static constexpr int kMisc = kBars + 12 * 8;
+  static constexpr int kG = kQ + kTerms * kTileBytes;         // [buffer][term of G] two atoms
+  static constexpr int kStg = kG + NG * 2 * kPbAtoms;         // [NS] 64 rows of drel_h or drel_w, fp32
+  static constexpr int kStgBytes = 64 * 64 * 4;
+  static constexpr int kBars = kStg + NS * kStgBytes;
+  static constexpr int kMisc = kBars + 26 * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
 enum : int {
-  kPbStgFull = 0,   // [2] drel_h, drel_w of a tile landed
-  kPbStgFree = 2,   // [2] the builders have read them
-  kPbGFull = 4,     // G (and q) of one table written
-  kPbMmaDone = 5,   // its products are complete
-  kPbDqFull = 6,    // [2] dq of a tile is in TMEM
-  kPbDqFree = 8,    // [2] and has been read
-  kPbAllDone = 10,
-  kPbBars = 11
+  kPbStgFull = 0,   // [4] a half of drel landed
+  kPbStgFree = 4,   // [4] four warps have read it
+  kPbGFull = 8,     // [2] G (and with the first table q) written
+  kPbMmaDone = 10,  // [2] its products are complete
+  kPbDqFull = 12,   // [2] dq of a tile is in TMEM
+  kPbDqFree = 14,   // [2] and has been read
+  kPbDtFull = 16,   // [table][2] dT of a tile
+  kPbDtFree = 20,   // [table][2]
+  kPbAllDone = 24,  // every product is complete
+  kPbBars = 25
 };
 
 // 16-bit operand element (row, i) of a K-major 128 x 128 tile, 128-byte swizzled.
@@ -76,10 +86,39 @@ __device__ __forceinline__ void pb_terms(const uint4& u, uint4& t1, uint4& t2) {
   t2 = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
+// 16 rows of G (both terms) from their staged drel rows of L floats: LPR lanes a row, a pair of columns
+// (i, i + 1) each, ATOMS times 2 LPR columns.  Lane l < 16 holds row l's coordinate, or one so large
+// that the row comes out as zeros.
+template <int LPR, int ATOMS>
+__device__ __forceinline__ void pb_rows(const float* stg, uint8_t* g, int coord, int L, int lane) {
+  constexpr int RPI = 32 / LPR;
+  const int sub = lane / LPR, p = lane % LPR;
+  const uint32_t n = static_cast<uint32_t>(L);
+  stg += L - 1 - 2 * p;
+  g += (p & 3) * 4;
+  #pragma unroll 8
+  for (int it = 0; it < 16 / RPI; ++it) {
+    const int rl = it * RPI + sub;
+    const int c = __shfl_sync(0xffffffffu, coord, rl);
+    const int k0 = c + L - 1 - 2 * p;
+    const float* src = stg + rl * L + c;
+    uint8_t* at = g + rl * 128 + (((p >> 2) ^ (rl & 7)) << 4);
+    #pragma unroll
+    for (int a = 0; a < ATOMS; ++a) {
+      const float v0 = static_cast<uint32_t>(k0 - 64 * a) < n ? src[-64 * a] : 0.f;
+      const float v1 = static_cast<uint32_t>(k0 - 64 * a - 1) < n ? src[-64 * a - 1] : 0.f;
+      const uint32_t g1 = pack_bf16x2(v0, v1);
+      const float2 h = unpack_in(g1, kBF16);
+      *reinterpret_cast<uint32_t*>(at + a * kTileBytes) = g1;
+      *reinterpret_cast<uint32_t*>(at + a * kTileBytes + kPbAtoms) = pack_bf16x2(v0 - h.x, v1 - h.y);
+    }
+  }
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a) {
   using SM = PbSmem<BF16>;
-  constexpr int TERMS = SM::kTerms;
+  constexpr int TERMS = SM::kTerms, NG = SM::NG, NS = SM::NS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -98,84 +137,91 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kPbBars; ++i) {
-      const int n = (i == kPbStgFree || i == kPbStgFree + 1 || i == kPbGFull)
-                        ? kPbBuilders
-                        : ((i == kPbDqFree || i == kPbDqFree + 1) ? kBlockM : 1);
-      mbar_init(&bars[i], n);
+      const bool half = (i >= kPbStgFree && i < kPbStgFree + 4) || (i >= kPbDtFree && i < kPbDtFree + 4);
+      const bool all = i == kPbGFull || i == kPbGFull + 1 || i == kPbDqFree || i == kPbDqFree + 1;
+      mbar_init(&bars[i], all ? 256 : (half ? 128 : 1));
     }
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(slot, 256);
+    tmem_alloc(slot, 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *slot;   // dq of even and odd tiles [0, 64), [64, 128), dT_h [128, 192), dT_w [192, 256)
+  const uint32_t tbase = *slot;   // dq of even and odd tiles [0, 64), [64, 128), dT [128 + 128 table + 64 parity, + 64)
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- drel, one tile ahead
-    if (lane == 0) {
+  if (warp < 4) {
+    regs_release<kPbRegsCtl>();
+    if (warp == 0 && lane == 0) {
+      // -------------------------------------------------------------- drel, half a tile of a table at a time
       bool ok = true;
-      for (int t = 0; ok && t < T; ++t) {
-        const long long tile = tile_of(t);
-        const int rows = rows_of(tile);
-        for (int tb = 0; tb < 2; ++tb) {
-          ok = mbar_wait(&bars[kPbStgFree + tb], (t & 1) ^ 1, abort_flag, status);
-          if (!ok) break;
-          const int L = tb == 0 ? a.H : a.W;
-          const float* src = (tb == 0 ? a.drel_h : a.drel_w) + static_cast<size_t>(tile) * kBlockM * L;
-          float* dst = reinterpret_cast<float*>(smem + SM::kStg + tb * SM::kStgBytes);
-          // bulk copies go by 16 bytes; the last tile may end up to three floats further
-          const int n = rows * L, whole = n & ~3;
-          for (int e = whole; e < n; ++e) dst[e] = src[e];
-          mbar_arrive_expect_tx(&bars[kPbStgFull + tb], static_cast<uint32_t>(whole) * 4);
-          if (whole > 0) bulk_load(dst, src, static_cast<uint32_t>(whole) * 4, &bars[kPbStgFull + tb]);
+      for (int j = 0; ok && j < 4 * T; ++j) {
+        const long long tile = tile_of(j >> 2);
+        const int tb = (j >> 1) & 1, half = j & 1, L = tb == 0 ? a.H : a.W;
+        const int rows = max(0, min(64, rows_of(tile) - 64 * half));
+        ok = mbar_wait(&bars[kPbStgFree + j % NS], ((j / NS) & 1) ^ 1, abort_flag, status);
+        if (!ok) break;
+        const float* src = (tb == 0 ? a.drel_h : a.drel_w) + (static_cast<size_t>(tile) * kBlockM + 64 * half) * L;
+        float* dst = reinterpret_cast<float*>(smem + SM::kStg + (j % NS) * SM::kStgBytes);
+        // bulk copies go by 16 bytes; the last rows may end up to three floats further
+        const int n = rows * L, whole = n & ~3;
+        for (int e = whole; e < n; ++e) dst[e] = src[e];
+        mbar_arrive_expect_tx(&bars[kPbStgFull + j % NS], static_cast<uint32_t>(whole) * 4);
+        if (whole > 0) bulk_load(dst, src, static_cast<uint32_t>(whole) * 4, &bars[kPbStgFull + j % NS]);
+      }
+    } else if (warp == 1) {
+      // -------------------------------------------------------------- products
+      constexpr uint32_t id_dq = idesc_f16(kBlockM, 64, kBF16, kBF16, 0, 1);   // G K-major, T N-major
+      constexpr uint32_t id_dt = idesc_f16(kBlockM, 64, kBF16, kBF16, 1, 1);   // G^T M-major, q N-major
+      constexpr uint32_t kGBuf = (2 * kPbAtoms) >> 4, kG2 = kPbAtoms >> 4, kAtom = kTileBytes >> 4;
+      const uint64_t d_g = sdesc_sw128(smem_u32(smem + SM::kG), 16, 1024);
+      const uint64_t d_gt = sdesc_sw128(smem_u32(smem + SM::kG), kTileBytes, 1024);   // its two atoms lie along M
+      const uint64_t d_q = sdesc_sw128(smem_u32(smem + SM::kQ), 16, 1024);
+      for (int s = 0; s < 2 * T; ++s) {
+        const int t = s >> 1, tb = s & 1, buf = t & 1;
+        bool ok = mbar_wait(&bars[kPbGFull + s % NG], (s / NG) & 1, abort_flag, status);
+        if (t >= 2) {   // tile t - 2's dq and dT have been read
+          const uint32_t ph = ((t >> 1) - 1) & 1;
+          ok = ok && (tb == 1 || mbar_wait(&bars[kPbDqFree + buf], ph, abort_flag, status)) &&
+               mbar_wait(&bars[kPbDtFree + 2 * tb + buf], ph, abort_flag, status);
         }
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------------- MMA issuer
-    constexpr uint32_t id_dq = idesc_f16(kBlockM, 64, kBF16, kBF16, 0, 1);   // G K-major, T N-major
-    constexpr uint32_t id_dt = idesc_f16(kBlockM, 64, kBF16, kBF16, 1, 1);   // G^T M-major, q N-major
-    constexpr uint32_t kG2 = kPbAtoms >> 4, kAtom = kTileBytes >> 4;
-    const uint64_t d_g = sdesc_sw128(smem_u32(smem + SM::kG), 16, 1024);
-    const uint64_t d_gt = sdesc_sw128(smem_u32(smem + SM::kG), kTileBytes, 1024);   // its two atoms lie along M
-    const uint64_t d_q = sdesc_sw128(smem_u32(smem + SM::kQ), 16, 1024);
-    bool ok = true;
-    for (int s = 0; ok && s < 2 * T; ++s) {
-      const int t = s >> 1, tb = s & 1;
-      ok = warp_all(mbar_wait(&bars[kPbGFull], s & 1, abort_flag, status));
-      if (ok && tb == 0 && t >= 2) ok = warp_all(mbar_wait(&bars[kPbDqFree + (t & 1)], ((t >> 1) - 1) & 1, abort_flag, status));
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t d_t = sdesc_sw128(smem_u32(smem + SM::kT + tb * kTileBytes), 16, 1024);
-      const uint32_t dq = tbase + 64 * (t & 1), dt = tbase + 128 + 64 * tb;
-      const int ks = (2 * (tb == 0 ? a.H : a.W) + 14) / 16;   // 16-row steps over the table's 2L - 1 rows
-      // G1 X1 + G2 X1 (+ G1 X2)
-      for (int p = 0; p < 1 + TERMS; ++p) {
-        const uint32_t g = p == 1 ? kG2 : 0, x = p == 2 ? 2 * kAtom : 0;
-        for (int k = 0; k < ks; ++k)
-          umma_ss_w(dq, d_g + g + (k / 4) * kAtom + 2 * (k % 4), d_t + x + 128 * k, id_dq, (tb > 0 || p > 0 || k > 0) ? 1u : 0u);
-      }
-      if (tb == 1) umma_commit_w(&bars[kPbDqFull + (t & 1)]);
-      for (int p = 0; p < 1 + TERMS; ++p) {
-        const uint32_t g = p == 1 ? kG2 : 0, x = p == 2 ? kAtom : 0;
+        if (!warp_all(ok)) break;
+        tc_fence_after();
+        const uint64_t d_t = sdesc_sw128(smem_u32(smem + SM::kT + tb * kTileBytes), 16, 1024);
+        const uint32_t gb = (s % NG) * kGBuf;
+        const uint32_t dq = tbase + 64 * buf, dt = tbase + 128 + 128 * tb + 64 * buf;
+        const int ks = (2 * (tb == 0 ? a.H : a.W) + 14) / 16;   // 16-row steps over the table's 2L - 1 rows
+        // G1 X1 + G2 X1 (+ G1 X2)
         #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          umma_ss_w(dt, d_gt + g + 128 * k, d_q + x + 128 * k, id_dt, (t > 0 || p > 0 || k > 0) ? 1u : 0u);
+        for (int p = 0; p < 1 + TERMS; ++p) {
+          const uint32_t g = gb + (p == 1 ? kG2 : 0), x = p == 2 ? 2 * kAtom : 0;
+          for (int k = 0; k < ks; ++k)
+            umma_ss_w(dq, d_g + g + (k / 4) * kAtom + 2 * (k % 4), d_t + x + 128 * k, id_dq,
+                      (tb > 0 || p > 0 || k > 0) ? 1u : 0u);
+        }
+        if (tb == 1) umma_commit_w(&bars[kPbDqFull + buf]);
+        #pragma unroll
+        for (int p = 0; p < 1 + TERMS; ++p) {
+          const uint32_t g = gb + (p == 1 ? kG2 : 0), x = p == 2 ? kAtom : 0;
+          #pragma unroll
+          for (int k = 0; k < 8; ++k)
+            umma_ss_w(dt, d_gt + g + 128 * k, d_q + x + 128 * k, id_dt, (p > 0 || k > 0) ? 1u : 0u);
+        }
+        umma_commit_w(&bars[kPbDtFull + 2 * tb + buf]);
+        umma_commit_w(&bars[kPbMmaDone + s % NG]);
       }
-      umma_commit_w(&bars[kPbMmaDone]);
+      // every product issued above completes before TMEM is released
+      umma_commit_w(&bars[kPbAllDone]);
+      mbar_wait_budget(&bars[kPbAllDone], 0, kWaitBudgetCycles);
+      __syncwarp();
     }
-    umma_commit_w(&bars[kPbAllDone]);
-    mbar_wait_budget(&bars[kPbAllDone], 0, kWaitBudgetCycles);
-    __syncwarp();
-  } else if (warp < 2 + kPbBuilders / 32) {
+  } else if (warp < 12) {
     // ---------------------------------------------------------------- builders
-    const int tid = threadIdx.x - 64;
-    const int row0 = 16 * (warp - 2);   // a warp forms 16 rows of G, whose coordinates its lanes hold
-    int qh = 0, qw = 0;
+    regs_release<kPbRegsBuild>();
+    const int tid = threadIdx.x - 128;
+    const int half = (warp - 4) >> 2, row0 = 16 * (warp - 4);   // a warp forms 16 rows of G
     // the tables' columns [c0, c0 + 64), rows past 2L - 1 as zeros
     for (int e = tid; e < 2 * kBlockM * 8; e += kPbBuilders) {
       const int tb = e >> 10, row = (e >> 3) & 127, ch = e & 7;
@@ -205,15 +251,34 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
     };
     load_q(0);
     bool ok = true;
+    int qh = 0, qw = 0;
     for (int s = 0; ok && s < 2 * T; ++s) {
-      const int t = s >> 1, tb = s & 1;
-      const long long tile = tile_of(t);
-      const int rows = rows_of(tile), L = tb == 0 ? a.H : a.W;
-      // the previous table's products have read G, and its tile's q
-      if (s > 0) ok = warp_all(mbar_wait(&bars[kPbMmaDone], (s - 1) & 1, abort_flag, status));
-      if (ok) ok = warp_all(mbar_wait(&bars[kPbStgFull + tb], t & 1, abort_flag, status));
-      if (!ok) break;
+      const int t = s >> 1, tb = s & 1, L = tb == 0 ? a.H : a.W;
+      const int j = 2 * s + half;
       if (tb == 0) {
+        const long long g = tile_of(t) * kBlockM + row0 + (lane & 15);
+        const int n = static_cast<int>(g % a.N);
+        qh = n / a.W;
+        qw = n - qh * a.W;
+        if (g >= a.tokens) qh = qw = 1 << 20;   // a row past the last token: zeros
+      }
+      // this buffer's last products are complete, and the half has landed
+      ok = (s < NG || mbar_wait(&bars[kPbMmaDone + s % NG], (s / NG - 1) & 1, abort_flag, status)) &&
+           mbar_wait(&bars[kPbStgFull + j % NS], (j / NS) & 1, abort_flag, status);
+      ok = warp_all(ok);
+      if (!ok) break;
+      const float* stg = reinterpret_cast<const float*>(smem + SM::kStg + (j % NS) * SM::kStgBytes) + (row0 & 63) * L;
+      uint8_t* g = smem + SM::kG + (s % NG) * 2 * kPbAtoms + row0 * 128;
+      const int c = tb == 0 ? qh : qw;
+      if (L <= 8) pb_rows<8, 1>(stg, g, c, L, lane);         // 15 table rows at most: 16 columns of G
+      else if (L <= 16) pb_rows<16, 1>(stg, g, c, L, lane);  // 31: 32
+      else if (L <= 32) pb_rows<32, 1>(stg, g, c, L, lane);  // 63: 64
+      else pb_rows<32, 2>(stg, g, c, L, lane);
+      mbar_arrive(&bars[kPbStgFree + j % NS]);
+      if (tb == 0) {
+        // the last tile's products have read its q
+        if (s > 0) ok = warp_all(mbar_wait(&bars[kPbMmaDone + (s - 1) % NG], ((s - 1) / NG) & 1, abort_flag, status));
+        if (!ok) break;
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int e = tid + i * kPbBuilders;
@@ -225,95 +290,72 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
         }
         if (t + 1 < T) load_q(t + 1);
       }
-      if (tb == 0) {
-        const long long g = tile * kBlockM + row0 + (lane & 15);
-        const int n = static_cast<int>(g % a.N);
-        qh = n / a.W;
-        qw = n - qh * a.W;
-      }
-      const float* stg = reinterpret_cast<const float*>(smem + SM::kStg + tb * SM::kStgBytes);
-      // pairs (i, i + 1) of the first 16 ks columns of this warp's 16 rows of G, row by row
-      const int pairs = 8 * ((2 * L + 14) / 16);
-      const uint32_t magic = 0xffffffffu / pairs + 1;   // e / pairs = umulhi(e, magic) for these e
-      #pragma unroll 4
-      for (int e = lane; e < 16 * pairs; e += 32) {
-        const int rl = static_cast<int>(__umulhi(e, magic)), i = 2 * (e - rl * pairs), row = row0 + rl;
-        const int k0 = __shfl_sync(0xffffffffu, tb == 0 ? qh : qw, rl) + L - 1 - i, k1 = k0 - 1;
-        const float v0 = (row < rows && k0 >= 0 && k0 < L) ? stg[row * L + k0] : 0.f;
-        const float v1 = (row < rows && k1 >= 0 && k1 < L) ? stg[row * L + k1] : 0.f;
-        const uint32_t g1 = pack_bf16x2(v0, v1);
-        const float2 h = unpack_in(g1, kBF16);
-        uint8_t* at = smem + SM::kG + pb_off(row, i);
-        *reinterpret_cast<uint32_t*>(at) = g1;
-        *reinterpret_cast<uint32_t*>(at + kPbAtoms) = pack_bf16x2(v0 - h.x, v1 - h.y);
-      }
       fence_proxy_async_smem();
-      mbar_arrive(&bars[kPbGFull]);
-      mbar_arrive(&bars[kPbStgFree + tb]);
+      mbar_arrive(&bars[kPbGFull + s % NG]);
     }
   } else {
-    // ---------------------------------------------------------------- dq, and the tables at the end
-    const int wq = warp & 3, r = wq * 32 + lane;
+    // ---------------------------------------------------------------- dq, half of the columns each, and one table's dT
+    regs_claim<kPbRegsOut>();
+    const int tb = (warp - 12) >> 2, wq = warp & 3, r = wq * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+    float acc[64];
+    #pragma unroll
+    for (int e = 0; e < 64; ++e) acc[e] = 0.f;
     bool ok = true;
     for (int t = 0; ok && t < T; ++t) {
+      const int buf = t & 1;
+      const uint32_t ph = (t >> 1) & 1;
       const long long tile = tile_of(t);
       const bool valid = r < rows_of(tile);
-      const size_t at = (static_cast<size_t>(tile) * kBlockM + r) * a.D + c0;
-      ok = warp_all(mbar_wait(&bars[kPbDqFull + (t & 1)], (t >> 1) & 1, abort_flag, status));
+      const size_t at = (static_cast<size_t>(tile) * kBlockM + r) * a.D + c0 + 32 * tb;
+      float x[32];
+      if (a.dq_in && valid) {   // on its way while the products run
+        #pragma unroll
+        for (int c = 0; c < 32; c += 8) load8(a.dq_in, at + c, *reinterpret_cast<float(*)[8]>(&x[c]), a.grad_fmt);
+      }
+      uint32_t u[32];
+      ok = warp_all(mbar_wait(&bars[kPbDqFull + buf], ph, abort_flag, status));
       if (!ok) break;
       tc_fence_after();
-      uint32_t u[2][32];
-      tmem_ld32(tbase + lanes + 64 * (t & 1), u[0]);
-      tmem_ld32(tbase + lanes + 64 * (t & 1) + 32, u[1]);
+      tmem_ld32(tbase + lanes + 64 * buf + 32 * tb, u);
       tmem_wait_ld();
       tc_fence_before();
-      mbar_arrive(&bars[kPbDqFree + (t & 1)]);
+      mbar_arrive(&bars[kPbDqFree + buf]);
       if (valid) {
         #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int c = 0; c < 32; c += 8) {
+          float v[8];
           #pragma unroll
-          for (int c = 0; c < 32; c += 8) {
-            float v[8];
-            #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(u[h][c + e]);
-            if (a.dq_in) {
-              float x[8];
-              load8(a.dq_in, at + 32 * h + c, x, a.grad_fmt);
-              #pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] += x[e];
-            }
-            store8(a.dq, at + 32 * h + c, v, a.grad_fmt);
-          }
-      }
-    }
-    if (ok) ok = warp_all(mbar_wait(&bars[kPbAllDone], 0, abort_flag, status));
-    if (ok) {
-      tc_fence_after();
-      const int LH = 2 * a.H - 1, LW = 2 * a.W - 1;
-      float* part = a.parts + static_cast<size_t>(blockIdx.x) * (LH + LW) * a.D + c0;
-      #pragma unroll
-      for (int tb = 0; tb < 2; ++tb)
-        #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t u[32];
-          tmem_ld32(tbase + lanes + 128 + 64 * tb + 32 * h, u);
-          tmem_wait_ld();
-          if (r < (tb == 0 ? LH : LW)) {
-            float4* dst = reinterpret_cast<float4*>(part + static_cast<size_t>((tb == 0 ? 0 : LH) + r) * a.D + 32 * h);
-            #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              dst[c] = make_float4(__uint_as_float(u[4 * c]), __uint_as_float(u[4 * c + 1]), __uint_as_float(u[4 * c + 2]),
-                                   __uint_as_float(u[4 * c + 3]));
-          }
+          for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(u[c + e]) + (a.dq_in ? x[c + e] : 0.f);
+          store8(a.dq, at + c, v, a.grad_fmt);
         }
+      }
+      ok = warp_all(mbar_wait(&bars[kPbDtFull + 2 * tb + buf], ph, abort_flag, status));
+      if (!ok) break;
+      tc_fence_after();
+      #pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        tmem_ld32(tbase + lanes + 128 + 128 * tb + 64 * buf + 32 * h, u);
+        tmem_wait_ld();
+        #pragma unroll
+        for (int e = 0; e < 32; ++e) acc[32 * h + e] += __uint_as_float(u[e]);
+      }
+      tc_fence_before();
+      mbar_arrive(&bars[kPbDtFree + 2 * tb + buf]);
+    }
+    const int LH = 2 * a.H - 1, LW = 2 * a.W - 1;
+    if (ok && r < (tb == 0 ? LH : LW)) {
+      float* dst = a.parts + (static_cast<size_t>(blockIdx.x) * (LH + LW) + (tb == 0 ? 0 : LH) + r) * a.D + c0;
+      #pragma unroll
+      for (int e = 0; e < 64; e += 4)
+        *reinterpret_cast<float4*>(dst + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
     }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tbase, 256);
+    tmem_dealloc(tbase, 512);
   }
 }
 
