@@ -682,72 +682,75 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // leave through the same area, before any row is copied in
         if (seg > 0) ok = wg_sync() && ok;
         // The tile's rows of rel_w, then of rel_h, are one contiguous block
-        // each: every warp copies a quarter of the rows into the staging area,
-        // a row per pass with the lanes along it (coalesced), scaled by log2e.
-        // Rows past N read as 0.
+        // each.  Rows past N read as 0.
         const size_t row0 = static_cast<size_t>(bh) * N + static_cast<size_t>(qt) * kBlockM;
         const int nrows = min(kBlockM, N - qt * kBlockM);
-        // Loads for 8 rows go out together before any store (the stores could
-        // alias the source as far as the compiler knows).
-        auto copy_rows = [&](const void* src, int len, int stride) {
-          for (int rb = wq; rb < kBlockM; rb += 32) {
-            float v[8][2];
-            #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              const int rr = rb + 4 * u;
-              #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int c = lane + 32 * h;
-                v[u][h] = (rr < nrows && c < len)
-                              ? load_elem(src, (row0 + rr) * static_cast<size_t>(len) + c, args.bias_fmt)
-                              : 0.f;
-              }
-            }
-            #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int c = lane + 32 * h;
-                if (c < len) area[(rb + 4 * u) * stride + c] = kLog2e * v[u][h];
-              }
-            }
-          }
-        };
-        // An fp32 bias is copied as it is with cp.async: every element of
-        // the tile's rows goes out at once (element e of the block to thread
+        // The block is copied as it is with cp.async: every 4-byte word of
+        // the tile's rows goes out at once (word e of the block to thread
         // e mod 128, so a warp reads 128 contiguous bytes), without a round
         // trip through registers per batch of rows; the log2e scaling is
-        // applied where the rows are read.  Rows past N are written as 0.
+        // applied where the rows are read.  A row of a 16-bit bias with an even length is
+        // half as many words, which go to the end of its staging row and are widened there by
+        // the row's own thread (copying 16-bit rows in batches through registers took the 64x64
+        // grid from 355 to 623 us); rows of an odd length do not start at whole words, and
+        // every thread loads its own.
         const bool raw = args.bias_fmt == kF32;
-        auto copy_rows_async = [&](const float* src, int len, int stride) {
-          const int step_r = kBlockM / len, step_c = kBlockM - step_r * len;
-          int rr = r / len, c = r - rr * len;
-          for (int e = r; e < kBlockM * len; e += kBlockM) {
-            cp_async4(area + rr * stride + c, src + (row0 + (rr < nrows ? rr : 0)) * static_cast<size_t>(len) + c,
+        auto copy_rows_async = [&](const void* p, int words, int at, int stride) {
+          const float* src = static_cast<const float*>(p);
+          const int step_r = kBlockM / words, step_c = kBlockM - step_r * words;
+          int rr = r / words, c = r - rr * words;
+          for (int e = r; e < kBlockM * words; e += kBlockM) {
+            cp_async4(area + rr * stride + at + c, src + (row0 + (rr < nrows ? rr : 0)) * static_cast<size_t>(words) + c,
                       rr < nrows ? 4u : 0u);
             rr += step_r;
             c += step_c;
-            if (c >= len) {
-              c -= len;
+            if (c >= words) {
+              c -= words;
               ++rr;
             }
           }
           cp_async_wait_all();
         };
-        if (raw) copy_rows_async(static_cast<const float*>(args.rel_w), W, kBiasStride);
-        else copy_rows(args.rel_w, W, kBiasStride);
+        auto copy_rows = [&](const void* p, int len, int stride) {
+          if (raw) copy_rows_async(p, len, 0, stride);
+          else if ((len & 1) == 0) copy_rows_async(p, len / 2, len / 2, stride);
+        };
+        // this thread's row, once its words are there: base-2 values
+        auto own_row = [&](const void* p, int len, float* row) {
+          if (raw) {
+            for (int c = 0; c < len; ++c) row[c] *= kLog2e;
+          } else if ((len & 1) == 0) {
+            for (int c = 0; c < len; c += 2) {   // the words not yet read lie past what is written
+              const float2 x = unpack_in(__float_as_uint(row[(len + c) / 2]), args.bias_fmt);
+              row[c] = kLog2e * x.x;
+              row[c + 1] = kLog2e * x.y;
+            }
+          } else {
+            #pragma unroll 1
+            for (int c0 = 0; c0 < len; c0 += 8) {
+              float x[8];
+              #pragma unroll
+              for (int c = 0; c < 8; ++c)
+                x[c] = (r < nrows && c0 + c < len) ? load_elem(p, (row0 + r) * static_cast<size_t>(len) + c0 + c, args.bias_fmt)
+                                                   : 0.f;
+              #pragma unroll
+              for (int c = 0; c < 8; ++c)
+                if (c0 + c < len) row[c0 + c] = kLog2e * x[c];
+            }
+          }
+        };
+        copy_rows(args.rel_w, W, kBiasStride);
         ok = wg_sync() && ok;
-        const float* stg = area + r * kBiasStride;
+        float* stg = area + r * kBiasStride;
+        if (!raw) own_row(args.rel_w, W, stg);
         const float wscale = raw ? kLog2e : 1.0f;
         #pragma unroll
         for (int kw = 0; kw < WP; ++kw) bw[kw] = kw < W ? wscale * stg[kw] : NEG_INF;
         // every thread has its rel_w row before the area is reused for rel_h
         ok = wg_sync() && ok;
-        if (raw) copy_rows_async(static_cast<const float*>(args.rel_h), H, HS);
-        else copy_rows(args.rel_h, H, HS);
+        copy_rows(args.rel_h, H, HS);
         ok = wg_sync() && ok;
-        if (raw)
-          for (int kh = 0; kh < H; ++kh) bh_row[kh] *= kLog2e;   // this thread's own row
+        own_row(args.rel_h, H, bh_row);
         if (kPadRows)
           for (int kh = H; kh < Hpad; ++kh) bh_row[kh] = NEG_INF;
         if (!ok) return false;

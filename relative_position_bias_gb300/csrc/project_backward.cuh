@@ -8,15 +8,14 @@
 //
 // A CTA takes every gridDim.x-th tile of 128 tokens (of any heads: a token's coordinates are
 // all that matters) and 64 columns of head_dim.  drel comes by bulk copies, half a tile of one table at a
-// time and ahead of its use; eight warps form G in shared memory, K-major (tokens by table rows); the same G,
-// read M-major, serves dT.  Two G buffers (bf16 inputs; one fits with fp16, whose operands take twice the
-// room), so that the next table's G is formed while the products of this one run.
+// time and ahead of its use; sixteen warps form G in shared memory, K-major (tokens by table rows); the same G,
+// read M-major, serves dT.
 //
-// Precision: tensor-core operands have 16 bits, drel has 32.  G is split into two bf16 terms,
-// G = G1 + G2 to 2^-16 (a single one would leave 2^-8 in the tables' gradients, which
-// are fp32 sums over all tokens).  bf16 and not fp16, because a gradient may have any size; fp16
-// q and tables are split into two bf16 terms as well, exactly (11 bits = 8 + 3), and the product
-// of the two small terms, 2^-16 of the whole, is left out.  The tensor core adds to its accumulator with
+// Precision: tensor-core operands have 16 bits, drel has 32.  G is split into three bf16 terms for dT
+// (what is left is 2^-24 of a value: the tables' gradients are fp32 sums over all tokens) and the first two
+// serve dq (2^-16; one term would leave 2^-8).  bf16 and not fp16, because a gradient may have any size; fp16
+// q and tables are split into two bf16 terms as well, exactly (11 bits = 8 + 3); products of terms
+// below 2^-16 of the whole are left out.  The tensor core adds to its accumulator with
 // truncation, 2^-24 a step and always towards zero: over all of a CTA's tiles that left 1e-4 of the tables'
 // gradients, so dT leaves TMEM after every tile and is summed in fp32 registers; the CTAs' partial sums are
 // added in a fixed order by relpos_pb_tables_kernel.
@@ -26,21 +25,20 @@
 
 namespace dera {
 
-// warpgroups: control (warp 0 copies, warp 1 products), two that form G, two that take dq and dT
-constexpr int kPbThreads = 640, kPbBuilders = 256;
-constexpr int kPbLaunchRegs = 96, kPbRegsCtl = 40, kPbRegsBuild = 80, kPbRegsOut = 136;
-static_assert(kPbRegsCtl + 2 * kPbRegsBuild + 2 * kPbRegsOut <= 5 * kPbLaunchRegs, "register split exceeds the launch pool");
+// warpgroups: control (warp 0 copies, warp 1 products), four that form G, two that take dq and dT
+constexpr int kPbBuilders = 512, kPbThreads = 128 + kPbBuilders + 256;
+constexpr int kPbLaunchRegs = 72, kPbRegsCtl = 40, kPbRegsBuild = 48, kPbRegsOut = 136;
+static_assert(kPbRegsCtl + 4 * kPbRegsBuild + 2 * kPbRegsOut <= 7 * kPbLaunchRegs, "register split exceeds the launch pool");
 constexpr int kPbAtoms = 2 * kTileBytes;   // a 128 x 128 operand of 16-bit values: two atoms of 64 columns
 
 template <bool BF16>
 struct PbSmem {
   static constexpr int kTerms = BF16 ? 1 : 2;                 // bf16 terms of q and the tables
-  static constexpr int NG = BF16 ? 2 : 1;                     // buffers of G
-  static constexpr int NS = BF16 ? 3 : 4;                     // staged halves of drel
+  static constexpr int NS = BF16 ? 5 : 2;                     // staged halves of drel
   static constexpr int kT = 0;                                // [term][table] 128 rows x 64 columns
   static constexpr int kQ = kT + 2 * kTerms * kTileBytes;     // [term]
-  static constexpr int kG = kQ + kTerms * kTileBytes;         // [buffer][term of G] two atoms
-  static constexpr int kStg = kG + NG * 2 * kPbAtoms;         // [NS] 64 rows of drel_h or drel_w, fp32
+  static constexpr int kG = kQ + kTerms * kTileBytes;         // [three terms] two atoms
+  static constexpr int kStg = kG + 3 * kPbAtoms;              // [NS] 64 rows of drel_h or drel_w, fp32
   static constexpr int kStgBytes = 64 * 64 * 4;
   static constexpr int kBars = kStg + NS * kStgBytes;
   static constexpr int kMisc = kBars + 26 * 8;
@@ -49,10 +47,10 @@ struct PbSmem {
 };
 
 enum : int {
-  kPbStgFull = 0,   // [4] a half of drel landed
-  kPbStgFree = 4,   // [4] four warps have read it
-  kPbGFull = 8,     // [2] G (and with the first table q) written
-  kPbMmaDone = 10,  // [2] its products are complete
+  kPbStgFull = 0,   // [5] a half of drel landed
+  kPbStgFree = 5,   // [5] eight warps have read it
+  kPbGFull = 10,    // G (and with the first table q) written
+  kPbMmaDone = 11,  // its products are complete
   kPbDqFull = 12,   // [2] dq of a tile is in TMEM
   kPbDqFree = 14,   // [2] and has been read
   kPbDtFull = 16,   // [table][2] dT of a tile
@@ -86,8 +84,8 @@ __device__ __forceinline__ void pb_terms(const uint4& u, uint4& t1, uint4& t2) {
   t2 = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-// 16 rows of G (both terms) from their staged drel rows of L floats: LPR lanes a row, a pair of columns
-// (i, i + 1) each, ATOMS times 2 LPR columns.  Lane l < 16 holds row l's coordinate, or one so large
+// 8 rows of G (its three terms) from their staged drel rows of L floats: LPR lanes a row, a pair of columns
+// (i, i + 1) each, ATOMS times 2 LPR columns.  Lane l < 8 holds row l's coordinate, or one so large
 // that the row comes out as zeros.
 template <int LPR, int ATOMS>
 __device__ __forceinline__ void pb_rows(const float* stg, uint8_t* g, int coord, int L, int lane) {
@@ -96,8 +94,8 @@ __device__ __forceinline__ void pb_rows(const float* stg, uint8_t* g, int coord,
   const uint32_t n = static_cast<uint32_t>(L);
   stg += L - 1 - 2 * p;
   g += (p & 3) * 4;
-  #pragma unroll 8
-  for (int it = 0; it < 16 / RPI; ++it) {
+  #pragma unroll 4
+  for (int it = 0; it < 8 / RPI; ++it) {
     const int rl = it * RPI + sub;
     const int c = __shfl_sync(0xffffffffu, coord, rl);
     const int k0 = c + L - 1 - 2 * p;
@@ -109,8 +107,12 @@ __device__ __forceinline__ void pb_rows(const float* stg, uint8_t* g, int coord,
       const float v1 = static_cast<uint32_t>(k0 - 64 * a - 1) < n ? src[-64 * a - 1] : 0.f;
       const uint32_t g1 = pack_bf16x2(v0, v1);
       const float2 h = unpack_in(g1, kBF16);
+      const float r0 = v0 - h.x, r1 = v1 - h.y;   // exact
+      const uint32_t g2 = pack_bf16x2(r0, r1);
+      const float2 m = unpack_in(g2, kBF16);
       *reinterpret_cast<uint32_t*>(at + a * kTileBytes) = g1;
-      *reinterpret_cast<uint32_t*>(at + a * kTileBytes + kPbAtoms) = pack_bf16x2(v0 - h.x, v1 - h.y);
+      *reinterpret_cast<uint32_t*>(at + a * kTileBytes + kPbAtoms) = g2;
+      *reinterpret_cast<uint32_t*>(at + a * kTileBytes + 2 * kPbAtoms) = pack_bf16x2(r0 - m.x, r1 - m.y);
     }
   }
 }
@@ -118,7 +120,7 @@ __device__ __forceinline__ void pb_rows(const float* stg, uint8_t* g, int coord,
 template <bool BF16>
 __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a) {
   using SM = PbSmem<BF16>;
-  constexpr int TERMS = SM::kTerms, NG = SM::NG, NS = SM::NS;
+  constexpr int TERMS = SM::kTerms, NS = SM::NS;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -137,9 +139,12 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kPbBars; ++i) {
-      const bool half = (i >= kPbStgFree && i < kPbStgFree + 4) || (i >= kPbDtFree && i < kPbDtFree + 4);
-      const bool all = i == kPbGFull || i == kPbGFull + 1 || i == kPbDqFree || i == kPbDqFree + 1;
-      mbar_init(&bars[i], all ? 256 : (half ? 128 : 1));
+      int n = 1;
+      if (i >= kPbStgFree && i < kPbStgFree + 5) n = kPbBuilders / 2;
+      else if (i == kPbGFull) n = kPbBuilders;
+      else if (i == kPbDqFree || i == kPbDqFree + 1) n = 256;
+      else if (i >= kPbDtFree && i < kPbDtFree + 4) n = 128;
+      mbar_init(&bars[i], n);
     }
     fence_mbar_init();
   }
@@ -175,13 +180,13 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
       // -------------------------------------------------------------- products
       constexpr uint32_t id_dq = idesc_f16(kBlockM, 64, kBF16, kBF16, 0, 1);   // G K-major, T N-major
       constexpr uint32_t id_dt = idesc_f16(kBlockM, 64, kBF16, kBF16, 1, 1);   // G^T M-major, q N-major
-      constexpr uint32_t kGBuf = (2 * kPbAtoms) >> 4, kG2 = kPbAtoms >> 4, kAtom = kTileBytes >> 4;
+      constexpr uint32_t kGTerm = kPbAtoms >> 4, kAtom = kTileBytes >> 4;
       const uint64_t d_g = sdesc_sw128(smem_u32(smem + SM::kG), 16, 1024);
       const uint64_t d_gt = sdesc_sw128(smem_u32(smem + SM::kG), kTileBytes, 1024);   // its two atoms lie along M
       const uint64_t d_q = sdesc_sw128(smem_u32(smem + SM::kQ), 16, 1024);
       for (int s = 0; s < 2 * T; ++s) {
         const int t = s >> 1, tb = s & 1, buf = t & 1;
-        bool ok = mbar_wait(&bars[kPbGFull + s % NG], (s / NG) & 1, abort_flag, status);
+        bool ok = mbar_wait(&bars[kPbGFull], s & 1, abort_flag, status);
         if (t >= 2) {   // tile t - 2's dq and dT have been read
           const uint32_t ph = ((t >> 1) - 1) & 1;
           ok = ok && (tb == 1 || mbar_wait(&bars[kPbDqFree + buf], ph, abort_flag, status)) &&
@@ -190,38 +195,38 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
         if (!warp_all(ok)) break;
         tc_fence_after();
         const uint64_t d_t = sdesc_sw128(smem_u32(smem + SM::kT + tb * kTileBytes), 16, 1024);
-        const uint32_t gb = (s % NG) * kGBuf;
         const uint32_t dq = tbase + 64 * buf, dt = tbase + 128 + 128 * tb + 64 * buf;
         const int ks = (2 * (tb == 0 ? a.H : a.W) + 14) / 16;   // 16-row steps over the table's 2L - 1 rows
-        // G1 X1 + G2 X1 (+ G1 X2)
+        // dq: G1 T1 + G2 T1 (+ G1 T2)
         #pragma unroll
         for (int p = 0; p < 1 + TERMS; ++p) {
-          const uint32_t g = gb + (p == 1 ? kG2 : 0), x = p == 2 ? 2 * kAtom : 0;
+          const uint32_t g = p == 1 ? kGTerm : 0, x = p == 2 ? 2 * kAtom : 0;
           for (int k = 0; k < ks; ++k)
             umma_ss_w(dq, d_g + g + (k / 4) * kAtom + 2 * (k % 4), d_t + x + 128 * k, id_dq,
                       (tb > 0 || p > 0 || k > 0) ? 1u : 0u);
         }
         if (tb == 1) umma_commit_w(&bars[kPbDqFull + buf]);
+        // dT: G1 q1 + G2 q1 + G3 q1 (+ G1 q2 + G2 q2)
         #pragma unroll
-        for (int p = 0; p < 1 + TERMS; ++p) {
-          const uint32_t g = gb + (p == 1 ? kG2 : 0), x = p == 2 ? kAtom : 0;
+        for (int p = 0; p < (TERMS == 1 ? 3 : 5); ++p) {
+          const uint32_t g = (p < 3 ? p : p - 3) * kGTerm, x = p < 3 ? 0 : kAtom;
           #pragma unroll
           for (int k = 0; k < 8; ++k)
             umma_ss_w(dt, d_gt + g + 128 * k, d_q + x + 128 * k, id_dt, (p > 0 || k > 0) ? 1u : 0u);
         }
         umma_commit_w(&bars[kPbDtFull + 2 * tb + buf]);
-        umma_commit_w(&bars[kPbMmaDone + s % NG]);
+        umma_commit_w(&bars[kPbMmaDone]);
       }
       // every product issued above completes before TMEM is released
       umma_commit_w(&bars[kPbAllDone]);
       mbar_wait_budget(&bars[kPbAllDone], 0, kWaitBudgetCycles);
       __syncwarp();
     }
-  } else if (warp < 12) {
+  } else if (warp < 4 + kPbBuilders / 32) {
     // ---------------------------------------------------------------- builders
     regs_release<kPbRegsBuild>();
     const int tid = threadIdx.x - 128;
-    const int half = (warp - 4) >> 2, row0 = 16 * (warp - 4);   // a warp forms 16 rows of G
+    const int half = (warp - 4) >> 3, row0 = 8 * (warp - 4);   // a warp forms 8 rows of G
     // the tables' columns [c0, c0 + 64), rows past 2L - 1 as zeros
     for (int e = tid; e < 2 * kBlockM * 8; e += kPbBuilders) {
       const int tb = e >> 10, row = (e >> 3) & 127, ch = e & 7;
@@ -235,13 +240,13 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
       *reinterpret_cast<uint4*>(at) = t1;
       if (TERMS == 2) *reinterpret_cast<uint4*>(at + 2 * kTileBytes) = t2;
     }
-    // this thread's four 16-byte chunks of a tile's q
-    uint4 qv[4];
+    // this thread's two 16-byte chunks of a tile's q
+    uint4 qv[2];
     auto load_q = [&](int t) {
       const long long tile = tile_of(t);
       const int rows = rows_of(tile);
       #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const int e = tid + i * kPbBuilders, row = e >> 3, ch = e & 7;
         qv[i] = make_uint4(0u, 0u, 0u, 0u);
         if (row < rows)
@@ -256,19 +261,19 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
       const int t = s >> 1, tb = s & 1, L = tb == 0 ? a.H : a.W;
       const int j = 2 * s + half;
       if (tb == 0) {
-        const long long g = tile_of(t) * kBlockM + row0 + (lane & 15);
+        const long long g = tile_of(t) * kBlockM + row0 + (lane & 7);
         const int n = static_cast<int>(g % a.N);
         qh = n / a.W;
         qw = n - qh * a.W;
         if (g >= a.tokens) qh = qw = 1 << 20;   // a row past the last token: zeros
       }
-      // this buffer's last products are complete, and the half has landed
-      ok = (s < NG || mbar_wait(&bars[kPbMmaDone + s % NG], (s / NG - 1) & 1, abort_flag, status)) &&
+      // the last products have read G (and q), and the half has landed
+      ok = (s == 0 || mbar_wait(&bars[kPbMmaDone], (s - 1) & 1, abort_flag, status)) &&
            mbar_wait(&bars[kPbStgFull + j % NS], (j / NS) & 1, abort_flag, status);
       ok = warp_all(ok);
       if (!ok) break;
       const float* stg = reinterpret_cast<const float*>(smem + SM::kStg + (j % NS) * SM::kStgBytes) + (row0 & 63) * L;
-      uint8_t* g = smem + SM::kG + (s % NG) * 2 * kPbAtoms + row0 * 128;
+      uint8_t* g = smem + SM::kG + row0 * 128;
       const int c = tb == 0 ? qh : qw;
       if (L <= 8) pb_rows<8, 1>(stg, g, c, L, lane);         // 15 table rows at most: 16 columns of G
       else if (L <= 16) pb_rows<16, 1>(stg, g, c, L, lane);  // 31: 32
@@ -276,11 +281,8 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
       else pb_rows<32, 2>(stg, g, c, L, lane);
       mbar_arrive(&bars[kPbStgFree + j % NS]);
       if (tb == 0) {
-        // the last tile's products have read its q
-        if (s > 0) ok = warp_all(mbar_wait(&bars[kPbMmaDone + (s - 1) % NG], ((s - 1) / NG) & 1, abort_flag, status));
-        if (!ok) break;
         #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           const int e = tid + i * kPbBuilders;
           uint4 t1, t2;
           pb_terms<BF16>(qv[i], t1, t2);
@@ -291,12 +293,12 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
         if (t + 1 < T) load_q(t + 1);
       }
       fence_proxy_async_smem();
-      mbar_arrive(&bars[kPbGFull + s % NG]);
+      mbar_arrive(&bars[kPbGFull]);
     }
   } else {
     // ---------------------------------------------------------------- dq, half of the columns each, and one table's dT
     regs_claim<kPbRegsOut>();
-    const int tb = (warp - 12) >> 2, wq = warp & 3, r = wq * 32 + lane;
+    const int tb = (warp - 4 - kPbBuilders / 32) >> 2, wq = warp & 3, r = wq * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     float acc[64];
     #pragma unroll
