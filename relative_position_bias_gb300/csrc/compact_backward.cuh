@@ -32,7 +32,7 @@ namespace dera {
 
 constexpr int kCbColsThreads = 128 + 512;   // TMA, S and dP, accumulators, idle; two pairs of softmax warpgroups
 // registers at launch (the most that 640 threads get), and what the two kinds of warps make of them
-constexpr int kCbColsLaunchRegs = 96, kCbColsRegsCtl = 40, kCbColsRegsSmx = 104;
+constexpr int kCbColsLaunchRegs = 96, kCbColsRegsCtl = 64, kCbColsRegsSmx = 104;
 static_assert(kCbColsRegsCtl + 4 * kCbColsRegsSmx <= 5 * kCbColsLaunchRegs, "register split exceeds the launch pool");
 
 // Key steps of the rows kernel: KHT whole grid rows of WP >= W columns, so that a column's kw
@@ -61,15 +61,12 @@ enum : int {
 
 constexpr int cb_align(int x) { return (x + 1023) / 1024 * 1024; }
 
-// rows: NB steps in flight, one softmax warpgroup each.  Registers: the block launches with what
-// its threads get, then the control warps give most of theirs to the softmax warpgroups (a split larger
-// than the launch pool would block, so the host checks the compiled count).
+// rows: NB steps in flight, one softmax warpgroup each.  (Registers moved from the control warps to the
+// softmax warps, 56 and 152 instead of 128 each, measured the same.)
 template <int D>
 struct CbRowsDims {
   static constexpr int NB = D == 64 ? 3 : 2;
   static constexpr int kThreads = 128 * (NB + 1);   // TMA, S and dP, accumulators, idle; then the softmax threads
-  static constexpr int kLaunchRegs = NB == 3 ? 128 : 168, kRegsCtl = 56, kRegsSmx = NB == 3 ? 152 : 224;
-  static_assert(kRegsCtl + NB * kRegsSmx <= (NB + 1) * kLaunchRegs, "register split exceeds the launch pool");
   // TMEM columns: S_b [128 b, 128 b + 64) (dZ_b over it), dP_b 64 further, dq, then q and dO as packed pairs
   static constexpr uint32_t tmDQ = 128 * NB, tmQ = tmDQ + D, tmDO = tmQ + D / 2;
   static_assert(tmDO + D / 2 <= 512, "TMEM");
@@ -293,7 +290,6 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
   auto stage = [&](int i) { return smem + SM::kRing + (i % KS) * SM::kStage; };
 
   if (warp < 4) {
-    regs_release<DM::kRegsCtl>();
     if (warp == 0 && lane == 0) {
       // -------------------------------------------------------------- TMA
       tma_prefetch_desc(&tm_k);
@@ -365,7 +361,6 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     }
   } else {
     // ---------------------------------------------------------------- softmax threads
-    regs_claim<DM::kRegsSmx>();
     const int H = a.H, W = a.W, N = a.N;
     const int wg = (warp >> 2) - 1, wq = warp & 3, r = wq * 32 + lane;
     const int n = unit.tile * kBlockM + r;

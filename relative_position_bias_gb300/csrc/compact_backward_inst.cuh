@@ -27,8 +27,7 @@ template <int WP, bool BF16, int D>
 static cudaError_t launch_cb_rows(const CbMaps& m, const CbArgs& a, unsigned grid, cudaStream_t s) {
   auto kernel = relpos_cb_rows_kernel<WP, BF16, D>;
   using SM = CbRowsSmem<WP, D>;
-  static std::atomic<int> fits{0};
-  const cudaError_t e = cb_prepare(kernel, SM::kAlloc, CbRowsDims<D>::kLaunchRegs, fits);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kAlloc);
   if (e != cudaSuccess) return e;
   kernel<<<grid, CbRowsDims<D>::kThreads, SM::kAlloc, s>>>(m.kg, m.vg, a);
   return cudaGetLastError();

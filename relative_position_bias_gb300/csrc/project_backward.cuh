@@ -27,7 +27,7 @@ namespace dera {
 
 // warpgroups: control (warp 0 copies, warp 1 products), four that form G, two that take dq and dT
 constexpr int kPbBuilders = 512, kPbThreads = 128 + kPbBuilders + 256;
-constexpr int kPbLaunchRegs = 72, kPbRegsCtl = 40, kPbRegsBuild = 48, kPbRegsOut = 136;
+constexpr int kPbLaunchRegs = 72, kPbRegsCtl = 64, kPbRegsBuild = 48, kPbRegsOut = 120;
 static_assert(kPbRegsCtl + 4 * kPbRegsBuild + 2 * kPbRegsOut <= 7 * kPbLaunchRegs, "register split exceeds the launch pool");
 constexpr int kPbAtoms = 2 * kTileBytes;   // a 128 x 128 operand of 16-bit values: two atoms of 64 columns
 
@@ -84,38 +84,69 @@ __device__ __forceinline__ void pb_terms(const uint4& u, uint4& t1, uint4& t2) {
   t2 = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-// 8 rows of G (its three terms) from their staged drel rows of L floats: LPR lanes a row, a pair of columns
-// (i, i + 1) each, ATOMS times 2 LPR columns.  Lane l < 8 holds row l's coordinate, or one so large
-// that the row comes out as zeros.
-template <int LPR, int ATOMS>
-__device__ __forceinline__ void pb_rows(const float* stg, uint8_t* g, int coord, int L, int lane) {
-  constexpr int RPI = 32 / LPR;
-  const int sub = lane / LPR, p = lane % LPR;
-  const uint32_t n = static_cast<uint32_t>(L);
-  stg += L - 1 - 2 * p;
-  g += (p & 3) * 4;
-  #pragma unroll 4
-  for (int it = 0; it < 8 / RPI; ++it) {
-    const int rl = it * RPI + sub;
-    const int c = __shfl_sync(0xffffffffu, coord, rl);
-    const int k0 = c + L - 1 - 2 * p;
-    const float* src = stg + rl * L + c;
-    uint8_t* at = g + rl * 128 + (((p >> 2) ^ (rl & 7)) << 4);
+// A warp's 8 rows of G.  A row is zero but for the window of columns [c, c + L - 1] that holds its drel row
+// in reverse (c its coordinate), so a lane takes one pair of columns (i, i + 1) of each row, i = 2 lane + c
+// rounded down to even, and a lane below 8 the last column of a window of 64 that starts at an odd c.  The
+// terms are formed in registers while the last table's products still read G, and only stored after.
+struct PbRows {
+  uint32_t t[8][3], last[3];
+
+  // stg: the rows' staged drel, L floats each.  Lane l < 8 holds row l's coordinate, or -1 for a row of zeros.
+  __device__ __forceinline__ void form(const float* stg, int coord, int L, int lane) {
     #pragma unroll
-    for (int a = 0; a < ATOMS; ++a) {
-      const float v0 = static_cast<uint32_t>(k0 - 64 * a) < n ? src[-64 * a] : 0.f;
-      const float v1 = static_cast<uint32_t>(k0 - 64 * a - 1) < n ? src[-64 * a - 1] : 0.f;
-      const uint32_t g1 = pack_bf16x2(v0, v1);
-      const float2 h = unpack_in(g1, kBF16);
-      const float r0 = v0 - h.x, r1 = v1 - h.y;   // exact
-      const uint32_t g2 = pack_bf16x2(r0, r1);
-      const float2 m = unpack_in(g2, kBF16);
-      *reinterpret_cast<uint32_t*>(at + a * kTileBytes) = g1;
-      *reinterpret_cast<uint32_t*>(at + a * kTileBytes + kPbAtoms) = g2;
-      *reinterpret_cast<uint32_t*>(at + a * kTileBytes + 2 * kPbAtoms) = pack_bf16x2(r0 - m.x, r1 - m.y);
+    for (int r = 0; r < 8; ++r) {
+      const int c = __shfl_sync(0xffffffffu, coord, r);
+      const int k0 = (c & 1) + L - 1 - 2 * lane, k1 = k0 - 1;   // of columns i and i + 1
+      // read somewhere in the row whatever they are, so that all rows' loads are in flight at once
+      const float v0 = stg[r * L + min(max(k0, 0), L - 1)], v1 = stg[r * L + max(k1, 0)];
+      split(c >= 0 && k0 >= 0 && k0 < L ? v0 : 0.f, c >= 0 && k1 >= 0 ? v1 : 0.f, t[r]);
+    }
+    split((lane < 8 && L == 64 && coord >= 0 && (coord & 1)) ? stg[lane * L] : 0.f, 0.f, last);
+  }
+  static __device__ __forceinline__ void split(float v0, float v1, uint32_t (&t)[3]) {
+    t[0] = pack_bf16x2(v0, v1);
+    const float2 h = unpack_in(t[0], kBF16);
+    const float r0 = v0 - h.x, r1 = v1 - h.y;   // exact, as is the next difference
+    t[1] = pack_bf16x2(r0, r1);
+    const float2 m = unpack_in(t[1], kBF16);
+    t[2] = pack_bf16x2(r0 - m.x, r1 - m.y);
+  }
+  // g: the rows' first term; columns [0, 8 chunks) are written.
+  __device__ __forceinline__ void store(uint8_t* g, int coord, int chunks, int lane) const {
+    const int ch = lane & 15;
+    if (ch < chunks) {
+      #pragma unroll
+      for (int r = 0; r < 8; r += 2) {
+        const int row = r + (lane >> 4);
+        uint8_t* at = g + (ch >> 3) * kTileBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+        #pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(at + k * kPbAtoms) = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    __syncwarp();
+    #pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int c = __shfl_sync(0xffffffffu, coord, r);
+      const int i = (c & ~1) + 2 * lane;
+      if (c >= 0 && i < 8 * chunks) {
+        uint8_t* at = g + pb_off(r, i);
+        #pragma unroll
+        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t*>(at + k * kPbAtoms) = t[r][k];
+      }
+    }
+    if (lane < 8 && chunks == 16 && coord >= 0 && (coord & 1)) {
+      const int i = coord - 1 + 64;
+      if (i < 128) {
+        uint8_t* at = g + pb_off(lane, i);
+        // a window of fewer than 64 columns ends inside the lanes' pairs, whose zeros these would overwrite
+        if (last[0] | last[1] | last[2]) {
+          #pragma unroll
+          for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t*>(at + k * kPbAtoms) = last[k];
+        }
+      }
     }
   }
-}
+};
 
 template <bool BF16>
 __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a) {
@@ -265,20 +296,19 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
         const int n = static_cast<int>(g % a.N);
         qh = n / a.W;
         qw = n - qh * a.W;
-        if (g >= a.tokens) qh = qw = 1 << 20;   // a row past the last token: zeros
+        if (g >= a.tokens) qh = qw = -1;   // a row past the last token: zeros
       }
-      // the last products have read G (and q), and the half has landed
-      ok = (s == 0 || mbar_wait(&bars[kPbMmaDone], (s - 1) & 1, abort_flag, status)) &&
-           mbar_wait(&bars[kPbStgFull + j % NS], (j / NS) & 1, abort_flag, status);
-      ok = warp_all(ok);
+      ok = warp_all(mbar_wait(&bars[kPbStgFull + j % NS], (j / NS) & 1, abort_flag, status));
       if (!ok) break;
-      const float* stg = reinterpret_cast<const float*>(smem + SM::kStg + (j % NS) * SM::kStgBytes) + (row0 & 63) * L;
-      uint8_t* g = smem + SM::kG + row0 * 128;
       const int c = tb == 0 ? qh : qw;
-      if (L <= 8) pb_rows<8, 1>(stg, g, c, L, lane);         // 15 table rows at most: 16 columns of G
-      else if (L <= 16) pb_rows<16, 1>(stg, g, c, L, lane);  // 31: 32
-      else if (L <= 32) pb_rows<32, 1>(stg, g, c, L, lane);  // 63: 64
-      else pb_rows<32, 2>(stg, g, c, L, lane);
+      PbRows rows;
+      rows.form(reinterpret_cast<const float*>(smem + SM::kStg + (j % NS) * SM::kStgBytes) + (row0 & 63) * L, c, L, lane);
+      // the last products have read G (and q)
+      if (s > 0) ok = warp_all(mbar_wait(&bars[kPbMmaDone], (s - 1) & 1, abort_flag, status));
+      if (!ok) break;
+      rows.store(smem + SM::kG + row0 * 128, c, 2 * ((2 * L + 14) / 16), lane);
+      // Only now: the stores need every staged value in a register.  An arrival straight after form() let
+      // the next copy overwrite rows whose loads were still under way.
       mbar_arrive(&bars[kPbStgFree + j % NS]);
       if (tb == 0) {
         #pragma unroll
@@ -310,11 +340,6 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
       const long long tile = tile_of(t);
       const bool valid = r < rows_of(tile);
       const size_t at = (static_cast<size_t>(tile) * kBlockM + r) * a.D + c0 + 32 * tb;
-      float x[32];
-      if (a.dq_in && valid) {   // on its way while the products run
-        #pragma unroll
-        for (int c = 0; c < 32; c += 8) load8(a.dq_in, at + c, *reinterpret_cast<float(*)[8]>(&x[c]), a.grad_fmt);
-      }
       uint32_t u[32];
       ok = warp_all(mbar_wait(&bars[kPbDqFull + buf], ph, abort_flag, status));
       if (!ok) break;
@@ -326,9 +351,10 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
       if (valid) {
         #pragma unroll
         for (int c = 0; c < 32; c += 8) {
-          float v[8];
+          float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          if (a.dq_in) load8(a.dq_in, at + c, v, a.grad_fmt);
           #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(u[c + e]) + (a.dq_in ? x[c + e] : 0.f);
+          for (int e = 0; e < 8; ++e) v[e] += __uint_as_float(u[c + e]);
           store8(a.dq, at + c, v, a.grad_fmt);
         }
       }
