@@ -149,9 +149,9 @@ DERA_API dera_status dera_relpos_project_backward_workspace_size(int BH, int H, 
  *      attention's own part of dq), or NULL for none; it may be dq itself.
  * out: dq [BH,N,head_dim] in grad_dtype (DERA_F32 or in_dtype); drel_pos_h [2H-1,head_dim], drel_pos_w
  *      [2W-1,head_dim] fp32, summed over every batch and head.
- * Precision: fp32 sums; drel_h and drel_w enter the products of dq as two bf16 terms each (what is
- *      left out is 2^-16 of a value at most), those of the tables as three (2^-24), and with fp16 q and the
- *      tables as two bf16 terms, exactly.
+ * Precision: fp32 sums; drel_h and drel_w enter the products as three bf16 terms each (what is left
+ *      out is 2^-24 of a value), two (2^-16) for a 16-bit dq, and with fp16 q and the tables as two
+ *      bf16 terms, exactly.
  * Errors: as for dera_relpos_project; DERA_ERR_SCRATCH as above.  BH = 0 writes zero table gradients.
  */
 DERA_API dera_status dera_relpos_project_backward(const void* q, const void* rel_pos_h, const void* rel_pos_w,

@@ -1,33 +1,17 @@
 // Launch of the compact-bias backward for one head dimension; included by one .cu for each, so that
 // the build compiles them side by side.
 #pragma once
-#include <atomic>
-
 #include "compact_backward.cuh"
+#include "launch.cuh"
 
 namespace dera {
-
-// Sets up a kernel whose warps split their registers: the split needs the launch pool it was computed
-// for, and a build that compiled to fewer registers is refused rather than launched into a wait that
-// never ends.
-template <class K>
-static cudaError_t cb_prepare(K kernel, int smem, int launch_regs, std::atomic<int>& fits) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  if (fits.load(std::memory_order_relaxed) == 0) {   // 0 unknown, 1 fits, -1 refused
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, kernel);
-    if (e != cudaSuccess) return e;
-    fits.store(fa.numRegs >= launch_regs ? 1 : -1, std::memory_order_relaxed);
-  }
-  return fits.load(std::memory_order_relaxed) > 0 ? cudaSuccess : cudaErrorInvalidKernelImage;
-}
 
 template <int WP, bool BF16, int D>
 static cudaError_t launch_cb_rows(const CbMaps& m, const CbArgs& a, unsigned grid, cudaStream_t s) {
   auto kernel = relpos_cb_rows_kernel<WP, BF16, D>;
   using SM = CbRowsSmem<WP, D>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::kAlloc);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = prepare_kernel(kernel, SM::kAlloc, 0, done);
   if (e != cudaSuccess) return e;
   kernel<<<grid, CbRowsDims<D>::kThreads, SM::kAlloc, s>>>(m.kg, m.vg, a);
   return cudaGetLastError();
@@ -36,8 +20,8 @@ static cudaError_t launch_cb_rows(const CbMaps& m, const CbArgs& a, unsigned gri
 template <bool BF16, int D>
 static cudaError_t launch_cb_cols(const CbMaps& m, const CbArgs& a, unsigned grid, cudaStream_t s) {
   auto kernel = relpos_cb_cols_kernel<BF16, D>;
-  static std::atomic<int> fits{0};
-  const cudaError_t e = cb_prepare(kernel, CbColsSmem<D>::kAlloc, kCbColsLaunchRegs, fits);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = prepare_kernel(kernel, CbColsSmem<D>::kAlloc, kCbColsLaunchRegs, done);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

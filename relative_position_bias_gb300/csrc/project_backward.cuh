@@ -11,9 +11,9 @@
 // time and ahead of its use; sixteen warps form G in shared memory, K-major (tokens by table rows); the same G,
 // read M-major, serves dT.
 //
-// Precision: tensor-core operands have 16 bits, drel has 32.  G is split into three bf16 terms for dT
-// (what is left is 2^-24 of a value: the tables' gradients are fp32 sums over all tokens) and the first two
-// serve dq (2^-16; one term would leave 2^-8).  bf16 and not fp16, because a gradient may have any size; fp16
+// Precision: tensor-core operands have 16 bits, drel has 32.  G is split into three bf16 terms
+// (what is left is 2^-24 of a value: the tables' gradients are fp32 sums over all tokens), of which the first two
+// serve a 16-bit dq (2^-16; one term would leave 2^-8).  bf16 and not fp16, because a gradient may have any size; fp16
 // q and tables are split into two bf16 terms as well, exactly (11 bits = 8 + 3); products of terms
 // below 2^-16 of the whole are left out.  The tensor core adds to its accumulator with
 // truncation, 2^-24 a step and always towards zero: over all of a CTA's tiles that left 1e-4 of the tables'
@@ -84,69 +84,38 @@ __device__ __forceinline__ void pb_terms(const uint4& u, uint4& t1, uint4& t2) {
   t2 = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-// A warp's 8 rows of G.  A row is zero but for the window of columns [c, c + L - 1] that holds its drel row
-// in reverse (c its coordinate), so a lane takes one pair of columns (i, i + 1) of each row, i = 2 lane + c
-// rounded down to even, and a lane below 8 the last column of a window of 64 that starts at an odd c.  The
-// terms are formed in registers while the last table's products still read G, and only stored after.
-struct PbRows {
-  uint32_t t[8][3], last[3];
-
-  // stg: the rows' staged drel, L floats each.  Lane l < 8 holds row l's coordinate, or -1 for a row of zeros.
-  __device__ __forceinline__ void form(const float* stg, int coord, int L, int lane) {
+// 8 rows of G (its three terms) from their staged drel rows of L floats: LPR lanes a row, a pair of columns
+// (i, i + 1) each, ATOMS times 2 LPR columns.  Lane l < 8 holds row l's coordinate, or one so large
+// that the row comes out as zeros.
+template <int LPR, int ATOMS>
+__device__ __forceinline__ void pb_rows(const float* stg, uint8_t* g, int coord, int L, int lane) {
+  constexpr int RPI = 32 / LPR;
+  const int sub = lane / LPR, p = lane % LPR;
+  const uint32_t n = static_cast<uint32_t>(L);
+  stg += L - 1 - 2 * p;
+  g += (p & 3) * 4;
+  #pragma unroll 4
+  for (int it = 0; it < 8 / RPI; ++it) {
+    const int rl = it * RPI + sub;
+    const int c = __shfl_sync(0xffffffffu, coord, rl);
+    const int k0 = c + L - 1 - 2 * p;
+    const float* src = stg + rl * L + c;
+    uint8_t* at = g + rl * 128 + (((p >> 2) ^ (rl & 7)) << 4);
     #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int c = __shfl_sync(0xffffffffu, coord, r);
-      const int k0 = (c & 1) + L - 1 - 2 * lane, k1 = k0 - 1;   // of columns i and i + 1
-      // read somewhere in the row whatever they are, so that all rows' loads are in flight at once
-      const float v0 = stg[r * L + min(max(k0, 0), L - 1)], v1 = stg[r * L + max(k1, 0)];
-      split(c >= 0 && k0 >= 0 && k0 < L ? v0 : 0.f, c >= 0 && k1 >= 0 ? v1 : 0.f, t[r]);
-    }
-    split((lane < 8 && L == 64 && coord >= 0 && (coord & 1)) ? stg[lane * L] : 0.f, 0.f, last);
-  }
-  static __device__ __forceinline__ void split(float v0, float v1, uint32_t (&t)[3]) {
-    t[0] = pack_bf16x2(v0, v1);
-    const float2 h = unpack_in(t[0], kBF16);
-    const float r0 = v0 - h.x, r1 = v1 - h.y;   // exact, as is the next difference
-    t[1] = pack_bf16x2(r0, r1);
-    const float2 m = unpack_in(t[1], kBF16);
-    t[2] = pack_bf16x2(r0 - m.x, r1 - m.y);
-  }
-  // g: the rows' first term; columns [0, 8 chunks) are written.
-  __device__ __forceinline__ void store(uint8_t* g, int coord, int chunks, int lane) const {
-    const int ch = lane & 15;
-    if (ch < chunks) {
-      #pragma unroll
-      for (int r = 0; r < 8; r += 2) {
-        const int row = r + (lane >> 4);
-        uint8_t* at = g + (ch >> 3) * kTileBytes + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-        #pragma unroll
-        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4*>(at + k * kPbAtoms) = make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-    __syncwarp();
-    #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int c = __shfl_sync(0xffffffffu, coord, r);
-      const int i = (c & ~1) + 2 * lane;
-      if (c >= 0 && i < 8 * chunks) {
-        uint8_t* at = g + pb_off(r, i);
-        #pragma unroll
-        for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t*>(at + k * kPbAtoms) = t[r][k];
-      }
-    }
-    if (lane < 8 && chunks == 16 && coord >= 0 && (coord & 1)) {
-      const int i = coord - 1 + 64;
-      if (i < 128) {
-        uint8_t* at = g + pb_off(lane, i);
-        // a window of fewer than 64 columns ends inside the lanes' pairs, whose zeros these would overwrite
-        if (last[0] | last[1] | last[2]) {
-          #pragma unroll
-          for (int k = 0; k < 3; ++k) *reinterpret_cast<uint32_t*>(at + k * kPbAtoms) = last[k];
-        }
-      }
+    for (int a = 0; a < ATOMS; ++a) {
+      const float v0 = static_cast<uint32_t>(k0 - 64 * a) < n ? src[-64 * a] : 0.f;
+      const float v1 = static_cast<uint32_t>(k0 - 64 * a - 1) < n ? src[-64 * a - 1] : 0.f;
+      const uint32_t g1 = pack_bf16x2(v0, v1);
+      const float2 h = unpack_in(g1, kBF16);
+      const float r0 = v0 - h.x, r1 = v1 - h.y;   // exact
+      const uint32_t g2 = pack_bf16x2(r0, r1);
+      const float2 m = unpack_in(g2, kBF16);
+      *reinterpret_cast<uint32_t*>(at + a * kTileBytes) = g1;
+      *reinterpret_cast<uint32_t*>(at + a * kTileBytes + kPbAtoms) = g2;
+      *reinterpret_cast<uint32_t*>(at + a * kTileBytes + 2 * kPbAtoms) = pack_bf16x2(r0 - m.x, r1 - m.y);
     }
   }
-};
+}
 
 template <bool BF16>
 __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a) {
@@ -228,16 +197,16 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
         const uint64_t d_t = sdesc_sw128(smem_u32(smem + SM::kT + tb * kTileBytes), 16, 1024);
         const uint32_t dq = tbase + 64 * buf, dt = tbase + 128 + 128 * tb + 64 * buf;
         const int ks = (2 * (tb == 0 ? a.H : a.W) + 14) / 16;   // 16-row steps over the table's 2L - 1 rows
-        // dq: G1 T1 + G2 T1 (+ G1 T2)
+        // dq and dT: G1 X1 + G2 X1 + G3 X1 (+ G1 X2 + G2 X2); a 16-bit dq does without G3 T1 and G2 T2
         #pragma unroll
-        for (int p = 0; p < 1 + TERMS; ++p) {
-          const uint32_t g = p == 1 ? kGTerm : 0, x = p == 2 ? 2 * kAtom : 0;
+        for (int p = 0; p < (TERMS == 1 ? 3 : 5); ++p) {
+          if ((p == 2 || p == 4) && a.grad_fmt != kF32) continue;
+          const uint32_t g = (p < 3 ? p : p - 3) * kGTerm, x = p < 3 ? 0 : 2 * kAtom;
           for (int k = 0; k < ks; ++k)
             umma_ss_w(dq, d_g + g + (k / 4) * kAtom + 2 * (k % 4), d_t + x + 128 * k, id_dq,
                       (tb > 0 || p > 0 || k > 0) ? 1u : 0u);
         }
         if (tb == 1) umma_commit_w(&bars[kPbDqFull + buf]);
-        // dT: G1 q1 + G2 q1 + G3 q1 (+ G1 q2 + G2 q2)
         #pragma unroll
         for (int p = 0; p < (TERMS == 1 ? 3 : 5); ++p) {
           const uint32_t g = (p < 3 ? p : p - 3) * kGTerm, x = p < 3 ? 0 : kAtom;
@@ -296,20 +265,21 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
         const int n = static_cast<int>(g % a.N);
         qh = n / a.W;
         qw = n - qh * a.W;
-        if (g >= a.tokens) qh = qw = -1;   // a row past the last token: zeros
+        if (g >= a.tokens) qh = qw = 1 << 20;   // a row past the last token: zeros
       }
-      ok = warp_all(mbar_wait(&bars[kPbStgFull + j % NS], (j / NS) & 1, abort_flag, status));
+      // the last products have read G (and q), and the half has landed
+      ok = (s == 0 || mbar_wait(&bars[kPbMmaDone], (s - 1) & 1, abort_flag, status)) &&
+           mbar_wait(&bars[kPbStgFull + j % NS], (j / NS) & 1, abort_flag, status);
+      ok = warp_all(ok);
       if (!ok) break;
+      const float* stg = reinterpret_cast<const float*>(smem + SM::kStg + (j % NS) * SM::kStgBytes) + (row0 & 63) * L;
+      uint8_t* g = smem + SM::kG + row0 * 128;
       const int c = tb == 0 ? qh : qw;
-      PbRows rows;
-      rows.form(reinterpret_cast<const float*>(smem + SM::kStg + (j % NS) * SM::kStgBytes) + (row0 & 63) * L, c, L, lane);
-      // the last products have read G (and q)
-      if (s > 0) ok = warp_all(mbar_wait(&bars[kPbMmaDone], (s - 1) & 1, abort_flag, status));
-      if (!ok) break;
-      rows.store(smem + SM::kG + row0 * 128, c, 2 * ((2 * L + 14) / 16), lane);
-      // Only now: the stores need every staged value in a register.  An arrival straight after form() let
-      // the next copy overwrite rows whose loads were still under way.
-      mbar_arrive(&bars[kPbStgFree + j % NS]);
+      if (L <= 8) pb_rows<8, 1>(stg, g, c, L, lane);         // 15 table rows at most: 16 columns of G
+      else if (L <= 16) pb_rows<16, 1>(stg, g, c, L, lane);  // 31: 32
+      else if (L <= 32) pb_rows<32, 1>(stg, g, c, L, lane);  // 63: 64
+      else pb_rows<32, 2>(stg, g, c, L, lane);
+      mbar_arrive(&bars[kPbStgFree + j % NS]);   // after the stores, which need every staged value in a register
       if (tb == 0) {
         #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -340,6 +310,13 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
       const long long tile = tile_of(t);
       const bool valid = r < rows_of(tile);
       const size_t at = (static_cast<size_t>(tile) * kBlockM + r) * a.D + c0 + 32 * tb;
+      // 16-bit dq_in: on its way while the products run
+      const bool early = a.dq_in && a.grad_fmt != kF32 && valid;
+      uint4 x[4];
+      if (early) {
+        #pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] = *(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dq_in) + at) + c);
+      }
       uint32_t u[32];
       ok = warp_all(mbar_wait(&bars[kPbDqFull + buf], ph, abort_flag, status));
       if (!ok) break;
@@ -352,7 +329,8 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
         #pragma unroll
         for (int c = 0; c < 32; c += 8) {
           float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          if (a.dq_in) load8(a.dq_in, at + c, v, a.grad_fmt);
+          if (early) unpack8(x[c / 8], v, a.grad_fmt);
+          else if (a.dq_in) load8(a.dq_in, at + c, v, a.grad_fmt);
           #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] += __uint_as_float(u[c + e]);
           store8(a.dq, at + c, v, a.grad_fmt);

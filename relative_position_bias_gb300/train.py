@@ -61,6 +61,11 @@ def _want(t: torch.Tensor, shape, name: str) -> None:
         _expect(t, shape, name)   # says what is wrong
 
 
+def _like(t: torch.Tensor, dtype: torch.dtype) -> torch.Tensor:
+    """An empty tensor of (contiguous) t's shape."""
+    return torch.empty_like(t) if t.dtype == dtype else torch.empty_like(t, dtype=dtype)
+
+
 def _launch_stream(device: torch.device, stream) -> int | None:
     """Handle of the stream to launch on (the current one of `device` unless given)."""
     if stream is None and device.type == "cuda":
@@ -226,8 +231,8 @@ def qk_norm_rope_backward(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor
     kv = (B, N, hk, d)
     views, (hqs, hks, hdq, hdk, hdv) = _heads((q, k, dq, dk, dv), (q.shape, kv, q.shape, kv, kv),
                                               ("q", "k", "dq", "dk", "dv"))
-    dqw = torch.empty(d, dtype=torch.float32, device=dev) if norm else None
-    dkw = torch.empty(d, dtype=torch.float32, device=dev) if norm else None
+    dqw = _like(q_weight, torch.float32) if norm else None
+    dkw = _like(k_weight, torch.float32) if norm else None
     st = _launch_stream(dev, stream)
     keep, ws, ws_bytes = None, None, 0
     if norm:
@@ -258,7 +263,7 @@ def attention_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h: torc
         raise TypeError("q, k, v must share a dtype")
     if rel_h.dtype != rel_w.dtype:
         raise TypeError("rel_h and rel_w must share a dtype")
-    out = torch.empty((BH, N, d), dtype=out_dtype or q.dtype, device=q.device)
+    out = _like(q, out_dtype or q.dtype)
     lse = torch.empty((BH, N), dtype=torch.float32, device=q.device)
     st = _launch_stream(q.device, stream)
     ws, ws_bytes = _workspace(q.device, BH, H, W, d, workspace, st)
@@ -297,11 +302,8 @@ def attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h:
     if lse.dtype != torch.float32:
         raise TypeError("lse must be float32")
     dev = q.device
-    dq = torch.empty(size, dtype=gd, device=dev)
-    dk = torch.empty(size, dtype=gd, device=dev)
-    dv = torch.empty(size, dtype=gd, device=dev)
-    drel_h = torch.empty(size_h, dtype=torch.float32, device=dev)
-    drel_w = torch.empty(size_w, dtype=torch.float32, device=dev)
+    dq, dk, dv = _like(q, gd), _like(k, gd), _like(v, gd)
+    drel_h, drel_w = _like(rel_h, torch.float32), _like(rel_w, torch.float32)
     st = _launch_stream(dev, stream)
     keep, ws, ws_bytes = _scratch(dev, stream, st, workspace, "dera_relpos_attention_backward_workspace_size", BH, H, W, d)
     _check(api.load_library().dera_relpos_attention_backward(
@@ -338,9 +340,7 @@ def project_backward(q: torch.Tensor, rel_pos_h: torch.Tensor, rel_pos_w: torch.
     _same(drel_w, (BH, N, W), torch.float32, "drel_w")
     _same(dq, (BH, N, d), gd, "dq")
     dev = q.device
-    out = torch.empty(size, dtype=gd, device=dev)
-    dth = torch.empty(size_h, dtype=torch.float32, device=dev)
-    dtw = torch.empty(size_w, dtype=torch.float32, device=dev)
+    out, dth, dtw = _like(q, gd), _like(rel_pos_h, torch.float32), _like(rel_pos_w, torch.float32)
     st = _launch_stream(dev, stream)
     keep, ws, ws_bytes = _scratch(dev, stream, st, workspace, "dera_relpos_project_backward_workspace_size", BH, H, W, d)
     _check(api.load_library().dera_relpos_project_backward(
