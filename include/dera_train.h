@@ -103,7 +103,7 @@ DERA_API dera_status dera_qk_norm_rope_backward(const dera_heads* q, const dera_
  * log-sum-exp, lse[b, n] = log2(sum_m exp(Z[b, n, m])), Z = scale q k^T + rel_h + rel_w, [BH, N] fp32.
  * A bias of -inf masks its keys, and so does one of -1e38 or below; a row with every key masked
  * gives out = 0 and lse = -inf.  q, k and v must be finite everywhere, at masked keys too (the
- * products read them), and a bias must not be +inf or NaN.  Everything else as for dera_relpos_attention
+ * products read them), and a bias at most 1e38 and not NaN.  Everything else as for dera_relpos_attention
  * (workspace: dera_relpos_workspace_size).
  */
 DERA_API dera_status dera_relpos_attention_lse(const void* q, const void* k, const void* v, const void* rel_h,
@@ -120,13 +120,14 @@ DERA_API dera_status dera_relpos_attention_backward_workspace_size(int BH, int H
  *   dv = P^T dout,  dk = scale dZ^T q,  dq = scale dZ k,
  *   drel_h[n, kh] = sum_kw dZ[n, kh W + kw],  drel_w[n, kw] = sum_kh dZ[n, kh W + kw].
  * in:  q, k, v, rel_h, rel_w as given to the forward, out [BH,N,head_dim] and lse [BH,N] as it gave
- *      them (out in out_dtype: DERA_F32 or in_dtype), dout [BH,N,head_dim] in in_dtype.
+ *      them (out in out_dtype: DERA_F32 or in_dtype), dout [BH,N,head_dim] in in_dtype, finite everywhere.
  * out: dq, dk, dv [BH,N,head_dim] in grad_dtype (DERA_F32 or in_dtype); drel_h [BH,N,H],
  *      drel_w [BH,N,W] fp32.
  * Precision: P, dZ and the sums are fp32; P and dZ are rounded to in_dtype (relative 2^-8 for
  *      bf16, 2^-11 for fp16) as operands of the products dv, dk and dq, whose accumulators are
  *      fp32; drel_h and drel_w are summed before that rounding.  With fp16 a P or dZ below 2^-25 is
- *      lost there and a |dZ| of 65520 or more overflows.
+ *      lost there and a |dZ| of 65520 or more overflows.  On a grid of one row (column) drel_h (drel_w) is 0
+ *      by mathematics, and what out's rounding leaves of that in numbers.
  * Errors: as for dera_relpos_attention; DERA_ERR_SCRATCH if the workspace is NULL or smaller
  *      than the size above; DERA_ERR_SHAPE if BH * ceil(N / 128) passes 2^30.
  */

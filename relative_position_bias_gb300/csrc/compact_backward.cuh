@@ -152,6 +152,14 @@ __device__ __forceinline__ void cb_teardown(uint32_t tbase, int warp) {
   }
 }
 
+// Waits until the ring's copies have landed, all `issued` of them: at once after a whole run, and with
+// a limit if some role gave up.
+template <int KS>
+__device__ __forceinline__ void cb_drain(uint64_t* bars, int issued) {
+  for (int i = max(0, issued - KS); i < issued; ++i)
+    mbar_wait_budget(&bars[kCbRingFull + i % KS], (i / KS) & 1, kWaitBudgetCycles);
+}
+
 // Row `row` of a [BH, N, D] tensor (zeros if !valid) into TMEM as an A operand: this thread's lane, D / 2
 // columns of packed pairs.  Reading A from TMEM leaves shared memory, which a 128 x 64 product
 // would keep busy for 48 cycles a step of 16 (4 KB of A, 2 KB of B; the product takes 32), to B.
@@ -295,7 +303,8 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
       const float* hl = a.hl + (static_cast<size_t>(bh) * a.n_blocks + 2 * unit.tile) * a.H * kCbRow;
-      for (int i = 0; i < steps; ++i) {
+      int i = 0;
+      for (; i < steps; ++i) {
         if (!mbar_wait(&bars[kCbRingEmpty + i % KS], ((i / KS) & 1) ^ 1, abort_flag, status)) break;
         uint64_t* full = &bars[kCbRingFull + i % KS];
         const int kh0 = (unit.i0 + i) * KHT;
@@ -310,6 +319,7 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         for (int b = 0; b < 2; ++b)
           bulk_load(stage(i) + SM::kHl + b * SM::kHlBlock, hl + (static_cast<size_t>(b) * a.H + kh0) * kCbRow, hb, full);
       }
+      cb_drain<KS>(bars, i);
     } else if (warp == 1) {
       // -------------------------------------------------------------- S and dP
       constexpr uint32_t id_s = idesc_f16(kBlockM, BN, fmt, fmt, 0, 0);   // both K-major
@@ -573,7 +583,8 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           }
         }
         const uint32_t wb = static_cast<uint32_t>(a.W) * kCbRow * 4, hb = static_cast<uint32_t>(kh_count) * kCbRow * 4;
-        for (int i = 0; i < steps; ++i) {
+        int i = 0;
+        for (; i < steps; ++i) {
           if (!mbar_wait(&bars[kCbRingEmpty + i % KS], ((i / KS) & 1) ^ 1, abort_flag, status)) break;
           uint64_t* full = &bars[kCbRingFull + i % KS];
           const int blk = unit.i0 + i;
@@ -588,6 +599,7 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
           bulk_load(stage(i) + SM::kBias + wb, a.hl + (at * a.H + kh_first) * kCbRow, hb, full);
           bulk_load(stage(i) + SM::kND, a.nD + at * 64, 256, full);
         }
+        cb_drain<KS>(bars, i);
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------------- S^T and dP^T

@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
     if (warp == 0 && lane == 0) {
       // -------------------------------------------------------------- drel, half a tile of a table at a time
       bool ok = true;
-      for (int j = 0; ok && j < 4 * T; ++j) {
+      int j = 0;
+      for (; j < 4 * T; ++j) {
         const long long tile = tile_of(j >> 2);
         const int tb = (j >> 1) & 1, half = j & 1, L = tb == 0 ? a.H : a.W;
         const int rows = max(0, min(64, rows_of(tile) - 64 * half));
@@ -176,6 +177,9 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
         mbar_arrive_expect_tx(&bars[kPbStgFull + j % NS], static_cast<uint32_t>(whole) * 4);
         if (whole > 0) bulk_load(dst, src, static_cast<uint32_t>(whole) * 4, &bars[kPbStgFull + j % NS]);
       }
+      // the copies have landed: at once after a whole run, and with a limit if some role gave up
+      for (int i = max(0, j - NS); i < j; ++i)
+        mbar_wait_budget(&bars[kPbStgFull + i % NS], (i / NS) & 1, kWaitBudgetCycles);
     } else if (warp == 1) {
       // -------------------------------------------------------------- products
       constexpr uint32_t id_dq = idesc_f16(kBlockM, 64, kBF16, kBF16, 0, 1);   // G K-major, T N-major

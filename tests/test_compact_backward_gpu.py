@@ -237,3 +237,41 @@ def test_empty_batch_and_scratch():
         rpb.attention_backward(x["q"], x["k"], x["v"], x["rel_h"], x["rel_w"], out, lse, x["dout"], 2, 3,
                                workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert ei.value.status == 9
+
+
+def test_more_heads_than_a_grid_dimension():
+    """66000 problems of one token: P = 1, so dv = dout, and dq, dk and the bias's gradients vanish."""
+    BH = 66000
+    g = torch.Generator(device="cuda").manual_seed(12)
+    q, k, v, do = (torch.randn(BH, 1, 64, generator=g, device="cuda").to(BF) for _ in range(4))
+    rh, rw = torch.randn(BH, 1, 1, generator=g, device="cuda"), torch.randn(BH, 1, 1, generator=g, device="cuda")
+    out, lse = rpb.attention_lse(q, k, v, rh, rw, 1, 1)
+    # out = v but for v's conversion to fp16 in the forward, which moves a |v| below 2^-14 by up to 2^-25
+    assert ((out.float() - v.float()).abs() <= 2.0 ** -25 + 2.0 ** -8 * v.float().abs() * (v.float().abs() < 2.0 ** -14)).all()
+    dq, dk, dv, dh, dw = rpb.attention_backward(q, k, v, rh, rw, out, lse, do, 1, 1, grad_dtype=BF)
+    assert torch.equal(dv, do)
+    # dZ = P (dP - D) with dP = D: the roundings of two sums of 64 products of size 4 and of the exponent
+    assert dh.abs().max() <= 2.0 ** -10 and torch.equal(dh, dw)
+    assert dq.abs().max() <= 2.0 ** -8 and dk.abs().max() <= 2.0 ** -8
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own buffers, give what they give one after the other."""
+    xs = [make(20, 16, 20, 64, BF, seed=s) for s in (13, 14)]
+    want = [run(x, 16, 20, 0.125) for x in xs]
+    ds = [{n: t.cuda() for n, t in x.items()} for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(5):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                d = ds[i]
+                o, l = rpb.attention_lse(d["q"], d["k"], d["v"], d["rel_h"], d["rel_w"], 16, 20, 0.125)
+                got[i] = (o, l, rpb.attention_backward(d["q"], d["k"], d["v"], d["rel_h"], d["rel_w"], o, l, d["dout"],
+                                                       16, 20, 0.125))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        for x, y in zip(a[2], b[2]):
+            assert torch.equal(x, y)

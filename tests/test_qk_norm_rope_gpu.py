@@ -231,3 +231,27 @@ def test_graph_and_other_stream():
     torch.cuda.synchronize()
     for a, b in zip(outs, want):
         assert torch.equal(a, b)
+
+
+def test_largest_head_count_and_long_rows():
+    """Heads up to the limit in one dimension of the grid, and a token axis past a block's runs."""
+    q, k, v, kw, dz = make(1, 2, 16384, 1, 64, BF, True, 64, False, 0, seed=7)
+    check_forward(q, k, v, kw, rpb.qk_norm_rope(q, k, v, **kw), BF, "heads")
+    q, k, v, kw, dz = make(3, 9001, 1, 1, 64, HF, True, 64, True, 0, seed=8)
+    check_forward(q, k, v, kw, rpb.qk_norm_rope(q, k, v, **kw), HF, "tokens")
+    grads = rpb.qk_norm_rope_backward(q, k, *dz, grad_dtype=HF, **kw)
+    for i, (name, x) in enumerate((("q", q), ("k", k))):
+        okw = oracle_kw(kw, name)
+        _, dw = oracle.qk_norm_rope_backward(f64(x), f64(dz[i]), **okw)
+        back, _ = oracle.qk_norm_rope_backward(f64(x), f64(dz[i]), **{**okw, "weight": None})
+        xf = f64(x)
+        terms = np.abs(back * xf / np.sqrt((xf * xf).mean(-1, keepdims=True) + 1e-6)).sum((0, 1, 2))
+        assert (np.abs(f64(grads[3 + i]) - dw) <= 2.0 ** -18 * terms).all()
+
+
+def test_other_device_tensors_are_refused():
+    q, k, v, kw, dz = make(1, 4, 2, 1, 64, BF, True, 64, False, 0)
+    kw["cos"] = kw["cos"].cpu()
+    with pytest.raises(rpb.DeraError) as e:
+        rpb.qk_norm_rope(q, k, v, **kw)
+    assert e.value.status == 6
