@@ -154,7 +154,10 @@ DERA_API dera_status dera_relpos_fused(const void* q, const void* k, const void*
  * not used by another call in flight.  Its contents need no initialisation
  * and are never cleared: each launch marks its arrivals with a 64-bit tag that
  * no earlier launch of the process used, so whatever an earlier call (or one
- * that stopped early) left behind is ignored.
+ * that stopped early) left behind is ignored.  A launch captured in a graph
+ * keeps its tag, which the pieces take back out of the counters, so the graph
+ * may be replayed any number of times; after a replay that stopped early
+ * (dera_relpos_device_status), clear the workspace or capture anew.
  */
 DERA_API dera_status dera_relpos_workspace_size(int BH, int H, int W, int head_dim, size_t* bytes);
 

@@ -1042,6 +1042,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         //    second and merges both published slots.  Whatever an earlier
         //    (or stopped) launch left holds another tag, so the counters
         //    never need clearing.
+        //  - Whichever piece merges was the last to look at the counter and
+        //    leaves a value there that is not the tag: a captured launch
+        //    comes back with the same tag at every replay.
         // Both merges combine the pieces in the same order (the unit's first
         // piece, then its second) from the same fp32 values, so the result
         // does not depend on which path ran.  O is merged and stored 64
@@ -1084,7 +1087,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         };
         unsigned long long* counter = args.counters + 2 * static_cast<size_t>(sg.u) + wg;
         if (r == 0) {
-          merge_flag[wg] = ld_acquire_gpu(counter) == args.tag;
+          const bool there = ld_acquire_gpu(counter) == args.tag;
+          if (there) *counter = ~args.tag;
+          merge_flag[wg] = there;
           mbar_arrive(&bars[kBarMergeGo + wg]);
         }
         ok = warp_all(mbar_wait(&bars[kBarMergeGo + wg], pseg & 1, abort_flag, status));
@@ -1141,7 +1146,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int pw = ppub++;
           if (r == 0) {
             const bool w_ok = mbar_wait(&bars[kBarPartWritten + wg], pw & 1, abort_flag, status);
-            merge_flag[wg] = w_ok && atomic_exch_acq_rel_gpu(counter, args.tag) == args.tag;
+            const bool there = w_ok && atomic_exch_acq_rel_gpu(counter, args.tag) == args.tag;
+            if (there) *counter = ~args.tag;
+            merge_flag[wg] = there;
             mbar_arrive(&bars[kBarMergeGo + wg]);
           }
           ok = warp_all(mbar_wait(&bars[kBarMergeGo + wg], pseg & 1, abort_flag, status));

@@ -50,7 +50,7 @@ struct AttnArgs {
   int* status;         // device status word
   float* partials;     // [2 * gridDim.x][2][slot_floats<D>()] partial results (split units only)
   unsigned long long* counters;  // [n_units][2] arrival tags per unit and query tile (split units only)
-  unsigned long long tag;        // this launch's arrival tag: no earlier launch of the process used it
+  unsigned long long tag;        // this launch's arrival tag: no other launch of the process has it, but every replay of a captured one
   int BH, H, W, N;
   int n_qtiles;        // ceil(N / 128)
   int n_pairs;         // ceil(n_qtiles / 2): query-tile pairs per head

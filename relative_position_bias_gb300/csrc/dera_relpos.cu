@@ -200,7 +200,8 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Arrival tags of the split schedule's per-unit counters: a 64-bit sequence
 // from a random start, so no two launches of this process share a tag and
-// counters left by any earlier launch (finished or stopped) never match.
+// counters left by any earlier launch (finished or stopped) never match.  A replayed launch keeps its
+// tag; the kernel takes the tag out of every counter that its two pieces have passed.
 static unsigned long long next_launch_tag() {
   static std::atomic<unsigned long long> next{[] {
     unsigned long long seed = 0x9e3779b97f4a7c15ull ^ static_cast<unsigned long long>(

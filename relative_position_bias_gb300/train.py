@@ -16,7 +16,7 @@ import os
 import torch
 
 from . import api
-from .api import DERA_F32, _check, _expect, _ptr, _workspace
+from .api import DERA_F32, _check, _expect, _ptr
 
 HEADER = os.path.join(os.path.dirname(api.HEADER), "dera_train.h")
 _CODE = api._DTYPE_CODE
@@ -251,7 +251,8 @@ def attention_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h: torc
                   workspace=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Training forward of the two-step form via ``dera_relpos_attention_lse``: ``(out, lse)``, lse
     ``[BH, N]`` fp32 (base 2).  A bias of -inf masks its keys; a row with every key masked gives
-    out = 0 and lse = -inf.  ``workspace`` as in :func:`~relative_position_bias_gb300.attention`."""
+    out = 0 and lse = -inf.  ``workspace``: a caller-owned uint8 tensor that no other call in flight
+    uses, None for a buffer of this call, or False for none (whole units)."""
     BH, N, d = q.shape
     scale = d ** -0.5 if scale is None else scale
     size = (BH, H * W, d)
@@ -266,7 +267,9 @@ def attention_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h: torc
     out = _like(q, out_dtype or q.dtype)
     lse = torch.empty((BH, N), dtype=torch.float32, device=q.device)
     st = _launch_stream(q.device, stream)
-    ws, ws_bytes = _workspace(q.device, BH, H, W, d, workspace, st)
+    # a buffer of this call, not the stream's: graphs captured on one stream may be replayed side by side
+    keep, ws, ws_bytes = ((None, None, 0) if workspace is False else
+                          _scratch(q.device, stream, st, workspace, "dera_relpos_workspace_size", BH, H, W, d))
     _check(api.load_library().dera_relpos_attention_lse(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), rel_h.data_ptr(), rel_w.data_ptr(), out.data_ptr(), lse.data_ptr(),
         BH, H, W, d, scale, _dtype(q.dtype), _dtype(rel_h.dtype), _dtype(out.dtype), ws, ws_bytes, st))

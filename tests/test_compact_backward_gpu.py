@@ -275,3 +275,60 @@ def test_two_calls_at_once():
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
         for x, y in zip(a[2], b[2]):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("entry", ["attention_lse", "attention", "fused"])
+def test_replays_of_split_units(entry):
+    """A graph whose units are cut in two, replayed on new inputs each time: the pieces that an earlier
+    replay left behind are not taken for this one's."""
+    H, W, BH = 64, 64, 12
+    assert rpb.workspace_size(BH, H, W, 64) > 0
+    x = {n: t.cuda() for n, t in make(BH, H, W, 64, BF, seed=15).items()}
+    g = torch.Generator().manual_seed(2)
+    th, tw = ((0.3 * torch.randn(2 * L - 1, 64, generator=g)).to(BF).cuda() for L in (H, W))
+
+    def step():
+        if entry == "fused":
+            return (rpb.fused(x["q"], x["k"], x["v"], th, tw, H, W, 0.125),)
+        if entry == "attention":
+            return (rpb.attention(x["q"], x["k"], x["v"], x["rel_h"], x["rel_w"], H, W, 0.125),)
+        return rpb.attention_lse(x["q"], x["k"], x["v"], x["rel_h"], x["rel_w"], H, W, 0.125)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        res = step()
+    for _ in range(4):
+        for n in ("q", "v"):
+            x[n].mul_(-0.75)
+        graph.replay()
+        got = [t.clone() for t in res]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+
+
+def test_two_graphs_at_once():
+    """Two graphs captured one after the other share no scratch: replayed at the same time on two streams."""
+    H, W, BH = 64, 64, 12
+    assert rpb.workspace_size(BH, H, W, 64) > 0
+    xs = [{n: t.cuda() for n, t in make(BH, H, W, 64, BF, seed=s).items()} for s in (16, 17)]
+    want, graphs, res = [], [], []
+    for x in xs:
+        call = lambda: rpb.attention_lse(x["q"], x["k"], x["v"], x["rel_h"], x["rel_w"], H, W, 0.125)
+        want.append(call())
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            res.append(call())
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for r in res:
+            for t in r:
+                t.zero_()
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(res, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
