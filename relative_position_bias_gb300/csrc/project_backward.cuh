@@ -3,22 +3,29 @@
 // With G[r][i] = drel[r][coord(r) - i + L - 1] (0 outside the row; coord is qh or qw), which
 // holds a token's bias gradient by table row,
 //   dq[r] = dq_in[r] + G_h[r] T_h + G_w[r] T_w,   dT = G^T q,
-// so both are plain products once G is formed.  What bounds the pass is memory (4 (H + W)
-// bytes of drel, and q, dq_in and dq, per token); the products take half as long.
+// so both are plain products once G is formed.  What a pass cannot do without is its memory traffic: 4 (H + W)
+// bytes of drel, and q, dq_in and dq, per token.
 //
 // A CTA takes every gridDim.x-th tile of 128 tokens (of any heads: a token's coordinates are
-// all that matters) and 64 columns of head_dim.  drel comes by bulk copies, half a tile of one table at a
+// all that matters) and 64 columns of head_dim.  drel comes by bulk copies, 64 tokens of one table at a
 // time and ahead of its use; sixteen warps form G in shared memory, K-major (tokens by table rows); the same G,
-// read M-major, serves dT.
+// read M-major, serves dT.  G's two halves of 64 tokens are formed in turn, each while the products of the other
+// run (dq's have M = 64 for this; dT's sum over tokens, 64 at a time).
+//
+// Measured on 96 heads of 64 x 64 tokens, head_dim 64, bf16 (337 MB): 150 us, 2.2 TB/s; 157 us with both halves
+// formed together before the products.  No one part bounds it: without its products it takes 133 us, without forming
+// G 119, without either 81 (timings only).  Forming G is some 1300 issue slots a scheduler and half, in
+// chains of loads, conversions and stores that 48 registers a thread do not overlap further; splitting by truncation
+// (fewer conversions), whole sectors of dq per store, one arrival a warp and G held in registers ahead
+// of its buffer measured the same or slower.
 //
 // Precision: tensor-core operands have 16 bits, drel has 32.  G is split into three bf16 terms
 // (what is left is 2^-24 of a value: the tables' gradients are fp32 sums over all tokens), of which the first two
-// serve a 16-bit dq (2^-16; one term would leave 2^-8).  bf16 and not fp16, because a gradient may have any size; fp16
+// serve a 16-bit dq (2^-16; one term would leave 2^-8).  With two terms the tables' gradients were 2.5e-6 off
+// (relative, the case above), with three 4e-7.  bf16 and not fp16, because a gradient may have any size; fp16
 // q and tables are split into two bf16 terms as well, exactly (11 bits = 8 + 3); products of terms
-// below 2^-16 of the whole are left out.  The tensor core adds to its accumulator with
-// truncation, 2^-24 a step and always towards zero: over all of a CTA's tiles that left 1e-4 of the tables'
-// gradients, so dT leaves TMEM after every tile and is summed in fp32 registers; the CTAs' partial sums are
-// added in a fixed order by relpos_pb_tables_kernel.
+// below 2^-16 of the whole are left out.  dT leaves TMEM after every tile and is summed in fp32 registers, where
+// sums are rounded to nearest; the CTAs' partial sums are added in a fixed order by relpos_pb_tables_kernel.
 #pragma once
 #include "common.cuh"
 #include "train.cuh"
@@ -41,22 +48,22 @@ struct PbSmem {
   static constexpr int kStg = kG + 3 * kPbAtoms;              // [NS] 64 rows of drel_h or drel_w, fp32
   static constexpr int kStgBytes = 64 * 64 * 4;
   static constexpr int kBars = kStg + NS * kStgBytes;
-  static constexpr int kMisc = kBars + 26 * 8;
+  static constexpr int kMisc = kBars + 28 * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
 enum : int {
   kPbStgFull = 0,   // [5] a half of drel landed
-  kPbStgFree = 5,   // [5] eight warps have read it
-  kPbGFull = 10,    // G (and with the first table q) written
-  kPbMmaDone = 11,  // its products are complete
-  kPbDqFull = 12,   // [2] dq of a tile is in TMEM
-  kPbDqFree = 14,   // [2] and has been read
-  kPbDtFull = 16,   // [table][2] dT of a tile
-  kPbDtFree = 20,   // [table][2]
-  kPbAllDone = 24,  // every product is complete
-  kPbBars = 25
+  kPbStgFree = 5,   // [5] and has been read
+  kPbGFull = 10,    // [half] 64 rows of G (and with the first table of q) written
+  kPbMmaDone = 12,  // [half] their products are complete
+  kPbDqFull = 14,   // [2] dq of a tile is in TMEM
+  kPbDqFree = 16,   // [2] and has been read
+  kPbDtFull = 18,   // [table][2] dT of a tile
+  kPbDtFree = 22,   // [table][2]
+  kPbAllDone = 26,  // every product is complete
+  kPbBars = 27
 };
 
 // 16-bit operand element (row, i) of a K-major 128 x 128 tile, 128-byte swizzled.
@@ -84,27 +91,32 @@ __device__ __forceinline__ void pb_terms(const uint4& u, uint4& t1, uint4& t2) {
   t2 = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-// 8 rows of G (its three terms) from their staged drel rows of L floats: LPR lanes a row, a pair of columns
-// (i, i + 1) each, ATOMS times 2 LPR columns.  Lane l < 8 holds row l's coordinate, or one so large
-// that the row comes out as zeros.
+// 4 rows of G (its three terms) from their staged drel rows of L floats: LPR lanes a row, a pair of columns
+// (i, i + 1) each, ATOMS times 2 LPR columns.  The first is row r8 (0 or 4) of a swizzle
+// group.  Lane l < 4 holds row l's coordinate, or one so large that the row comes out as zeros.
 template <int LPR, int ATOMS>
-__device__ __forceinline__ void pb_rows(const float* stg, uint8_t* g, int coord, int L, int lane) {
+__device__ __forceinline__ void pb_rows(const float* stg, uint8_t* g, int r8, int coord, int L, int lane) {
   constexpr int RPI = 32 / LPR;
   const int sub = lane / LPR, p = lane % LPR;
   const uint32_t n = static_cast<uint32_t>(L);
+  // a row's values lie two apart from lane to lane: the lower lanes read their even one first, the
+  // upper lanes their odd one, and the warp's 32 words are in different banks
+  const int odd = LPR == 32 ? p >> 4 : 0;
   stg += L - 1 - 2 * p;
   g += (p & 3) * 4;
-  #pragma unroll 4
-  for (int it = 0; it < 8 / RPI; ++it) {
+  #pragma unroll
+  for (int it = 0; it < 4 / RPI; ++it) {
     const int rl = it * RPI + sub;
     const int c = __shfl_sync(0xffffffffu, coord, rl);
     const int k0 = c + L - 1 - 2 * p;
     const float* src = stg + rl * L + c;
-    uint8_t* at = g + rl * 128 + (((p >> 2) ^ (rl & 7)) << 4);
+    uint8_t* at = g + rl * 128 + (((p >> 2) ^ (r8 + rl)) << 4);
     #pragma unroll
     for (int a = 0; a < ATOMS; ++a) {
-      const float v0 = static_cast<uint32_t>(k0 - 64 * a) < n ? src[-64 * a] : 0.f;
-      const float v1 = static_cast<uint32_t>(k0 - 64 * a - 1) < n ? src[-64 * a - 1] : 0.f;
+      const int k1 = 64 * a + odd, k2 = 64 * a + (odd ^ 1);
+      const float x1 = static_cast<uint32_t>(k0 - k1) < n ? src[-k1] : 0.f;
+      const float x2 = static_cast<uint32_t>(k0 - k2) < n ? src[-k2] : 0.f;
+      const float v0 = odd ? x2 : x1, v1 = odd ? x1 : x2;
       const uint32_t g1 = pack_bf16x2(v0, v1);
       const float2 h = unpack_in(g1, kBF16);
       const float r0 = v0 - h.x, r1 = v1 - h.y;   // exact
@@ -140,8 +152,7 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
     *abort_flag = 0;
     for (int i = 0; i < kPbBars; ++i) {
       int n = 1;
-      if (i >= kPbStgFree && i < kPbStgFree + 5) n = kPbBuilders / 2;
-      else if (i == kPbGFull) n = kPbBuilders;
+      if (i >= kPbStgFree && i < kPbGFull + 2) n = kPbBuilders;
       else if (i == kPbDqFree || i == kPbDqFree + 1) n = 256;
       else if (i >= kPbDtFree && i < kPbDtFree + 4) n = 128;
       mbar_init(&bars[i], n);
@@ -155,7 +166,7 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tbase = *slot;   // dq of even and odd tiles [0, 64), [64, 128), dT [128 + 128 table + 64 parity, + 64)
+  const uint32_t tbase = *slot;   // dq [128 parity + 64 half, + 64), dT [256 + 128 table + 64 parity, + 64)
 
   if (warp < 4) {
     regs_release<kPbRegsCtl>();
@@ -182,16 +193,16 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
         mbar_wait_budget(&bars[kPbStgFull + i % NS], (i / NS) & 1, kWaitBudgetCycles);
     } else if (warp == 1) {
       // -------------------------------------------------------------- products
-      constexpr uint32_t id_dq = idesc_f16(kBlockM, 64, kBF16, kBF16, 0, 1);   // G K-major, T N-major
+      constexpr uint32_t id_dq = idesc_f16(64, 64, kBF16, kBF16, 0, 1);          // G K-major, T N-major
       constexpr uint32_t id_dt = idesc_f16(kBlockM, 64, kBF16, kBF16, 1, 1);   // G^T M-major, q N-major
-      constexpr uint32_t kGTerm = kPbAtoms >> 4, kAtom = kTileBytes >> 4;
+      constexpr uint32_t kGTerm = kPbAtoms >> 4, kAtom = kTileBytes >> 4, kHalf = kAtom / 2;
       const uint64_t d_g = sdesc_sw128(smem_u32(smem + SM::kG), 16, 1024);
       const uint64_t d_gt = sdesc_sw128(smem_u32(smem + SM::kG), kTileBytes, 1024);   // its two atoms lie along M
       const uint64_t d_q = sdesc_sw128(smem_u32(smem + SM::kQ), 16, 1024);
-      for (int s = 0; s < 2 * T; ++s) {
-        const int t = s >> 1, tb = s & 1, buf = t & 1;
-        bool ok = mbar_wait(&bars[kPbGFull], s & 1, abort_flag, status);
-        if (t >= 2) {   // tile t - 2's dq and dT have been read
+      for (int s = 0; s < 4 * T; ++s) {
+        const int t = s >> 2, tb = (s >> 1) & 1, half = s & 1, buf = t & 1;
+        bool ok = mbar_wait(&bars[kPbGFull + half], (s >> 1) & 1, abort_flag, status);
+        if (t >= 2 && half == 0) {   // tile t - 2's dq and dT have been read
           const uint32_t ph = ((t >> 1) - 1) & 1;
           ok = ok && (tb == 1 || mbar_wait(&bars[kPbDqFree + buf], ph, abort_flag, status)) &&
                mbar_wait(&bars[kPbDtFree + 2 * tb + buf], ph, abort_flag, status);
@@ -199,27 +210,27 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
         if (!warp_all(ok)) break;
         tc_fence_after();
         const uint64_t d_t = sdesc_sw128(smem_u32(smem + SM::kT + tb * kTileBytes), 16, 1024);
-        const uint32_t dq = tbase + 64 * buf, dt = tbase + 128 + 128 * tb + 64 * buf;
+        const uint32_t dq = tbase + 128 * buf + 64 * half, dt = tbase + 256 + 128 * tb + 64 * buf;
         const int ks = (2 * (tb == 0 ? a.H : a.W) + 14) / 16;   // 16-row steps over the table's 2L - 1 rows
         // dq and dT: G1 X1 + G2 X1 + G3 X1 (+ G1 X2 + G2 X2); a 16-bit dq does without G3 T1 and G2 T2
         #pragma unroll
         for (int p = 0; p < (TERMS == 1 ? 3 : 5); ++p) {
           if ((p == 2 || p == 4) && a.grad_fmt != kF32) continue;
-          const uint32_t g = (p < 3 ? p : p - 3) * kGTerm, x = p < 3 ? 0 : 2 * kAtom;
+          const uint32_t g = (p < 3 ? p : p - 3) * kGTerm + half * kHalf, x = p < 3 ? 0 : 2 * kAtom;
           for (int k = 0; k < ks; ++k)
             umma_ss_w(dq, d_g + g + (k / 4) * kAtom + 2 * (k % 4), d_t + x + 128 * k, id_dq,
                       (tb > 0 || p > 0 || k > 0) ? 1u : 0u);
         }
-        if (tb == 1) umma_commit_w(&bars[kPbDqFull + buf]);
+        if (tb == 1 && half == 1) umma_commit_w(&bars[kPbDqFull + buf]);
         #pragma unroll
         for (int p = 0; p < (TERMS == 1 ? 3 : 5); ++p) {
-          const uint32_t g = (p < 3 ? p : p - 3) * kGTerm, x = p < 3 ? 0 : kAtom;
+          const uint32_t g = (p < 3 ? p : p - 3) * kGTerm + half * kHalf, x = (p < 3 ? 0 : kAtom) + half * kHalf;
           #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_ss_w(dt, d_gt + g + 128 * k, d_q + x + 128 * k, id_dt, (p > 0 || k > 0) ? 1u : 0u);
+          for (int k = 0; k < 4; ++k)
+            umma_ss_w(dt, d_gt + g + 128 * k, d_q + x + 128 * k, id_dt, (half > 0 || p > 0 || k > 0) ? 1u : 0u);
         }
-        umma_commit_w(&bars[kPbDtFull + 2 * tb + buf]);
-        umma_commit_w(&bars[kPbMmaDone]);
+        umma_commit_w(&bars[kPbMmaDone + half]);
+        if (half == 1) umma_commit_w(&bars[kPbDtFull + 2 * tb + buf]);
       }
       // every product issued above completes before TMEM is released
       umma_commit_w(&bars[kPbAllDone]);
@@ -230,7 +241,7 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
     // ---------------------------------------------------------------- builders
     regs_release<kPbRegsBuild>();
     const int tid = threadIdx.x - 128;
-    const int half = (warp - 4) >> 3, row0 = 8 * (warp - 4);   // a warp forms 8 rows of G
+    const int row0 = 4 * (warp - 4);   // a warp forms 4 rows of each half of G
     // the tables' columns [c0, c0 + 64), rows past 2L - 1 as zeros
     for (int e = tid; e < 2 * kBlockM * 8; e += kPbBuilders) {
       const int tb = e >> 10, row = (e >> 3) & 127, ch = e & 7;
@@ -244,7 +255,7 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
       *reinterpret_cast<uint4*>(at) = t1;
       if (TERMS == 2) *reinterpret_cast<uint4*>(at + 2 * kTileBytes) = t2;
     }
-    // this thread's two 16-byte chunks of a tile's q
+    // this thread's 16-byte chunk of either half of a tile's q
     uint4 qv[2];
     auto load_q = [&](int t) {
       const long long tile = tile_of(t);
@@ -260,44 +271,44 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
     };
     load_q(0);
     bool ok = true;
-    int qh = 0, qw = 0;
-    for (int s = 0; ok && s < 2 * T; ++s) {
-      const int t = s >> 1, tb = s & 1, L = tb == 0 ? a.H : a.W;
-      const int j = 2 * s + half;
-      if (tb == 0) {
-        const long long g = tile_of(t) * kBlockM + row0 + (lane & 7);
+    int qh[2] = {0, 0}, qw[2] = {0, 0};
+    for (int t = 0; ok && t < T; ++t) {
+      #pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const long long g = tile_of(t) * kBlockM + 64 * half + row0 + (lane & 3);
         const int n = static_cast<int>(g % a.N);
-        qh = n / a.W;
-        qw = n - qh * a.W;
-        if (g >= a.tokens) qh = qw = 1 << 20;   // a row past the last token: zeros
+        qh[half] = n / a.W;
+        qw[half] = n - qh[half] * a.W;
+        if (g >= a.tokens) qh[half] = qw[half] = 1 << 20;   // a row past the last token: zeros
       }
-      // the last products have read G (and q), and the half has landed
-      ok = (s == 0 || mbar_wait(&bars[kPbMmaDone], (s - 1) & 1, abort_flag, status)) &&
-           mbar_wait(&bars[kPbStgFull + j % NS], (j / NS) & 1, abort_flag, status);
-      ok = warp_all(ok);
-      if (!ok) break;
-      const float* stg = reinterpret_cast<const float*>(smem + SM::kStg + (j % NS) * SM::kStgBytes) + (row0 & 63) * L;
-      uint8_t* g = smem + SM::kG + row0 * 128;
-      const int c = tb == 0 ? qh : qw;
-      if (L <= 8) pb_rows<8, 1>(stg, g, c, L, lane);         // 15 table rows at most: 16 columns of G
-      else if (L <= 16) pb_rows<16, 1>(stg, g, c, L, lane);  // 31: 32
-      else if (L <= 32) pb_rows<32, 1>(stg, g, c, L, lane);  // 63: 64
-      else pb_rows<32, 2>(stg, g, c, L, lane);
-      mbar_arrive(&bars[kPbStgFree + j % NS]);   // after the stores, which need every staged value in a register
-      if (tb == 0) {
-        #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int e = tid + i * kPbBuilders;
+      #pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const int s = 4 * t + i, tb = i >> 1, half = i & 1, L = tb == 0 ? a.H : a.W;
+        // the last products of these 64 rows have read G (and q), and the half has landed
+        ok = (s < 2 || mbar_wait(&bars[kPbMmaDone + half], ((s >> 1) - 1) & 1, abort_flag, status)) &&
+             mbar_wait(&bars[kPbStgFull + s % NS], (s / NS) & 1, abort_flag, status);
+        ok = warp_all(ok);
+        if (!ok) break;
+        const float* stg = reinterpret_cast<const float*>(smem + SM::kStg + (s % NS) * SM::kStgBytes) + row0 * L;
+        uint8_t* g = smem + SM::kG + (64 * half + row0) * 128;
+        const int c = tb == 0 ? (half == 0 ? qh[0] : qh[1]) : (half == 0 ? qw[0] : qw[1]), r8 = row0 & 7;
+        if (L <= 8) pb_rows<8, 1>(stg, g, r8, c, L, lane);         // 15 table rows at most: 16 columns of G
+        else if (L <= 16) pb_rows<16, 1>(stg, g, r8, c, L, lane);  // 31: 32
+        else if (L <= 32) pb_rows<32, 1>(stg, g, r8, c, L, lane);  // 63: 64
+        else pb_rows<32, 2>(stg, g, r8, c, L, lane);
+        mbar_arrive(&bars[kPbStgFree + s % NS]);   // after the stores, which need every staged value in a register
+        if (tb == 0) {
+          const int e = tid + half * kPbBuilders;
           uint4 t1, t2;
-          pb_terms<BF16>(qv[i], t1, t2);
+          pb_terms<BF16>(half == 0 ? qv[0] : qv[1], t1, t2);
           uint8_t* at = smem + SM::kQ + pb_off(e >> 3, 8 * (e & 7));
           *reinterpret_cast<uint4*>(at) = t1;
           if (TERMS == 2) *reinterpret_cast<uint4*>(at + kTileBytes) = t2;
+          if (half == 1 && t + 1 < T) load_q(t + 1);
         }
-        if (t + 1 < T) load_q(t + 1);
+        fence_proxy_async_smem();
+        mbar_arrive(&bars[kPbGFull + half]);
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&bars[kPbGFull]);
     }
   } else {
     // ---------------------------------------------------------------- dq, half of the columns each, and one table's dT
@@ -312,43 +323,61 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
       const int buf = t & 1;
       const uint32_t ph = (t >> 1) & 1;
       const long long tile = tile_of(t);
-      const bool valid = r < rows_of(tile);
-      const size_t at = (static_cast<size_t>(tile) * kBlockM + r) * a.D + c0 + 32 * tb;
+      // a half's 64 rows lie in the first 16 lanes of each warp's 32; every other eight columns of a row are the
+      // other lanes', so that a row's two threads touch whole 32-byte sectors
+      const int row0 = 16 * wq + (lane & 15), rows = rows_of(tile);
+      const size_t at = (static_cast<size_t>(tile) * kBlockM + row0) * a.D + c0 + 32 * tb + (lane & 16) / 2;
+      const size_t at_half = 64 * static_cast<size_t>(a.D);
       // 16-bit dq_in: on its way while the products run
-      const bool early = a.dq_in && a.grad_fmt != kF32 && valid;
-      uint4 x[4];
+      const bool early = a.dq_in && a.grad_fmt != kF32;
+      uint4 x[2][2] = {};
       if (early) {
         #pragma unroll
-        for (int c = 0; c < 4; ++c) x[c] = *(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dq_in) + at) + c);
+        for (int h = 0; h < 2; ++h)
+          if (row0 + 64 * h < rows) {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dq_in) + at + h * at_half);
+            x[h][0] = p[0];
+            x[h][1] = p[2];
+          }
       }
-      uint32_t u[32];
       ok = warp_all(mbar_wait(&bars[kPbDqFull + buf], ph, abort_flag, status));
       if (!ok) break;
       tc_fence_after();
-      tmem_ld32(tbase + lanes + 64 * buf + 32 * tb, u);
-      tmem_wait_ld();
-      tc_fence_before();
-      mbar_arrive(&bars[kPbDqFree + buf]);
-      if (valid) {
+      #pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool valid = row0 + 64 * h < rows;
         #pragma unroll
-        for (int c = 0; c < 32; c += 8) {
+        for (int c = 0; c < 32; c += 16) {
+          const uint32_t from = tbase + lanes + 128 * buf + 64 * h + 32 * tb + c;
+          uint32_t lo[8], hi[8];
+          tmem_ld8(from, lo);
+          tmem_ld8(from + 8, hi);
+          tmem_wait_ld();
+          if (h == 1 && c == 16) {
+            tc_fence_before();
+            mbar_arrive(&bars[kPbDqFree + buf]);
+          }
           float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          if (early) unpack8(x[c / 8], v, a.grad_fmt);
-          else if (a.dq_in) load8(a.dq_in, at + c, v, a.grad_fmt);
+          if (early) unpack8(x[h][c / 16], v, a.grad_fmt);
+          else if (a.dq_in && valid) load8(a.dq_in, at + h * at_half + c, v, a.grad_fmt);
           #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += __uint_as_float(u[c + e]);
-          store8(a.dq, at + c, v, a.grad_fmt);
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t far = __shfl_sync(0xffffffffu, hi[e], lane & 15);
+            v[e] += __uint_as_float(lane < 16 ? lo[e] : far);
+          }
+          if (valid) store8(a.dq, at + h * at_half + c, v, a.grad_fmt);
         }
       }
       ok = warp_all(mbar_wait(&bars[kPbDtFull + 2 * tb + buf], ph, abort_flag, status));
       if (!ok) break;
       tc_fence_after();
       #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        tmem_ld32(tbase + lanes + 128 + 128 * tb + 64 * buf + 32 * h, u);
+      for (int h = 0; h < 64; h += 16) {
+        uint32_t u[16];
+        tmem_ld16(tbase + lanes + 256 + 128 * tb + 64 * buf + h, u);
         tmem_wait_ld();
         #pragma unroll
-        for (int e = 0; e < 32; ++e) acc[32 * h + e] += __uint_as_float(u[e]);
+        for (int e = 0; e < 16; ++e) acc[h + e] += __uint_as_float(u[e]);
       }
       tc_fence_before();
       mbar_arrive(&bars[kPbDtFree + 2 * tb + buf]);
