@@ -12,6 +12,10 @@
 // keeps one (token, slot) and walks over heads: the angles and weights of its slot are
 // loaded once and stay in registers.  Reads are whole rows of 128 or 256 bytes in
 // token order, writes whole rows of consecutive tokens of a head.
+//
+// Measured: forward, 8 x 4096 tokens, 3 x 16 heads of 128, fp16, 806 MB: 123 us, 6.5 TB/s (a plain copy reaches
+// 6.8).  Backward, 8 x 4096 tokens, 3 x 12 heads of 64, bf16, 404 MB: 78 us, 5.2 TB/s; it issues in 57 % of the
+// cycles (two sums of eight lanes a row) and waits for loads in most others.  The weights' sums are 5 us more.
 #pragma once
 #include <cstdint>
 
@@ -187,7 +191,8 @@ struct Grad8 {
 
 // The weights' gradients are sums over every row of every token: a block takes
 // every gridDim.x-th run of tokens and keeps its slots' sums in registers, one partial row
-// per block, which qk_weight_grad_kernel adds in a fixed order.
+// per block, which qk_weight_grad_kernel adds in a fixed order.  Four rows in flight a thread and three blocks an
+// SM: 78 us on the case above; three rows 93, two 95.
 template <bool BF16, int D, int MODE, bool NORM, bool ZF32>
 __global__ void __launch_bounds__(kQkThreads, 3) qk_norm_rope_bwd_kernel(const QkArgs a) {
   constexpr int LANES = D / 8, TOK = kQkThreads / LANES, WARPS = kQkThreads / 32, U = 4;
