@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -22,10 +23,9 @@ HEADER = os.path.join(os.path.dirname(api.HEADER), "dera_train.h")
 _CODE = api._DTYPE_CODE
 
 
-class _Heads(ctypes.Structure):
-    """``dera_heads``: a [B, N, heads, d] tensor by its strides."""
-    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_longlong), ("stride_token", ctypes.c_longlong),
-                ("stride_head", ctypes.c_longlong)]
+# ``dera_heads``: a [B, N, heads, d] tensor by its address and strides, packed as bytes (ctypes passes their
+# address; filling a ctypes array costs seven times as much)
+_pack_heads = struct.Struct("=4q").pack
 
 
 def declare(lib: ctypes.CDLL) -> None:
@@ -106,22 +106,16 @@ def _scratch(device: torch.device, stream, handle, workspace: torch.Tensor | Non
 
 
 # ------------------------------------------------------------------------ norms, rotation, layout
-def _heads(tensors, shapes, names):
-    """The ``dera_heads`` of some tensors (None: none), one after another, and their addresses."""
-    flat = []
-    for t, shape, name in zip(tensors, shapes, names):
-        if t is None:
-            flat += (0, 0, 0, 0)
-            continue
-        if t.shape != shape:
-            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        sb, st, sh, sd = t.stride()
-        if sd != 1:
-            raise ValueError(f"{name}: the last dimension must be contiguous")
-        flat += (t.data_ptr(), sb, st, sh)
-    views = (ctypes.c_int64 * len(flat))(*flat)
-    at = ctypes.addressof(views)
-    return views, [None if t is None else at + 32 * k for k, t in enumerate(tensors)]
+def _heads(t: torch.Tensor | None, shape, name: str) -> bytes | None:
+    """The ``dera_heads`` of a tensor (None: none)."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    sb, st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return _pack_heads(t.data_ptr(), sb, st, sh)
 
 
 def _same(t: torch.Tensor | None, shape: tuple, dtype, name: str) -> None:
@@ -178,7 +172,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None = None
     no norm).  ``cos``, ``sin`` ``[rows, rotary_dim / 2]`` fp32 (None: no rotation), row ``positions[b, n]``
     (int32) or ``n``; pairs ``(i, i + rotary_dim / 2)``, or ``(2i, 2i + 1)`` if ``interleaved``."""
     B, N, hq, hk, d, rot, rows, wcode = _qk_common(q, k, v, q_weight, k_weight, cos, sin, positions)
-    views, (hqs, hks, hvs) = _heads((q, k, v), (q.shape, (B, N, hk, d), (B, N, hk, d)), ("q", "k", "v"))
+    kv = (B, N, hk, d)
+    hqs, hks, hvs = _heads(q, q.shape, "q"), _heads(k, kv, "k"), _heads(v, kv, "v")
     dt, dev = q.dtype, q.device
     q_out = torch.empty((B * hq, N, d), dtype=dt, device=dev)
     k_out = torch.empty((B * hk, N, d), dtype=dt, device=dev)
@@ -229,8 +224,8 @@ def qk_norm_rope_backward(q: torch.Tensor, k: torch.Tensor, dq_out: torch.Tensor
     if dv is None and dv_out is not None:
         dv = torch.empty((B, N, hk, d), dtype=gd, device=dev)
     kv = (B, N, hk, d)
-    views, (hqs, hks, hdq, hdk, hdv) = _heads((q, k, dq, dk, dv), (q.shape, kv, q.shape, kv, kv),
-                                              ("q", "k", "dq", "dk", "dv"))
+    hqs, hks = _heads(q, q.shape, "q"), _heads(k, kv, "k")
+    hdq, hdk, hdv = _heads(dq, q.shape, "dq"), _heads(dk, kv, "dk"), _heads(dv, kv, "dv")
     dqw = _like(q_weight, torch.float32) if norm else None
     dkw = _like(k_weight, torch.float32) if norm else None
     st = _launch_stream(dev, stream)

@@ -37,8 +37,14 @@ def test_header_and_exports(lib):
 
 
 # ------------------------------------------------------------------------------ norms and rotation
+class Heads(ctypes.Structure):
+    """``dera_heads``"""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_longlong), ("stride_token", ctypes.c_longlong),
+                ("stride_head", ctypes.c_longlong)]
+
+
 def _h(p=FAKE, sb=64 * 12, st=64 * 4, sh=64):
-    return train._Heads(p, sb, st, sh)
+    return Heads(p, sb, st, sh)
 
 
 def _at(h):
@@ -68,13 +74,13 @@ def test_qk_norm_rope_refusals(lib, call):
         assert call(lib, **bad) == CODES["DERA_ERR_SHAPE"], bad
     for bad in (dict(in_dt=F32), dict(w_dt=F16), dict(w_dt=7)):
         assert call(lib, **bad) == CODES["DERA_ERR_DTYPE"], bad
-    for bad in (dict(qw=None), dict(kw=None), dict(q=train._Heads(None, 0, 0, 0)), dict(v=_h()) if call is _qk else dict(dv=_h())):
+    for bad in (dict(qw=None), dict(kw=None), dict(q=Heads(None, 0, 0, 0)), dict(v=_h()) if call is _qk else dict(dv=_h())):
         assert call(lib, **bad) == CODES["DERA_ERR_NULL"], bad
     for bad in (dict(q=_h(FAKE_MISALIGNED)), dict(k=_h(st=64 * 4 + 4)), dict(q=_h(sh=60))):
         assert call(lib, **bad) == CODES["DERA_ERR_ALIGN"], bad
     assert call(lib, q=_h(st=-256)) == CODES["DERA_ERR_SHAPE"]
     # an empty batch: no CUDA call, and without weights no pointer is looked at
-    assert call(lib, B=0, qw=None, kw=None, cos=None, sin=None, q=train._Heads(None, 0, 0, 0)) == 0
+    assert call(lib, B=0, qw=None, kw=None, cos=None, sin=None, q=Heads(None, 0, 0, 0)) == 0
     assert call(lib, N=0, rows=0, rot=0, qw=None, kw=None) == 0
 
 
