@@ -23,17 +23,7 @@ static cudaError_t launch_cb_cols(const CbMaps& m, const CbArgs& a, unsigned gri
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = prepare_kernel(kernel, CbColsSmem<D>::kAlloc, kCbColsLaunchRegs, done);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kCbColsThreads);
-  cfg.dynamicSmemBytes = CbColsSmem<D>::kAlloc;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, m.q64, m.dout64, m.k, m.v, a);
+  return launch_early(kernel, dim3(grid), dim3(kCbColsThreads), CbColsSmem<D>::kAlloc, s, m.q64, m.dout64, m.k, m.v, a);
 }
 
 template <bool BF16, int D>

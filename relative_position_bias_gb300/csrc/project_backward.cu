@@ -14,8 +14,7 @@ static cudaError_t launch_pb_t(const PbArgs& a, int ctas, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int total = (2 * a.H - 1 + 2 * a.W - 1) * a.D;
-  relpos_pb_tables_kernel<<<total / 32, 256, 0, s>>>(a, ctas);
-  return cudaGetLastError();
+  return launch_early(relpos_pb_tables_kernel, dim3(total / 32), dim3(256), 0, s, a, ctas);
 }
 
 cudaError_t launch_project_backward(const PbArgs& a, int ctas, bool bf16, cudaStream_t s) {

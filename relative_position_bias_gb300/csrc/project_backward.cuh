@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kPbThreads, 1) relpos_pb_kernel(const PbArgs a
   using SM = PbSmem<BF16>;
   constexpr int TERMS = SM::kTerms, NS = SM::NS;
   extern __shared__ uint8_t smem_raw[];
+  grid_launch_dependents();   // relpos_pb_tables_kernel starts as these blocks run out
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kBars);
@@ -405,6 +406,7 @@ __global__ void __launch_bounds__(256) relpos_pb_tables_kernel(const PbArgs a, i
   const int LH = 2 * a.H - 1, LW = 2 * a.W - 1, total = (LH + LW) * a.D;
   const int ol = threadIdx.x & 31, chunk = threadIdx.x >> 5, o = blockIdx.x * 32 + ol;   // total is a multiple of 32
   float acc = 0.f;
+  grid_wait_prerequisites();   // every partial is written
   #pragma unroll 8
   for (int p = chunk; p < n_parts; p += 8) acc += a.parts[static_cast<size_t>(p) * total + o];
   red[chunk][ol] = acc;

@@ -70,9 +70,8 @@ cudaError_t launch_qk(QkArgs& a, const QkPlan& p, int head_dim, int mode, bool b
   else
     e = bf16 ? pick<true, 64>(a, mode, norm, backward, grid, s) : pick<false, 64>(a, mode, norm, backward, grid, s);
   if (e != cudaSuccess || !backward || !norm) return e;
-  qk_weight_grad_kernel<<<dim3(head_dim / 32, 2), dim3(32, 32), 0, s>>>(a.parts, p.part_rows_q, p.part_rows_k, head_dim,
-                                                                       dqw, dkw);
-  return cudaGetLastError();
+  return launch_early(qk_weight_grad_kernel, dim3(head_dim / 32, 2), dim3(32, 32), 0, s,
+                      static_cast<const float*>(a.parts), p.part_rows_q, p.part_rows_k, head_dim, dqw, dkw);
 }
 
 }  // namespace dera

@@ -15,7 +15,8 @@
 //
 // Measured: forward, 8 x 4096 tokens, 3 x 16 heads of 128, fp16, 806 MB: 123 us, 6.5 TB/s (a plain copy reaches
 // 6.8).  Backward, 8 x 4096 tokens, 3 x 12 heads of 64, bf16, 404 MB: 78 us, 5.2 TB/s; it issues in 57 % of the
-// cycles (two sums of eight lanes a row) and waits for loads in most others.  The weights' sums are 5 us more.
+// cycles (two sums of eight lanes a row) and waits for loads in most others.  The weights' sums
+// are 4 us more (7 when their kernel was not launched ahead of this one's end).
 #pragma once
 #include <cstdint>
 
@@ -197,6 +198,7 @@ template <bool BF16, int D, int MODE, bool NORM, bool ZF32>
 __global__ void __launch_bounds__(kQkThreads, 3) qk_norm_rope_bwd_kernel(const QkArgs a) {
   constexpr int LANES = D / 8, TOK = kQkThreads / LANES, WARPS = kQkThreads / 32, U = 4;
   constexpr int fmt = BF16 ? kBF16 : kF16;
+  grid_launch_dependents();   // qk_weight_grad_kernel starts as these blocks run out
   __shared__ float red[WARPS][D];
   const QkBlock blk(a, blockIdx.y);
   const int lane = threadIdx.x & 31, slot = threadIdx.x % LANES;
@@ -280,6 +282,7 @@ __global__ void __launch_bounds__(kQkThreads, 3) qk_norm_rope_bwd_kernel(const Q
 __global__ void __launch_bounds__(1024) qk_weight_grad_kernel(const float* parts, int rows_q, int rows_k, int D,
                                                              float* dqw, float* dkw) {
   __shared__ float red[32][33];
+  grid_wait_prerequisites();   // every partial row is written
   const bool is_k = blockIdx.y == 1;
   const float* p = parts + (is_k ? static_cast<size_t>(rows_q) * D : 0) + blockIdx.x * 32 + threadIdx.x;
   const int rows = is_k ? rows_k : rows_q;

@@ -7,6 +7,23 @@
 
 namespace dera {
 
+// A launch whose blocks may start before the kernel ahead of it in the stream is complete; it has to wait for
+// that one itself (grid_wait_prerequisites).
+template <class Kernel, class... Args>
+cudaError_t launch_early(Kernel kernel, dim3 grid, dim3 threads, size_t smem, cudaStream_t s, const Args&... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = threads;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 constexpr int kQkThreads = 256;
 
 struct HeadsPtr {
