@@ -189,3 +189,42 @@ def test_training_step(d, dtype):
     graph.replay()
     for a, b in zip(cap, step()):
         assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 elements: the last heads are what a call on them alone gives.
+
+    attention_lse: P is rounded to 11 bits (2^-11 of a value) relative to a running maximum that may differ between the two
+    calls, so outputs differ by 2 * 2^-11 of sum P |v| <= max |v| each, and by their own rounding.
+    attention_backward, from the same out and lse: sums of 4096 terms in another order where a unit is
+    cut, 2 * 4096 * 2^-24 = 2^-11 of the sum of magnitudes, which for independent terms is some sqrt(4096)
+    times the result: 2^-5 in norm.  A wrong offset gives 1 or more."""
+    if torch.cuda.mem_get_info()[0] < 140e9:
+        pytest.skip("needs 140 GB")
+    BH, H, W, d = 8200, 64, 64, 64
+    N, tail = H * W, slice(BH - 2, BH)
+    g = torch.Generator(device="cuda").manual_seed(18)
+
+    def rn(*shape, dtype=BF):
+        return torch.empty(*shape, dtype=dtype, device="cuda").normal_(generator=g)
+    q, k, v, do = (rn(BH, N, d) for _ in range(4))
+    rh, rw = rn(BH, N, H, dtype=FL), rn(BH, N, W, dtype=FL)
+    assert rh.numel() > 2 ** 31 and q.numel() > 2 ** 31
+    out, lse = rpb.attention_lse(q, k, v, rh, rw, H, W)
+    grads = rpb.attention_backward(q, k, v, rh, rw, out, lse, do, H, W, grad_dtype=BF)
+    part = [t[tail].clone() for t in (q, k, v, rh, rw)]
+    o2, l2 = rpb.attention_lse(*part, H, W)
+    top = part[2].float().abs().max()
+    assert (out[tail].float() - o2.float()).abs().max() <= 2 * 2.0 ** -11 * top + 2 * 2.0 ** -8 * o2.float().abs().max()
+    assert (lse[tail] - l2).abs().max() <= 2.0 ** -9      # 2 * 2^-11 of the sum, in base 2
+    g2 = rpb.attention_backward(*part, out[tail].clone(), lse[tail].clone(), do[tail].clone(), H, W, grad_dtype=BF)
+    for a, b in zip(grads, g2):
+        assert (a[tail].float() - b.float()).norm() <= (2.0 ** -5 + 2 * 2.0 ** -8) * b.float().norm()
+    del k, v, do, rh, rw, out, lse
+    th, tw = rn(2 * H - 1, d), rn(2 * W - 1, d)
+    dq = rpb.project_backward(q, th, tw, grads[3], grads[4], H, W, dq=grads[0])[0]
+    want = rpb.project_backward(q[tail].clone(), th, tw, grads[3][tail].clone(), grads[4][tail].clone(), H, W,
+                                dq=grads[0][tail].clone())[0]
+    assert torch.equal(dq[tail], want)
+    del q, grads, part, g2, dq, want
+    torch.cuda.empty_cache()

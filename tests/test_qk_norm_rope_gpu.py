@@ -255,3 +255,28 @@ def test_other_device_tensors_are_refused():
     with pytest.raises(rpb.DeraError) as e:
         rpb.qk_norm_rope(q, k, v, **kw)
     assert e.value.status == 6
+
+
+def test_offsets_past_32_bits():
+    """A packed projection of more than 2^31 elements, forward and backward: the last batch is what a call on it
+    alone gives, bit for bit (rows are independent of one another)."""
+    if torch.cuda.mem_get_info()[0] < 80e9:
+        pytest.skip("needs 80 GB")
+    B, N, h, d = 240, 4096, 12, 64
+    g = torch.Generator(device="cuda").manual_seed(19)
+    x = torch.empty(B, N, 3 * h, d, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    assert x.numel() > 2 ** 31
+    w = torch.rand(d, generator=g, device="cuda") + 0.5
+    cos, sin = (torch.rand(N, d // 2, generator=g, device="cuda") for _ in range(2))
+    kw = dict(q_weight=w, k_weight=w, cos=cos, sin=sin)
+
+    def heads(t):
+        return t[:, :, :h], t[:, :, h:2 * h], t[:, :, 2 * h:]
+    z = rpb.qk_norm_rope(*heads(x), **kw)
+    one = x[-1:].clone()
+    z1 = rpb.qk_norm_rope(*heads(one), **kw)
+    assert all(torch.equal(a[-h:], b) for a, b in zip(z, z1))
+    dx = torch.empty_like(x)
+    rpb.qk_norm_rope_backward(*heads(x)[:2], *z, **kw, **dict(zip(("dq", "dk", "dv"), heads(dx))))
+    d1 = rpb.qk_norm_rope_backward(*heads(one)[:2], *z1, **kw, grad_dtype=torch.bfloat16)
+    assert all(torch.equal(a[-1:], b) for a, b in zip(heads(dx), d1))
