@@ -128,12 +128,12 @@ __device__ __forceinline__ CbCta cb_setup(uint8_t* smem_raw, int warp, int on_a,
   c.bars = reinterpret_cast<uint64_t*>(c.smem + SM::kBars);
   uint32_t* slot = reinterpret_cast<uint32_t*>(c.smem + SM::kMisc);
   c.abort_flag = reinterpret_cast<volatile int*>(c.smem + SM::kMisc + 4);
-  if (threadIdx.x == 0) {
-    *c.abort_flag = 0;
-    for (int i = 0; i < kCbBars; ++i) {
-      const int n = i == kCbAFull ? on_a : (((i >= kCbPFull && i < kCbPFull + 3) || i == kCbSFree || i == kCbSFree + 1) ? on_step : (i == kCbJoin ? all : 1));
-      mbar_init(&c.bars[i], n);
-    }
+  static_assert(kCbBars <= 32, "one thread a barrier");
+  if (threadIdx.x < kCbBars) {
+    const int i = threadIdx.x;
+    if (i == 0) *c.abort_flag = 0;
+    const bool step = (i >= kCbPFull && i < kCbPFull + 3) || i == kCbSFree || i == kCbSFree + 1;
+    mbar_init(&c.bars[i], i == kCbAFull ? on_a : (step ? on_step : (i == kCbJoin ? all : 1)));
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -164,24 +164,31 @@ __device__ __forceinline__ void cb_drain(uint64_t* bars, int issued) {
     mbar_wait_budget(&bars[kCbRingFull + i % KS], (i / KS) & 1, kWaitBudgetCycles);
 }
 
-// Row `row` of a [BH, N, D] tensor (zeros if !valid) into TMEM as an A operand: this thread's lane, D / 2
+// A row of a [BH, N, D] tensor (zeros if !valid) on its way into TMEM as an A operand: this thread's lane, D / 2
 // columns of packed pairs.  Reading A from TMEM leaves shared memory, which a 128 x 64 product
 // would keep busy for 48 cycles a step of 16 (4 KB of A, 2 KB of B; the product takes 32), to B.
 template <int D>
-__device__ __forceinline__ void cb_row_to_tmem(const void* src, size_t row, bool valid, uint32_t taddr) {
-  #pragma unroll
-  for (int h = 0; h < D / 64; ++h) {
-    uint32_t u[32];
+struct CbOwnRow {
+  uint4 v[D / 8];
+  __device__ __forceinline__ void load(const void* src, size_t row, bool valid) {
     #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (valid) v = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(src) + row * D + 64 * h + 8 * c));
-      u[4 * c] = v.x, u[4 * c + 1] = v.y, u[4 * c + 2] = v.z, u[4 * c + 3] = v.w;
+    for (int c = 0; c < D / 8; ++c) {
+      v[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (valid) v[c] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(src) + row * D + 8 * c));
     }
-    tmem_st32(taddr + 32 * h, u);
   }
-  tmem_wait_st();
-}
+  __device__ __forceinline__ void to_tmem(uint32_t taddr) const {
+    #pragma unroll
+    for (int h = 0; h < D / 64; ++h) {
+      uint32_t u[32];
+      #pragma unroll
+      for (int c = 0; c < 8; ++c)
+        u[4 * c] = v[8 * h + c].x, u[4 * c + 1] = v[8 * h + c].y, u[4 * c + 2] = v[8 * h + c].z, u[4 * c + 3] = v[8 * h + c].w;
+      tmem_st32(taddr + 32 * h, u);
+    }
+    tmem_wait_st();
+  }
+};
 
 // What a CTA computes: a whole unit (a 128-row tile of a head), or a piece of one of the
 // units past the last full wave of CTAs.
@@ -293,15 +300,30 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
   extern __shared__ uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_launch_dependents();   // cols reads nothing of this kernel: its blocks fill the SMs that run out of these
+  const int n_kv = (a.H + KHT - 1) / KHT;
+  const CbUnit unit(blockIdx.x, a.rows_full, a.rows_split, a.n_tiles, n_kv);
+  const int bh = unit.bh, steps = unit.i1 - unit.i0;
+  // a softmax thread's rw row, a part by each group, and q or dO's: on their way during the set-up
+  constexpr int kPart = (WP + NB - 1) / NB;
+  CbOwnRow<D> own;
+  float w[kPart], nDn = 0.f;
+  if (warp >= 4) {
+    const int wg = (warp >> 2) - 1, r = threadIdx.x & 127, n = unit.tile * kBlockM + r;
+    const float* src = a.rw + (static_cast<size_t>(bh) * a.n_blocks + 2 * unit.tile + (r >> 6)) * a.W * kCbRow;
+    if (wg < 2) own.load(wg == 0 ? a.q : a.dout, static_cast<size_t>(bh) * a.N + n, n < a.N);
+    #pragma unroll
+    for (int e = 0; e < kPart; ++e) {
+      const int kw = wg * kPart + e;
+      w[e] = kw < a.W ? __ldg(src + cb_at(kw, r & 63)) : -__int_as_float(0x7f800000);
+    }
+    nDn = __ldg(a.nD + static_cast<size_t>(bh) * a.n_blocks * 64 + n);
+  }
   const CbCta cta = cb_setup<SM>(smem_raw, warp, 2 * kBlockM, kBlockM, NB * kBlockM);
   uint8_t* smem = cta.smem;
   uint64_t* bars = cta.bars;
   volatile int* abort_flag = cta.abort_flag;
   const uint32_t tbase = cta.tbase;
   int* status = a.status;
-  const int n_kv = (a.H + KHT - 1) / KHT;
-  const CbUnit unit(blockIdx.x, a.rows_full, a.rows_split, a.n_tiles, n_kv);
-  const int bh = unit.bh, steps = unit.i1 - unit.i0;
   auto stage = [&](int i) { return smem + SM::kRing + (i % KS) * SM::kStage; };
 
   if (warp < 4) {
@@ -389,26 +411,14 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
     float* bw_row = reinterpret_cast<float*>(smem + SM::kBw) + r * SM::kBwStride;
     float* dh_row = reinterpret_cast<float*>(smem + SM::kDh) + r * 65;
-    const float nDn = __ldg(a.nD + static_cast<size_t>(bh) * a.n_blocks * 64 + n);
-    {
-      // this thread's rw row, a part by each group, and q or dO's, all loads in flight at once
-      const float* src = a.rw + (static_cast<size_t>(bh) * a.n_blocks + 2 * unit.tile + (r >> 6)) * W * kCbRow;
-      constexpr int kPart = (WP + NB - 1) / NB;
-      float w[kPart];
-      #pragma unroll
-      for (int e = 0; e < kPart; ++e) {
-        const int kw = wg * kPart + e;
-        w[e] = kw < W ? __ldg(src + cb_at(kw, r & 63)) : NEG_INF;
-      }
-      if (wg < 2) {
-        cb_row_to_tmem<D>(wg == 0 ? a.q : a.dout, row, row_valid, tbase + lanes + (wg == 0 ? DM::tmQ : DM::tmDO));
-        tc_fence_before();
-        mbar_arrive(&bars[kCbAFull]);
-      }
-      #pragma unroll
-      for (int e = 0; e < kPart; ++e)
-        if (wg * kPart + e < WP) bw_row[wg * kPart + e] = w[e];
+    if (wg < 2) {
+      own.to_tmem(tbase + lanes + (wg == 0 ? DM::tmQ : DM::tmDO));
+      tc_fence_before();
+      mbar_arrive(&bars[kCbAFull]);
     }
+    #pragma unroll
+    for (int e = 0; e < kPart; ++e)
+      if (wg * kPart + e < WP) bw_row[wg * kPart + e] = w[e];
     const float2 nD = make_float2(nDn, nDn);
     float dRW[WP];
     #pragma unroll
@@ -561,15 +571,20 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
   constexpr int fmt = BF16 ? kBF16 : kF16;
   extern __shared__ uint8_t smem_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_steps = (a.N + 63) / 64;
+  const CbUnit unit(blockIdx.x, a.cols_full, a.cols_split, a.n_tiles, n_steps);
+  const int bh = unit.bh, steps = unit.i1 - unit.i0;
+  CbOwnRow<D> own;   // k or v's row of a softmax thread of the first pair: on its way during the set-up
+  if (kTmemA && warp >= 4 && warp < 12) {
+    const int m = unit.tile * kBlockM + (threadIdx.x & 127);
+    own.load(warp < 8 ? a.k : a.v, static_cast<size_t>(bh) * a.N + m, m < a.N);
+  }
   const CbCta cta = cb_setup<SM>(smem_raw, warp, kTmemA ? 2 * kBlockM : 1, 2 * kBlockM, 1);
   uint8_t* smem = cta.smem;
   uint64_t* bars = cta.bars;
   volatile int* abort_flag = cta.abort_flag;
   const uint32_t tbase = cta.tbase;
   int* status = a.status;
-  const int n_steps = (a.N + 63) / 64;
-  const CbUnit unit(blockIdx.x, a.cols_full, a.cols_split, a.n_tiles, n_steps);
-  const int bh = unit.bh, steps = unit.i1 - unit.i0;
   auto stage = [&](int i) { return smem + SM::kRing + (i % KS) * SM::kStage; };
   // grid rows of the tile's keys
   const int m0 = unit.tile * kBlockM, kh_first = m0 / a.W;
@@ -681,8 +696,7 @@ relpos_cb_cols_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_con
     const int rw_at = kw * kCbRow, rw_x = kw & 7, hl_at = (a.W + kh - kh_first) * kCbRow, hl_x = kh & 7;
     const float2 sl2 = make_float2(a.scale_log2, a.scale_log2);
     if (kTmemA && half == 0) {
-      cb_row_to_tmem<D>(wg == 0 ? a.k : a.v, static_cast<size_t>(bh) * a.N + m0 + m, key_valid,
-                        tbase + lanes + (wg == 0 ? tmK : tmV));
+      own.to_tmem(tbase + lanes + (wg == 0 ? tmK : tmV));
       tc_fence_before();
       mbar_arrive(&bars[kCbAFull]);
     }
