@@ -23,9 +23,9 @@
 // each with its own S and dP in TMEM: while one exponentiates step i the tensor core forms S and dP
 // of the next steps for the others and adds step i - 1 to the accumulators.
 //
-// Measured, 12 heads of 64 x 64 tokens, bf16 (each kernel by itself, caches cold; together, overlapped, 211 us):
+// Measured, 12 heads of 64 x 64 tokens, bf16 (each kernel by itself, caches cold; together, overlapped, 210 us):
 //   head_dim 64    prep 16 us (38 MB read, as much written to L2), rows 106 (37 % of the tensor cycles), cols 116
-//                  (44 %), join 7.  336 us with head_dim 128.
+//                  (44 %), join 7.  330 us with head_dim 128.
 #pragma once
 #include <cfloat>
 
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kCbPrepThreads) relpos_cb_prep_kernel(const Cb
 // and the packed fp32 arithmetic about 400 on each scheduler.  It takes 870 to 1000: the chain from S through the
 // exponents to dZ is not hidden by three steps in flight, and TMEM has no room for a fourth.  A CTA's start and
 // end are 12,000 of its 68,000 cycles (64 steps).  Two CTAs an SM with one step in flight each were slower (249 us
-// for the call above instead of 211).
+// for the call above when one CTA took 213).
 template <int WP, bool BF16, int D>
 __global__ void __launch_bounds__(CbRowsDims<D>::kThreads, 1)
 relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
