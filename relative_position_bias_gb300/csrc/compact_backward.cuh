@@ -24,7 +24,7 @@
 // of the next steps for the others and adds step i - 1 to the accumulators.
 //
 // Measured, 12 heads of 64 x 64 tokens, bf16 (each kernel by itself, caches cold; together, overlapped, 210 us):
-//   head_dim 64    prep 16 us (38 MB read, as much written to L2), rows 106 (37 % of the tensor cycles), cols 116
+//   head_dim 64    prep 16 us (38 MB read, as much written to L2), rows 105 (38 % of the tensor cycles), cols 116
 //                  (44 %), join 7.  330 us with head_dim 128.
 #pragma once
 #include <cfloat>
