@@ -127,7 +127,7 @@ DERA_API dera_status dera_relpos_attention_backward_workspace_size(int BH, int H
  *      bf16, 2^-11 for fp16) as operands of the products dv, dk and dq, whose accumulators are
  *      fp32; drel_h and drel_w are summed before that rounding.  With fp16 a P or dZ below 2^-25 is
  *      lost there and a |dZ| of 65520 or more overflows.  On a grid of one row (column) drel_h (drel_w) is 0
- *      by mathematics, and what out's rounding leaves of that in numbers.
+ *      by mathematics (the softmax does not see a term that all keys share), and written as exact zeros.
  * Errors: as for dera_relpos_attention; DERA_ERR_SCRATCH if the workspace is NULL or smaller
  *      than the size above; DERA_ERR_SHAPE if BH * ceil(N / 128) passes 2^30.
  */

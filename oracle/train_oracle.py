@@ -79,7 +79,8 @@ def masked_attention(q, k, v, rel_h, rel_w, H: int, W: int, scale: float):
 
 
 def attention_backward_from(q, k, v, rel_h, rel_w, out, lse, dout, H: int, W: int, scale: float):
-    """``(dq, dk, dv, drel_h, drel_w)`` with P from the given base-2 ``lse`` and D from the given ``out``."""
+    """``(dq, dk, dv, drel_h, drel_w)`` with P from the given base-2 ``lse`` and D from the given ``out``.  On an axis
+    of length one the bias's gradient is zero whatever rounding ``out`` and ``lse`` have seen."""
     q, k, v, out, lse, dout = (_f64(t) for t in (q, k, v, out, lse, dout))
     BH, N, _ = q.shape
     dq, dk, dv = np.zeros_like(q), np.zeros_like(k), np.zeros_like(v)
@@ -93,7 +94,7 @@ def attention_backward_from(q, k, v, rel_h, rel_w, out, lse, dout, H: int, W: in
         dq[b] = scale * (dz @ k[b])
         dk[b] = scale * (dz.T @ q[b])
         grid = dz.reshape(N, H, W)
-        dh[b], dw[b] = grid.sum(2), grid.sum(1)
+        dh[b], dw[b] = grid.sum(2) * (H > 1), grid.sum(1) * (W > 1)
     return dq, dk, dv, dh, dw
 
 

@@ -4,6 +4,8 @@
 // the forward's base-2 log-sum-exp, D[n] = dO[n] . out[n] and dZ = P * (dO v^T - D):
 //   dv = P^T dO,  dk = scale dZ^T q,  dq = scale dZ k,
 //   drel_h[n, kh] = sum_kw dZ[n, (kh, kw)],  drel_w[n, kw] = sum_kh dZ[n, (kh, kw)].
+// A row's dZ add up to zero, so on an axis of length one the gradient is zero and written as that: the sum in
+// numbers would be what out's rounding leaves in D (1e-3 in fp16, 4e-2 in bf16).
 //
 // Kernels, in stream order:
 //   prep   one pass over the bias, out and dO: the exponent's two terms, laid out so that one bulk
@@ -511,12 +513,12 @@ relpos_cb_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             float v = sum[rr * (WP + 1) + c];
             #pragma unroll
             for (int b = 1; b < NB; ++b) v += sum[b * kSum + rr * (WP + 1) + c];
-            dw[rr * W + c] = v;
+            dw[rr * W + c] = W > 1 ? v : 0.f;
           }
         }
         #pragma unroll
         for (int cc = 0; cc < 64; cc += 32)
-          if (cc + lane < hn) a.drel_h[(row0 + rr) * H + h0 + cc + lane] = dh[rr * 65 + cc + lane];
+          if (cc + lane < hn) a.drel_h[(row0 + rr) * H + h0 + cc + lane] = H > 1 ? dh[rr * 65 + cc + lane] : 0.f;
       }
       // dq, 32 columns at a time
       tc_fence_after();

@@ -281,7 +281,8 @@ def attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h:
                        scale: float | None = None, grad_dtype: torch.dtype | None = None, stream=None,
                        workspace: torch.Tensor | None = None):
     """Gradients of :func:`attention_lse` via ``dera_relpos_attention_backward``:
-    ``(dq, dk, dv, drel_h, drel_w)``; dq, dk, dv in ``grad_dtype`` (default fp32), the bias's fp32.
+    ``(dq, dk, dv, drel_h, drel_w)``; dq, dk, dv in ``grad_dtype`` (default fp32), the bias's fp32
+    (exactly zero along an axis of length one).
     ``out`` and ``lse`` come from :func:`attention_lse`.  ``workspace``: a caller-owned uint8 tensor that
     no other call in flight uses, or None for a buffer of this call."""
     BH, N, d = q.shape

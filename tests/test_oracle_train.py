@@ -113,3 +113,20 @@ def test_project_backward_gradients():
     pq, pth, ptw = oracle.project_backward(q, th, tw, a[3], a[4], H, W)
     for x, y in zip((a[0] + pq, a[1], a[2], pth, ptw), want):
         assert np.allclose(x, y)
+
+
+def test_no_gradient_along_an_axis_of_length_one():
+    """A term that all keys of a row share moves no probability, also where out has been rounded."""
+    r = np.random.default_rng(4)
+    for H, W in ((1, 5), (5, 1), (1, 1)):
+        N = H * W
+        q, k, v, do = (r.standard_normal((2, N, 4)) for _ in range(4))
+        rh, rw = r.standard_normal((2, N, H)), r.standard_normal((2, N, W))
+        out, lse = oracle.masked_attention(q, k, v, rh, rw, H, W, 0.5)
+        grads = oracle.attention_backward_from(q, k, v, rh, rw, out.astype(np.float16), lse, do, H, W, 0.5)
+        if H == 1:
+            assert np.all(grads[3] == 0)
+            assert np.allclose(fd(lambda t: float((do * oracle.masked_attention(q, k, v, t, rw, H, W, 0.5)[0]).sum()), rh), 0,
+                               atol=1e-8)
+        if W == 1:
+            assert np.all(grads[4] == 0)
