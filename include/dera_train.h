@@ -101,10 +101,10 @@ DERA_API dera_status dera_qk_norm_rope_backward(const dera_heads* q, const dera_
 /*
  * Training forward of the two-step form: dera_relpos_attention that also writes every row's base-2
  * log-sum-exp, lse[b, n] = log2(sum_m exp(Z[b, n, m])), Z = scale q k^T + rel_h + rel_w, [BH, N] fp32.
- * A bias of -inf masks its keys, and so does one of -1e38 or below; a row with every key masked
- * gives out = 0 and lse = -inf.  q, k and v must be finite everywhere, at masked keys too (the
- * products read them), and a bias at most 1e38 and not NaN.  Everything else as for dera_relpos_attention
- * (workspace: dera_relpos_workspace_size).
+ * A bias of -inf masks its keys, and so does one of -1e38 (rounded to its type) or below, here, in
+ * dera_relpos_attention and in the backward; a row with every key masked gives out = 0 and lse = -inf.  q, k and v
+ * must be finite everywhere, at masked keys too (the products read them), and a bias at most 8e37 and not NaN.
+ * Everything else as for dera_relpos_attention (workspace: dera_relpos_workspace_size).
  */
 DERA_API dera_status dera_relpos_attention_lse(const void* q, const void* k, const void* v, const void* rel_h,
                               const void* rel_w, void* out, float* lse, int BH, int H, int W, int head_dim,

@@ -715,15 +715,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (raw) copy_rows_async(p, len, 0, stride);
           else if ((len & 1) == 0) copy_rows_async(p, len / 2, len / 2, stride);
         };
-        // this thread's row, once its words are there: base-2 values
+        // this thread's row of a 16-bit bias, once its words are there, in fp32
         auto own_row = [&](const void* p, int len, float* row) {
-          if (raw) {
-            for (int c = 0; c < len; ++c) row[c] *= kLog2e;
-          } else if ((len & 1) == 0) {
+          if ((len & 1) == 0) {
             for (int c = 0; c < len; c += 2) {   // the words not yet read lie past what is written
               const float2 x = unpack_in(__float_as_uint(row[(len + c) / 2]), args.bias_fmt);
-              row[c] = kLog2e * x.x;
-              row[c + 1] = kLog2e * x.y;
+              row[c] = x.x;
+              row[c + 1] = x.y;
             }
           } else {
             #pragma unroll 1
@@ -735,7 +733,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                                    : 0.f;
               #pragma unroll
               for (int c = 0; c < 8; ++c)
-                if (c0 + c < len) row[c0 + c] = kLog2e * x[c];
+                if (c0 + c < len) row[c0 + c] = x[c];
             }
           }
         };
@@ -743,19 +741,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ok = wg_sync() && ok;
         float* stg = area + r * kBiasStride;
         if (!raw) own_row(args.rel_w, W, stg);
-        const float wscale = raw ? kLog2e : 1.0f;
         #pragma unroll
-        for (int kw = 0; kw < WP; ++kw) bw[kw] = kw < W ? wscale * stg[kw] : NEG_INF;
+        for (int kw = 0; kw < WP; ++kw) bw[kw] = kw < W ? bias2(stg[kw]) : NEG_INF;
         // every thread has its rel_w row before the area is reused for rel_h
         ok = wg_sync() && ok;
         copy_rows(args.rel_h, H, HS);
         ok = wg_sync() && ok;
-        own_row(args.rel_h, H, bh_row);
+        if (!raw) own_row(args.rel_h, H, bh_row);
         if (kPadRows)
           for (int kh = H; kh < Hpad; ++kh) bh_row[kh] = NEG_INF;
         if (!ok) return false;
       }
       ++seg;
+      // rel_h of a grid row in base 2 (staged so by the fused prologue)
+      auto rel_h_of = [&](int kh) { return FUSED ? bh_row[kh] : bias2(bh_row[kh]); };
 
       // S is processed in blocks of kBlk columns (one TMEM load and one wait
       // each); narrow grids, with more grid rows per tile, use 16 to keep
@@ -866,13 +865,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // largest rel_h term (base 2) over the grid rows this segment covers
       float mbh = NEG_INF;
       for (int kh = sg.j0 * KHT; kh < min(sg.j1 * KHT, H); ++kh) mbh = fmaxf(mbh, bh_row[kh]);
+      if (!FUSED) mbh = bias2(mbh);
       for (int j = sg.j0; j < sg.j1; ++j, ++gi) {
         // the tile's rel_h terms, and whether to take it exact at once, are
         // settled before the wait for its S, which hides their latency
         const int kh0 = j * KHT;
         float bhv[KHT];
         #pragma unroll
-        for (int g = 0; g < KHT; ++g) bhv[g] = (kPadRows || kh0 + g < H) ? bh_row[kh0 + g] : NEG_INF;
+        for (int g = 0; g < KHT; ++g) bhv[g] = (kPadRows || kh0 + g < H) ? rel_h_of(kh0 + g) : NEG_INF;
         bool exact = j == sg.j0;
         if (!exact) {
           float hb = bhv[0];

@@ -227,7 +227,7 @@ __device__ __forceinline__ void cb_load_row(const void* src, size_t at, int L, i
     for (int c = 0; c < 16; ++c)
       if (4 * c < L) {
         const float4 v = __ldg(p + c);
-        x[4 * c] = kLog2e * v.x, x[4 * c + 1] = kLog2e * v.y, x[4 * c + 2] = kLog2e * v.z, x[4 * c + 3] = kLog2e * v.w;
+        x[4 * c] = bias2(v.x), x[4 * c + 1] = bias2(v.y), x[4 * c + 2] = bias2(v.z), x[4 * c + 3] = bias2(v.w);
       }
   } else if (fmt != kF32 && L % 8 == 0) {
     const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(src) + at);
@@ -237,12 +237,12 @@ __device__ __forceinline__ void cb_load_row(const void* src, size_t at, int L, i
         float v[8];
         unpack8(__ldg(p + c), v, fmt);
         #pragma unroll
-        for (int e = 0; e < 8; ++e) x[8 * c + e] = kLog2e * v[e];
+        for (int e = 0; e < 8; ++e) x[8 * c + e] = bias2(v[e]);
       }
   } else {
     #pragma unroll
     for (int c = 0; c < 64; ++c)
-      if (c < L) x[c] = kLog2e * load_elem(src, at + c, fmt);
+      if (c < L) x[c] = bias2(load_elem(src, at + c, fmt));
   }
 }
 

@@ -1,8 +1,11 @@
 """Axes of length one, and biases at the ends of their range, in the compact-bias attention and its backward.
 
 The bias's gradient along an axis of length one is zero by mathematics (the softmax does not see a term that all keys
-share), so it is exactly zero."""
+share), so it is exactly zero.  A bias of -1e38 or below masks its keys, whatever type it has: a call with such values
+gives the bits that -inf in their place gives."""
 from __future__ import annotations
+
+import math
 
 import pytest
 import torch
@@ -45,3 +48,28 @@ def test_axis_of_length_one(BH, H, W, dtype, d):
     grads = step(x, H, W)[2:]
     for L, g in ((H, grads[3]), (W, grads[4])):
         assert torch.count_nonzero(g) == 0 if L == 1 else torch.count_nonzero(g) > 0
+
+
+@pytest.mark.parametrize("value", [-1e38, -1.7e38, -2.3e38, "half", "lowest"])
+@pytest.mark.parametrize("bias", [FL, BF])
+@pytest.mark.parametrize("H,W,BH", [(9, 13, 5), (14, 14, 4), (64, 64, 3), (40, 33, 2)])
+def test_finite_masks(H, W, BH, bias, value):
+    """Some keys by either bias and whole rows by rel_h, in units that are cut (64x64 with a workspace) and whole ones."""
+    low = {"half": torch.finfo(bias).min / 2, "lowest": torch.finfo(bias).min}.get(value, value)
+    x = make(BH, H, W, 64, BF, bias, 7)
+    m = {n: torch.zeros_like(x[n], dtype=torch.bool) for n in ("rel_h", "rel_w")}
+    m["rel_h"][:, :, H - 2:] = True
+    m["rel_h"][:, 1::5] = True
+    m["rel_w"][:, 2::7] = True
+    m["rel_w"][:, :, 0] = True
+    empty = (m["rel_h"].all(-1) | m["rel_w"].all(-1))
+    both = [{**x, **{n: x[n].masked_fill(m[n], to) for n in m}} for to in (low, -math.inf)]
+    for workspace in (None, False):
+        got, want = (step(b, H, W, workspace=workspace) for b in both)
+        for name, a, b in zip(("out", "lse", "dq", "dk", "dv", "drel_h", "drel_w"), got, want):
+            assert torch.equal(a, b), f"{name} {workspace}"
+        assert torch.count_nonzero(got[0][empty]) == 0 and torch.isneginf(got[1][empty]).all()
+        assert torch.isfinite(got[1][~empty]).all()
+        assert torch.count_nonzero(got[2][empty]) == 0
+    one = [rpb.attention(b["q"], b["k"], b["v"], b["rel_h"], b["rel_w"], H, W) for b in both]
+    assert torch.equal(*one)
