@@ -119,6 +119,9 @@ DERA_API dera_status dera_relpos_attention_backward_workspace_size(int BH, int H
  * (P = 0 in a row whose lse is -inf), D[n] = dout[n] . out[n] and dZ = P * (dout v^T - D):
  *   dv = P^T dout,  dk = scale dZ^T q,  dq = scale dZ k,
  *   drel_h[n, kh] = sum_kw dZ[n, kh W + kw],  drel_w[n, kw] = sum_kh dZ[n, kh W + kw].
+ * lse is fp32, so that P is off by up to 2^-24 |lse| (times ln 2, relative): nothing for logits of ordinary size, 6e-4 in
+ * a row whose every key has a bias of -1e4.  A row whose lse is -2^20 or below (-1e9 on every key, say) counts as
+ * masked as a whole, P = 0: rows without keys are best given as -inf.
  * in:  q, k, v, rel_h, rel_w as given to the forward, out [BH,N,head_dim] and lse [BH,N] as it gave
  *      them (out in out_dtype: DERA_F32 or in_dtype), dout [BH,N,head_dim] in in_dtype, finite everywhere.
  * out: dq, dk, dv [BH,N,head_dim] in grad_dtype (DERA_F32 or in_dtype); drel_h [BH,N,H],

@@ -74,6 +74,9 @@ constexpr float kPredictMargin = 14.0f;
 // CTA no longer replayed); on the 64x64 inputs, head_dim 64 or 128, none does.
 constexpr float kWideGap = 32.0f;
 constexpr int kWideRows = 4;
+// Size (base 2) up to which a row's rel_w, and rel_h, is added to its logits as it is: what is added to it keeps its
+// bits down to 2^-14.
+constexpr float kFarBias = 1024.f;
 // Row-sum check at the end of a segment: the row sum l, in units of the
 // running maximum, must be at least the segment's valid key count times
 // 2^kMinRowSumLog2 (see the epilogue).
@@ -660,6 +663,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const int qw = row_valid ? n - qh * W : 0;
 
       float bw[WP];
+      float shift_w = 0.f, shift_h = 0.f;   // taken off the row's rel_w and rel_h (see below)
       if (FUSED) {
         ok = warp_all(mbar_wait(&bars[kBarGFull], seg & 1, abort_flag, status));
         tc_fence_after();
@@ -743,6 +747,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (!raw) own_row(args.rel_w, W, stg);
         #pragma unroll
         for (int kw = 0; kw < WP; ++kw) bw[kw] = kw < W ? bias2(stg[kw]) : NEG_INF;
+        // A term that all keys of a row share leaves the softmax as it is, but a large one takes the
+        // bits of everything that is added to it (-1e9 all below 2^6), the maximum's first, and P passes
+        // fp16's range: a row whose rel_w, or rel_h, is all further than kFarBias from zero goes without its
+        // largest and gets it back in lse.  Few rows are like that, and their first value tells the others apart
+        // (a maximum over every row took the 63x63 grid from 84.5 to 85.9 us).
+        if (!(fabsf(bw[0]) <= kFarBias)) {
+          float top = NEG_INF;
+          #pragma unroll
+          for (int kw = 0; kw < WP; ++kw) top = fmaxf(top, bw[kw]);
+          if (fabsf(top) > kFarBias && top != NEG_INF) {
+            shift_w = top;
+            #pragma unroll
+            for (int kw = 0; kw < WP; ++kw) bw[kw] -= top;
+          }
+        }
         // every thread has its rel_w row before the area is reused for rel_h
         ok = wg_sync() && ok;
         copy_rows(args.rel_h, H, HS);
@@ -754,7 +773,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       ++seg;
       // rel_h of a grid row in base 2 (staged so by the fused prologue)
-      auto rel_h_of = [&](int kh) { return FUSED ? bh_row[kh] : bias2(bh_row[kh]); };
+      auto rel_h_of = [&](int kh) { return FUSED ? bh_row[kh] : bias2(bh_row[kh]) - shift_h; };
 
       // S is processed in blocks of kBlk columns (one TMEM load and one wait
       // each); narrow grids, with more grid rows per tile, use 16 to keep
@@ -865,7 +884,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       // largest rel_h term (base 2) over the grid rows this segment covers
       float mbh = NEG_INF;
       for (int kh = sg.j0 * KHT; kh < min(sg.j1 * KHT, H); ++kh) mbh = fmaxf(mbh, bh_row[kh]);
-      if (!FUSED) mbh = bias2(mbh);
+      if (!FUSED) {
+        if (!(fabsf(bias2(bh_row[0])) <= kFarBias)) {
+          float top = mbh;   // of the whole row: the same in both pieces of a cut unit
+          for (int kh = 0; kh < H; ++kh) top = fmaxf(top, bh_row[kh]);
+          top = bias2(top);
+          if (fabsf(top) > kFarBias && top != NEG_INF) shift_h = top;
+        }
+        mbh = bias2(mbh) - shift_h;
+      }
       for (int j = sg.j0; j < sg.j1; ++j, ++gi) {
         // the tile's rel_h terms, and whether to take it exact at once, are
         // settled before the wait for its S, which hides their latency
@@ -1011,7 +1038,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       };
       if (sg.full(n_kv)) {
         const float inv_l = l == 0.f ? 0.f : 1.0f / l;   // a masked row gives zeros, and lse = -inf
-        if (args.lse != nullptr && row_valid) args.lse[static_cast<size_t>(bh) * N + n] = m_used + log2f(l);
+        if (args.lse != nullptr && row_valid) args.lse[static_cast<size_t>(bh) * N + n] = (m_used + log2f(l)) + (shift_h + shift_w);
         #pragma unroll
         for (int h = 0; h < Dm::kAtoms; ++h) {
           #pragma unroll
@@ -1069,7 +1096,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const float l_ab = fa * ma.y + fb * mb.y;
           const float inv_l = l_ab == 0.f ? 0.f : 1.0f / l_ab;
           if (h == 0 && args.lse != nullptr && row_valid)
-            args.lse[static_cast<size_t>(bh) * N + n] = mstar + log2f(l_ab);
+            args.lse[static_cast<size_t>(bh) * N + n] = (mstar + log2f(l_ab)) + (shift_h + shift_w);
           #pragma unroll
           for (int cc = 0; cc < 4; ++cc) {
             float v[16];

@@ -109,8 +109,8 @@ __device__ __forceinline__ float load_elem(const void* p, size_t i, int fmt) {
 // by log2(e) alone it would only from -2.36e38 on, and a row with nothing above it would get a softmax of what lies
 // below its rounding.  The factor of 4 is exact, so the product is rounded as kLog2e * x is, and overflows from
 // 2^126 = 8.5e37 on, which -1e38 rounded to bf16 (9.97e37) is past.  (A comparison and a select instead cost the
-// attention on a 63x63 grid 2 %.)
-__device__ __forceinline__ float bias2(float x) { return (4.f * x) * (0.25f * kLog2e); }
+// attention on a 63x63 grid 2 %.)  Rounded before anything is added to it, in the forward and the backward alike.
+__device__ __forceinline__ float bias2(float x) { return __fmul_rn(4.f * x, 0.25f * kLog2e); }
 
 // The two 16-bit values of a packed pair, low half first.
 __device__ __forceinline__ float2 unpack_in(uint32_t u, int fmt) {

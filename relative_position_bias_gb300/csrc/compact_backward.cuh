@@ -218,6 +218,7 @@ struct CbUnit {
 // 4 D of out and dO per query and writes 4 (H + W): bound by memory.  Half of the threads take rel_h, half
 // rel_w, a query's row each: all of its loads are in flight at once, and every store is a run of queries.
 constexpr int kCbPrepThreads = 2 * kBlockM;
+constexpr float kLostLse = -1048576.f;
 
 // A row of L <= 64 bias values in base 2, in fp32 (unused entries are left alone).
 __device__ __forceinline__ void cb_load_row(const void* src, size_t at, int L, int fmt, float (&x)[64]) {
@@ -272,13 +273,14 @@ __global__ void __launch_bounds__(kCbPrepThreads) relpos_cb_prep_kernel(const Cb
   const bool is_w = threadIdx.x >= kBlockM;
   const int r = threadIdx.x & (kBlockM - 1), L = is_w ? a.W : a.H;
   float x[64];
-  // rows past N take rw = 0 and hl = -inf, and so does a row without keys (lse = -inf)
+  // rows past N take rw = 0 and hl = -inf, and so does a row without keys: lse = -inf, or so low (a mask of -1e9 on
+  // every key) that its rounding leaves nothing of the probabilities (from 2^20 on they are off by 4 % and more)
   float off = 0.f;
   if (r < rows) {
     if (!is_w) off = a.lse[row0 + r];
     cb_load_row(is_w ? a.rel_w : a.rel_h, (row0 + r) * L, L, a.bias_fmt, x);
   }
-  const bool none = !is_w && (r >= rows || off == -inf);
+  const bool none = !is_w && (r >= rows || off <= kLostLse);
   float* dst = (is_w ? a.rw : a.hl) + (static_cast<size_t>(bh) * a.n_blocks + 2 * blockIdx.x + (r >> 6)) * L * kCbRow;
   #pragma unroll
   for (int c = 0; c < 64; ++c)

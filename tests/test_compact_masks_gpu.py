@@ -7,9 +7,11 @@ from __future__ import annotations
 
 import math
 
+import numpy as np
 import pytest
 import torch
 
+import oracle
 import relative_position_bias_gb300 as rpb
 from relative_position_bias_gb300 import build as rbuild
 
@@ -73,3 +75,49 @@ def test_finite_masks(H, W, BH, bias, value):
         assert torch.count_nonzero(got[2][empty]) == 0
     one = [rpb.attention(b["q"], b["k"], b["v"], b["rel_h"], b["rel_w"], H, W) for b in both]
     assert torch.equal(*one)
+
+
+@pytest.mark.parametrize("low", [-1e4, -1e9, -1e30, 1e9])
+@pytest.mark.parametrize("H,W,BH", [(8, 12, 3), (64, 64, 2)])
+def test_rows_far_from_zero(H, W, BH, low):
+    """A finite bias that all keys of a row share, however large: the softmax does not see it.  Logits spread over some 50
+    powers of two.  Every row's out within the forward's bound (2^-11 + 2^-9) max|v| and its own rounding; lse within
+    2^-13 and three roundings of fp32 (the shift's conversion to base 2, that constant, and the sum)."""
+    x = make(BH, H, W, 64, HF, FL, 8)
+    x["q"] = 2.5 * x["q"]
+    for n in ("rel_h", "rel_w"):
+        y = {m: t.clone() for m, t in x.items()}
+        y[n][:, 1::3] = low
+        for workspace in (None, False):
+            out, lse = rpb.attention_lse(y["q"], y["k"], y["v"], y["rel_h"], y["rel_w"], H, W, 0.25, workspace=workspace)
+            f = {m: t.double().cpu().numpy() for m, t in y.items()}
+            base = {m: f[m] for m in ("rel_h", "rel_w")}
+            base[n] = base[n].copy()
+            base[n][:, 1::3] = 0
+            want, l0 = oracle.masked_attention(f["q"], f["k"], f["v"], base["rel_h"], base["rel_w"], H, W, 0.25)
+            tol = (2.0 ** -11 + 2.0 ** -9) * np.abs(f["v"]).max() + 2.0 ** -11 * np.abs(want)
+            got = out.double().cpu().numpy()
+            assert np.isfinite(got).all(), n
+            assert (np.abs(got - want) <= tol).all(), n
+            l0[:, 1::3] += np.float32(low) / math.log(2.0)
+            assert (np.abs(lse.double().cpu().numpy() - l0) <= 2.0 ** -13 + 3 * 2.0 ** -24 * np.abs(l0)).all(), n
+
+
+@pytest.mark.parametrize("low", [-1e9, -1e30])
+@pytest.mark.parametrize("d", [64, 128])
+def test_gradients_beside_rows_far_from_zero(d, low):
+    """A row masked as a whole by a finite value whose lse says nothing of its probabilities gives no gradient: the
+    others get the bits that they get with -inf there."""
+    H, W = 11, 20
+    x = make(4, H, W, d, BF, FL, 10)
+    for n in ("rel_h", "rel_w"):
+        both = []
+        for to in (low, -math.inf):
+            y = {m: t.clone() for m, t in x.items()}
+            y[n][:, 2::5] = to
+            both.append(step(y, H, W))
+        rest = torch.arange(H * W, device="cuda") % 5 != 2
+        for a, b in zip(both[0][:2], both[1][:2]):
+            assert torch.equal(a[:, rest], b[:, rest])
+        for a, b in zip(both[0][2:], both[1][2:]):
+            assert torch.equal(a, b)
