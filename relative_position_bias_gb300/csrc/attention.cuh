@@ -692,12 +692,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // The block is copied as it is with cp.async: every 4-byte word of
         // the tile's rows goes out at once (word e of the block to thread
         // e mod 128, so a warp reads 128 contiguous bytes), without a round
-        // trip through registers per batch of rows; the log2e scaling is
-        // applied where the rows are read.  A row of a 16-bit bias with an even length is
+        // trip through registers per batch of rows; the scaling to base 2 is
+        // applied where values are read.  A row of a 16-bit bias with an even length is
         // half as many words, which go to the end of its staging row and are widened there by
         // the row's own thread (copying 16-bit rows in batches through registers took the 64x64
-        // grid from 355 to 623 us); rows of an odd length do not start at whole words, and
-        // every thread loads its own.
+        // grid from 355 to 623 us).  A row of an odd length lies in (len + 1) / 2 words, the first or the
+        // last of which it shares with a neighbour, and both copy that one.  Short ones are loaded by their own
+        // threads, value by value: 64 heads of 63x63 take 549 us so and 373 by words, 200 of 21x25 84 and 80, 300 of
+        // 17x17 68 and 71, of 15x15 23 and 25.
+        constexpr int kOddLoads = 20;
         const bool raw = args.bias_fmt == kF32;
         auto copy_rows_async = [&](const void* p, int words, int at, int stride) {
           const float* src = static_cast<const float*>(p);
@@ -715,9 +718,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           cp_async_wait_all();
         };
+        auto copy_odd = [&](const void* p, int len) {
+          const int words = (len + 1) / 2;
+          const size_t first = row0 * static_cast<size_t>(len);   // the block's first value
+          const int odd = static_cast<int>(first) & 1;
+          const float* base = static_cast<const float*>(p);
+          const float* src = base + first / 2;
+          // a tensor of an odd number of values ends in the middle of its last row's last word
+          const bool cut = nrows > 0 && row0 + nrows == static_cast<size_t>(args.BH) * N && ((first + nrows * len) & 1);
+          const int cut_row = cut ? nrows - 1 : -1;
+          const int step_r = kBlockM / words, step_c = kBlockM - step_r * words;
+          int rr = r / words, c = r - rr * words;
+          #pragma unroll 1
+          for (int e = r; e < kBlockM * words; e += kBlockM) {
+            const uint32_t bytes = rr < nrows ? ((rr == cut_row && c == words - 1) ? 2u : 4u) : 0u;
+            cp_async4(area + rr * kBiasStride + words + c, rr < nrows ? src + ((odd + rr * len) >> 1) + c : base, bytes);
+            rr += step_r;
+            c += step_c;
+            if (c >= words) {
+              c -= words;
+              ++rr;
+            }
+          }
+          cp_async_wait_all();
+        };
         auto copy_rows = [&](const void* p, int len, int stride) {
           if (raw) copy_rows_async(p, len, 0, stride);
           else if ((len & 1) == 0) copy_rows_async(p, len / 2, len / 2, stride);
+          else if (len > kOddLoads) copy_odd(p, len);
         };
         // this thread's row of a 16-bit bias, once its words are there, in fp32
         auto own_row = [&](const void* p, int len, float* row) {
@@ -727,7 +755,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               row[c] = x.x;
               row[c + 1] = x.y;
             }
-          } else {
+          } else if (len <= kOddLoads) {
             #pragma unroll 1
             for (int c0 = 0; c0 < len; c0 += 8) {
               float x[8];
@@ -738,6 +766,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               #pragma unroll
               for (int c = 0; c < 8; ++c)
                 if (c0 + c < len) row[c0 + c] = x[c];
+            }
+          } else {
+            const float* from = row + (len + 1) / 2;
+            const uint32_t skip = ((row0 + r) & 1) ? 16u : 0u;   // bits of the first word that are the row before's
+            uint32_t w = __float_as_uint(from[0]);
+            #pragma unroll 1
+            for (int c = 0; c < len; c += 2) {   // the words not yet read lie past what is written
+              const uint32_t next = __float_as_uint(from[c / 2 + 1]);
+              const float2 x = unpack_in(__funnelshift_r(w, next, skip), args.bias_fmt);
+              row[c] = x.x;
+              if (c + 1 < len) row[c + 1] = x.y;
+              w = next;
             }
           }
         };

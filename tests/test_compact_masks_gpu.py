@@ -121,3 +121,15 @@ def test_gradients_beside_rows_far_from_zero(d, low):
             assert torch.equal(a[:, rest], b[:, rest])
         for a, b in zip(both[0][2:], both[1][2:]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bias", [BF, HF])
+@pytest.mark.parametrize("BH,H,W", [(3, 1, 1), (5, 3, 7), (3, 13, 13), (3, 15, 9), (7, 35, 35), (3, 63, 63), (5, 63, 64), (3, 64, 61),
+                                    (3, 14, 13), (1, 5, 1)])
+def test_16_bit_bias_of_any_length(BH, H, W, bias):
+    """A 16-bit bias gives the bits of the same values in fp32: rows that start in the middle of a word, a tensor
+    that ends in one, tiles behind the last row."""
+    x = make(BH, H, W, 64, BF, bias, 9)
+    y = {**x, "rel_h": x["rel_h"].float(), "rel_w": x["rel_w"].float()}
+    for a, b in zip(step(x, H, W), step(y, H, W)):
+        assert torch.equal(a, b)
