@@ -51,17 +51,15 @@ template <int D, int MODE>
 struct Angles {
   float c[8], s[8];
   int partner;   // lane that holds the partners (kRotHalf)
+  bool turned;   // this thread's elements are among the first rotary_dim; the others pass as they are
 
   __device__ __forceinline__ void load(const QkArgs& a, long long t, int n, int slot, int lane) {
     partner = lane;
-    #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      c[i] = 1.f;
-      s[i] = 0.f;
-    }
+    turned = false;
     if (MODE == kRotNone) return;
     const int e0 = slot * 8, half = a.half;
     if (e0 >= 2 * half) return;
+    turned = true;
     const bool upper = MODE == kRotHalf && e0 >= half;
     if (MODE == kRotHalf) partner = lane + (upper ? -half / 8 : half / 8);
     const int p = a.positions ? a.positions[t] : n;
@@ -99,6 +97,7 @@ struct Angles {
     float p[8];
     #pragma unroll
     for (int i = 0; i < 8; ++i) p[i] = MODE == kRotHalf ? __shfl_sync(0xffffffffu, x[i], partner) : x[i ^ 1];
+    if (!turned) return;   // not even by an angle of zero: 0 times an infinite neighbour is NaN
     #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], c[i], sign * s[i] * p[i]);
   }
