@@ -1,4 +1,4 @@
-"""qk_norm_rope on rows with infinities past the rotation."""
+"""qk_norm_rope on rows with infinities past the rotation, and its weight gradients where a block takes several heads."""
 from __future__ import annotations
 
 import math
@@ -70,3 +70,42 @@ def test_infinite_gradient_stays_in_its_column(inter):
     keep = torch.arange(d, device="cuda") != 41
     for a, b in zip(got[3:], ref[3:]):
         assert torch.equal(a[keep], b[keep]) and not torch.isfinite(a[41])
+
+
+# heads a block: as many as leave eight blocks an SM; here 4 to 16, and head counts that are no multiple of it
+WEIGHT_CASES = [(4, 4096, 7, 5, 64, BF), (2, 4096, 7, 5, 128, HF), (8, 4096, 13, 6, 64, HF), (1, 2, 16384, 37, 64, BF),
+                (3, 8190, 9, 3, 128, BF)]
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("B,N,hq,hk,d,dtype", WEIGHT_CASES)
+def test_weight_gradients_of_many_heads(B, N, hq, hk, d, dtype, fp32):
+    """dq_weight and dk_weight against float64 sums over every row.
+
+    A column's sum of R terms is a chain of at most L = R / (partial rows) additions a lane, 5 + 8 more within a block and
+    2 * 32 more over the partial rows' sums; each rounds by 2^-24 of a partial sum, no more than the terms' sizes together:
+    (L + 128) 2^-24 of their sum bounds it.  The chain of a lane is its tokens times its heads, less than 1024 here, and
+    a term itself is off by 16 roundings and the reciprocal root's 2^-22."""
+    g = torch.Generator(device="cuda").manual_seed(B * N + hq)
+    q, k = (torch.randn(B, N, h, d, generator=g, device="cuda").to(dtype) for h in (hq, hk))
+    dz = [torch.randn(B * h, N, d, generator=g, device="cuda") for h in (hq, hk)]
+    dz = dz if fp32 else [t.to(dtype) for t in dz]
+    ang = torch.randn(N, d // 2, generator=g, device="cuda")
+    w = [1 + 0.3 * torch.randn(d, generator=g, device="cuda") for _ in range(2)]
+    got = rpb.qk_norm_rope_backward(q, k, *dz, q_weight=w[0], k_weight=w[1], cos=ang.cos(), sin=ang.sin())
+    c, s = ang.cos().double()[:, None], ang.sin().double()[:, None]
+    for x, z, dw, dx, wi in ((q, dz[0], got[3], got[0], w[0]), (k, dz[1], got[4], got[1], w[1])):
+        h = x.shape[2]
+        y = z.view(B, h, N, d).transpose(1, 2).double()
+        a, b = y[..., :d // 2], y[..., d // 2:]
+        back = torch.cat((a * c + b * s, b * c - a * s), -1)
+        xd = x.double()
+        r = (xd.square().mean(-1, keepdim=True) + 1e-6).rsqrt()
+        terms = back * xd * r
+        assert ((dw.double() - terms.sum((0, 1, 2))).abs() <= 1200 * 2.0 ** -24 * terms.abs().sum((0, 1, 2))).all()
+        # a row counted twice or left out is far outside: its term against the sum's random error
+        err = (dw.double() - terms.sum((0, 1, 2))).norm() / terms.square().sum((0, 1, 2)).sqrt().norm()
+        assert err <= 2.0 ** -10
+        gy = back * wi.double()
+        want = r * (gy - xd * r * r * (gy * xd).mean(-1, keepdim=True))
+        assert (dx.double() - want).norm() <= 2.0 ** -18 * want.norm()
