@@ -1,7 +1,7 @@
 """project_backward against the CPU float64 oracle, and a whole training step of the two-step form.
 
-Tolerances.  drel enters the products as two bf16 terms, which leave out at most 2^-16 of a value (with fp16 q and
-tables the product of the two small terms too, 2^-16); the sums are fp32.  A sum over K terms in fp32, in
+Tolerances.  drel enters the products as three bf16 terms, which leave out at most 2^-24 of a value (two, 2^-16, for a
+16-bit dq, and with fp16 q and tables products of small terms, 2^-16, too); the sums are fp32.  A sum over K terms in fp32, in
 any order, is off by at most K 2^-24 of the sum of their sizes, and by far less with terms of
 either sign; 2^-14 of that sum covers the split and chains of 1000.  dq is rounded once more (eps / 2).
 """
