@@ -32,7 +32,7 @@ def nvcc() -> str:
 
 
 def _inputs() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh"))]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".h"))]
     include = os.path.join(ROOT, "include")
     return files + [os.path.join(include, f) for f in os.listdir(include)] + [os.path.abspath(__file__)]
 

@@ -5,6 +5,8 @@
 
 #include <cstddef>
 
+#include "split.h"
+
 namespace dera {
 
 // A launch whose blocks may start before the kernel ahead of it in the stream is complete; it has to wait for
@@ -100,17 +102,6 @@ struct CbArgs {
   float scale, scale_log2;
   int out_fmt, grad_fmt, bias_fmt;
 };
-
-// Whole units and pieces per remaining unit, of `units` tiles that take `steps` steps each.
-struct CbSplit {
-  int full, split;
-  int tail(int units) const { return split > 1 ? units - full : 0; }
-  int blocks(int units) const { return full + (units - full) * split; }
-};
-void cb_split(int units, int rows_steps, int cols_steps, int sms, CbSplit* rows, CbSplit* cols);
-// Padded width of the rows kernel's key steps, and its steps for H grid rows.
-int cb_width(int W);
-int cb_rows_steps(int H, int W);
 
 struct CbMaps {
   CUtensorMap q64, dout64;      // 64-row tiles (cols kernel)
