@@ -116,31 +116,51 @@ def workspace_size(BH: int, H: int, W: int, head_dim: int = 64) -> int:
     return n.value
 
 
+def _capturing(device: torch.device, handle: int) -> bool:
+    """Whether the stream of this handle is being captured into a graph."""
+    if handle == torch.cuda.current_stream(device).cuda_stream:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _workspace(device: torch.device, BH: int, H: int, W: int, d: int, workspace, stream_handle):
-    """(pointer, bytes) of the scratch for one call: the caller's tensor, none, or a cached buffer.
+    """(tensor to keep alive until the launch, pointer, bytes) of the scratch for one call: the caller's
+    tensor, none, a cached buffer, or, for a captured call, a buffer of that call.
 
     The cached buffer is kept per (device, stream): calls on one stream are ordered by it, and
     calls on different streams, which may overlap on the GPU, never share scratch.  A buffer used
     on a stream other than the one current at its allocation is recorded on that stream, so the
-    allocator does not hand its memory out again before that stream's work is done."""
+    allocator does not hand its memory out again before that stream's work is done.  Graphs captured on
+    one stream may be replayed side by side, and after the cached buffer has made way for a larger one: a captured call
+    has memory of the graph's own pool."""
     if workspace is False or device.type != "cuda" or BH == 0:
-        return None, 0
+        return None, None, 0
     if isinstance(workspace, torch.Tensor):
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    handle = int(stream_handle or 0)
     with torch.cuda.device(device):
         need = workspace_size(BH, H, W, d)
-    if need == 0:
-        return None, 0
+        if need == 0:
+            return None, None, 0
+        captured = _capturing(device, handle)
+
+    def new() -> torch.Tensor:
+        buf = torch.empty(need, dtype=torch.uint8, device=device)
+        if handle != torch.cuda.current_stream(device).cuda_stream:
+            buf.record_stream(torch.cuda.ExternalStream(handle, device=device))
+        return buf
+
+    if captured:
+        buf = new()
+        return buf, buf.data_ptr(), need
     idx = device.index if device.index is not None else torch.cuda.current_device()
-    key = (idx, int(stream_handle or 0))
+    key = (idx, handle)
     with _lock:
         buf = _workspaces.get(key)
         if buf is None or buf.numel() < need:
-            buf = torch.empty(need, dtype=torch.uint8, device=device)
-            if int(stream_handle or 0) != torch.cuda.current_stream(device).cuda_stream:
-                buf.record_stream(torch.cuda.ExternalStream(int(stream_handle or 0), device=device))
-            _workspaces[key] = buf
-    return buf.data_ptr(), buf.numel()
+            buf = _workspaces[key] = new()
+    return buf, buf.data_ptr(), buf.numel()
 
 
 def _expect(t: torch.Tensor, shape: tuple, name: str) -> None:
@@ -177,8 +197,9 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h: torch.Te
               out: torch.Tensor | None = None, stream=None, workspace=None) -> torch.Tensor:
     """Attention with a compact bias via ``dera_relpos_attention``.
 
-    ``workspace``: None = a cached scratch buffer per (device, stream), False = no scratch (one
-    CTA per unit), or a caller-owned uint8 tensor, which no other call in flight may use."""
+    ``workspace``: None = a cached scratch buffer per (device, stream), or one of its own for a call that is
+    captured into a graph, False = no scratch (one CTA per unit), or a caller-owned uint8 tensor, which no other
+    call in flight may use."""
     BH, N, d = q.shape
     scale = d ** -0.5 if scale is None else scale
     if out is None:
@@ -193,7 +214,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h: torch.Te
         raise TypeError("rel_h and rel_w must share a dtype")
     lib = load_library()
     st = _stream(q.device, stream)
-    ws, ws_bytes = _workspace(q.device, BH, H, W, d, workspace, st)
+    keep, ws, ws_bytes = _workspace(q.device, BH, H, W, d, workspace, st)
     _check(lib.dera_relpos_attention(_ptr(q), _ptr(k), _ptr(v), _ptr(rel_h), _ptr(rel_w), _ptr(out), BH, H, W, d,
                                      float(scale), _code(q.dtype), _code(rel_h.dtype), _code(out.dtype), ws,
                                      ws_bytes, st))
@@ -217,7 +238,7 @@ def fused(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_pos_h: torch.Te
             raise TypeError("q, k, v and the tables must share a dtype")
     lib = load_library()
     st = _stream(q.device, stream)
-    ws, ws_bytes = _workspace(q.device, BH, H, W, d, workspace, st)
+    keep, ws, ws_bytes = _workspace(q.device, BH, H, W, d, workspace, st)
     _check(lib.dera_relpos_fused(_ptr(q), _ptr(k), _ptr(v), _ptr(rel_pos_h), _ptr(rel_pos_w), _ptr(out), BH, H, W,
                                  d, float(scale), _code(q.dtype), _code(out.dtype), ws, ws_bytes, st))
     return out
@@ -240,7 +261,7 @@ def fused_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_pos_h: torc
             raise TypeError("q, k, v and the tables must share a dtype")
     lib = load_library()
     st = _stream(q.device, stream)
-    ws, ws_bytes = _workspace(q.device, BH, H, W, d, workspace, st)
+    keep, ws, ws_bytes = _workspace(q.device, BH, H, W, d, workspace, st)
     _check(lib.dera_relpos_fused_lse(_ptr(q), _ptr(k), _ptr(v), _ptr(rel_pos_h), _ptr(rel_pos_w), _ptr(out), _ptr(lse),
                                      BH, H, W, d, float(scale), _code(q.dtype), _code(out.dtype), ws, ws_bytes, st))
     return out, lse
