@@ -86,7 +86,8 @@ DERA_API dera_status dera_qk_norm_rope_backward_workspace_size(int B, int N, int
  * out: dq, dk and (iff dv_out) dv in token order with the strides given, in grad_dtype
  *      (DERA_F32 or in_dtype); dq_weight, dk_weight [head_dim] fp32, iff weights.
  * workspace: at least the size above if weights are given (else it may be NULL).
- * An out-of-range position gives NaN as in the forward.  Other arguments and errors as for the forward;
+ * An out-of-range position gives NaN as in the forward, in that token's gradients and so in the weights'.
+ * Other arguments and errors as for the forward;
  *      DERA_ERR_SCRATCH for a missing or too small workspace.  B = 0 or N = 0 writes zero weight gradients.
  */
 DERA_API dera_status dera_qk_norm_rope_backward(const dera_heads* q, const dera_heads* k, const void* q_weight,
@@ -153,6 +154,7 @@ DERA_API dera_status dera_relpos_project_backward_workspace_size(int BH, int H, 
  *      attention's own part of dq), or NULL for none; it may be dq itself.
  * out: dq [BH,N,head_dim] in grad_dtype (DERA_F32 or in_dtype); drel_pos_h [2H-1,head_dim], drel_pos_w
  *      [2W-1,head_dim] fp32, summed over every batch and head.
+ * q, the tables, drel_h and drel_w must be finite everywhere (a table row's sum reads every token's q).
  * Precision: fp32 sums; drel_h and drel_w enter the products as three bf16 terms each (what is left
  *      out is 2^-24 of a value), two (2^-16) for a 16-bit dq, and with fp16 q and the tables as two
  *      bf16 terms, exactly.

@@ -14,8 +14,9 @@
 // token order, writes whole rows of consecutive tokens of a head.
 //
 // Measured: forward, 8 x 4096 tokens, 3 x 16 heads of 128, fp16, 806 MB: 123 us, 6.5 TB/s (a plain copy reaches
-// 6.8).  Backward, 8 x 4096 tokens, 3 x 12 heads of 64, bf16, 404 MB: 78 us, 5.2 TB/s; it issues in 57 % of the
-// cycles (two sums of eight lanes a row) and waits for loads in most others.  The weights' sums
+// 6.8).  Backward, 8 x 4096 tokens, 3 x 12 heads of 64, bf16, 404 MB: 76 us, 5.3 TB/s (705 MB in fp32 as the binding's
+// defaults give them: 138 us with the weights' sums, 5.1 TB/s); it issues in 57 % of the cycles (two sums of eight lanes a
+// row) and waits for loads in most others, those of its spilled registers among them.  The weights' sums
 // are 4 us more (7 when their kernel was not launched ahead of this one's end).
 #pragma once
 #include <cstdint>
@@ -192,7 +193,8 @@ struct Grad8 {
 // The weights' gradients are sums over every row of every token: a block takes
 // every gridDim.x-th run of tokens and keeps its slots' sums in registers, one partial row
 // per block, which qk_weight_grad_kernel adds in a fixed order.  Four rows in flight a thread and three blocks an
-// SM: 78 us on the case above; three rows 93, two 95.
+// SM: 76 us on the case above; three rows 93, two 95.  That leaves 80 registers a thread, which with a norm are too few
+// (half split: 144 bytes of spill stores and 260 of loads, with fp32 gradients 224 and 460; interleaved 104 and 136).
 template <bool BF16, int D, int MODE, bool NORM, bool ZF32>
 __global__ void __launch_bounds__(kQkThreads, 3) qk_norm_rope_bwd_kernel(const QkArgs a) {
   constexpr int LANES = D / 8, TOK = kQkThreads / LANES, WARPS = kQkThreads / 32, U = 4;
