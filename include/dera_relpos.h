@@ -109,6 +109,7 @@ DERA_API dera_status dera_relpos_project(const void* q, const void* rel_pos_h, c
  *      rel_h [BH,N,H], rel_w [BH,N,W] in bias_dtype (DERA_F32 | DERA_BF16 | DERA_F16).
  * out: out [BH,N,head_dim] in out_dtype (DERA_F32, or in_dtype).
  * A bias of -inf, or of -1e38 (rounded to its type) or below, masks its keys; a row with every key masked gives out = 0.
+ * A bias is at most 8e37 and not NaN; q, k and v are finite at masked keys too.
  * workspace / workspace_bytes: optional scratch, see dera_relpos_workspace_size.
  * Softmax runs in base 2 with fp32 accumulation; P is rounded to fp16 for the
  * P.V product (for bf16 inputs, V tiles are converted to fp16 on chip, so

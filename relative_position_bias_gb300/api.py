@@ -116,6 +116,15 @@ def workspace_size(BH: int, H: int, W: int, head_dim: int = 64) -> int:
     return n.value
 
 
+def _scratch_on(nbytes: int, device: torch.device, handle: int) -> torch.Tensor:
+    """A buffer for work on the stream of this handle, allocated as that stream's: freed as soon as the call returns,
+    it serves nothing but later work there, and in a capture it is of the graph's own pool."""
+    if handle == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _capturing(device: torch.device, handle: int) -> bool:
     """Whether the stream of this handle is being captured into a graph."""
     if handle == torch.cuda.current_stream(device).cuda_stream:
@@ -129,9 +138,7 @@ def _workspace(device: torch.device, BH: int, H: int, W: int, d: int, workspace,
     tensor, none, a cached buffer, or, for a captured call, a buffer of that call.
 
     The cached buffer is kept per (device, stream): calls on one stream are ordered by it, and
-    calls on different streams, which may overlap on the GPU, never share scratch.  A buffer used
-    on a stream other than the one current at its allocation is recorded on that stream, so the
-    allocator does not hand its memory out again before that stream's work is done.  Graphs captured on
+    calls on different streams, which may overlap on the GPU, never share scratch.  Graphs captured on
     one stream may be replayed side by side, and after the cached buffer has made way for a larger one: a captured call
     has memory of the graph's own pool."""
     if workspace is False or device.type != "cuda" or BH == 0:
@@ -143,23 +150,14 @@ def _workspace(device: torch.device, BH: int, H: int, W: int, d: int, workspace,
         need = workspace_size(BH, H, W, d)
         if need == 0:
             return None, None, 0
-        captured = _capturing(device, handle)
-
-    def new() -> torch.Tensor:
-        buf = torch.empty(need, dtype=torch.uint8, device=device)
-        if handle != torch.cuda.current_stream(device).cuda_stream:
-            buf.record_stream(torch.cuda.ExternalStream(handle, device=device))
-        return buf
-
-    if captured:
-        buf = new()
-        return buf, buf.data_ptr(), need
-    idx = device.index if device.index is not None else torch.cuda.current_device()
-    key = (idx, handle)
-    with _lock:
-        buf = _workspaces.get(key)
-        if buf is None or buf.numel() < need:
-            buf = _workspaces[key] = new()
+        if _capturing(device, handle):
+            buf = _scratch_on(need, device, handle)
+            return buf, buf.data_ptr(), need
+        key = (device.index if device.index is not None else torch.cuda.current_device(), handle)
+        with _lock:
+            buf = _workspaces.get(key)
+            if buf is None or buf.numel() < need:
+                buf = _workspaces[key] = _scratch_on(need, device, handle)
     return buf, buf.data_ptr(), buf.numel()
 
 
@@ -304,11 +302,7 @@ def fused_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_pos_h:
     if workspace is None:
         with torch.cuda.device(q.device):
             need = backward_workspace_size(BH, H, W, d)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-        if int(st or 0) != torch.cuda.current_stream(q.device).cuda_stream:
-            # freed when this call returns: the allocator must not hand it out again before
-            # the kernels on that stream are done with it
-            workspace.record_stream(torch.cuda.ExternalStream(int(st or 0), device=q.device))
+            workspace = _scratch_on(max(need, 1), q.device, int(st or 0))
     _check(lib.dera_relpos_fused_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(rel_pos_h), _ptr(rel_pos_w), _ptr(out),
                                           _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dth), _ptr(dtw),
                                           BH, H, W, d, float(scale), _code(q.dtype), _code(out.dtype), _code(gd),

@@ -91,16 +91,15 @@ def _size(entry: str, *sizes: int) -> int:
 
 def _scratch(device: torch.device, stream, handle, workspace: torch.Tensor | None, entry: str, *sizes: int) -> tuple:
     """(tensor to keep alive, pointer, bytes) of one call's scratch: the caller's, or a new buffer
-    that the allocator keeps until the work on the launching stream is done."""
+    of the launching stream."""
     if workspace is None:
         if device.type != "cuda":
             return None, None, 0
         need = _size_on(device.index, entry, *sizes)
         if need == 0:
             return None, None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None and int(handle or 0) != torch.cuda.current_stream(device).cuda_stream:
-            workspace.record_stream(torch.cuda.ExternalStream(int(handle or 0), device=device))
+        workspace = (torch.empty(need, dtype=torch.uint8, device=device) if stream is None
+                     else api._scratch_on(need, device, int(handle or 0)))
         return workspace, workspace.data_ptr(), need
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 

@@ -65,3 +65,33 @@ def test_graphs_of_one_stream_side_by_side(entry):
         torch.cuda.synchronize()
         for a, b in zip([*res, got], [*want, want_large]):
             assert all(torch.equal(s, t) for s, t in zip(a, b))
+
+
+@pytest.mark.parametrize("entry", ["attention", "fused"])
+def test_captured_stream_that_is_not_the_current_one(entry):
+    """A call into the caller's output whose stream is captured while another is current: its scratch is the graph's, not
+    memory that is handed out again once the call has returned."""
+    x = make(12, 4)
+    out = torch.empty_like(x["q"])
+
+    def run(**more):
+        bias = (x["rh"], x["rw"]) if entry == "attention" else (x["th"], x["tw"])
+        return getattr(rpb, entry)(x["q"], x["k"], x["v"], *bias, 64, 64, **more)
+    want = run()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    run(out=out, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        with torch.cuda.stream(other):
+            run(out=out, stream=side)
+    taken = [torch.full((1 << 22,), float("nan"), device="cuda") for _ in range(32)]   # what freed memory would go to
+    for _ in range(3):
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert all(t.isnan().all() for t in taken)

@@ -10,18 +10,15 @@ from relative_position_bias_gb300 import api
 
 
 class Buffer:
-    """Stands in for a tensor: a place of its own, and the streams it was recorded on."""
-    def __init__(self, n, at):
-        self.n, self.at, self.streams = n, at, []
+    """Stands in for a tensor: a place of its own, and the stream it was allocated on."""
+    def __init__(self, n, at, stream):
+        self.n, self.at, self.stream = n, at, stream
 
     def data_ptr(self):
         return self.at
 
     def numel(self):
         return self.n
-
-    def record_stream(self, s):
-        self.streams.append(s.cuda_stream)
 
 
 class Stream:
@@ -35,7 +32,7 @@ def cuda(monkeypatch):
     state = dict(need=1000, captured=set(), current=7, made=[])
 
     def empty(n, **_):
-        state["made"].append(Buffer(n, 4096 * (1 + len(state["made"]))))
+        state["made"].append(Buffer(n, 4096 * (1 + len(state["made"])), state["current"]))
         return state["made"][-1]
 
     @contextlib.contextmanager
@@ -66,7 +63,7 @@ def test_eager_calls_of_a_stream_share_a_buffer(cuda):
     assert get(7)[-2:] == (cuda["made"][-1].at, 2000)
     cuda["need"] = 500
     assert get(7)[-2:] == (cuda["made"][-1].at, 2000)     # a larger one serves
-    assert [m.streams for m in cuda["made"]] == [[], [8], []]
+    assert [m.stream for m in cuda["made"]] == [7, 8, 7]   # each of the stream that uses it
 
 
 def test_captured_calls_have_buffers_of_their_own(cuda):
@@ -81,7 +78,7 @@ def test_captured_calls_have_buffers_of_their_own(cuda):
     assert get(7)[-2] == eager[-2]
     cuda["captured"] = {8}                                # captured, but not the current stream
     side = get(8)
-    assert side[-2] == cuda["made"][-1].at and cuda["made"][-1].streams == [8]
+    assert side[-2] == cuda["made"][-1].at and cuda["made"][-1].stream == 8
     assert get(7)[-2] == eager[-2]
 
 
