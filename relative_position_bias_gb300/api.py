@@ -71,8 +71,9 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.dera_relpos_fused_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, f,
                                                    i, i, i, vp, sz, vp]
         lib.dera_relpos_fused_backward.restype = i
-        from . import train   # imports this module
+        from . import block, train   # import this module
         train.declare(lib)
+        block.declare(lib)
         _lib = lib
         return lib
 

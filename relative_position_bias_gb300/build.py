@@ -18,7 +18,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdera_relpos.so")
 SOURCES = ["dera_relpos.cu", "attention_w16.cu", "attention_w32.cu", "attention_w40.cu", "attention_w64.cu",
            "backward.cu", "train.cu", "qk_norm_rope.cu", "compact_backward_d64.cu", "compact_backward_d128.cu",
-           "project_backward.cu"]
+           "project_backward.cu", "block.cu", "layer_norm.cu", "linear_forward.cu", "linear_input.cu",
+           "linear_weight.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
                 "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -163,6 +163,16 @@ bool map_keys(CUtensorMap* m, const void* p, dera_dtype t, int BH, int H, int W,
   return make_map(m, p, tma_type(t), 4, dims, strides, box);
 }
 
+bool map_tokens(CUtensorMap* m, const HeadsPtr& t, dera_dtype dt, int B, int N, int heads, int d, int rows) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(B)};
+  // a stride that nothing steps by still has to be a valid one
+  auto bytes = [&](long long st) { return 2 * static_cast<cuuint64_t>(st > 0 ? st : d); };
+  const cuuint64_t strides[3] = {bytes(t.st), bytes(t.sh), bytes(t.sb)};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1};
+  return make_map(m, t.data, tma_type(dt), 4, dims, strides, box);
+}
+
 // table [2L-1, d], one 128-row box per 64 columns (rows past 2L-1 read as zero)
 static bool map_table(CUtensorMap* m, const void* p, dera_dtype t, int L, int d) {
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(2 * L - 1)};

@@ -8,8 +8,9 @@
 #include <cstddef>
 #include <initializer_list>
 
-#include "../../include/dera_relpos.h"
+#include "../../include/dera_train.h"
 #include "common.cuh"
+#include "train.cuh"
 
 namespace dera {
 
@@ -36,6 +37,15 @@ size_t align256(size_t x);
 bool map_rows(CUtensorMap* m, const void* p, dera_dtype t, int BH, int N, int d, int rows = 128);
 // k / v viewed as [BH, H, W, d], read in tiles of KHT grid rows x WP columns
 bool map_keys(CUtensorMap* m, const void* p, dera_dtype t, int BH, int H, int W, int d, int WP, int KHT);
+
+// tokens [B, N, heads, d] by their strides (elements), read in boxes of 64 elements by `rows` tokens
+bool map_tokens(CUtensorMap* m, const HeadsPtr& t, dera_dtype dt, int B, int N, int heads, int d, int rows);
+
+// A caller's workspace: large enough, 256-byte aligned, of device `dev`.
+dera_status check_workspace(const void* ws, size_t have, size_t need, int dev);
+// One tensor in token order, its strides made ready for the kernels (0 where the
+// dimension has size one).  `distinct`: no two rows may share an element.
+dera_status take_heads(const dera_heads* t, int B, int N, int heads, int d, bool distinct, HeadsPtr* out);
 
 // The attention launch of every entry (compact bias, or tables when `fused`).
 dera_status run_attention(const void* q, const void* k, const void* v, const void* a, const void* b, void* out,

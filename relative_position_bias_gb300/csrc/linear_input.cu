@@ -1,0 +1,7 @@
+#include "linear_inst.cuh"
+
+namespace dera {
+cudaError_t launch_linear_input(const LinMaps& m, const LinArgs& a, const LinPlan& p, cudaStream_t s) {
+  return launch_lin_all<kLinInput>(m, a, p, s);
+}
+}  // namespace dera

@@ -1,0 +1,236 @@
+// The products of linear.cuh for large sizes: a pair of CTAs multiplies a tile of 256 x BN (tcgen05.mma cta_group::2).
+//
+// Each CTA loads its 128 rows of A and half of B's rows, 32 KB a step of 64 for 256 x 256 x 64 products: half of the
+// shared memory, and of the traffic from L2, that two CTAs with tiles of their own would need.  A pair walks over tiles
+// with one pipeline of loads, and the accumulators have two buffers in TMEM, so that a tile's epilogue runs while the next tile's
+// products do.
+//
+// The tensor core cuts towards zero what it adds to its fp32 sum, so a long chain drifts: 3.4e-5 of the sum after
+// 30 000 terms.  The weight's gradient sums over tokens, without limit: its chains end after kLinChain steps (4096 tokens,
+// 5e-6), and the epilogue adds them in registers while the next chain runs in the other buffer.
+#pragma once
+#include "linear.cuh"
+
+namespace dera {
+
+constexpr int kPairThreads = 384;   // a warp that loads, one that multiplies, two that wait, eight of the epilogue
+constexpr int kPairEpi = 8;
+constexpr int kLinChain = 64;
+
+template <int BN>
+struct PairSmem {
+  static constexpr int kA = 128 * 128, kB = BN / 2 * 128;
+  static constexpr int kStage = kA + kB;
+  static constexpr int NS = BN == 256 ? 6 : 8;
+  static constexpr int kBars = NS * kStage;
+  static constexpr int kMisc = kBars + (2 * NS + 5) * 8;
+  static constexpr int kAlloc = kMisc + 16 + 1024;
+  static_assert(kAlloc <= 232448, "shared memory");
+};
+
+// One operand's rows [r0, r0 + ROWS) of batch b for contraction step s, as in lin_load.
+template <bool MN, int ROWS>
+__device__ __forceinline__ void lin_load_pair(uint8_t* dst, const CUtensorMap* m, uint32_t bar, int d, int r0, int b, int s,
+                                              int steps_batch) {
+  if (!MN) {
+    const int f = kLinStep * s, h = d ? f / d : 0;
+    tma_load_4d_pair(dst, m, bar, f - h * d, r0, h, b);
+  } else {
+    const int bb = s / steps_batch, row = (s - bb * steps_batch) * kLinStep;
+    #pragma unroll
+    for (int j = 0; j < ROWS / 64; ++j) {
+      const int f = r0 + 64 * j, h = d ? f / d : 0;
+      tma_load_4d_pair(dst + j * 64 * 128, m, bar, f - h * d, row, h, bb);
+    }
+  }
+}
+
+// One piece of work: a tile, and for the weight's gradient a piece of its contraction.
+struct PairItem {
+  int b, r0, c0, piece, s0, s1;
+  __device__ __forceinline__ PairItem(const LinArgs& a, int item, int bn) {
+    const int tile = item / a.pieces;
+    piece = item - tile * a.pieces;
+    const int mt = tile / a.n_tiles;
+    b = mt / a.m_tiles;
+    r0 = (mt - b * a.m_tiles) * 256;
+    c0 = (tile - mt * a.n_tiles) * bn;
+    s0 = piece * a.piece_steps;
+    s1 = min(s0 + a.piece_steps, a.steps);
+  }
+};
+
+template <int KIND, int BN, bool BF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                       const __grid_constant__ LinArgs a) {
+  using SM = PairSmem<BN>;
+  constexpr int NS = SM::NS;
+  constexpr bool A_MN = KIND == kLinWeight, B_MN = KIND != kLinForward;
+  constexpr bool CHAINS = KIND == kLinWeight;
+  constexpr int CHAIN = CHAINS ? kLinChain : 1 << 30;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBars);   // the even CTA's: both CTAs' loads of a step landed
+  uint64_t* empty = full + NS;                                      // each CTA's: the step's products are complete
+  uint64_t* acc_full = empty + NS;                                  // each CTA's [2]: a chain is complete
+  uint64_t* acc_empty = acc_full + 2;                               // the even CTA's [2]: and has been read by both
+  uint64_t* all_done = acc_empty + 2;
+  uint32_t* slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::kMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int items = a.batches * a.m_tiles * a.n_tiles * a.pieces;
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < 2 * NS + 2; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&acc_empty[i], 2 * kPairEpi);
+    mbar_init(all_done, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(slot, 2 * BN);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tbase = *slot;
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------- loads: each CTA its rows
+      int n = 0;
+      bool ok = true;
+      for (int item = pair; ok && item < items; item += pairs) {
+        const PairItem w(a, item, BN);
+        for (int s = w.s0; s < w.s1; ++s, ++n) {
+          const int st = n % NS;
+          ok = mbar_wait(&empty[st], ((n / NS) & 1) ^ 1, abort_flag, a.status);
+          if (!ok) break;
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * SM::kStage);
+          const uint32_t bar = cluster_map(&full[st], 0);
+          lin_load_pair<A_MN, 128>(smem + st * SM::kStage, &map_a, bar, a.a_d, w.r0 + 128 * static_cast<int>(rank), w.b, s,
+                                   a.steps_batch);
+          lin_load_pair<B_MN, BN / 2>(smem + st * SM::kStage + SM::kA, &map_b, bar, a.b_d,
+                                      w.c0 + BN / 2 * static_cast<int>(rank), 0, s, a.steps_batch);
+        }
+      }
+      // both CTAs' copies have landed: at once after a whole run, and with a limit if some role gave up
+      if (rank == 0)
+        for (int i = max(0, n - NS); i < n; ++i) mbar_wait_budget(&full[i % NS], (i / NS) & 1, kWaitBudgetCycles);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // ------------------------------------------------------------- products, for both CTAs
+      constexpr uint32_t fmt = BF16 ? 1 : 0;
+      constexpr uint32_t id = idesc_f16(256, BN, fmt, fmt, A_MN, B_MN);
+      constexpr uint32_t ka = A_MN ? 128 : 2, kb = B_MN ? 128 : 2;   // 16 contraction elements further, in 16 bytes
+      const uint64_t da = sdesc_sw128(smem_u32(smem), A_MN ? 8192 : 16, 1024);
+      const uint64_t db = sdesc_sw128(smem_u32(smem) + SM::kA, B_MN ? 8192 : 16, 1024);
+      int n = 0, chain = 0;
+      bool ok = true;
+      for (int item = pair; ok && item < items; item += pairs) {
+        const PairItem w(a, item, BN);
+        for (int s = w.s0; ok && s < w.s1; ++chain) {
+          const int end = min(w.s1, CHAINS ? s + CHAIN : w.s1), buf = chain & 1;
+          ok = warp_all(mbar_wait(&acc_empty[buf], ((chain >> 1) & 1) ^ 1, abort_flag, a.status));
+          if (!ok) break;
+          tc_fence_after();
+          for (int first = s; s < end; ++s, ++n) {
+            const int st = n % NS;
+            ok = warp_all(mbar_wait(&full[st], (n / NS) & 1, abort_flag, a.status));
+            if (!ok) break;
+            tc_fence_after();
+            #pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_ss_pair_w(tbase + BN * buf, da + st * (SM::kStage >> 4) + ka * k, db + st * (SM::kStage >> 4) + kb * k, id,
+                             (s > first || k > 0) ? 1u : 0u);
+            umma_commit_pair_w(&empty[st]);
+          }
+          if (ok) umma_commit_pair_w(&acc_full[buf]);
+        }
+      }
+      // every product issued above is complete before TMEM is released or the other CTA leaves
+      umma_commit_pair_w(all_done);
+      mbar_wait_budget(all_done, 0, kWaitBudgetCycles);
+      __syncwarp();
+    }
+  } else if (warp >= 4) {
+    // --------------------------------------------------------------- epilogue: a warp 32 rows of half of the columns
+    constexpr int COLS = BN / 2;
+    const int quarter = warp & 3, col0 = COLS * ((warp - 4) >> 2);
+    const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    int chain = 0;
+    bool ok = true;
+    for (int item = pair; ok && item < items; item += pairs) {
+      const PairItem w(a, item, BN);
+      const int row = w.r0 + 128 * static_cast<int>(rank) + 32 * quarter + lane;
+      const bool valid = row < a.rows;
+      float acc[CHAINS ? COLS : 1];
+      for (int s = w.s0; s < w.s1; ++chain) {
+        const int buf = chain & 1;
+        const bool first = s == w.s0;
+        s = min(w.s1, CHAINS ? s + CHAIN : w.s1);
+        ok = warp_all(mbar_wait(&acc_full[buf], (chain >> 1) & 1, abort_flag, a.status));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t at = tbase + BN * buf + lanes + col0;
+        if (CHAINS) {
+          #pragma unroll
+          for (int c = 0; c < COLS; c += 16) {
+            uint32_t u[16];
+            tmem_ld16(at + c, u);
+            tmem_wait_ld();
+            #pragma unroll
+            for (int j = 0; j < 16; ++j)
+              acc[CHAINS ? c + j : 0] = first ? __uint_as_float(u[j]) : acc[CHAINS ? c + j : 0] + __uint_as_float(u[j]);
+          }
+        } else {
+          #pragma unroll 1
+          for (int c = 0; c < COLS; c += 32) {
+            uint32_t u[32];
+            tmem_ld32(at + c, u);
+            tmem_wait_ld();
+            if (c + 32 == COLS) {   // the last of this warp's columns are in registers
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster(cluster_map(&acc_empty[buf], 0));
+            }
+            const int f = w.c0 + col0 + c;
+            float v[32];
+            #pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+            if (valid && f < a.cols) lin_finish<KIND>(a, v, w.b, row, f);
+          }
+        }
+        if (CHAINS) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_map(&acc_empty[buf], 0));
+        }
+      }
+      if (CHAINS && ok && valid) {
+        const size_t stride = a.cols;
+        float* part = a.parts ? a.parts + (static_cast<size_t>(w.piece) * a.rows + row) * stride : nullptr;
+        #pragma unroll
+        for (int c = 0; c < COLS; c += 8) {
+          const int f = w.c0 + col0 + c;
+          if (f < a.cols) {
+            const float(&v)[8] = *reinterpret_cast<const float(*)[8]>(&acc[CHAINS ? c : 0]);
+            if (part) store8(part, f, v, kF32);
+            else store8(a.out, static_cast<size_t>(row) * stride + f, v, a.out_fmt);
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();
+  if (warp == 1) tmem_dealloc_pair(tbase, 2 * BN);
+}
+
+}  // namespace dera

@@ -10,9 +10,7 @@
 
 using namespace dera;
 
-namespace {
-
-constexpr int kMaxHeads = 16384;   // so that the groups of q, k and v fit one grid dimension
+namespace dera {
 
 dera_status check_workspace(const void* ws, size_t have, size_t need, int dev) {
   if (need == 0) return DERA_OK;
@@ -21,8 +19,6 @@ dera_status check_workspace(const void* ws, size_t have, size_t need, int dev) {
   return check_ptr(ws, dev);
 }
 
-// One tensor in token order, its strides made ready for the kernels (0 where the
-// dimension has size one).  `distinct`: no two rows may share an element.
 dera_status take_heads(const dera_heads* t, int B, int N, int heads, int d, bool distinct, HeadsPtr* out) {
   if (!t || !t->data) return DERA_ERR_NULL;
   if (reinterpret_cast<uintptr_t>(t->data) % 16 != 0) return DERA_ERR_ALIGN;
@@ -50,6 +46,12 @@ dera_status take_heads(const dera_heads* t, int B, int N, int heads, int d, bool
   }
   return DERA_OK;
 }
+
+}  // namespace dera
+
+namespace {
+
+constexpr int kMaxHeads = 16384;   // so that the groups of q, k and v fit one grid dimension
 
 dera_status check_qk(int B, int N, int q_heads, int kv_heads, int head_dim) {
   if (head_dim != 64 && head_dim != 128) return DERA_ERR_HEAD_DIM;
