@@ -27,22 +27,54 @@ struct LinSmem {
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
-// One operand's rows [r0, r0 + ROWS) of batch b for contraction step s.
+// Where an operand's loads are: rows [r0, r0 + ROWS) of a tile, contraction steps one after another.  One thread walks it, so
+// that a step is additions only: with divisions it took longer than the step's products.
 template <bool MN, int ROWS>
-__device__ __forceinline__ void lin_load(uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int d, int r0, int b, int s,
-                                         int steps_batch) {
-  if (!MN) {
-    const int f = kLinStep * s, h = d ? f / d : 0;
-    tma_load_4d(dst, m, bar, f - h * d, r0, h, b);
-  } else {
-    const int bb = s / steps_batch, row = (s - bb * steps_batch) * kLinStep;
-    #pragma unroll
-    for (int j = 0; j < ROWS / 64; ++j) {
-      const int f = r0 + 64 * j, h = d ? f / d : 0;
-      tma_load_4d(dst + j * 64 * 128, m, bar, f - h * d, row, h, bb);
+struct LinCursor {
+  int d, steps_batch;
+  int b, h, f, row, left;   // of the next step: batch, head and feature in it, row; steps left in the batch
+  int fj[ROWS >= 64 ? ROWS / 64 : 1], hj[ROWS >= 64 ? ROWS / 64 : 1];   // MN: features and heads of the 64-column blocks
+  // d: features a head (0: one head); batch: of a K-major operand
+  __device__ __forceinline__ LinCursor(int d_, int r0, int batch, int s, int steps_batch_) : d(d_), steps_batch(steps_batch_) {
+    if (!MN) {
+      f = kLinStep * s;
+      h = d ? f / d : 0;
+      f -= h * d;
+      row = r0;
+      b = batch;
+    } else {
+      b = s / steps_batch;
+      left = steps_batch - (s - b * steps_batch);
+      row = (s - b * steps_batch) * kLinStep;
+      #pragma unroll
+      for (int j = 0; j < ROWS / 64; ++j) {
+        hj[j] = d ? (r0 + 64 * j) / d : 0;
+        fj[j] = r0 + 64 * j - hj[j] * d;
+      }
     }
   }
-}
+  // load(dst, feature, row, head, batch) for each box of the step, and on to the next one
+  template <class Load>
+  __device__ __forceinline__ void step(uint8_t* dst, Load&& load) {
+    if (!MN) {
+      load(dst, f, row, h, b);
+      f += kLinStep;
+      if (f == d) {
+        f = 0;
+        ++h;
+      }
+    } else {
+      #pragma unroll
+      for (int j = 0; j < ROWS / 64; ++j) load(dst + j * 64 * 128, fj[j], row, hj[j], b);
+      row += kLinStep;
+      if (--left == 0) {
+        left = steps_batch;
+        row = 0;
+        ++b;
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ size_t lin_at(const LinView& v, int b, int n, int f) {
   const int h = v.d ? f / v.d : 0;
@@ -54,70 +86,141 @@ __device__ __forceinline__ void store_elem(void* p, size_t i, float x, int fmt) 
   else reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(pack_in(x, 0.f, fmt));
 }
 
-// 32 neighbouring columns from f of one row (token n of batch b, or a row of dW): what becomes of them, and their store.
-template <int KIND>
-__device__ __forceinline__ void lin_finish(const LinArgs& a, float (&v)[32], int b, int n, int f) {
-  const int left = min(4, (a.cols - f) / 8);   // columns come in eights
-  if (KIND == kLinForward) {
-    const size_t at = lin_at(a.out_at, b, n, f);
-    if (a.bias) {
-      #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float x[8];
-        if (j < left) {
-          load8(a.bias, f + 8 * j, x, a.bias_fmt);
-          #pragma unroll
-          for (int e = 0; e < 8; ++e) v[8 * j + e] += x[e];
-        }
-      }
-    }
-    if (a.pre) {
-      #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < left) store8(a.pre, at + 8 * j, *reinterpret_cast<const float(*)[8]>(&v[8 * j]), a.fmt);
-    }
-    if (a.act != kActNone)
-      with_act(a.act, [&](auto A) {
-        #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = act_of<decltype(A)::value>(v[j]);
-      });
-    if (a.aux) {
-      const size_t from = lin_at(a.aux_at, b, n, f);
-      #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float x[8];
-        if (j < left) {
-          load8(a.aux, from + 8 * j, x, a.aux_fmt);
-          #pragma unroll
-          for (int e = 0; e < 8; ++e) v[8 * j + e] += x[e];
-        }
-      }
-    }
-  }
-  if (KIND == kLinInput && a.aux) {
-    const size_t from = lin_at(a.aux_at, b, n, f);
-    float x[32];
-    #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float y[8];
-      #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = 0.f;
-      if (j < left) load8(a.aux, from + 8 * j, y, a.aux_fmt);
-      #pragma unroll
-      for (int e = 0; e < 8; ++e) x[8 * j + e] = y[e];
-    }
-    with_act(a.act, [&](auto A) {
-      #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] *= act_slope<decltype(A)::value>(x[j]);
-    });
-  }
-  const size_t at = lin_at(a.out_at, b, n, f);
+// An epilogue warp's part of a tile: 32 rows of D, COLS columns, in pieces of 32 x 32.  A piece comes out of TMEM a row a
+// lane and passes through 4 KB of shared memory, so that four lanes have a row's 32 columns, eight each: what is read and
+// written then is whole 64-byte (fp32: 128-byte) runs of eight rows at a time.  (A row a lane, 32 addresses an instruction: 216 us
+// instead of 154 for 32768 x 1024 x 4096, and 327 with a residual.)
+struct LinWarp {
+  float4* stage;       // [32][8], 16-byte chunks of row r permuted by r % 8
+  int b, row0, f0;     // batch, first row and column
+};
+
+__device__ __forceinline__ void lin_turn(float4* stage, const float (&u)[32], float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();   // the last piece has been read
   #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (j < left) store8(a.out, at + 8 * j, *reinterpret_cast<const float(*)[8]>(&v[8 * j]), a.out_fmt);
+  for (int c = 0; c < 8; ++c)
+    stage[lane * 8 + (c ^ (lane & 7))] = make_float4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+  __syncwarp();
+  #pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2), c = 2 * (lane & 3);
+    const float4 lo = stage[r * 8 + (c ^ (r & 7))], hi = stage[r * 8 + ((c + 1) ^ (r & 7))];
+    v[8 * i] = lo.x, v[8 * i + 1] = lo.y, v[8 * i + 2] = lo.z, v[8 * i + 3] = lo.w;
+    v[8 * i + 4] = hi.x, v[8 * i + 5] = hi.y, v[8 * i + 6] = hi.z, v[8 * i + 7] = hi.w;
+  }
 }
 
-// The same with the operands swapped: one feature f of `count` tokens from n.
+// Eight columns of four rows of a tensor beside D, 8 rows apart from `at` (in its own type, fp32 in two parts).
+struct LinAux {
+  uint4 lo[4], hi[4];
+  __device__ __forceinline__ void load(const void* p, size_t at, long long step, int fmt, const bool (&there)[4]) {
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = hi[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (!there[i]) continue;
+      const char* q = static_cast<const char*>(p) + (at + i * step) * (fmt == kF32 ? 4 : 2);
+      lo[i] = *reinterpret_cast<const uint4*>(q);
+      if (fmt == kF32) hi[i] = *reinterpret_cast<const uint4*>(q + 16);
+    }
+  }
+  __device__ __forceinline__ void get(int i, float (&x)[8], int fmt) const {
+    if (fmt == kF32) {
+      x[0] = __uint_as_float(lo[i].x), x[1] = __uint_as_float(lo[i].y), x[2] = __uint_as_float(lo[i].z), x[3] = __uint_as_float(lo[i].w);
+      x[4] = __uint_as_float(hi[i].x), x[5] = __uint_as_float(hi[i].y), x[6] = __uint_as_float(hi[i].z), x[7] = __uint_as_float(hi[i].w);
+    } else {
+      unpack8(lo[i], x, fmt);
+    }
+  }
+};
+
+// wait() returns whether D is complete (of the whole warp), done() says that it has been read.
+template <int KIND, int COLS, class Wait, class Done>
+__device__ __forceinline__ bool lin_epilogue(const LinArgs& a, const LinWarp& w, uint32_t taddr, Wait&& wait, Done&& done) {
+  const int lane = threadIdx.x & 31, row = w.row0 + (lane >> 2), col = 8 * (lane & 3);
+  bool there[4];
+  LinAux x;
+  const size_t out_row = static_cast<size_t>(w.b * a.out_at.sb + row * a.out_at.sn);
+  const size_t aux_row = static_cast<size_t>(w.b * a.aux_at.sb + row * a.aux_at.sn);
+  auto at = [&](const LinView& v, int f) {   // offset of feature f
+    const int h = v.d ? f / v.d : 0;
+    return h * v.sh + (f - h * v.d);
+  };
+  auto begin = [&](int c) {   // what of piece c is inside, and the loads beside it
+    const int f = w.f0 + c + col;
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) there[i] = row + 8 * i < a.rows && f < a.cols;
+    if (a.aux) x.load(a.aux, aux_row + at(a.aux_at, f), 8 * a.aux_at.sn, a.aux_fmt, there);
+  };
+  begin(0);
+  if (!wait()) return false;
+  #pragma unroll 1
+  for (int c = 0; c < COLS; c += 32) {
+    uint32_t u[32];
+    tmem_ld32(taddr + c, u);
+    tmem_wait_ld();
+    if (c + 32 == COLS) done();
+    float v[32];
+    {
+      float t[32];
+      #pragma unroll
+      for (int j = 0; j < 32; ++j) t[j] = __uint_as_float(u[j]);
+      lin_turn(w.stage, t, v);
+    }
+    const int f = w.f0 + c + col;
+    const size_t to = out_row + at(a.out_at, f);
+    const long long step = 8 * a.out_at.sn;
+    if (KIND == kLinForward) {
+      if (a.bias && f < a.cols) {
+        float y[8];
+        load8(a.bias, f, y, a.bias_fmt);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i)
+          #pragma unroll
+          for (int e = 0; e < 8; ++e) v[8 * i + e] += y[e];
+      }
+      if (a.pre) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (there[i]) store8(a.pre, to + i * step, *reinterpret_cast<const float(*)[8]>(&v[8 * i]), a.fmt);
+      }
+      if (a.act != kActNone)
+        with_act(a.act, [&](auto A) {
+          #pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = act_of<decltype(A)::value>(v[j]);
+        });
+      if (a.aux) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float y[8];
+          x.get(i, y, a.aux_fmt);
+          #pragma unroll
+          for (int e = 0; e < 8; ++e) v[8 * i + e] += y[e];
+        }
+      }
+    }
+    if (KIND == kLinInput && a.aux)
+      with_act(a.act, [&](auto A) {
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float y[8];
+          x.get(i, y, a.aux_fmt);
+          #pragma unroll
+          for (int e = 0; e < 8; ++e) v[8 * i + e] *= act_slope<decltype(A)::value>(y[e]);
+        }
+      });
+    bool now[4];
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) now[i] = there[i];
+    if (c + 32 < COLS) begin(c + 32);
+    #pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (now[i]) store8(a.out, to + i * step, *reinterpret_cast<const float(*)[8]>(&v[8 * i]), a.out_fmt);
+  }
+  return true;
+}
+
+// With the operands swapped: one feature f of `count` tokens from n.
 template <int KIND>
 __device__ __forceinline__ void lin_finish_turned(const LinArgs& a, float (&v)[32], int n, int f, int count) {
   if (KIND == kLinForward) {
@@ -188,13 +291,19 @@ __global__ void __launch_bounds__(kLinThreads) linear_kernel(const __grid_consta
   const uint32_t tbase = *slot;
   if (warp == 4) {
     if (lane == 0) {
+      LinCursor<A_MN, 128> at_a(a.a_d, r0, b, 0, a.steps_batch);
+      LinCursor<B_MN, BN> at_b(a.b_d, c0, 0, 0, a.steps_batch);
       int s = 0;
       for (; s < a.steps; ++s) {
         const int st = s % NS;
         if (!mbar_wait(&empty[st], ((s / NS) & 1) ^ 1, abort_flag, a.status)) break;
         mbar_arrive_expect_tx(&full[st], SM::kStage);
-        lin_load<A_MN, 128>(smem + st * SM::kStage, &map_a, &full[st], a.a_d, r0, b, s, a.steps_batch);
-        lin_load<B_MN, BN>(smem + st * SM::kStage + SM::kA, &map_b, &full[st], a.b_d, c0, 0, s, a.steps_batch);
+        at_a.step(smem + st * SM::kStage, [&](uint8_t* dst, int f, int row, int h, int bb) {
+          tma_load_4d(dst, &map_a, &full[st], f, row, h, bb);
+        });
+        at_b.step(smem + st * SM::kStage + SM::kA, [&](uint8_t* dst, int f, int row, int h, int bb) {
+          tma_load_4d(dst, &map_b, &full[st], f, row, h, bb);
+        });
       }
       // the copies have landed: at once after a whole run, and with a limit if some role gave up
       for (int i = max(0, s - NS); i < s; ++i) mbar_wait_budget(&full[i % NS], (i / NS) & 1, kWaitBudgetCycles);
@@ -221,22 +330,28 @@ __global__ void __launch_bounds__(kLinThreads) linear_kernel(const __grid_consta
     mbar_wait_budget(done, 0, kWaitBudgetCycles);
     __syncwarp();
   } else {
-    const bool ok = mbar_wait(done, 0, abort_flag, a.status);
-    if (warp_all(ok)) {
+    const uint32_t taddr = tbase + (static_cast<uint32_t>(32 * warp) << 16);
+    auto wait = [&] {
+      const bool ok = warp_all(mbar_wait(done, 0, abort_flag, a.status));
       tc_fence_after();
+      return ok;
+    };
+    if (!TURNED) {
+      // every product has read its operands: their shared memory serves the epilogue
+      const LinWarp w = {reinterpret_cast<float4*>(smem) + 256 * warp, b, r0 + 32 * warp, c0};
+      lin_epilogue<KIND, BN>(a, w, taddr, wait, [] {});
+    } else if (wait()) {
       const int row = r0 + 32 * warp + lane;
       const bool valid = row < a.rows;
       #pragma unroll 1
       for (int c = 0; c < BN && c0 + c < a.cols; c += 32) {
         uint32_t u[32];
-        tmem_ld32(tbase + (static_cast<uint32_t>(32 * warp) << 16) + c, u);
+        tmem_ld32(taddr + c, u);
         tmem_wait_ld();
         float v[32];
         #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
-        if (!valid) continue;
-        if (TURNED) lin_finish_turned<KIND>(a, v, c0 + c, row, min(32, a.cols - c0 - c));
-        else lin_finish<KIND>(a, v, b, row, c0 + c);
+        if (valid) lin_finish_turned<KIND>(a, v, c0 + c, row, min(32, a.cols - c0 - c));
       }
     }
   }

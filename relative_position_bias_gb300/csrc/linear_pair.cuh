@@ -22,28 +22,12 @@ struct PairSmem {
   static constexpr int kA = 128 * 128, kB = BN / 2 * 128;
   static constexpr int kStage = kA + kB;
   static constexpr int NS = BN == 256 ? 6 : 8;
-  static constexpr int kBars = NS * kStage;
+  static constexpr int kEpi = NS * kStage;             // 4 KB an epilogue warp
+  static constexpr int kBars = kEpi + kPairEpi * 4096;
   static constexpr int kMisc = kBars + (2 * NS + 5) * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory");
 };
-
-// One operand's rows [r0, r0 + ROWS) of batch b for contraction step s, as in lin_load.
-template <bool MN, int ROWS>
-__device__ __forceinline__ void lin_load_pair(uint8_t* dst, const CUtensorMap* m, uint32_t bar, int d, int r0, int b, int s,
-                                              int steps_batch) {
-  if (!MN) {
-    const int f = kLinStep * s, h = d ? f / d : 0;
-    tma_load_4d_pair(dst, m, bar, f - h * d, r0, h, b);
-  } else {
-    const int bb = s / steps_batch, row = (s - bb * steps_batch) * kLinStep;
-    #pragma unroll
-    for (int j = 0; j < ROWS / 64; ++j) {
-      const int f = r0 + 64 * j, h = d ? f / d : 0;
-      tma_load_4d_pair(dst + j * 64 * 128, m, bar, f - h * d, row, h, bb);
-    }
-  }
-}
 
 // One piece of work: a tile, and for the weight's gradient a piece of its contraction.
 struct PairItem {
@@ -101,20 +85,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------- loads: each CTA its rows
+      const uint32_t full0 = cluster_map(full, 0);
       int n = 0;
       bool ok = true;
       for (int item = pair; ok && item < items; item += pairs) {
         const PairItem w(a, item, BN);
+        LinCursor<A_MN, 128> at_a(a.a_d, w.r0 + 128 * static_cast<int>(rank), w.b, w.s0, a.steps_batch);
+        LinCursor<B_MN, BN / 2> at_b(a.b_d, w.c0 + BN / 2 * static_cast<int>(rank), 0, w.s0, a.steps_batch);
         for (int s = w.s0; s < w.s1; ++s, ++n) {
           const int st = n % NS;
           ok = mbar_wait(&empty[st], ((n / NS) & 1) ^ 1, abort_flag, a.status);
           if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * SM::kStage);
-          const uint32_t bar = cluster_map(&full[st], 0);
-          lin_load_pair<A_MN, 128>(smem + st * SM::kStage, &map_a, bar, a.a_d, w.r0 + 128 * static_cast<int>(rank), w.b, s,
-                                   a.steps_batch);
-          lin_load_pair<B_MN, BN / 2>(smem + st * SM::kStage + SM::kA, &map_b, bar, a.b_d,
-                                      w.c0 + BN / 2 * static_cast<int>(rank), 0, s, a.steps_batch);
+          const uint32_t bar = full0 + 8 * st;
+          at_a.step(smem + st * SM::kStage, [&](uint8_t* dst, int f, int row, int h, int bb) {
+            tma_load_4d_pair(dst, &map_a, bar, f, row, h, bb);
+          });
+          at_b.step(smem + st * SM::kStage + SM::kA, [&](uint8_t* dst, int f, int row, int h, int bb) {
+            tma_load_4d_pair(dst, &map_b, bar, f, row, h, bb);
+          });
         }
       }
       // both CTAs' copies have landed: at once after a whole run, and with a limit if some role gave up
@@ -163,22 +152,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     constexpr int COLS = BN / 2;
     const int quarter = warp & 3, col0 = COLS * ((warp - 4) >> 2);
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+    float4* stage = reinterpret_cast<float4*>(smem + SM::kEpi) + 256 * (warp - 4);
+    const uint32_t empty0 = cluster_map(acc_empty, 0);
     int chain = 0;
     bool ok = true;
+    auto wait = [&] {
+      ok = warp_all(mbar_wait(&acc_full[chain & 1], (chain >> 1) & 1, abort_flag, a.status));
+      tc_fence_after();
+      return ok;
+    };
+    auto done = [&] {   // this warp's columns of the chain are in registers
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(empty0 + 8 * (chain & 1));
+    };
     for (int item = pair; ok && item < items; item += pairs) {
       const PairItem w(a, item, BN);
-      const int row = w.r0 + 128 * static_cast<int>(rank) + 32 * quarter + lane;
-      const bool valid = row < a.rows;
-      float acc[CHAINS ? COLS : 1];
-      for (int s = w.s0; s < w.s1; ++chain) {
-        const int buf = chain & 1;
-        const bool first = s == w.s0;
-        s = min(w.s1, CHAINS ? s + CHAIN : w.s1);
-        ok = warp_all(mbar_wait(&acc_full[buf], (chain >> 1) & 1, abort_flag, a.status));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t at = tbase + BN * buf + lanes + col0;
-        if (CHAINS) {
+      const LinWarp lw = {stage, w.b, w.r0 + 128 * static_cast<int>(rank) + 32 * quarter, w.c0 + col0};
+      if constexpr (!CHAINS) {
+        ok = lin_epilogue<KIND, COLS>(a, lw, tbase + BN * (chain & 1) + lanes + col0, wait, done);
+        ++chain;
+      } else {
+        float acc[COLS];
+        #pragma unroll
+        for (int c = 0; c < COLS; ++c) acc[c] = 0.f;
+        for (int s = w.s0; ok && s < w.s1; s += CHAIN, ++chain) {
+          if (!wait()) break;
+          const uint32_t at = tbase + BN * (chain & 1) + lanes + col0;
           #pragma unroll
           for (int c = 0; c < COLS; c += 16) {
             uint32_t u[16];
@@ -186,42 +186,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             tmem_wait_ld();
             #pragma unroll
             for (int j = 0; j < 16; ++j)
-              acc[CHAINS ? c + j : 0] = first ? __uint_as_float(u[j]) : acc[CHAINS ? c + j : 0] + __uint_as_float(u[j]);
+              acc[c + j] += __uint_as_float(u[j]);
           }
-        } else {
-          #pragma unroll 1
-          for (int c = 0; c < COLS; c += 32) {
-            uint32_t u[32];
-            tmem_ld32(at + c, u);
-            tmem_wait_ld();
-            if (c + 32 == COLS) {   // the last of this warp's columns are in registers
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(cluster_map(&acc_empty[buf], 0));
-            }
-            const int f = w.c0 + col0 + c;
-            float v[32];
-            #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
-            if (valid && f < a.cols) lin_finish<KIND>(a, v, w.b, row, f);
-          }
+          done();
         }
-        if (CHAINS) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(cluster_map(&acc_empty[buf], 0));
-        }
-      }
-      if (CHAINS && ok && valid) {
-        const size_t stride = a.cols;
-        float* part = a.parts ? a.parts + (static_cast<size_t>(w.piece) * a.rows + row) * stride : nullptr;
+        if (!ok) break;
+        void* to = a.parts ? static_cast<void*>(a.parts + static_cast<size_t>(w.piece) * a.rows * a.cols) : a.out;
+        const int fmt = a.parts ? kF32 : a.out_fmt, row = lw.row0 + (lane >> 1);
         #pragma unroll
-        for (int c = 0; c < COLS; c += 8) {
-          const int f = w.c0 + col0 + c;
-          if (f < a.cols) {
-            const float(&v)[8] = *reinterpret_cast<const float(*)[8]>(&acc[CHAINS ? c : 0]);
-            if (part) store8(part, f, v, kF32);
-            else store8(a.out, static_cast<size_t>(row) * stride + f, v, a.out_fmt);
+        for (int c = 0; c < COLS; c += 16) {
+          // as lin_turn, 16 columns at a time for want of registers: two lanes a row
+          __syncwarp();
+          #pragma unroll
+          for (int j = 0; j < 4; ++j)
+            stage[lane * 4 + (j ^ ((lane >> 1) & 3))] = make_float4(acc[c + 4 * j], acc[c + 4 * j + 1], acc[c + 4 * j + 2], acc[c + 4 * j + 3]);
+          __syncwarp();
+          const int f = lw.f0 + c + 8 * (lane & 1);
+          #pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = 16 * i + (lane >> 1), j = 2 * (lane & 1);
+            const float4 lo = stage[r * 4 + (j ^ ((r >> 1) & 3))], hi = stage[r * 4 + ((j + 1) ^ ((r >> 1) & 3))];
+            const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            if (row + 16 * i < a.rows && f < a.cols) store8(to, static_cast<size_t>(row + 16 * i) * a.cols + f, v, fmt);
           }
         }
       }
