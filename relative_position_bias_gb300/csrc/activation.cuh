@@ -7,7 +7,7 @@
 //   silu         u s(u)
 //
 // An epilogue of a product over K terms has about K / 2 issue slots an element (a tensor core takes 128 x 256 x 64 in
-// 512 cycles, four schedulers issue for 32 elements each), so Phi has to be had for a dozen instructions:
+// 512 cycles, four schedulers issue for 32 elements each), so Phi has to be had for ten instructions:
 //   Phi(-z) = exp(-z^2 / 2) t P(t),  t = 1 / (1 + 0.36 z),  z >= 0,
 // with P of degree 6 fitted to erfcx(z / sqrt 2) / 2 over [0, 14] for the smallest largest relative error (reweighted least
 // squares): 9e-7, in the tail too.  Its exponential serves the density in the derivative.
@@ -42,59 +42,93 @@ __device__ __forceinline__ float max_nan(float x, float y) {
 // would be multiplied by zero.
 constexpr float kActFar = 64.f;
 
+// Everything is on pairs: packed fp32 arithmetic takes half the issue slots.
+__device__ __forceinline__ float2 pair_of(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 fmul2(float2 x, float2 y) { return __fmul2_rn(x, y); }
+__device__ __forceinline__ float2 rcp2(float2 x) { return make_float2(rcp_approx(x.x), rcp_approx(x.y)); }
+__device__ __forceinline__ float2 exp2_2(float2 x) { return make_float2(ex2_approx(x.x), ex2_approx(x.y)); }
+
 // Phi(-z) for z >= 0; *e = exp(-z^2 / 2).
-__device__ __forceinline__ float normal_tail(float z, float* e) {
-  const float t = rcp_approx(fmaf(0.36f, z, 1.f));
-  float p = 0.0470557399f;
-  p = fmaf(p, t, -0.17976281f);
-  p = fmaf(p, t, 0.180951446f);
-  p = fmaf(p, t, 0.0265510548f);
-  p = fmaf(p, t, 0.139718652f);
-  p = fmaf(p, t, 0.141772568f);
-  p = fmaf(p, t, 0.143713042f);
-  *e = ex2_approx(-0.5f * kLog2e * (z * z));
-  return p * t * *e;
+__device__ __forceinline__ float2 normal_tail(float2 z, float2* e) {
+  const float2 t = rcp2(ffma2(pair_of(0.36f), z, pair_of(1.f)));
+  float2 p = ffma2(pair_of(0.0470557399f), t, pair_of(-0.17976281f));
+  p = ffma2(p, t, pair_of(0.180951446f));
+  p = ffma2(p, t, pair_of(0.0265510548f));
+  p = ffma2(p, t, pair_of(0.139718652f));
+  p = ffma2(p, t, pair_of(0.141772568f));
+  p = ffma2(p, t, pair_of(0.143713042f));
+  *e = exp2_2(fmul2(fmul2(z, z), pair_of(-0.5f * kLog2e)));
+  return fmul2(fmul2(p, t), *e);
 }
 
-__device__ __forceinline__ float sigmoid(float v) { return rcp_approx(1.f + ex2_approx(-kLog2e * v)); }
+// s(c v)
+__device__ __forceinline__ float2 sigmoid(float2 v, float c) {
+  return rcp2(fadd2(exp2_2(fmul2(v, pair_of(-kLog2e * c))), pair_of(1.f)));
+}
 
 constexpr float kTanhB = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kTanhC = 0.044715f;
 
 template <int ACT>
-__device__ __forceinline__ float act_of(float u) {
-  if (ACT == kActRelu) return u < 0.f ? 0.f : u;   // NaN stays
+__device__ __forceinline__ float2 act_of(float2 u) {
+  if (ACT == kActRelu) return make_float2(u.x < 0.f ? 0.f : u.x, u.y < 0.f ? 0.f : u.y);   // NaN stays
   if (ACT == kActGelu) {
-    float e;
-    const float z = min_nan(fabsf(u), kActFar);
-    return fmaf(-z, normal_tail(z, &e), fmaxf(u, 0.f));   // u - u Phi(-u) for u > 0, u Phi(u) below
+    float2 e;
+    const float2 n = make_float2(max_nan(-fabsf(u.x), -kActFar), max_nan(-fabsf(u.y), -kActFar));   // -z
+    // u - u Phi(-u) for u > 0, u Phi(u) below
+    return ffma2(n, normal_tail(make_float2(-n.x, -n.y), &e), make_float2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
   }
-  if (ACT == kActGeluTanh) return u * sigmoid(kTanhB * u * fmaf(kTanhC * u, u, 1.f));
-  if (ACT == kActQuickGelu) return u * sigmoid(1.702f * u);
-  if (ACT == kActSilu) return u * sigmoid(u);
+  if (ACT == kActGeluTanh)
+    return fmul2(u, sigmoid(fmul2(u, ffma2(fmul2(u, u), pair_of(kTanhC), pair_of(1.f))), kTanhB));
+  if (ACT == kActQuickGelu) return fmul2(u, sigmoid(u, 1.702f));
+  if (ACT == kActSilu) return fmul2(u, sigmoid(u, 1.f));
   return u;
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_slope(float u) {
-  if (ACT == kActNone) return 1.f;
-  if (ACT == kActRelu) return u > 0.f ? 1.f : 0.f;
-  const float v = max_nan(min_nan(u, kActFar), -kActFar);
+__device__ __forceinline__ float2 act_slope(float2 u) {
+  if (ACT == kActNone) return pair_of(1.f);
+  if (ACT == kActRelu) return make_float2(u.x > 0.f ? 1.f : 0.f, u.y > 0.f ? 1.f : 0.f);
+  const float2 v = make_float2(max_nan(min_nan(u.x, kActFar), -kActFar), max_nan(min_nan(u.y, kActFar), -kActFar));
   if (ACT == kActGelu) {
-    float e;
-    const float q = normal_tail(fabsf(v), &e);
-    return fmaf(v * 0.3989422804014327f, e, v < 0.f ? q : 1.f - q);   // Phi + u exp(-u^2 / 2) / sqrt(2 pi)
+    float2 e;
+    const float2 q = normal_tail(make_float2(fabsf(v.x), fabsf(v.y)), &e);
+    // Phi + u exp(-u^2 / 2) / sqrt(2 pi)
+    return ffma2(fmul2(v, pair_of(0.3989422804014327f)), e,
+                 make_float2(v.x < 0.f ? q.x : 1.f - q.x, v.y < 0.f ? q.y : 1.f - q.y));
   }
+  // s + m s (1 - s), m = u times the slope of the sigmoid's argument
+  float2 s, m;
   if (ACT == kActGeluTanh) {
-    const float s = sigmoid(kTanhB * v * fmaf(kTanhC * v, v, 1.f));
-    return fmaf(kTanhB * v * fmaf(3.f * kTanhC * v, v, 1.f), s * (1.f - s), s);
+    const float2 w = fmul2(v, v);
+    s = sigmoid(fmul2(v, ffma2(w, pair_of(kTanhC), pair_of(1.f))), kTanhB);
+    m = fmul2(fmul2(v, pair_of(kTanhB)), ffma2(w, pair_of(3.f * kTanhC), pair_of(1.f)));
+  } else {
+    constexpr float c = ACT == kActQuickGelu ? 1.702f : 1.f;
+    s = sigmoid(v, c);
+    m = fmul2(v, pair_of(c));
   }
-  if (ACT == kActQuickGelu) {
-    const float s = sigmoid(1.702f * v);
-    return fmaf(1.702f * v, s * (1.f - s), s);
+  return ffma2(fmul2(m, s), ffma2(s, pair_of(-1.f), pair_of(1.f)), s);
+}
+
+// x[i] = act(x[i]), and x[i] *= act'(u[i]), for an even number of values
+template <int ACT, int N>
+__device__ __forceinline__ void act_all(float (&x)[N]) {
+  #pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 y = act_of<ACT>(make_float2(x[i], x[i + 1]));
+    x[i] = y.x;
+    x[i + 1] = y.y;
   }
-  const float s = sigmoid(v);
-  return fmaf(v, s * (1.f - s), s);
+}
+template <int ACT, int N>
+__device__ __forceinline__ void slope_all(float (&x)[N], const float (&u)[N]) {
+  #pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 y = fmul2(make_float2(x[i], x[i + 1]), act_slope<ACT>(make_float2(u[i], u[i + 1])));
+    x[i] = y.x;
+    x[i + 1] = y.y;
+  }
 }
 
 // f.template operator()<ACT>() for the activation `act` (kActNone too): a switch outside of a loop over elements.

@@ -79,11 +79,10 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const ActArgs a) {
       float u[8], z[8];
       load8(a.pre, i, u, a.fmt);
       load8(a.dy, i, z, a.z_fmt);
-      #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] *= act_slope<ACT>(u[e]);
+      slope_all<ACT>(z, u);
       store8(a.dpre, i, z, a.out_fmt);
     } else {
-      const float z = load_elem(a.dy, i, a.z_fmt) * act_slope<ACT>(load_elem(a.pre, i, a.fmt));
+      const float z = load_elem(a.dy, i, a.z_fmt) * act_slope<ACT>(pair_of(load_elem(a.pre, i, a.fmt))).x;
       if (a.out_fmt == kF32) static_cast<float*>(a.dpre)[i] = z;
       else static_cast<uint16_t*>(a.dpre)[i] = static_cast<uint16_t>(pack_in(z, 0.f, a.out_fmt));
     }

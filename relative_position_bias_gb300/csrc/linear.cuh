@@ -95,28 +95,30 @@ struct LinWarp {
   int b, row0, f0;     // batch, first row and column
 };
 
-__device__ __forceinline__ void lin_turn(float4* stage, const float (&u)[32], float (&v)[32]) {
+__device__ __forceinline__ void lin_put(float4* stage, const uint32_t (&u)[32]) {
   const int lane = threadIdx.x & 31;
-  __syncwarp();   // the last piece has been read
   #pragma unroll
   for (int c = 0; c < 8; ++c)
-    stage[lane * 8 + (c ^ (lane & 7))] = make_float4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
-  __syncwarp();
+    reinterpret_cast<uint4*>(stage)[lane * 8 + (c ^ (lane & 7))] = make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+}
+// Eight columns of rows 16 half + lane / 4 and eight further.
+__device__ __forceinline__ void lin_get(const float4* stage, int half, float (&v)[16]) {
+  const int lane = threadIdx.x & 31;
   #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2), c = 2 * (lane & 3);
+  for (int i = 0; i < 2; ++i) {
+    const int r = 16 * half + 8 * i + (lane >> 2), c = 2 * (lane & 3);
     const float4 lo = stage[r * 8 + (c ^ (r & 7))], hi = stage[r * 8 + ((c + 1) ^ (r & 7))];
     v[8 * i] = lo.x, v[8 * i + 1] = lo.y, v[8 * i + 2] = lo.z, v[8 * i + 3] = lo.w;
     v[8 * i + 4] = hi.x, v[8 * i + 5] = hi.y, v[8 * i + 6] = hi.z, v[8 * i + 7] = hi.w;
   }
 }
 
-// Eight columns of four rows of a tensor beside D, 8 rows apart from `at` (in its own type, fp32 in two parts).
+// Eight columns of two rows of a tensor beside D, `step` elements apart, as they lie (fp32 in two parts).
 struct LinAux {
-  uint4 lo[4], hi[4];
-  __device__ __forceinline__ void load(const void* p, size_t at, long long step, int fmt, const bool (&there)[4]) {
+  uint4 lo[2], hi[2];
+  __device__ __forceinline__ void load(const void* p, size_t at, long long step, int fmt, const bool (&there)[2]) {
     #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       lo[i] = hi[i] = make_uint4(0u, 0u, 0u, 0u);
       if (!there[i]) continue;
       const char* q = static_cast<const char*>(p) + (at + i * step) * (fmt == kF32 ? 4 : 2);
@@ -124,12 +126,18 @@ struct LinAux {
       if (fmt == kF32) hi[i] = *reinterpret_cast<const uint4*>(q + 16);
     }
   }
-  __device__ __forceinline__ void get(int i, float (&x)[8], int fmt) const {
-    if (fmt == kF32) {
-      x[0] = __uint_as_float(lo[i].x), x[1] = __uint_as_float(lo[i].y), x[2] = __uint_as_float(lo[i].z), x[3] = __uint_as_float(lo[i].w);
-      x[4] = __uint_as_float(hi[i].x), x[5] = __uint_as_float(hi[i].y), x[6] = __uint_as_float(hi[i].z), x[7] = __uint_as_float(hi[i].w);
-    } else {
-      unpack8(lo[i], x, fmt);
+  __device__ __forceinline__ void get(float (&x)[16], int fmt) const {
+    #pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float y[8];
+      if (fmt == kF32) {
+        y[0] = __uint_as_float(lo[i].x), y[1] = __uint_as_float(lo[i].y), y[2] = __uint_as_float(lo[i].z), y[3] = __uint_as_float(lo[i].w);
+        y[4] = __uint_as_float(hi[i].x), y[5] = __uint_as_float(hi[i].y), y[6] = __uint_as_float(hi[i].z), y[7] = __uint_as_float(hi[i].w);
+      } else {
+        unpack8(lo[i], y, fmt);
+      }
+      #pragma unroll
+      for (int e = 0; e < 8; ++e) x[8 * i + e] = y[e];
     }
   }
 };
@@ -138,19 +146,26 @@ struct LinAux {
 template <int KIND, int COLS, class Wait, class Done>
 __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, const LinWarp& w, uint32_t taddr, Wait&& wait, Done&& done) {
   const int lane = threadIdx.x & 31, row = w.row0 + (lane >> 2), col = 8 * (lane & 3);
-  bool there[4];
-  LinAux x;
   const size_t out_row = static_cast<size_t>(w.b * a.out_at.sb + row * a.out_at.sn);
   const size_t aux_row = static_cast<size_t>(w.b * a.aux_at.sb + row * a.aux_at.sn);
+  const long long out_step = 8 * a.out_at.sn, aux_step = 8 * a.aux_at.sn;
   auto at = [&](const LinView& v, int f) {   // offset of feature f
     const int h = v.d ? f / v.d : 0;
     return h * v.sh + (f - h * v.d);
   };
-  auto begin = [&](int c) {   // what of piece c is inside, and the loads beside it
+  float bias[8];
+  LinAux x;
+  auto begin = [&](int c) {   // the loads beside the first half of piece c
     const int f = w.f0 + c + col;
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) there[i] = row + 8 * i < a.rows && f < a.cols;
-    if (a.aux) x.load(a.aux, aux_row + at(a.aux_at, f), 8 * a.aux_at.sn, a.aux_fmt, there);
+    if (KIND == kLinForward) {
+      #pragma unroll
+      for (int e = 0; e < 8; ++e) bias[e] = 0.f;
+      if (a.bias && f < a.cols) load8(a.bias, f, bias, a.bias_fmt);
+    }
+    if (a.aux) {
+      const bool there[2] = {f < a.cols && row < a.rows, f < a.cols && row + 8 < a.rows};
+      x.load(a.aux, aux_row + at(a.aux_at, f), aux_step, a.aux_fmt, there);
+    }
   };
   begin(0);
   if (!wait()) return false;
@@ -158,64 +173,47 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, const LinWarp& w,
   for (int c = 0; c < COLS; c += 32) {
     uint32_t u[32];
     tmem_ld32(taddr + c, u);
+    if (c > 0) begin(c);
     tmem_wait_ld();
+    __syncwarp();   // the last piece has been read from the stage
+    lin_put(w.stage, u);
     if (c + 32 == COLS) done();
-    float v[32];
-    {
-      float t[32];
-      #pragma unroll
-      for (int j = 0; j < 32; ++j) t[j] = __uint_as_float(u[j]);
-      lin_turn(w.stage, t, v);
-    }
+    __syncwarp();
     const int f = w.f0 + c + col;
+    const bool in = f < a.cols;
     const size_t to = out_row + at(a.out_at, f);
-    const long long step = 8 * a.out_at.sn;
-    if (KIND == kLinForward) {
-      if (a.bias && f < a.cols) {
-        float y[8];
-        load8(a.bias, f, y, a.bias_fmt);
+    #pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const bool there[2] = {in && row + 16 * half < a.rows, in && row + 16 * half + 8 < a.rows};
+      if (half == 1 && a.aux) x.load(a.aux, aux_row + at(a.aux_at, f) + 2 * aux_step, aux_step, a.aux_fmt, there);
+      float v[16];
+      lin_get(w.stage, half, v);
+      const float(&v0)[8] = *reinterpret_cast<const float(*)[8]>(&v[0]);
+      const float(&v1)[8] = *reinterpret_cast<const float(*)[8]>(&v[8]);
+      const size_t i0 = to + 2 * half * out_step, i1 = i0 + out_step;
+      if (KIND == kLinForward) {
         #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 16; ++j) v[j] += bias[j & 7];
+        if (a.pre) {
+          if (there[0]) store8(a.pre, i0, v0, a.fmt);
+          if (there[1]) store8(a.pre, i1, v1, a.fmt);
+        }
+        if (a.act != kActNone) with_act(a.act, [&](auto A) { act_all<decltype(A)::value>(v); });
+        if (a.aux) {
+          float y[16];
+          x.get(y, a.aux_fmt);
           #pragma unroll
-          for (int e = 0; e < 8; ++e) v[8 * i + e] += y[e];
-      }
-      if (a.pre) {
-        #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (there[i]) store8(a.pre, to + i * step, *reinterpret_cast<const float(*)[8]>(&v[8 * i]), a.fmt);
-      }
-      if (a.act != kActNone)
-        with_act(a.act, [&](auto A) {
-          #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = act_of<decltype(A)::value>(v[j]);
-        });
-      if (a.aux) {
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float y[8];
-          x.get(i, y, a.aux_fmt);
-          #pragma unroll
-          for (int e = 0; e < 8; ++e) v[8 * i + e] += y[e];
+          for (int j = 0; j < 16; ++j) v[j] += y[j];
         }
       }
+      if (KIND == kLinInput && a.aux) {
+        float y[16];
+        x.get(y, a.aux_fmt);
+        with_act(a.act, [&](auto A) { slope_all<decltype(A)::value>(v, y); });
+      }
+      if (there[0]) store8(a.out, i0, v0, a.out_fmt);
+      if (there[1]) store8(a.out, i1, v1, a.out_fmt);
     }
-    if (KIND == kLinInput && a.aux)
-      with_act(a.act, [&](auto A) {
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float y[8];
-          x.get(i, y, a.aux_fmt);
-          #pragma unroll
-          for (int e = 0; e < 8; ++e) v[8 * i + e] *= act_slope<decltype(A)::value>(y[e]);
-        }
-      });
-    bool now[4];
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) now[i] = there[i];
-    if (c + 32 < COLS) begin(c + 32);
-    #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (now[i]) store8(a.out, to + i * step, *reinterpret_cast<const float(*)[8]>(&v[8 * i]), a.out_fmt);
   }
   return true;
 }
@@ -234,8 +232,7 @@ __device__ __forceinline__ void lin_finish_turned(const LinArgs& a, float (&v)[3
     }
     if (a.act != kActNone)
       with_act(a.act, [&](auto A) {
-        #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = act_of<decltype(A)::value>(v[j]);
+        act_all<decltype(A)::value>(v);
       });
     if (a.aux) {
       #pragma unroll
@@ -248,8 +245,7 @@ __device__ __forceinline__ void lin_finish_turned(const LinArgs& a, float (&v)[3
     #pragma unroll
     for (int j = 0; j < 32; ++j) x[j] = j < count ? load_elem(a.aux, lin_at(a.aux_at, 0, n + j, f), a.aux_fmt) : 0.f;
     with_act(a.act, [&](auto A) {
-      #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] *= act_slope<decltype(A)::value>(x[j]);
+      slope_all<decltype(A)::value>(v, x);
     });
   }
   #pragma unroll

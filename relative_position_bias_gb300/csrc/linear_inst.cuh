@@ -20,9 +20,9 @@ template <int KIND, int BN, bool BF16>
 static cudaError_t launch_lin_pair(const LinMaps& m, const LinArgs& a, int pairs, cudaStream_t s) {
   auto kernel = linear_pair_kernel<KIND, BN, BF16>;
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = prepare_kernel(kernel, PairSmem<BN>::kAlloc, 0, done);
+  cudaError_t e = prepare_kernel(kernel, PairSmem<KIND, BN>::kAlloc, 0, done);
   if (e != cudaSuccess) return e;
-  kernel<<<2 * pairs, kPairThreads, PairSmem<BN>::kAlloc, s>>>(m.a, m.b, a);
+  kernel<<<2 * pairs, pair_threads(KIND), PairSmem<KIND, BN>::kAlloc, s>>>(m.a, m.b, a);
   return cudaGetLastError();
 }
 

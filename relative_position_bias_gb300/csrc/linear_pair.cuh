@@ -13,17 +13,19 @@
 
 namespace dera {
 
-constexpr int kPairThreads = 384;   // a warp that loads, one that multiplies, two that wait, eight of the epilogue
-constexpr int kPairEpi = 8;
+// A warp that loads, one that multiplies, two that wait, and the epilogue's: sixteen, four a scheduler, since a warp alone
+// issues in a sixth of its cycles; eight for the weight's gradient, which keeps 128 columns of sums a thread.
+constexpr int pair_epi(int kind) { return kind == kLinWeight ? 8 : 16; }
+constexpr int pair_threads(int kind) { return 128 + 32 * pair_epi(kind); }
 constexpr int kLinChain = 64;
 
-template <int BN>
+template <int KIND, int BN>
 struct PairSmem {
   static constexpr int kA = 128 * 128, kB = BN / 2 * 128;
   static constexpr int kStage = kA + kB;
-  static constexpr int NS = BN == 256 ? 6 : 8;
+  static constexpr int NS = BN == 256 ? (KIND == kLinWeight ? 6 : 5) : 6;
   static constexpr int kEpi = NS * kStage;             // 4 KB an epilogue warp
-  static constexpr int kBars = kEpi + kPairEpi * 4096;
+  static constexpr int kBars = kEpi + pair_epi(KIND) * 4096;
   static constexpr int kMisc = kBars + (2 * NS + 5) * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory");
@@ -45,10 +47,10 @@ struct PairItem {
 };
 
 template <int KIND, int BN, bool BF16>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                        const __grid_constant__ LinArgs a) {
-  using SM = PairSmem<BN>;
+  using SM = PairSmem<KIND, BN>;
   constexpr int NS = SM::NS;
   constexpr bool A_MN = KIND == kLinWeight, B_MN = KIND != kLinForward;
   constexpr bool CHAINS = KIND == kLinWeight;
@@ -70,7 +72,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < 2 * NS + 2; ++i) mbar_init(&full[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&acc_empty[i], 2 * kPairEpi);
+    for (int i = 0; i < 2; ++i) mbar_init(&acc_empty[i], 2 * pair_epi(KIND));
     mbar_init(all_done, 1);
     fence_mbar_init();
   }
@@ -148,8 +150,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       __syncwarp();
     }
   } else if (warp >= 4) {
-    // --------------------------------------------------------------- epilogue: a warp 32 rows of half of the columns
-    constexpr int COLS = BN / 2;
+    // --------------------------------------------------------------- epilogue: a warp 32 rows of its columns
+    constexpr int COLS = BN / (pair_epi(KIND) / 4);
     const int quarter = warp & 3, col0 = COLS * ((warp - 4) >> 2);
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     float4* stage = reinterpret_cast<float4*>(smem + SM::kEpi) + 256 * (warp - 4);
@@ -164,7 +166,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     auto done = [&] {   // this warp's columns of the chain are in registers
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(empty0 + 8 * (chain & 1));
+      if (lane == 0) mbar_arrive_cluster_relaxed(empty0 + 8 * (chain & 1));
     };
     for (int item = pair; ok && item < items; item += pairs) {
       const PairItem w(a, item, BN);
@@ -195,7 +197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int fmt = a.parts ? kF32 : a.out_fmt, row = lw.row0 + (lane >> 1);
         #pragma unroll
         for (int c = 0; c < COLS; c += 16) {
-          // as lin_turn, 16 columns at a time for want of registers: two lanes a row
+          // as lin_put and lin_get, 16 columns at a time for want of registers: two lanes a row
           __syncwarp();
           #pragma unroll
           for (int j = 0; j < 4; ++j)
