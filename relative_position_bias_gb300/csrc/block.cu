@@ -44,7 +44,9 @@ dera_status check_ptrs(std::initializer_list<Ptr> ptrs, int dev) {
 }
 
 size_t ln_workspace(int rows, int cols, int sms) {
-  return align256(static_cast<size_t>(ln_plan(rows, cols, true, sms).grid) * 2 * cols * sizeof(float));
+  // by either plan: whether rows are whole 16-byte chunks is for the call to say
+  const int grid = std::max(ln_plan(rows, cols, true, true, sms).grid, ln_plan(rows, cols, true, false, sms).grid);
+  return align256(static_cast<size_t>(grid) * 2 * cols * sizeof(float));
 }
 
 // ---------------------------------------------------------------------------------------- linear
@@ -215,8 +217,11 @@ dera_status dera_layer_norm(const void* x, const void* weight, const void* bias,
   a.x_fmt = fmt_of(in_dtype);
   a.w_fmt = fmt_of(weight_dtype);
   a.y_fmt = fmt_of(out_dtype);
+  a.status = status_ptr(dev);
+  if (!a.status) return DERA_ERR_CUDA;
   const bool vec = cols % 8 == 0 && a.xs % 8 == 0 && aligned(x, 16) && aligned(y, 16);
-  return status_of(launch_ln(a, ln_plan(rows, cols, false, sm_count(dev)), vec, static_cast<cudaStream_t>(stream)));
+  const int sms = sm_count(dev);
+  return status_of(launch_ln(a, ln_plan(rows, cols, false, vec, sms), vec, sms, static_cast<cudaStream_t>(stream)));
 }
 
 dera_status dera_layer_norm_backward_workspace_size(int rows, int cols, size_t* bytes) {
@@ -275,8 +280,10 @@ dera_status dera_layer_norm_backward(const void* dy, const void* x, const float*
   a.w_fmt = fmt_of(weight_dtype);
   a.y_fmt = fmt_of(dout_dtype);
   a.dx_fmt = fmt_of(grad_dtype);
+  a.status = status_ptr(dev);
+  if (!a.status) return DERA_ERR_CUDA;
   const bool vec = cols % 8 == 0 && a.xs % 8 == 0 && aligned(x, 16) && aligned(dy, 16) && aligned(dres, 16) && aligned(dx, 16);
-  return status_of(launch_ln_backward(a, ln_plan(rows, cols, true, sms), vec, dweight, dbias, s));
+  return status_of(launch_ln_backward(a, ln_plan(rows, cols, true, vec, sms), vec, dweight, dbias, s));
 }
 
 dera_status dera_linear_workspace_size(int B, int N, int heads, int head_dim, int out_features, size_t* bytes) {

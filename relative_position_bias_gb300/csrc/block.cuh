@@ -29,15 +29,17 @@ struct LnArgs {
   long long rows, xs;
   float eps;
   int C, tpr;             // tpr: threads a row
+  int sets;               // sets of rows in the ring
+  int* status;
   int x_fmt, w_fmt, y_fmt, dx_fmt;   // y_fmt: dy's too
 };
 
 // How a layer norm's rows are cut.
 struct LnPlan {
-  int threads, tpr, grid;
+  int threads, tpr, grid, blocks;   // blocks: of an SM
 };
-LnPlan ln_plan(long long rows, int C, bool backward, int sms);
-cudaError_t launch_ln(LnArgs& a, const LnPlan& p, bool vec, cudaStream_t s);
+LnPlan ln_plan(long long rows, int C, bool backward, bool vec, int sms);
+cudaError_t launch_ln(LnArgs& a, const LnPlan& p, bool vec, int sms, cudaStream_t s);
 cudaError_t launch_ln_backward(LnArgs& a, const LnPlan& p, bool vec, float* dw, float* db, cudaStream_t s);
 // d1[c], d2[c]: the first n1 and the other columns of `rows` partial rows of n, summed
 cudaError_t launch_partial_rows(const float* parts, int rows, int n, int n1, float* d1, float* d2, cudaStream_t s);
