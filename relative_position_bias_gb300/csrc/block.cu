@@ -120,7 +120,13 @@ bool cut(LinArgs* a, const LinPlan& p, int batches, int rows, int cols) {
   a->cols = cols;
   a->m_tiles = ceil_div(rows, p.pairs ? 256 : 128);
   a->n_tiles = ceil_div(cols, p.bn);
-  return static_cast<double>(batches) * a->m_tiles * a->n_tiles * a->pieces < 2147483647.0;
+  if (static_cast<double>(batches) * a->m_tiles * a->n_tiles * a->pieces >= 2147483647.0) return false;
+  int far = p.pairs;
+  a->by_piece = far % a->pieces;
+  a->by_n = (far /= a->pieces) % a->n_tiles;
+  a->by_m = (far /= a->n_tiles) % a->m_tiles;
+  a->by_b = far / a->m_tiles;
+  return true;
 }
 
 // How D of tokens (rows) by features is cut.

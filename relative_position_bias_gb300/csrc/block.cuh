@@ -81,6 +81,7 @@ struct LinArgs {
   int batches, m_tiles, n_tiles;   // m_tiles: of one batch
   int steps, steps_batch;          // contraction steps of 64, and those of one batch where it runs over tokens
   int pieces, piece_steps;         // kLinWeight: pieces of the contraction, each of so many steps (the last fewer)
+  int by_piece, by_n, by_m, by_b;  // how far a pair's next tile is, as digits of (batch, m, n, piece)
   int act, fmt, bias_fmt, aux_fmt, out_fmt;
 };
 

@@ -34,16 +34,14 @@ struct LinCursor {
   int d, steps_batch;
   int b, h, f, row, left;   // of the next step: batch, head and feature in it, row; steps left in the batch
   int fj[ROWS >= 64 ? ROWS / 64 : 1], hj[ROWS >= 64 ? ROWS / 64 : 1];   // MN: features and heads of the 64-column blocks
-  // d: features a head (0: one head); batch: of a K-major operand
+  // d: features a head (0: one head); batch: of a K-major operand, whose steps begin at 0
   __device__ __forceinline__ LinCursor(int d_, int r0, int batch, int s, int steps_batch_) : d(d_), steps_batch(steps_batch_) {
     if (!MN) {
-      f = kLinStep * s;
-      h = d ? f / d : 0;
-      f -= h * d;
+      f = h = 0;
       row = r0;
       b = batch;
     } else {
-      b = s / steps_batch;
+      b = s > 0 ? s / steps_batch : 0;
       left = steps_batch - (s - b * steps_batch);
       row = (s - b * steps_batch) * kLinStep;
       #pragma unroll
@@ -182,7 +180,7 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, const LinWarp& w,
     const int f = w.f0 + c + col;
     const bool in = f < a.cols;
     const size_t to = out_row + at(a.out_at, f);
-    #pragma unroll
+    #pragma unroll 1   // a kernel's first tile waits for its code as well
     for (int half = 0; half < 2; ++half) {
       const bool there[2] = {in && row + 16 * half < a.rows, in && row + 16 * half + 8 < a.rows};
       if (half == 1 && a.aux) x.load(a.aux, aux_row + at(a.aux_at, f) + 2 * aux_step, aux_step, a.aux_fmt, there);
@@ -272,6 +270,10 @@ __global__ void __launch_bounds__(kLinThreads) linear_kernel(const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile = blockIdx.x, mt = tile / a.n_tiles, b = mt / a.m_tiles;
   const int r0 = (mt - b * a.m_tiles) * 128, c0 = (tile - mt * a.n_tiles) * BN;
+  if (threadIdx.x == 128) {
+    tma_prefetch_desc(&map_a);
+    tma_prefetch_desc(&map_b);
+  }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < 2 * NS + 1; ++i) mbar_init(&full[i], 1);

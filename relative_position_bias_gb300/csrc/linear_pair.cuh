@@ -31,19 +31,44 @@ struct PairSmem {
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
-// One piece of work: a tile, and for the weight's gradient a piece of its contraction.
+// One piece of work: a tile, and for the weight's gradient a piece of its contraction.  A pair's pieces are `pairs` apart;
+// it goes from one to the next by digits (a division here stalls the pipeline: three took as long as a step's products).
+template <int BN>
 struct PairItem {
-  int b, r0, c0, piece, s0, s1;
-  __device__ __forceinline__ PairItem(const LinArgs& a, int item, int bn) {
+  int mt, nt, piece, b;
+  bool any;
+  __device__ __forceinline__ PairItem(const LinArgs& a, int item, int items) {
+    any = item < items;
     const int tile = item / a.pieces;
     piece = item - tile * a.pieces;
-    const int mt = tile / a.n_tiles;
-    b = mt / a.m_tiles;
-    r0 = (mt - b * a.m_tiles) * 256;
-    c0 = (tile - mt * a.n_tiles) * bn;
-    s0 = piece * a.piece_steps;
-    s1 = min(s0 + a.piece_steps, a.steps);
+    const int m = tile / a.n_tiles;
+    nt = tile - m * a.n_tiles;
+    b = m / a.m_tiles;
+    mt = m - b * a.m_tiles;
   }
+  __device__ __forceinline__ void next(const LinArgs& a) {
+    piece += a.by_piece;
+    nt += a.by_n;
+    mt += a.by_m;
+    b += a.by_b;
+    if (piece >= a.pieces) {
+      piece -= a.pieces;
+      ++nt;
+    }
+    if (nt >= a.n_tiles) {
+      nt -= a.n_tiles;
+      ++mt;
+    }
+    if (mt >= a.m_tiles) {
+      mt -= a.m_tiles;
+      ++b;
+    }
+    any = b < a.batches;
+  }
+  __device__ __forceinline__ int r0() const { return mt * 256; }
+  __device__ __forceinline__ int c0() const { return nt * BN; }
+  __device__ __forceinline__ int s0(const LinArgs& a) const { return piece * a.piece_steps; }
+  __device__ __forceinline__ int s1(const LinArgs& a) const { return min((piece + 1) * a.piece_steps, a.steps); }
 };
 
 template <int KIND, int BN, bool BF16>
@@ -67,8 +92,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::kMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int items = a.batches * a.m_tiles * a.n_tiles * a.pieces;
+  PairItem<BN> w(a, blockIdx.x >> 1, a.batches * a.m_tiles * a.n_tiles * a.pieces);
+  if (threadIdx.x == 64) {
+    tma_prefetch_desc(&map_a);
+    tma_prefetch_desc(&map_b);
+  }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < 2 * NS + 2; ++i) mbar_init(&full[i], 1);
@@ -90,11 +118,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
       const uint32_t full0 = cluster_map(full, 0);
       int n = 0;
       bool ok = true;
-      for (int item = pair; ok && item < items; item += pairs) {
-        const PairItem w(a, item, BN);
-        LinCursor<A_MN, 128> at_a(a.a_d, w.r0 + 128 * static_cast<int>(rank), w.b, w.s0, a.steps_batch);
-        LinCursor<B_MN, BN / 2> at_b(a.b_d, w.c0 + BN / 2 * static_cast<int>(rank), 0, w.s0, a.steps_batch);
-        for (int s = w.s0; s < w.s1; ++s, ++n) {
+      for (; ok && w.any; w.next(a)) {
+        const int s0 = w.s0(a), s1 = w.s1(a);
+        LinCursor<A_MN, 128> at_a(a.a_d, w.r0() + 128 * static_cast<int>(rank), w.b, s0, a.steps_batch);
+        LinCursor<B_MN, BN / 2> at_b(a.b_d, w.c0() + BN / 2 * static_cast<int>(rank), 0, s0, a.steps_batch);
+        for (int s = s0; s < s1; ++s, ++n) {
           const int st = n % NS;
           ok = mbar_wait(&empty[st], ((n / NS) & 1) ^ 1, abort_flag, a.status);
           if (!ok) break;
@@ -123,10 +151,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
       const uint64_t db = sdesc_sw128(smem_u32(smem) + SM::kA, B_MN ? 8192 : 16, 1024);
       int n = 0, chain = 0;
       bool ok = true;
-      for (int item = pair; ok && item < items; item += pairs) {
-        const PairItem w(a, item, BN);
-        for (int s = w.s0; ok && s < w.s1; ++chain) {
-          const int end = min(w.s1, CHAINS ? s + CHAIN : w.s1), buf = chain & 1;
+      for (; ok && w.any; w.next(a)) {
+        const int s1 = w.s1(a);
+        for (int s = w.s0(a); ok && s < s1; ++chain) {
+          const int end = min(s1, CHAINS ? s + CHAIN : s1), buf = chain & 1;
           ok = warp_all(mbar_wait(&acc_empty[buf], ((chain >> 1) & 1) ^ 1, abort_flag, a.status));
           if (!ok) break;
           tc_fence_after();
@@ -168,9 +196,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster_relaxed(empty0 + 8 * (chain & 1));
     };
-    for (int item = pair; ok && item < items; item += pairs) {
-      const PairItem w(a, item, BN);
-      const LinWarp lw = {stage, w.b, w.r0 + 128 * static_cast<int>(rank) + 32 * quarter, w.c0 + col0};
+    for (; ok && w.any; w.next(a)) {
+      const LinWarp lw = {stage, w.b, w.r0() + 128 * static_cast<int>(rank) + 32 * quarter, w.c0() + col0};
       if constexpr (!CHAINS) {
         ok = lin_epilogue<KIND, COLS>(a, lw, tbase + BN * (chain & 1) + lanes + col0, wait, done);
         ++chain;
@@ -178,7 +205,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
         float acc[COLS];
         #pragma unroll
         for (int c = 0; c < COLS; ++c) acc[c] = 0.f;
-        for (int s = w.s0; ok && s < w.s1; s += CHAIN, ++chain) {
+        const int s0 = w.s0(a), s1 = w.s1(a);
+        for (int s = s0; ok && s < s1; s += CHAIN, ++chain) {
           if (!wait()) break;
           const uint32_t at = tbase + BN * (chain & 1) + lanes + col0;
           #pragma unroll
@@ -217,7 +245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
   }
   __syncwarp();
   tc_fence_before();
-  cluster_sync_all();
+  cluster_sync_all_relaxed();
   if (warp == 1) tmem_dealloc_pair(tbase, 2 * BN);
 }
 
