@@ -118,7 +118,9 @@ bool cut(LinArgs* a, const LinPlan& p, int batches, int rows, int cols) {
   a->batches = batches;
   a->rows = rows;
   a->cols = cols;
-  a->m_tiles = ceil_div(rows, p.pairs ? 256 : 128);
+  a->pieces = p.pieces;
+  a->piece_steps = p.piece_steps;
+  a->m_tiles = ceil_div(rows, p.turned ? 128 : 256);
   a->n_tiles = ceil_div(cols, p.bn);
   if (static_cast<double>(batches) * a->m_tiles * a->n_tiles * a->pieces >= 2147483647.0) return false;
   int far = p.pairs;
@@ -129,21 +131,28 @@ bool cut(LinArgs* a, const LinPlan& p, int batches, int rows, int cols) {
   return true;
 }
 
-// How D of tokens (rows) by features is cut.
-LinPlan token_plan(const Tokens& tok, int features, int sms) {
+// How D of tokens (rows) by features is cut, `steps` steps long.
+LinPlan token_plan(const Tokens& tok, int features, int steps, int sms) {
   LinPlan p = {};
+  p.pieces = 1;
+  p.piece_steps = steps;
   if (tok.merged && tok.N <= 128) {
     p.turned = true;
     p.bn = turned_columns(tok.N);
+    // the largest cluster that leaves every CTA two steps or more, and no more CTAs than there are SMs
+    const int tiles = ceil_div(features, 128);
+    while (p.pieces < 8 && 4 * p.pieces <= steps && 2 * p.pieces * tiles <= sms) p.pieces *= 2;
     return p;
   }
-  const int pairs = sms / 2;
+  const int pairs = std::max(1, sms / 2);
   const double m = static_cast<double>(tok.B) * ceil_div(tok.N, 256);
   const double wide = m * ceil_div(features, 256), narrow = m * ceil_div(features, 128);
-  p.bn = 128;
-  if (narrow < pairs || pairs < 1) return p;   // not a tile for every pair: one CTA a tile
-  // waves of tiles, the narrow ones a little over half the time
-  if (std::ceil(wide / pairs) <= 0.55 * std::ceil(narrow / pairs)) p.bn = 256;
+  // Time in us by tiles of 256 x 256 and of 256 x 128, fitted to sizes between 196 x 768 x 768 and 9728 x 4096 x 2048: start, end and
+  // first loads, and for every wave its steps, or its epilogue where that takes longer.  A narrow tile's step takes not half but
+  // 0.85 of a wide one's (the loads of a step are 3/4).
+  const double t_wide = 7 + std::ceil(wide / pairs) * std::max(0.27 * steps, 3.0);
+  const double t_narrow = 5.3 + std::ceil(narrow / pairs) * std::max(0.23 * steps, 2.4);
+  p.bn = t_wide <= t_narrow ? 256 : 128;
   p.pairs = static_cast<int>(std::min<double>(pairs, p.bn == 256 ? wide : narrow));
   return p;
 }
@@ -151,7 +160,6 @@ LinPlan token_plan(const Tokens& tok, int features, int sms) {
 // How dW = [out, K] is cut: tiles and pieces of the contraction over `steps` steps.
 struct WeightPlan {
   LinPlan p;
-  int pieces, piece_steps;
   size_t bytes;   // of the pieces
 };
 WeightPlan weight_plan(int out, int K, int steps, int sms) {
@@ -169,11 +177,11 @@ WeightPlan weight_plan(int out, int K, int steps, int sms) {
     }
   }
   WeightPlan w = {};
-  w.piece_steps = ceil_div(steps, pieces);
-  w.pieces = ceil_div(steps, w.piece_steps);
+  w.p.piece_steps = ceil_div(steps, pieces);
+  w.p.pieces = ceil_div(steps, w.p.piece_steps);
   w.p.bn = 256;
-  w.p.pairs = static_cast<int>(std::min<double>(pairs, tiles * w.pieces));
-  w.bytes = w.pieces > 1 ? align256(static_cast<size_t>(w.pieces) * out * K * sizeof(float)) : 0;
+  w.p.pairs = static_cast<int>(std::min<double>(pairs, tiles * w.p.pieces));
+  w.bytes = w.p.pieces > 1 ? align256(static_cast<size_t>(w.p.pieces) * out * K * sizeof(float)) : 0;
   return w;
 }
 
@@ -336,16 +344,14 @@ dera_status dera_linear(const dera_heads* x, const void* weight, const void* bia
   a.fmt = fmt_of(in_dtype);
   a.bias_fmt = fmt_of(bias_dtype);
   a.aux_fmt = a.out_fmt = fmt_of(out_dtype);
-  const LinPlan p = token_plan(tok, out_features, sm_count(dev));
-  a.pieces = 1;
-  a.piece_steps = a.steps;
+  const LinPlan p = token_plan(tok, out_features, a.steps, sm_count(dev));
   if (!(p.turned ? cut(&a, p, 1, out_features, tok.N) : cut(&a, p, tok.B, tok.N, out_features))) return DERA_ERR_SHAPE;
   LinMaps m;
   const HeadsPtr xm = tok.of(xt, N), wm = rows_of(weight, out_features, K);
   CUtensorMap *mx = p.turned ? &m.b : &m.a, *mw = p.turned ? &m.a : &m.b;
   (p.turned ? a.b_d : a.a_d) = heads > 1 ? head_dim : 0;
   if (!map_tokens(mx, xm, in_dtype, tok.B, tok.N, heads, head_dim, p.turned ? p.bn : 128) ||
-      !map_tokens(mw, wm, in_dtype, 1, out_features, 1, K, p.turned ? 128 : (p.pairs ? p.bn / 2 : p.bn)))
+      !map_tokens(mw, wm, in_dtype, 1, out_features, 1, K, p.turned ? 128 : p.bn / 2))
     return DERA_ERR_CUDA;
   return status_of(launch_linear_forward(m, a, p, static_cast<cudaStream_t>(stream)));
 }
@@ -420,9 +426,7 @@ dera_status dera_linear_backward(const void* dy, const dera_heads* x, const void
     a.act = input_activation;
     a.fmt = a.aux_fmt = fmt_of(in_dtype);
     a.out_fmt = fmt_of(grad_dtype);
-    a.pieces = 1;
-    a.piece_steps = a.steps;
-    const LinPlan p = token_plan(tok, K, sms);
+    const LinPlan p = token_plan(tok, K, a.steps, sms);
     LinMaps m;
     CUtensorMap *mg = p.turned ? &m.b : &m.a, *mw = p.turned ? &m.a : &m.b;
     if (!(p.turned ? cut(&a, p, 1, K, tok.N) : cut(&a, p, tok.B, tok.N, K))) return DERA_ERR_SHAPE;
@@ -446,17 +450,15 @@ dera_status dera_linear_backward(const void* dy, const dera_heads* x, const void
     a.fmt = fmt_of(in_dtype);
     a.out_fmt = fmt_of(weight_grad_dtype);
     const WeightPlan w = weight_plan(out_features, K, a.steps, sms);
-    a.pieces = w.pieces;
-    a.piece_steps = w.piece_steps;
     if (!cut(&a, w.p, 1, out_features, K)) return DERA_ERR_SHAPE;
-    if (w.pieces > 1) a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums_bytes(out_features, sms));
+    if (w.p.pieces > 1) a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums_bytes(out_features, sms));
     LinMaps m;
     if (!map_tokens(&m.a, tok.of(gt, N), in_dtype, tok.B, tok.N, 1, out_features, 64) ||
         !map_tokens(&m.b, tok.of(xt, N), in_dtype, tok.B, tok.N, h, d, 64))
       return DERA_ERR_CUDA;
     DERA_TRY(status_of(launch_linear_weight(m, a, w.p, s)));
-    if (w.pieces > 1)
-      DERA_TRY(status_of(launch_sum_pieces(a.parts, w.pieces, static_cast<long long>(out_features) * K, dweight, a.out_fmt, s)));
+    if (w.p.pieces > 1)
+      DERA_TRY(status_of(launch_sum_pieces(a.parts, w.p.pieces, static_cast<long long>(out_features) * K, dweight, a.out_fmt, s)));
   }
   if (dbias) {
     float* parts = static_cast<float*>(workspace);

@@ -80,7 +80,8 @@ struct LinArgs {
   int rows, cols;        // of D: rows of one batch, and columns
   int batches, m_tiles, n_tiles;   // m_tiles: of one batch
   int steps, steps_batch;          // contraction steps of 64, and those of one batch where it runs over tokens
-  int pieces, piece_steps;         // kLinWeight: pieces of the contraction, each of so many steps (the last fewer)
+  int pieces;                      // kLinWeight, turned: pieces of the contraction
+  int piece_steps;                 // kLinWeight: steps of a piece (the last may have fewer)
   int by_piece, by_n, by_m, by_b;  // how far a pair's next tile is, as digits of (batch, m, n, piece)
   int act, fmt, bias_fmt, aux_fmt, out_fmt;
 };
@@ -92,7 +93,8 @@ struct LinMaps {
 struct LinPlan {
   int bn;                // columns of a tile
   bool turned;
-  int pairs;             // pairs of CTAs that share tiles of 256 rows (0: one CTA a tile of 128)
+  int pairs;             // pairs of CTAs that share tiles of 256 rows (0: turned)
+  int pieces, piece_steps;
 };
 // out[i] = the sum of `pieces` arrays of n values, in order
 cudaError_t launch_sum_pieces(const float* parts, int pieces, long long n, void* out, int out_fmt, cudaStream_t s);

@@ -2,7 +2,7 @@
 //
 //   y = act(x W^T + bias) + residual,   dx = (dy W) * slope(input_pre),   dW = dy^T x
 //
-// D = A B^T in tiles of 128 x BN.  Each operand is read by TMA from where it lies, in boxes of 64 elements (one 128-byte
+// D = A B^T in tiles.  Each operand is read by TMA from where it lies, in boxes of 64 elements (one 128-byte
 // swizzle atom) by its rows: K-major where the contraction is its contiguous dimension, else M- or N-major, so
 // nothing is transposed on the way.  Tokens are addressed as (batch, token, head, element): the attention's output is read from
 // its heads, and a gradient written to them.  What lies past an edge reads as zero.
@@ -20,7 +20,7 @@ template <int BN>
 struct LinSmem {
   static constexpr int kA = 128 * 128, kB = BN * 128;
   static constexpr int kStage = kA + kB;
-  static constexpr int NS = BN >= 128 ? 6 : 8;
+  static constexpr int NS = BN == 128 ? 6 : 8;
   static constexpr int kBars = NS * kStage;
   static constexpr int kMisc = kBars + (2 * NS + 1) * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
@@ -34,10 +34,12 @@ struct LinCursor {
   int d, steps_batch;
   int b, h, f, row, left;   // of the next step: batch, head and feature in it, row; steps left in the batch
   int fj[ROWS >= 64 ? ROWS / 64 : 1], hj[ROWS >= 64 ? ROWS / 64 : 1];   // MN: features and heads of the 64-column blocks
-  // d: features a head (0: one head); batch: of a K-major operand, whose steps begin at 0
+  // d: features a head (0: one head); batch: of a K-major operand
   __device__ __forceinline__ LinCursor(int d_, int r0, int batch, int s, int steps_batch_) : d(d_), steps_batch(steps_batch_) {
     if (!MN) {
-      f = h = 0;
+      f = kLinStep * s;
+      h = d && s > 0 ? f / d : 0;
+      f -= h * d;
       row = r0;
       b = batch;
     } else {
@@ -74,9 +76,9 @@ struct LinCursor {
   }
 };
 
-__device__ __forceinline__ size_t lin_at(const LinView& v, int b, int n, int f) {
+__device__ __forceinline__ long long lin_feature(const LinView& v, int f) {   // offset of feature f in its token
   const int h = v.d ? f / v.d : 0;
-  return static_cast<size_t>(b * v.sb + n * v.sn + h * v.sh + (f - h * v.d));
+  return h * v.sh + (f - h * v.d);
 }
 
 __device__ __forceinline__ void store_elem(void* p, size_t i, float x, int fmt) {
@@ -147,10 +149,6 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, const LinWarp& w,
   const size_t out_row = static_cast<size_t>(w.b * a.out_at.sb + row * a.out_at.sn);
   const size_t aux_row = static_cast<size_t>(w.b * a.aux_at.sb + row * a.aux_at.sn);
   const long long out_step = 8 * a.out_at.sn, aux_step = 8 * a.aux_at.sn;
-  auto at = [&](const LinView& v, int f) {   // offset of feature f
-    const int h = v.d ? f / v.d : 0;
-    return h * v.sh + (f - h * v.d);
-  };
   float bias[8];
   LinAux x;
   auto begin = [&](int c) {   // the loads beside the first half of piece c
@@ -162,7 +160,7 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, const LinWarp& w,
     }
     if (a.aux) {
       const bool there[2] = {f < a.cols && row < a.rows, f < a.cols && row + 8 < a.rows};
-      x.load(a.aux, aux_row + at(a.aux_at, f), aux_step, a.aux_fmt, there);
+      x.load(a.aux, aux_row + lin_feature(a.aux_at, f), aux_step, a.aux_fmt, there);
     }
   };
   begin(0);
@@ -179,11 +177,11 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, const LinWarp& w,
     __syncwarp();
     const int f = w.f0 + c + col;
     const bool in = f < a.cols;
-    const size_t to = out_row + at(a.out_at, f);
+    const size_t to = out_row + lin_feature(a.out_at, f);
     #pragma unroll 1   // a kernel's first tile waits for its code as well
     for (int half = 0; half < 2; ++half) {
       const bool there[2] = {in && row + 16 * half < a.rows, in && row + 16 * half + 8 < a.rows};
-      if (half == 1 && a.aux) x.load(a.aux, aux_row + at(a.aux_at, f) + 2 * aux_step, aux_step, a.aux_fmt, there);
+      if (half == 1 && a.aux) x.load(a.aux, aux_row + lin_feature(a.aux_at, f) + 2 * aux_step, aux_step, a.aux_fmt, there);
       float v[16];
       lin_get(w.stage, half, v);
       const float(&v0)[8] = *reinterpret_cast<const float(*)[8]>(&v[0]);
@@ -216,49 +214,48 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, const LinWarp& w,
   return true;
 }
 
-// With the operands swapped: one feature f of `count` tokens from n.
-template <int KIND>
-__device__ __forceinline__ void lin_finish_turned(const LinArgs& a, float (&v)[32], int n, int f, int count) {
+// With the operands swapped: one feature f of T tokens from n, `count` of them there.
+template <int KIND, int T>
+__device__ __forceinline__ void lin_finish_turned(const LinArgs& a, float (&v)[T], int n, int f, int count) {
+  static_assert(T % 2 == 0, "pairs");
+  const size_t out = static_cast<size_t>(n * a.out_at.sn + lin_feature(a.out_at, f));
+  const size_t aux = static_cast<size_t>(n * a.aux_at.sn + lin_feature(a.aux_at, f));
+  float x[T];
+  if (a.aux) {
+    #pragma unroll
+    for (int j = 0; j < T; ++j) x[j] = j < count ? load_elem(a.aux, aux + j * a.aux_at.sn, a.aux_fmt) : 0.f;
+  }
   if (KIND == kLinForward) {
     const float bias = a.bias ? load_elem(a.bias, f, a.bias_fmt) : 0.f;
     #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] += bias;
+    for (int j = 0; j < T; ++j) v[j] += bias;
     if (a.pre) {
       #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < count) store_elem(a.pre, lin_at(a.out_at, 0, n + j, f), v[j], a.fmt);
+      for (int j = 0; j < T; ++j)
+        if (j < count) store_elem(a.pre, out + j * a.out_at.sn, v[j], a.fmt);
     }
-    if (a.act != kActNone)
-      with_act(a.act, [&](auto A) {
-        act_all<decltype(A)::value>(v);
-      });
+    if (a.act != kActNone) with_act(a.act, [&](auto A) { act_all<decltype(A)::value>(v); });
     if (a.aux) {
       #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < count) v[j] += load_elem(a.aux, lin_at(a.aux_at, 0, n + j, f), a.aux_fmt);
+      for (int j = 0; j < T; ++j) v[j] += x[j];
     }
   }
-  if (KIND == kLinInput && a.aux) {
-    float x[32];
-    #pragma unroll
-    for (int j = 0; j < 32; ++j) x[j] = j < count ? load_elem(a.aux, lin_at(a.aux_at, 0, n + j, f), a.aux_fmt) : 0.f;
-    with_act(a.act, [&](auto A) {
-      slope_all<decltype(A)::value>(v, x);
-    });
-  }
+  if (KIND == kLinInput && a.aux) with_act(a.act, [&](auto A) { slope_all<decltype(A)::value>(v, x); });
   #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (j < count) store_elem(a.out, lin_at(a.out_at, 0, n + j, f), v[j], a.out_fmt);
+  for (int j = 0; j < T; ++j)
+    if (j < count) store_elem(a.out, out + j * a.out_at.sn, v[j], a.out_fmt);
 }
 
-// One tile a CTA.
-template <int KIND, int BN, bool TURNED, bool BF16>
-__global__ void __launch_bounds__(kLinThreads) linear_kernel(const __grid_constant__ CUtensorMap map_a,
-                                                             const __grid_constant__ CUtensorMap map_b,
-                                                             const __grid_constant__ LinArgs a) {
+// Up to 128 tokens: 128 features by BN tokens a tile, the features as rows, so that a product of few tokens still fills the tensor
+// core's 128 rows.  What counts then is how many SMs read the weight: a cluster of CTAs shares a tile, each with a piece of the
+// contraction, and each adds up all of their parts for its share of the tokens, through distributed shared memory and in order.
+template <int KIND, int BN, bool BF16>
+__global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_constant__ CUtensorMap map_a,
+                                                                 const __grid_constant__ CUtensorMap map_b,
+                                                                 const __grid_constant__ LinArgs a) {
   using SM = LinSmem<BN>;
   constexpr int NS = SM::NS;
-  constexpr bool A_MN = KIND == kLinInput && TURNED, B_MN = KIND == kLinInput && !TURNED;   // W's columns in the input's gradient
+  constexpr bool A_MN = KIND == kLinInput;   // W's columns in the input's gradient
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -267,9 +264,11 @@ __global__ void __launch_bounds__(kLinThreads) linear_kernel(const __grid_consta
   uint64_t* done = empty + NS;
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::kMisc + 4);
+  float* part = reinterpret_cast<float*>(smem);   // [BN][128] once the products are done
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tile = blockIdx.x, mt = tile / a.n_tiles, b = mt / a.m_tiles;
-  const int r0 = (mt - b * a.m_tiles) * 128, c0 = (tile - mt * a.n_tiles) * BN;
+  const int rank = static_cast<int>(cluster_rank()), pieces = a.pieces;
+  const int r0 = blockIdx.x / pieces * 128;
+  const int s0 = rank * a.steps / pieces, s1 = (rank + 1) * a.steps / pieces;
   if (threadIdx.x == 128) {
     tma_prefetch_desc(&map_a);
     tma_prefetch_desc(&map_b);
@@ -289,12 +288,12 @@ __global__ void __launch_bounds__(kLinThreads) linear_kernel(const __grid_consta
   const uint32_t tbase = *slot;
   if (warp == 4) {
     if (lane == 0) {
-      LinCursor<A_MN, 128> at_a(a.a_d, r0, b, 0, a.steps_batch);
-      LinCursor<B_MN, BN> at_b(a.b_d, c0, 0, 0, a.steps_batch);
-      int s = 0;
-      for (; s < a.steps; ++s) {
-        const int st = s % NS;
-        if (!mbar_wait(&empty[st], ((s / NS) & 1) ^ 1, abort_flag, a.status)) break;
+      LinCursor<A_MN, 128> at_a(a.a_d, r0, 0, s0, a.steps);
+      LinCursor<false, BN> at_b(a.b_d, 0, 0, s0, a.steps);
+      int n = 0;
+      for (int s = s0; s < s1; ++s, ++n) {
+        const int st = n % NS;
+        if (!mbar_wait(&empty[st], ((n / NS) & 1) ^ 1, abort_flag, a.status)) break;
         mbar_arrive_expect_tx(&full[st], SM::kStage);
         at_a.step(smem + st * SM::kStage, [&](uint8_t* dst, int f, int row, int h, int bb) {
           tma_load_4d(dst, &map_a, &full[st], f, row, h, bb);
@@ -304,55 +303,76 @@ __global__ void __launch_bounds__(kLinThreads) linear_kernel(const __grid_consta
         });
       }
       // the copies have landed: at once after a whole run, and with a limit if some role gave up
-      for (int i = max(0, s - NS); i < s; ++i) mbar_wait_budget(&full[i % NS], (i / NS) & 1, kWaitBudgetCycles);
+      for (int i = max(0, n - NS); i < n; ++i) mbar_wait_budget(&full[i % NS], (i / NS) & 1, kWaitBudgetCycles);
     }
     __syncwarp();
   } else if (warp == 5) {
     constexpr uint32_t fmt = BF16 ? 1 : 0;
-    constexpr uint32_t id = idesc_f16(128, BN, fmt, fmt, A_MN, B_MN);
-    constexpr uint32_t ka = A_MN ? 128 : 2, kb = B_MN ? 128 : 2;   // 16 contraction elements further, in 16 bytes
+    constexpr uint32_t id = idesc_f16(128, BN, fmt, fmt, A_MN, 0);
+    constexpr uint32_t ka = A_MN ? 128 : 2;   // 16 contraction elements further, in 16 bytes
     const uint64_t da = sdesc_sw128(smem_u32(smem), A_MN ? 8192 : 16, 1024);
-    const uint64_t db = sdesc_sw128(smem_u32(smem) + SM::kA, B_MN ? 8192 : 16, 1024);
-    for (int s = 0; s < a.steps; ++s) {
-      const int st = s % NS;
-      const bool ok = mbar_wait(&full[st], (s / NS) & 1, abort_flag, a.status);
+    const uint64_t db = sdesc_sw128(smem_u32(smem) + SM::kA, 16, 1024);
+    for (int n = 0; n < s1 - s0; ++n) {
+      const int st = n % NS;
+      const bool ok = mbar_wait(&full[st], (n / NS) & 1, abort_flag, a.status);
       if (!warp_all(ok)) break;
       tc_fence_after();
       #pragma unroll
       for (int k = 0; k < 4; ++k)
-        umma_ss_w(tbase, da + st * (SM::kStage >> 4) + ka * k, db + st * (SM::kStage >> 4) + kb * k, id,
-                  (s > 0 || k > 0) ? 1u : 0u);
+        umma_ss_w(tbase, da + st * (SM::kStage >> 4) + ka * k, db + st * (SM::kStage >> 4) + 2 * k, id,
+                  (n > 0 || k > 0) ? 1u : 0u);
       umma_commit_w(&empty[st]);
     }
     umma_commit_w(done);
     mbar_wait_budget(done, 0, kWaitBudgetCycles);
     __syncwarp();
-  } else {
-    const uint32_t taddr = tbase + (static_cast<uint32_t>(32 * warp) << 16);
-    auto wait = [&] {
-      const bool ok = warp_all(mbar_wait(done, 0, abort_flag, a.status));
-      tc_fence_after();
-      return ok;
-    };
-    if (!TURNED) {
-      // every product has read its operands: their shared memory serves the epilogue
-      const LinWarp w = {reinterpret_cast<float4*>(smem) + 256 * warp, b, r0 + 32 * warp, c0};
-      lin_epilogue<KIND, BN>(a, w, taddr, wait, [] {});
-    } else if (wait()) {
-      const int row = r0 + 32 * warp + lane;
-      const bool valid = row < a.rows;
+  }
+  const bool ok = warp < 4 && warp_all(mbar_wait(done, 0, abort_flag, a.status));
+  const uint32_t taddr = tbase + (static_cast<uint32_t>(32 * warp) << 16);
+  const int f = r0 + threadIdx.x;   // this thread's feature
+  tc_fence_after();
+  if (pieces > 1) {
+    if (ok) {
       #pragma unroll 1
-      for (int c = 0; c < BN && c0 + c < a.cols; c += 32) {
+      for (int c = 0; c < BN; c += 32) {
         uint32_t u[32];
         tmem_ld32(taddr + c, u);
         tmem_wait_ld();
-        float v[32];
         #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
-        if (valid) lin_finish_turned<KIND>(a, v, c0 + c, row, min(32, a.cols - c0 - c));
+        for (int j = 0; j < 32; ++j) part[(c + j) * 128 + threadIdx.x] = __uint_as_float(u[j]);
       }
     }
+    __syncwarp();
+    cluster_sync_all();
+    // this CTA's share of the tokens, four at a time; every CTA's part of them, one after another
+    const int share = BN / pieces;
+    if (warp < 4 && f < a.rows) {
+      #pragma unroll 1
+      for (int t = rank * share; t < (rank + 1) * share && t < a.cols; t += 4) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int p = 0; p < pieces; ++p) {
+          const uint32_t from = cluster_map(part + t * 128 + threadIdx.x, p);
+          #pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] += ld_cluster(from + j * 512);
+        }
+        lin_finish_turned<KIND>(a, v, t, f, min(4, a.cols - t));
+      }
+    }
+    __syncwarp();
+    cluster_sync_all_relaxed();   // no CTA leaves while its part is read
+  } else if (ok) {
+    #pragma unroll 1
+    for (int c = 0; c < BN && c < a.cols; c += 16) {
+      uint32_t u[16];
+      tmem_ld16(taddr + c, u);
+      tmem_wait_ld();
+      float v[16];
+      #pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(u[j]);
+      if (f < a.rows) lin_finish_turned<KIND>(a, v, c, f, min(16, a.cols - c));
+    }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   if (warp == 5) tmem_dealloc(tbase, BN);

@@ -6,14 +6,24 @@
 
 namespace dera {
 
-template <int KIND, int BN, bool TURNED, bool BF16>
-static cudaError_t launch_lin(const LinMaps& m, const LinArgs& a, cudaStream_t s) {
-  auto kernel = linear_kernel<KIND, BN, TURNED, BF16>;
+template <int KIND, int BN, bool BF16>
+static cudaError_t launch_lin_few(const LinMaps& m, const LinArgs& a, cudaStream_t s) {
+  auto kernel = linear_few_kernel<KIND, BN, BF16>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = prepare_kernel(kernel, LinSmem<BN>::kAlloc, 0, done);
   if (e != cudaSuccess) return e;
-  kernel<<<a.batches * a.m_tiles * a.n_tiles, kLinThreads, LinSmem<BN>::kAlloc, s>>>(m.a, m.b, a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = a.pieces;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.m_tiles * a.pieces);
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = LinSmem<BN>::kAlloc;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, a);
 }
 
 template <int KIND, int BN, bool BF16>
@@ -29,14 +39,14 @@ static cudaError_t launch_lin_pair(const LinMaps& m, const LinArgs& a, int pairs
 // Tokens by features: the gradient of the weight has only pairs.
 template <int KIND, bool BF16>
 static cudaError_t launch_lin_kind(const LinMaps& m, const LinArgs& a, const LinPlan& p, cudaStream_t s) {
-  if (p.pairs > 0)
-    return p.bn == 256 ? launch_lin_pair<KIND, 256, BF16>(m, a, p.pairs, s) : launch_lin_pair<KIND, 128, BF16>(m, a, p.pairs, s);
   if constexpr (KIND != kLinWeight) {
-    if (!p.turned) return launch_lin<KIND, 128, false, BF16>(m, a, s);
-    if (p.bn == 32) return launch_lin<KIND, 32, true, BF16>(m, a, s);
-    return p.bn == 64 ? launch_lin<KIND, 64, true, BF16>(m, a, s) : launch_lin<KIND, 128, true, BF16>(m, a, s);
+    if (p.turned) {
+      if (p.bn == 32) return launch_lin_few<KIND, 32, BF16>(m, a, s);
+      return p.bn == 64 ? launch_lin_few<KIND, 64, BF16>(m, a, s) : launch_lin_few<KIND, 128, BF16>(m, a, s);
+    }
+    if (p.bn == 128) return launch_lin_pair<KIND, 128, BF16>(m, a, p.pairs, s);
   }
-  return cudaErrorInvalidValue;
+  return launch_lin_pair<KIND, 256, BF16>(m, a, p.pairs, s);
 }
 
 template <int KIND>

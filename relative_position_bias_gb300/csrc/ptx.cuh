@@ -250,6 +250,11 @@ __device__ __forceinline__ uint32_t cluster_map(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 // Arrives on a barrier of either CTA without releasing memory: for what tcgen05.fence orders (a release at cluster
 // scope would wait for every store of this thread).
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {

@@ -71,6 +71,9 @@ SIZES = {
     "tokens": (32, 1, 768, 264, 0, HF, F32),
     "tokens_heads": (5, 1, 256, 72, 64, BF, BF),
     "thirty_three": (1, 33, 200, 136, 0, HF, HF),
+    "long_contraction": (1, 17, 4096, 520, 0, BF, BF),
+    "odd_pieces": (3, 40, 1096, 264, 0, HF, HF),
+    "few_heads_long": (1, 70, 2304, 72, 128, BF, F32),
     "sixty_five": (5, 13, 640, 1000, 0, BF, F32),
     "tile": (1, 128, 64, 128, 0, BF, BF),
     "past_a_tile": (1, 129, 72, 136, 0, BF, BF),
