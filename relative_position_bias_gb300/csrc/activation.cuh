@@ -42,22 +42,28 @@ __device__ __forceinline__ float max_nan(float x, float y) {
 // would be multiplied by zero.
 constexpr float kActFar = 64.f;
 
-// Everything is on pairs: packed fp32 arithmetic takes half the issue slots.
+// Everything is on pairs: packed fp32 arithmetic takes half the issue slots.  Exponentials and reciprocals have 16 lanes a clock
+// and SM: two for each of the 128 x 256 elements of a tile's half take 4096 cycles, half of its products' time at K = 1024.
 __device__ __forceinline__ float2 pair_of(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 fmul2(float2 x, float2 y) { return __fmul2_rn(x, y); }
 __device__ __forceinline__ float2 rcp2(float2 x) { return make_float2(rcp_approx(x.x), rcp_approx(x.y)); }
 __device__ __forceinline__ float2 exp2_2(float2 x) { return make_float2(ex2_approx(x.x), ex2_approx(x.y)); }
 
-// Phi(-z) for z >= 0; *e = exp(-z^2 / 2).
-__device__ __forceinline__ float2 normal_tail(float2 z, float2* e) {
-  const float2 t = rcp2(ffma2(pair_of(0.36f), z, pair_of(1.f)));
+// Phi(-|u|); *e = exp(-u^2 / 2), z = |u|, cut to kActFar and never NaN: the elements of a pair share a reciprocal, and one that is
+// NaN becomes it through e alone.
+__device__ __forceinline__ float2 normal_tail(float2 u, float2* z_, float2* e) {
+  const float2 z = make_float2(fminf(fabsf(u.x), kActFar), fminf(fabsf(u.y), kActFar));
+  *z_ = z;
+  // both reciprocals from one, of the product (the arguments lie between 1 and 25)
+  const float2 d = ffma2(pair_of(0.36f), z, pair_of(1.f));
+  const float2 t = fmul2(pair_of(rcp_approx(d.x * d.y)), make_float2(d.y, d.x));
   float2 p = ffma2(pair_of(0.0470557399f), t, pair_of(-0.17976281f));
   p = ffma2(p, t, pair_of(0.180951446f));
   p = ffma2(p, t, pair_of(0.0265510548f));
   p = ffma2(p, t, pair_of(0.139718652f));
   p = ffma2(p, t, pair_of(0.141772568f));
   p = ffma2(p, t, pair_of(0.143713042f));
-  *e = exp2_2(fmul2(fmul2(z, z), pair_of(-0.5f * kLog2e)));
+  *e = exp2_2(fmul2(fmul2(u, u), pair_of(-0.5f * kLog2e)));
   return fmul2(fmul2(p, t), *e);
 }
 
@@ -73,10 +79,10 @@ template <int ACT>
 __device__ __forceinline__ float2 act_of(float2 u) {
   if (ACT == kActRelu) return make_float2(u.x < 0.f ? 0.f : u.x, u.y < 0.f ? 0.f : u.y);   // NaN stays
   if (ACT == kActGelu) {
-    float2 e;
-    const float2 n = make_float2(max_nan(-fabsf(u.x), -kActFar), max_nan(-fabsf(u.y), -kActFar));   // -z
+    float2 z, e;
+    const float2 q = normal_tail(u, &z, &e);
     // u - u Phi(-u) for u > 0, u Phi(u) below
-    return ffma2(n, normal_tail(make_float2(-n.x, -n.y), &e), make_float2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
+    return ffma2(make_float2(-z.x, -z.y), q, make_float2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
   }
   if (ACT == kActGeluTanh)
     return fmul2(u, sigmoid(fmul2(u, ffma2(fmul2(u, u), pair_of(kTanhC), pair_of(1.f))), kTanhB));
@@ -89,14 +95,14 @@ template <int ACT>
 __device__ __forceinline__ float2 act_slope(float2 u) {
   if (ACT == kActNone) return pair_of(1.f);
   if (ACT == kActRelu) return make_float2(u.x > 0.f ? 1.f : 0.f, u.y > 0.f ? 1.f : 0.f);
-  const float2 v = make_float2(max_nan(min_nan(u.x, kActFar), -kActFar), max_nan(min_nan(u.y, kActFar), -kActFar));
   if (ACT == kActGelu) {
-    float2 e;
-    const float2 q = normal_tail(make_float2(fabsf(v.x), fabsf(v.y)), &e);
+    float2 z, e;
+    const float2 q = normal_tail(u, &z, &e);
     // Phi + u exp(-u^2 / 2) / sqrt(2 pi)
-    return ffma2(fmul2(v, pair_of(0.3989422804014327f)), e,
-                 make_float2(v.x < 0.f ? q.x : 1.f - q.x, v.y < 0.f ? q.y : 1.f - q.y));
+    return ffma2(fmul2(make_float2(copysignf(z.x, u.x), copysignf(z.y, u.y)), pair_of(0.3989422804014327f)), e,
+                 make_float2(u.x < 0.f ? q.x : 1.f - q.x, u.y < 0.f ? q.y : 1.f - q.y));
   }
+  const float2 v = make_float2(max_nan(min_nan(u.x, kActFar), -kActFar), max_nan(min_nan(u.y, kActFar), -kActFar));
   // s + m s (1 - s), m = u times the slope of the sigmoid's argument
   float2 s, m;
   if (ACT == kActGeluTanh) {

@@ -64,7 +64,7 @@ dera_status take_tokens(const dera_heads* t, int B, int N, int heads, int d, boo
   const long long st[3] = {out->sb, out->st, out->sh};
   const int n[3] = {B, N, heads};
   for (int i = 0; i < 3; ++i)
-    if ((n[i] > 1 && st[i] == 0) || st[i] >= (1ll << 38)) return DERA_ERR_SHAPE;
+    if ((n[i] > 1 && st[i] == 0) || st[i] >= (1ll << 37)) return DERA_ERR_SHAPE;
   return DERA_OK;
 }
 
@@ -346,13 +346,21 @@ dera_status dera_linear(const dera_heads* x, const void* weight, const void* bia
   a.aux_fmt = a.out_fmt = fmt_of(out_dtype);
   const LinPlan p = token_plan(tok, out_features, a.steps, sm_count(dev));
   if (!(p.turned ? cut(&a, p, 1, out_features, tok.N) : cut(&a, p, tok.B, tok.N, out_features))) return DERA_ERR_SHAPE;
-  LinMaps m;
+  LinMaps m = {};
   const HeadsPtr xm = tok.of(xt, N), wm = rows_of(weight, out_features, K);
   CUtensorMap *mx = p.turned ? &m.b : &m.a, *mw = p.turned ? &m.a : &m.b;
   (p.turned ? a.b_d : a.a_d) = heads > 1 ? head_dim : 0;
   if (!map_tokens(mx, xm, in_dtype, tok.B, tok.N, heads, head_dim, p.turned ? p.bn : 128) ||
       !map_tokens(mw, wm, in_dtype, 1, out_features, 1, K, p.turned ? 128 : p.bn / 2))
     return DERA_ERR_CUDA;
+  if (!p.turned) {
+    const HeadsPtr ym = tok.of(rows_of(y, N, out_features), N), rm = {const_cast<char*>(static_cast<const char*>(residual)), ym.sb, ym.st, 0},
+                   pm = {static_cast<char*>(pre), ym.sb, ym.st, 0};
+    if (!map_boxes(&m.out, ym, out_dtype, tok.B, tok.N, 1, out_features) ||
+        (residual && !map_boxes(&m.aux, rm, out_dtype, tok.B, tok.N, 1, out_features)) ||
+        (pre && !map_boxes(&m.pre, pm, in_dtype, tok.B, tok.N, 1, out_features)))
+      return DERA_ERR_CUDA;
+  }
   return status_of(launch_linear_forward(m, a, p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -427,11 +435,14 @@ dera_status dera_linear_backward(const void* dy, const dera_heads* x, const void
     a.fmt = a.aux_fmt = fmt_of(in_dtype);
     a.out_fmt = fmt_of(grad_dtype);
     const LinPlan p = token_plan(tok, K, a.steps, sms);
-    LinMaps m;
+    LinMaps m = {};
     CUtensorMap *mg = p.turned ? &m.b : &m.a, *mw = p.turned ? &m.a : &m.b;
     if (!(p.turned ? cut(&a, p, 1, K, tok.N) : cut(&a, p, tok.B, tok.N, K))) return DERA_ERR_SHAPE;
     if (!map_tokens(mg, tok.of(gt, N), in_dtype, tok.B, tok.N, 1, out_features, p.turned ? p.bn : 128) ||
         !map_tokens(mw, rows_of(weight, out_features, K), in_dtype, 1, out_features, 1, K, 64))
+      return DERA_ERR_CUDA;
+    if (!p.turned && (!map_boxes(&m.out, tok.of(dt, N), grad_dtype, tok.B, tok.N, h, d) ||
+                      (pt.data && !map_boxes(&m.aux, tok.of(pt, N), in_dtype, tok.B, tok.N, h, d))))
       return DERA_ERR_CUDA;
     DERA_TRY(status_of(launch_linear_input(m, a, p, s)));
   }
@@ -452,7 +463,7 @@ dera_status dera_linear_backward(const void* dy, const dera_heads* x, const void
     const WeightPlan w = weight_plan(out_features, K, a.steps, sms);
     if (!cut(&a, w.p, 1, out_features, K)) return DERA_ERR_SHAPE;
     if (w.p.pieces > 1) a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums_bytes(out_features, sms));
-    LinMaps m;
+    LinMaps m = {};
     if (!map_tokens(&m.a, tok.of(gt, N), in_dtype, tok.B, tok.N, 1, out_features, 64) ||
         !map_tokens(&m.b, tok.of(xt, N), in_dtype, tok.B, tok.N, h, d, 64))
       return DERA_ERR_CUDA;

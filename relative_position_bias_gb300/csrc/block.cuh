@@ -88,6 +88,7 @@ struct LinArgs {
 
 struct LinMaps {
   CUtensorMap a, b;
+  CUtensorMap out, aux, pre;   // pairs, but for dW: boxes of 32 rows x 32 columns of what lies beside D
 };
 
 struct LinPlan {

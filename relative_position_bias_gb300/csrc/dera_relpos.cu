@@ -132,13 +132,14 @@ dera_status check_ptr(const void* p, int dev) {
 }
 
 static bool make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int rank, const cuuint64_t* dims,
-              const cuuint64_t* strides_bytes, const cuuint32_t* box) {
+              const cuuint64_t* strides_bytes, const cuuint32_t* box,
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint32_t es[5] = {1, 1, 1, 1, 1};
   std::memset(m, 0, sizeof(*m));
   return fn(m, dt, rank, const_cast<void*>(base), dims, strides_bytes, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -171,6 +172,17 @@ bool map_tokens(CUtensorMap* m, const HeadsPtr& t, dera_dtype dt, int B, int N, 
   const cuuint64_t strides[3] = {bytes(t.st), bytes(t.sh), bytes(t.sb)};
   const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1};
   return make_map(m, t.data, tma_type(dt), 4, dims, strides, box);
+}
+
+bool map_boxes(CUtensorMap* m, const HeadsPtr& t, dera_dtype dt, int B, int N, int heads, int d) {
+  const int size = dt == DERA_F32 ? 4 : 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(B)};
+  auto bytes = [&](long long st) { return size * static_cast<cuuint64_t>(st > 0 ? st : d); };
+  const cuuint64_t strides[3] = {bytes(t.st), bytes(t.sh), bytes(t.sb)};
+  const cuuint32_t box[4] = {32, 32, 1, 1};
+  return make_map(m, t.data, dt == DERA_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : tma_type(dt), 4, dims, strides, box,
+                  size == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // table [2L-1, d], one 128-row box per 64 columns (rows past 2L-1 read as zero)

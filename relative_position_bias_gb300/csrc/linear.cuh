@@ -86,132 +86,154 @@ __device__ __forceinline__ void store_elem(void* p, size_t i, float x, int fmt) 
   else reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(pack_in(x, 0.f, fmt));
 }
 
-// An epilogue warp's part of a tile: 32 rows of D, COLS columns, in pieces of 32 x 32.  A piece comes out of TMEM a row a
-// lane and passes through 4 KB of shared memory, so that four lanes have a row's 32 columns, eight each: what is read and
-// written then is whole 64-byte (fp32: 128-byte) runs of eight rows at a time.  (A row a lane, 32 addresses an instruction: 216 us
-// instead of 154 for 32768 x 1024 x 4096, and 327 with a residual.)
-struct LinWarp {
-  float4* stage;       // [32][8], 16-byte chunks of row r permuted by r % 8
-  int b, row0, f0;     // batch, first row and column
+// An epilogue warp's part of a tile: 32 rows of D, COLS columns, 32 at a time, a row a lane as TMEM gives them.  What is read and
+// written beside D goes through 4 KB of shared memory a warp by TMA, in boxes of 32 rows x 32 columns (64 bytes a row in 16 bits, 128 in
+// fp32, swizzled so that lanes meet different banks): whole lines of memory, asynchronously, and edges are left to TMA.  (Plain
+// stores from this layout touch 32 lines an instruction, 216 us for 32768 x 1024 x 4096; turned in shared memory first they need
+// twice the shared-memory traffic and wait for it, 156, and 195 where gelu's argument is kept.)
+struct LinEpi {
+  uint8_t* slot;       // 4 KB: [2][32 rows x 64 bytes] or [32 rows x 128 bytes]
+  uint64_t* bars;      // [2]: a box beside D landed
+  uint32_t phases;     // bit i: of the next one
+  const CUtensorMap* out;
+  const CUtensorMap* aux;
+  const CUtensorMap* pre;
 };
 
-__device__ __forceinline__ void lin_put(float4* stage, const uint32_t (&u)[32]) {
+// 16-byte chunk c of this lane's row in a box of 64- or 128-byte rows.
+template <bool WIDE>
+__device__ __forceinline__ uint4* lin_chunk(uint8_t* slot, int c) {
   const int lane = threadIdx.x & 31;
-  #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    reinterpret_cast<uint4*>(stage)[lane * 8 + (c ^ (lane & 7))] = make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+  return reinterpret_cast<uint4*>(slot + (WIDE ? lane * 128 + ((c ^ (lane & 7)) << 4) : lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)));
 }
-// Eight columns of rows 16 half + lane / 4 and eight further.
-__device__ __forceinline__ void lin_get(const float4* stage, int half, float (&v)[16]) {
-  const int lane = threadIdx.x & 31;
-  #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = 16 * half + 8 * i + (lane >> 2), c = 2 * (lane & 3);
-    const float4 lo = stage[r * 8 + (c ^ (r & 7))], hi = stage[r * 8 + ((c + 1) ^ (r & 7))];
-    v[8 * i] = lo.x, v[8 * i + 1] = lo.y, v[8 * i + 2] = lo.z, v[8 * i + 3] = lo.w;
-    v[8 * i + 4] = hi.x, v[8 * i + 5] = hi.y, v[8 * i + 6] = hi.z, v[8 * i + 7] = hi.w;
+__device__ __forceinline__ void lin_write(uint8_t* slot, const float (&v)[32], int fmt) {
+  if (fmt == kF32) {
+    #pragma unroll
+    for (int c = 0; c < 8; ++c)
+      *lin_chunk<true>(slot, c) = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                                             __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+  } else {
+    #pragma unroll
+    for (int c = 0; c < 4; ++c) *lin_chunk<false>(slot, c) = pack8(*reinterpret_cast<const float(*)[8]>(&v[8 * c]), fmt);
   }
 }
-
-// Eight columns of two rows of a tensor beside D, `step` elements apart, as they lie (fp32 in two parts).
-struct LinAux {
-  uint4 lo[2], hi[2];
-  __device__ __forceinline__ void load(const void* p, size_t at, long long step, int fmt, const bool (&there)[2]) {
+__device__ __forceinline__ void lin_read(uint8_t* slot, float (&x)[32], int fmt) {
+  if (fmt == kF32) {
     #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      lo[i] = hi[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (!there[i]) continue;
-      const char* q = static_cast<const char*>(p) + (at + i * step) * (fmt == kF32 ? 4 : 2);
-      lo[i] = *reinterpret_cast<const uint4*>(q);
-      if (fmt == kF32) hi[i] = *reinterpret_cast<const uint4*>(q + 16);
+    for (int c = 0; c < 8; ++c) {
+      const uint4 u = *lin_chunk<true>(slot, c);
+      x[4 * c] = __uint_as_float(u.x), x[4 * c + 1] = __uint_as_float(u.y);
+      x[4 * c + 2] = __uint_as_float(u.z), x[4 * c + 3] = __uint_as_float(u.w);
     }
-  }
-  __device__ __forceinline__ void get(float (&x)[16], int fmt) const {
+  } else {
     #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float y[8];
-      if (fmt == kF32) {
-        y[0] = __uint_as_float(lo[i].x), y[1] = __uint_as_float(lo[i].y), y[2] = __uint_as_float(lo[i].z), y[3] = __uint_as_float(lo[i].w);
-        y[4] = __uint_as_float(hi[i].x), y[5] = __uint_as_float(hi[i].y), y[6] = __uint_as_float(hi[i].z), y[7] = __uint_as_float(hi[i].w);
-      } else {
-        unpack8(lo[i], y, fmt);
-      }
-      #pragma unroll
-      for (int e = 0; e < 8; ++e) x[8 * i + e] = y[e];
-    }
+    for (int c = 0; c < 4; ++c) unpack8(*lin_chunk<false>(slot, c), *reinterpret_cast<float(*)[8]>(&x[8 * c]), fmt);
   }
-};
+}
 
 // wait() returns whether D is complete (of the whole warp), done() says that it has been read.
 template <int KIND, int COLS, class Wait, class Done>
-__device__ __forceinline__ bool lin_epilogue(const LinArgs& a, const LinWarp& w, uint32_t taddr, Wait&& wait, Done&& done) {
-  const int lane = threadIdx.x & 31, row = w.row0 + (lane >> 2), col = 8 * (lane & 3);
-  const size_t out_row = static_cast<size_t>(w.b * a.out_at.sb + row * a.out_at.sn);
-  const size_t aux_row = static_cast<size_t>(w.b * a.aux_at.sb + row * a.aux_at.sn);
-  const long long out_step = 8 * a.out_at.sn, aux_step = 8 * a.aux_at.sn;
-  float bias[8];
-  LinAux x;
-  auto begin = [&](int c) {   // the loads beside the first half of piece c
-    const int f = w.f0 + c + col;
-    if (KIND == kLinForward) {
-      #pragma unroll
-      for (int e = 0; e < 8; ++e) bias[e] = 0.f;
-      if (a.bias && f < a.cols) load8(a.bias, f, bias, a.bias_fmt);
-    }
-    if (a.aux) {
-      const bool there[2] = {f < a.cols && row < a.rows, f < a.cols && row + 8 < a.rows};
-      x.load(a.aux, aux_row + lin_feature(a.aux_at, f), aux_step, a.aux_fmt, there);
-    }
+__device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32_t taddr, int b, int row0, int f0, volatile int* abort_flag,
+                                             Wait&& wait, Done&& done) {
+  static_assert(COLS == 32 || COLS == 64, "one or two pieces");
+  const int lane = threadIdx.x & 31;
+  // two boxes at once where both are of 16 bits and the sum before the activation needs none; else one after another
+  const bool out16 = a.out_fmt != kF32, two = out16 && !a.pre;
+  uint8_t* const out_slot = e.slot + (out16 && a.pre ? 2048 : 0);
+  const bool rows_in = row0 < a.rows;
+  auto fetch = [&](int c) {   // by one lane: what is beside columns c of D
+    const int f = f0 + c, i = two ? (c >> 5) & 1 : 0;
+    if (!rows_in || f >= a.cols) return;
+    const int h = a.aux_at.d ? f / a.aux_at.d : 0;
+    mbar_arrive_expect_tx(&e.bars[i], a.aux_fmt == kF32 ? 4096 : 2048);
+    tma_load_4d(out_slot + 2048 * i, e.aux, &e.bars[i], f - h * a.aux_at.d, row0, h, b);
   };
-  begin(0);
-  if (!wait()) return false;
-  #pragma unroll 1
-  for (int c = 0; c < COLS; c += 32) {
-    uint32_t u[32];
-    tmem_ld32(taddr + c, u);
-    if (c > 0) begin(c);
-    tmem_wait_ld();
-    __syncwarp();   // the last piece has been read from the stage
-    lin_put(w.stage, u);
-    if (c + 32 == COLS) done();
-    __syncwarp();
-    const int f = w.f0 + c + col;
-    const bool in = f < a.cols;
-    const size_t to = out_row + lin_feature(a.out_at, f);
-    #pragma unroll 1   // a kernel's first tile waits for its code as well
-    for (int half = 0; half < 2; ++half) {
-      const bool there[2] = {in && row + 16 * half < a.rows, in && row + 16 * half + 8 < a.rows};
-      if (half == 1 && a.aux) x.load(a.aux, aux_row + lin_feature(a.aux_at, f) + 2 * aux_step, aux_step, a.aux_fmt, there);
-      float v[16];
-      lin_get(w.stage, half, v);
-      const float(&v0)[8] = *reinterpret_cast<const float(*)[8]>(&v[0]);
-      const float(&v1)[8] = *reinterpret_cast<const float(*)[8]>(&v[8]);
-      const size_t i0 = to + 2 * half * out_step, i1 = i0 + out_step;
-      if (KIND == kLinForward) {
-        #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] += bias[j & 7];
-        if (a.pre) {
-          if (there[0]) store8(a.pre, i0, v0, a.fmt);
-          if (there[1]) store8(a.pre, i1, v1, a.fmt);
-        }
-        if (a.act != kActNone) with_act(a.act, [&](auto A) { act_all<decltype(A)::value>(v); });
-        if (a.aux) {
-          float y[16];
-          x.get(y, a.aux_fmt);
-          #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] += y[j];
-        }
-      }
-      if (KIND == kLinInput && a.aux) {
-        float y[16];
-        x.get(y, a.aux_fmt);
-        with_act(a.act, [&](auto A) { slope_all<decltype(A)::value>(v, y); });
-      }
-      if (there[0]) store8(a.out, i0, v0, a.out_fmt);
-      if (there[1]) store8(a.out, i1, v1, a.out_fmt);
+  float bias[COLS / 32];   // a column a lane: every lane reading all 32 took 1100 cycles a piece
+  #pragma unroll
+  for (int c = 0; c < COLS / 32; ++c) {
+    const int f = f0 + 32 * c + lane;
+    bias[c] = KIND == kLinForward && a.bias && f < a.cols ? load_elem(a.bias, f, a.bias_fmt) : 0.f;
+  }
+  if (lane == 0) {
+    bulk_wait_read();   // the last tile's boxes
+    if (a.aux) {
+      fetch(0);
+      if (two && COLS > 32) fetch(32);
     }
   }
-  return true;
+  if (!wait()) {   // loads beside D land before this warp leaves (with a limit)
+    if (a.aux && lane == 0 && rows_in)
+      for (int c = 0; c < (two ? COLS : 32) && f0 + c < a.cols; c += 32)
+        mbar_wait_budget(&e.bars[c >> 5], e.phases >> (c >> 5) & 1, kWaitBudgetCycles);
+    return false;
+  }
+  bool ok = true;
+  #pragma unroll 1
+  for (int c = 0; c < COLS; c += 32) {
+    float v[32];
+    {
+      uint32_t u[32];
+      tmem_ld32(taddr + c, u);
+      tmem_wait_ld();
+      #pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+    }
+    if (c + 32 == COLS) done();
+    const int f = f0 + c, i = two ? (c >> 5) & 1 : 0;
+    if (!rows_in || f >= a.cols) continue;
+    uint8_t* const slot = out_slot + 2048 * i;
+    if (!two && c > 0) {   // the last piece's boxes have been read
+      if (lane == 0) {
+        bulk_wait_read();
+        if (a.aux) fetch(c);
+      }
+      __syncwarp();
+    }
+    if (KIND == kLinForward && a.bias) {
+      const float own = COLS > 32 && c > 0 ? bias[COLS / 32 - 1] : bias[0];
+      #pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, own, j);
+    }
+    float x[32];
+    if (a.aux) {
+      ok = warp_all(mbar_wait(&e.bars[i], e.phases >> i & 1, abort_flag, a.status));
+      e.phases ^= 1u << i;
+      if (!ok) break;
+      lin_read(slot, x, a.aux_fmt);
+      __syncwarp();   // rows of different types do not lie at the same bytes
+    }
+    const int h = a.out_at.d ? f / a.out_at.d : 0, fh = f - h * a.out_at.d;
+    if (KIND == kLinForward) {
+      if (a.pre) {
+        lin_write(e.slot, v, a.fmt);
+        if (!out16) {   // its bytes are the output's as well
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_4d(e.pre, e.slot, fh, row0, h, b);
+            bulk_commit();
+            bulk_wait_read();
+          }
+          __syncwarp();
+        }
+      }
+      if (a.act != kActNone) with_act(a.act, [&](auto A) { act_all<decltype(A)::value>(v); });
+      if (a.aux) {
+        #pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += x[j];
+      }
+    }
+    if (KIND == kLinInput && a.aux) with_act(a.act, [&](auto A) { slope_all<decltype(A)::value>(v, x); });
+    lin_write(slot, v, a.out_fmt);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (KIND == kLinForward && a.pre && out16) tma_store_4d(e.pre, e.slot, fh, row0, h, b);
+      tma_store_4d(e.out, slot, fh, row0, h, b);
+      bulk_commit();
+    }
+  }
+  return ok;
 }
 
 // With the operands swapped: one feature f of T tokens from n, `count` of them there.

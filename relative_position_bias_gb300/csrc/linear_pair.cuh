@@ -26,7 +26,7 @@ struct PairSmem {
   static constexpr int NS = BN == 256 ? (KIND == kLinWeight ? 6 : 5) : 6;
   static constexpr int kEpi = NS * kStage;             // 4 KB an epilogue warp
   static constexpr int kBars = kEpi + pair_epi(KIND) * 4096;
-  static constexpr int kMisc = kBars + (2 * NS + 5) * 8;
+  static constexpr int kMisc = kBars + (2 * NS + 5 + 2 * pair_epi(KIND)) * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory");
 };
@@ -73,8 +73,7 @@ struct PairItem {
 
 template <int KIND, int BN, bool BF16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 1)
-    linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                       const __grid_constant__ LinArgs a) {
+    linear_pair_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
   using SM = PairSmem<KIND, BN>;
   constexpr int NS = SM::NS;
   constexpr bool A_MN = KIND == kLinWeight, B_MN = KIND != kLinForward;
@@ -88,20 +87,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
   uint64_t* acc_full = empty + NS;                                  // each CTA's [2]: a chain is complete
   uint64_t* acc_empty = acc_full + 2;                               // the even CTA's [2]: and has been read by both
   uint64_t* all_done = acc_empty + 2;
+  uint64_t* beside = all_done + 1;                                  // [warp][2]: boxes beside D
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::kMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   PairItem<BN> w(a, blockIdx.x >> 1, a.batches * a.m_tiles * a.n_tiles * a.pieces);
   if (threadIdx.x == 64) {
-    tma_prefetch_desc(&map_a);
-    tma_prefetch_desc(&map_b);
+    tma_prefetch_desc(&maps.a);
+    tma_prefetch_desc(&maps.b);
   }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < 2 * NS + 2; ++i) mbar_init(&full[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&acc_empty[i], 2 * pair_epi(KIND));
     mbar_init(all_done, 1);
+    for (int i = 0; i < 2 * pair_epi(KIND); ++i) mbar_init(&beside[i], 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -129,10 +130,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
           if (rank == 0) mbar_arrive_expect_tx(&full[st], 2 * SM::kStage);
           const uint32_t bar = full0 + 8 * st;
           at_a.step(smem + st * SM::kStage, [&](uint8_t* dst, int f, int row, int h, int bb) {
-            tma_load_4d_pair(dst, &map_a, bar, f, row, h, bb);
+            tma_load_4d_pair(dst, &maps.a, bar, f, row, h, bb);
           });
           at_b.step(smem + st * SM::kStage + SM::kA, [&](uint8_t* dst, int f, int row, int h, int bb) {
-            tma_load_4d_pair(dst, &map_b, bar, f, row, h, bb);
+            tma_load_4d_pair(dst, &maps.b, bar, f, row, h, bb);
           });
         }
       }
@@ -182,7 +183,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
     constexpr int COLS = BN / (pair_epi(KIND) / 4);
     const int quarter = warp & 3, col0 = COLS * ((warp - 4) >> 2);
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-    float4* stage = reinterpret_cast<float4*>(smem + SM::kEpi) + 256 * (warp - 4);
+    uint8_t* const slot4k = smem + SM::kEpi + 4096 * (warp - 4);
+    LinEpi epi = {slot4k, beside + 2 * (warp - 4), 0, &maps.out, &maps.aux, &maps.pre};
     const uint32_t empty0 = cluster_map(acc_empty, 0);
     int chain = 0;
     bool ok = true;
@@ -197,9 +199,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
       if (lane == 0) mbar_arrive_cluster_relaxed(empty0 + 8 * (chain & 1));
     };
     for (; ok && w.any; w.next(a)) {
-      const LinWarp lw = {stage, w.b, w.r0() + 128 * static_cast<int>(rank) + 32 * quarter, w.c0() + col0};
+      const int row0 = w.r0() + 128 * static_cast<int>(rank) + 32 * quarter, f0 = w.c0() + col0;
       if constexpr (!CHAINS) {
-        ok = lin_epilogue<KIND, COLS>(a, lw, tbase + BN * (chain & 1) + lanes + col0, wait, done);
+        ok = lin_epilogue<KIND, COLS>(a, epi, tbase + BN * (chain & 1) + lanes + col0, w.b, row0, f0, abort_flag, wait, done);
         ++chain;
       } else {
         float acc[COLS];
@@ -222,16 +224,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
         }
         if (!ok) break;
         void* to = a.parts ? static_cast<void*>(a.parts + static_cast<size_t>(w.piece) * a.rows * a.cols) : a.out;
-        const int fmt = a.parts ? kF32 : a.out_fmt, row = lw.row0 + (lane >> 1);
+        const int fmt = a.parts ? kF32 : a.out_fmt, row = row0 + (lane >> 1);
+        float4* stage = reinterpret_cast<float4*>(slot4k);
         #pragma unroll
         for (int c = 0; c < COLS; c += 16) {
-          // as lin_put and lin_get, 16 columns at a time for want of registers: two lanes a row
+          // through shared memory, so that two lanes have 16 columns of a row: 64 bytes a run
           __syncwarp();
           #pragma unroll
           for (int j = 0; j < 4; ++j)
             stage[lane * 4 + (j ^ ((lane >> 1) & 3))] = make_float4(acc[c + 4 * j], acc[c + 4 * j + 1], acc[c + 4 * j + 2], acc[c + 4 * j + 3]);
           __syncwarp();
-          const int f = lw.f0 + c + 8 * (lane & 1);
+          const int f = f0 + c + 8 * (lane & 1);
           #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int r = 16 * i + (lane >> 1), j = 2 * (lane & 1);
@@ -243,6 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
       }
     }
   }
+  bulk_wait_read();   // this thread's stores
   __syncwarp();
   tc_fence_before();
   cluster_sync_all_relaxed();

@@ -144,7 +144,7 @@ def test_linear_refusals(lib, call):
         assert call(lib, **bad) == CODES["DERA_ERR_NULL"], bad
     for bad in (dict(x=_x(FAKE_MISALIGNED)), dict(x=_x(st=60)), dict(w=FAKE_MISALIGNED)):
         assert call(lib, **bad) == CODES["DERA_ERR_ALIGN"], bad
-    for bad in (dict(x=_x(st=-64)), dict(x=_x(st=0)), dict(x=_x(sb=0)), dict(x=_x(sb=1 << 38))):
+    for bad in (dict(x=_x(st=-64)), dict(x=_x(st=0)), dict(x=_x(sb=0)), dict(x=_x(sb=1 << 37))):
         assert call(lib, **bad) == CODES["DERA_ERR_SHAPE"], bad
     assert call(lib, B=1, N=1, x=_x(sb=0, st=0, sh=0)) in PAST
     more = {} if call is _lin else dict(dx=_x(st=128, sh=64))

@@ -162,6 +162,28 @@ def test_activation_values_far_out():
             assert abs(s[3] - 0.5) <= 2.0 ** -20 and s[7] != s[7], (act, s)
 
 
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_a_nan_stays_alone(act):
+    """Neighbours share instructions, and gelu's a reciprocal (of the product of two arguments, so that last bits depend on the
+    neighbour): none of a NaN or an infinity."""
+    g = torch.Generator().manual_seed(11)
+    pre = torch.randn(64, generator=g).cuda()
+    one = torch.ones(64, device="cuda")
+    for k, bad in ((5, float("nan")), (8, float("inf")), (11, -float("inf")), (14, 3e38)):
+        pre[k] = bad
+    got = rpb.activation_backward(one, pre, act)
+    keep = torch.ones(64, dtype=torch.bool, device="cuda")
+    keep[[5, 8, 11, 14]] = False
+    u = pre[keep].double().cpu().numpy()
+    near(got[keep], ob.activation_slope(u, act), tol.slope(u, act) + 2.0 ** -24, act)
+    for N in (7, 200):   # and in the forward: a bias of such values makes whole columns of them
+        x = torch.zeros(N, 64, device="cuda", dtype=BF)
+        y = rpb.linear(x, torch.zeros(64, 64, device="cuda", dtype=BF), pre, activation=act, out_dtype=F32)
+        want = ob.activation(u, act)
+        near(y[:, keep], np.broadcast_to(want, (N, len(want))), rounding(want, F32) + tol.act(u, act), act)
+        assert y[:, 5].isnan().all()
+
+
 @pytest.mark.parametrize("N", [9, 200])
 def test_strides(N):
     """Slices of a packed buffer, batches and heads in any order, for input and gradient."""
