@@ -185,6 +185,9 @@ WeightPlan weight_plan(int out, int K, int steps, int sms) {
   return w;
 }
 
+// Columns of the epilogue's boxes (as the kernel takes them): 128 bytes of the output's type.
+int box_columns(dera_dtype out) { return out == DERA_F32 ? 32 : 64; }
+
 dera_status status_of(cudaError_t e) { return e == cudaSuccess ? DERA_OK : DERA_ERR_CUDA; }
 
 int sum_blocks(int sms) { return 2 * std::max(sms, 1); }
@@ -356,9 +359,10 @@ dera_status dera_linear(const dera_heads* x, const void* weight, const void* bia
   if (!p.turned) {
     const HeadsPtr ym = tok.of(rows_of(y, N, out_features), N), rm = {const_cast<char*>(static_cast<const char*>(residual)), ym.sb, ym.st, 0},
                    pm = {static_cast<char*>(pre), ym.sb, ym.st, 0};
-    if (!map_boxes(&m.out, ym, out_dtype, tok.B, tok.N, 1, out_features) ||
-        (residual && !map_boxes(&m.aux, rm, out_dtype, tok.B, tok.N, 1, out_features)) ||
-        (pre && !map_boxes(&m.pre, pm, in_dtype, tok.B, tok.N, 1, out_features)))
+    const int box = box_columns(out_dtype);
+    if (!map_boxes(&m.out, ym, out_dtype, tok.B, tok.N, 1, out_features, box) ||
+        (residual && !map_boxes(&m.aux, rm, out_dtype, tok.B, tok.N, 1, out_features, box)) ||
+        (pre && !map_boxes(&m.pre, pm, in_dtype, tok.B, tok.N, 1, out_features, box)))
       return DERA_ERR_CUDA;
   }
   return status_of(launch_linear_forward(m, a, p, static_cast<cudaStream_t>(stream)));
@@ -441,8 +445,9 @@ dera_status dera_linear_backward(const void* dy, const dera_heads* x, const void
     if (!map_tokens(mg, tok.of(gt, N), in_dtype, tok.B, tok.N, 1, out_features, p.turned ? p.bn : 128) ||
         !map_tokens(mw, rows_of(weight, out_features, K), in_dtype, 1, out_features, 1, K, 64))
       return DERA_ERR_CUDA;
-    if (!p.turned && (!map_boxes(&m.out, tok.of(dt, N), grad_dtype, tok.B, tok.N, h, d) ||
-                      (pt.data && !map_boxes(&m.aux, tok.of(pt, N), in_dtype, tok.B, tok.N, h, d))))
+    const int box = box_columns(grad_dtype);
+    if (!p.turned && (!map_boxes(&m.out, tok.of(dt, N), grad_dtype, tok.B, tok.N, h, d, box) ||
+                      (pt.data && !map_boxes(&m.aux, tok.of(pt, N), in_dtype, tok.B, tok.N, h, d, box))))
       return DERA_ERR_CUDA;
     DERA_TRY(status_of(launch_linear_input(m, a, p, s)));
   }

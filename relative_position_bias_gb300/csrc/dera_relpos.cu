@@ -174,15 +174,15 @@ bool map_tokens(CUtensorMap* m, const HeadsPtr& t, dera_dtype dt, int B, int N, 
   return make_map(m, t.data, tma_type(dt), 4, dims, strides, box);
 }
 
-bool map_boxes(CUtensorMap* m, const HeadsPtr& t, dera_dtype dt, int B, int N, int heads, int d) {
+bool map_boxes(CUtensorMap* m, const HeadsPtr& t, dera_dtype dt, int B, int N, int heads, int d, int cols) {
   const int size = dt == DERA_F32 ? 4 : 2;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(B)};
   auto bytes = [&](long long st) { return size * static_cast<cuuint64_t>(st > 0 ? st : d); };
   const cuuint64_t strides[3] = {bytes(t.st), bytes(t.sh), bytes(t.sb)};
-  const cuuint32_t box[4] = {32, 32, 1, 1};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(cols), 32, 1, 1};
   return make_map(m, t.data, dt == DERA_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : tma_type(dt), 4, dims, strides, box,
-                  size == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+                  size * cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // table [2L-1, d], one 128-row box per 64 columns (rows past 2L-1 read as zero)

@@ -41,8 +41,8 @@ bool map_keys(CUtensorMap* m, const void* p, dera_dtype t, int BH, int H, int W,
 // tokens [B, N, heads, d] by their strides (elements), read in boxes of 64 elements by `rows` tokens
 bool map_tokens(CUtensorMap* m, const HeadsPtr& t, dera_dtype dt, int B, int N, int heads, int d, int rows);
 
-// the same, any type, in boxes of 32 tokens x 32 elements (rows of 64 or 128 bytes, swizzled as wide)
-bool map_boxes(CUtensorMap* m, const HeadsPtr& t, dera_dtype dt, int B, int N, int heads, int d);
+// the same, any type, in boxes of 32 tokens x `cols` elements (rows of 64 or 128 bytes, swizzled as wide)
+bool map_boxes(CUtensorMap* m, const HeadsPtr& t, dera_dtype dt, int B, int N, int heads, int d, int cols);
 
 // A caller's workspace: large enough, 256-byte aligned, of device `dev`.
 dera_status check_workspace(const void* ws, size_t have, size_t need, int dev);

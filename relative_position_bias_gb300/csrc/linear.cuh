@@ -86,13 +86,13 @@ __device__ __forceinline__ void store_elem(void* p, size_t i, float x, int fmt) 
   else reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(pack_in(x, 0.f, fmt));
 }
 
-// An epilogue warp's part of a tile: 32 rows of D, COLS columns, 32 at a time, a row a lane as TMEM gives them.  What is read and
-// written beside D goes through 4 KB of shared memory a warp by TMA, in boxes of 32 rows x 32 columns (64 bytes a row in 16 bits, 128 in
-// fp32, swizzled so that lanes meet different banks): whole lines of memory, asynchronously, and edges are left to TMA.  (Plain
-// stores from this layout touch 32 lines an instruction, 216 us for 32768 x 1024 x 4096; turned in shared memory first they need
-// twice the shared-memory traffic and wait for it, 156, and 195 where gelu's argument is kept.)
+// An epilogue warp's part of a tile: 32 rows of D, COLS columns, a row a lane as TMEM gives them.  What is read and written beside D
+// goes through 8 KB of shared memory a warp by TMA, in boxes of 32 rows x 128 bytes (64 columns in 16 bits, 32 in fp32),
+// swizzled so that lanes meet different banks: whole lines of memory, asynchronously, and edges are left to TMA.  (Plain stores from
+// this layout touch 32 lines an instruction: 216 us for 32768 x 1024 x 4096; turned in shared memory first, 156, and 195 where gelu's
+// argument is kept.)
 struct LinEpi {
-  uint8_t* slot;       // 4 KB: [2][32 rows x 64 bytes] or [32 rows x 128 bytes]
+  uint8_t* slot;       // [2][32 rows x 128 bytes]
   uint64_t* bars;      // [2]: a box beside D landed
   uint32_t phases;     // bit i: of the next one
   const CUtensorMap* out;
@@ -100,34 +100,41 @@ struct LinEpi {
   const CUtensorMap* pre;
 };
 
-// 16-byte chunk c of this lane's row in a box of 64- or 128-byte rows.
-template <bool WIDE>
+// 16-byte chunk c of this lane's row in a box of 128-byte (or, narrow, 64-byte) rows.
 __device__ __forceinline__ uint4* lin_chunk(uint8_t* slot, int c) {
   const int lane = threadIdx.x & 31;
-  return reinterpret_cast<uint4*>(slot + (WIDE ? lane * 128 + ((c ^ (lane & 7)) << 4) : lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)));
+  return reinterpret_cast<uint4*>(slot + lane * 128 + ((c ^ (lane & 7)) << 4));
 }
-__device__ __forceinline__ void lin_write(uint8_t* slot, const float (&v)[32], int fmt) {
+__device__ __forceinline__ uint4* lin_chunk_narrow(uint8_t* slot, int c) {
+  const int lane = threadIdx.x & 31;
+  return reinterpret_cast<uint4*>(slot + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4));
+}
+// 32 columns of this lane's row: of fp32 a whole box; of 16 bits half `half` of one, or a narrow one.
+__device__ __forceinline__ void lin_write(uint8_t* slot, const float* v, int fmt, int half, bool narrow) {
   if (fmt == kF32) {
     #pragma unroll
     for (int c = 0; c < 8; ++c)
-      *lin_chunk<true>(slot, c) = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                                             __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+      *lin_chunk(slot, c) = make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                                       __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
   } else {
     #pragma unroll
-    for (int c = 0; c < 4; ++c) *lin_chunk<false>(slot, c) = pack8(*reinterpret_cast<const float(*)[8]>(&v[8 * c]), fmt);
+    for (int c = 0; c < 4; ++c)
+      *(narrow ? lin_chunk_narrow(slot, c) : lin_chunk(slot, c + 4 * half)) =
+          pack8(*reinterpret_cast<const float(*)[8]>(&v[8 * c]), fmt);
   }
 }
-__device__ __forceinline__ void lin_read(uint8_t* slot, float (&x)[32], int fmt) {
+__device__ __forceinline__ void lin_read(uint8_t* slot, float (&x)[32], int fmt, int half, bool narrow) {
   if (fmt == kF32) {
     #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const uint4 u = *lin_chunk<true>(slot, c);
+      const uint4 u = *lin_chunk(slot, c);
       x[4 * c] = __uint_as_float(u.x), x[4 * c + 1] = __uint_as_float(u.y);
       x[4 * c + 2] = __uint_as_float(u.z), x[4 * c + 3] = __uint_as_float(u.w);
     }
   } else {
     #pragma unroll
-    for (int c = 0; c < 4; ++c) unpack8(*lin_chunk<false>(slot, c), *reinterpret_cast<float(*)[8]>(&x[8 * c]), fmt);
+    for (int c = 0; c < 4; ++c)
+      unpack8(*(narrow ? lin_chunk_narrow(slot, c) : lin_chunk(slot, c + 4 * half)), *reinterpret_cast<float(*)[8]>(&x[8 * c]), fmt);
   }
 }
 
@@ -135,18 +142,26 @@ __device__ __forceinline__ void lin_read(uint8_t* slot, float (&x)[32], int fmt)
 template <int KIND, int COLS, class Wait, class Done>
 __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32_t taddr, int b, int row0, int f0, volatile int* abort_flag,
                                              Wait&& wait, Done&& done) {
-  static_assert(COLS == 32 || COLS == 64, "one or two pieces");
+  static_assert(COLS == 64 || COLS == 128, "one or two groups of 64 columns");
+  constexpr int GROUPS = COLS / 64;
   const int lane = threadIdx.x & 31;
-  // two boxes at once where both are of 16 bits and the sum before the activation needs none; else one after another
-  const bool out16 = a.out_fmt != kF32, two = out16 && !a.pre;
-  uint8_t* const out_slot = e.slot + (out16 && a.pre ? 2048 : 0);
+  // 16-bit output: a box a group of 64 columns, each in a slot of its own, or the output's in one and the activation's argument in the
+  // other.  fp32: a box each half of a group; an argument kept goes through the half's slot first.
+  const bool out16 = a.out_fmt != kF32, own = out16 && !a.pre;
   const bool rows_in = row0 < a.rows;
-  auto fetch = [&](int c) {   // by one lane: what is beside columns c of D
-    const int f = f0 + c, i = two ? (c >> 5) & 1 : 0;
+  auto fetch = [&](int f, int i, int bytes) {   // by one lane: the box beside D from column f into slot i
     if (!rows_in || f >= a.cols) return;
     const int h = a.aux_at.d ? f / a.aux_at.d : 0;
-    mbar_arrive_expect_tx(&e.bars[i], a.aux_fmt == kF32 ? 4096 : 2048);
-    tma_load_4d(out_slot + 2048 * i, e.aux, &e.bars[i], f - h * a.aux_at.d, row0, h, b);
+    mbar_arrive_expect_tx(&e.bars[i], bytes);
+    tma_load_4d(e.slot + 4096 * i, e.aux, &e.bars[i], f - h * a.aux_at.d, row0, h, b);
+  };
+  auto fetch_group = [&](int f) {
+    if (out16) {
+      fetch(f, 0, 4096);
+    } else {
+      fetch(f, 0, a.aux_fmt == kF32 ? 4096 : 2048);
+      fetch(f + 32, 1, a.aux_fmt == kF32 ? 4096 : 2048);
+    }
   };
   float bias[COLS / 32];   // a column a lane: every lane reading all 32 took 1100 cycles a piece
   #pragma unroll
@@ -157,83 +172,97 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32
   if (lane == 0) {
     bulk_wait_read();   // the last tile's boxes
     if (a.aux) {
-      fetch(0);
-      if (two && COLS > 32) fetch(32);
+      fetch_group(f0);
+      if (own && GROUPS > 1) fetch(f0 + 64, 1, 4096);
     }
   }
   if (!wait()) {   // loads beside D land before this warp leaves (with a limit)
     if (a.aux && lane == 0 && rows_in)
-      for (int c = 0; c < (two ? COLS : 32) && f0 + c < a.cols; c += 32)
-        mbar_wait_budget(&e.bars[c >> 5], e.phases >> (c >> 5) & 1, kWaitBudgetCycles);
+      for (int i = 0; i < 2; ++i)
+        if (f0 + (own ? 64 : 32) * i < a.cols && (i == 0 || !out16 || (own && GROUPS > 1)))
+          mbar_wait_budget(&e.bars[i], e.phases >> i & 1, kWaitBudgetCycles);
     return false;
   }
-  bool ok = true;
   #pragma unroll 1
-  for (int c = 0; c < COLS; c += 32) {
-    float v[32];
-    {
-      uint32_t u[32];
-      tmem_ld32(taddr + c, u);
-      tmem_wait_ld();
-      #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
-    }
-    if (c + 32 == COLS) done();
-    const int f = f0 + c, i = two ? (c >> 5) & 1 : 0;
-    if (!rows_in || f >= a.cols) continue;
-    uint8_t* const slot = out_slot + 2048 * i;
-    if (!two && c > 0) {   // the last piece's boxes have been read
+  for (int g = 0; g < GROUPS; ++g) {
+    uint32_t u[2][32];
+    tmem_ld32(taddr + 64 * g, u[0]);
+    tmem_ld32(taddr + 64 * g + 32, u[1]);
+    tmem_wait_ld();
+    if (g + 1 == GROUPS) done();
+    const int fg = f0 + 64 * g;
+    if (!rows_in || fg >= a.cols) continue;
+    if (g > 0 && !own) {   // the last group's boxes have been read
       if (lane == 0) {
         bulk_wait_read();
-        if (a.aux) fetch(c);
+        if (a.aux) fetch_group(fg);
       }
       __syncwarp();
     }
-    if (KIND == kLinForward && a.bias) {
-      const float own = COLS > 32 && c > 0 ? bias[COLS / 32 - 1] : bias[0];
+    const int h = a.out_at.d ? fg / a.out_at.d : 0, fh = fg - h * a.out_at.d;
+    #pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int f = fg + 32 * half;
+      if (f >= a.cols) break;
+      const int i = out16 ? (own ? g : 0) : half;   // its slot
+      uint8_t* const slot = e.slot + 4096 * i;
+      float v[32];
       #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, own, j);
-    }
-    float x[32];
-    if (a.aux) {
-      ok = warp_all(mbar_wait(&e.bars[i], e.phases >> i & 1, abort_flag, a.status));
-      e.phases ^= 1u << i;
-      if (!ok) break;
-      lin_read(slot, x, a.aux_fmt);
-      __syncwarp();   // rows of different types do not lie at the same bytes
-    }
-    const int h = a.out_at.d ? f / a.out_at.d : 0, fh = f - h * a.out_at.d;
-    if (KIND == kLinForward) {
-      if (a.pre) {
-        lin_write(e.slot, v, a.fmt);
-        if (!out16) {   // its bytes are the output's as well
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_4d(e.pre, e.slot, fh, row0, h, b);
-            bulk_commit();
-            bulk_wait_read();
+      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[half][j]);
+      if (KIND == kLinForward && a.bias) {
+        const float at = GROUPS > 1 && g > 0 ? bias[COLS / 32 - 2 + half] : bias[half];
+        #pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, at, j);
+      }
+      float x[32];
+      if (a.aux) {
+        if (!out16 || half == 0) {
+          const bool ok = warp_all(mbar_wait(&e.bars[i], e.phases >> i & 1, abort_flag, a.status));
+          e.phases ^= 1u << i;
+          if (!ok) {
+            if (!out16 && half == 0 && lane == 0 && f + 32 < a.cols) mbar_wait_budget(&e.bars[1], e.phases >> 1 & 1, kWaitBudgetCycles);
+            if (own && g + 1 < GROUPS && lane == 0 && fg + 64 < a.cols) mbar_wait_budget(&e.bars[1], e.phases >> 1 & 1, kWaitBudgetCycles);
+            return false;
           }
-          __syncwarp();
+        }
+        lin_read(slot, x, a.aux_fmt, half, !out16);
+        if (!out16) __syncwarp();   // rows of different types do not lie at the same bytes
+      }
+      if (KIND == kLinForward) {
+        if (a.pre) {
+          if (out16) {
+            lin_write(e.slot + 4096, v, a.fmt, half, false);
+          } else {
+            lin_write(slot, v, a.fmt, 0, true);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_4d(e.pre, slot, fh + 32 * half, row0, h, b);
+              bulk_commit();
+              bulk_wait_read();
+            }
+            __syncwarp();
+          }
+        }
+        if (a.act != kActNone) with_act(a.act, [&](auto A) { act_all<decltype(A)::value>(v); });
+        if (a.aux) {
+          #pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] += x[j];
         }
       }
-      if (a.act != kActNone) with_act(a.act, [&](auto A) { act_all<decltype(A)::value>(v); });
-      if (a.aux) {
-        #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += x[j];
+      if (KIND == kLinInput && a.aux) with_act(a.act, [&](auto A) { slope_all<decltype(A)::value>(v, x); });
+      lin_write(slot, v, a.out_fmt, half, false);
+      if (out16 && half == 0 && f + 32 < a.cols) continue;   // the other half of the box
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (KIND == kLinForward && a.pre && out16) tma_store_4d(e.pre, e.slot + 4096, fh, row0, h, b);
+        tma_store_4d(e.out, slot, out16 ? fh : fh + 32 * half, row0, h, b);
+        bulk_commit();
       }
     }
-    if (KIND == kLinInput && a.aux) with_act(a.act, [&](auto A) { slope_all<decltype(A)::value>(v, x); });
-    lin_write(slot, v, a.out_fmt);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      if (KIND == kLinForward && a.pre && out16) tma_store_4d(e.pre, e.slot, fh, row0, h, b);
-      tma_store_4d(e.out, slot, fh, row0, h, b);
-      bulk_commit();
-    }
   }
-  return ok;
+  return true;
 }
 
 // With the operands swapped: one feature f of T tokens from n, `count` of them there.

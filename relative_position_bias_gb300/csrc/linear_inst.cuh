@@ -32,7 +32,7 @@ static cudaError_t launch_lin_pair(const LinMaps& m, const LinArgs& a, int pairs
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = prepare_kernel(kernel, PairSmem<KIND, BN>::kAlloc, 0, done);
   if (e != cudaSuccess) return e;
-  kernel<<<2 * pairs, pair_threads(KIND), PairSmem<KIND, BN>::kAlloc, s>>>(m, a);
+  kernel<<<2 * pairs, kPairThreads, PairSmem<KIND, BN>::kAlloc, s>>>(m, a);
   return cudaGetLastError();
 }
 

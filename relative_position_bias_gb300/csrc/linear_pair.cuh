@@ -13,10 +13,11 @@
 
 namespace dera {
 
-// A warp that loads, one that multiplies, two that wait, and the epilogue's: sixteen, four a scheduler, since a warp alone
-// issues in a sixth of its cycles; eight for the weight's gradient, which keeps 128 columns of sums a thread.
-constexpr int pair_epi(int kind) { return kind == kLinWeight ? 8 : 16; }
-constexpr int pair_threads(int kind) { return 128 + 32 * pair_epi(kind); }
+// A warp that loads, one that multiplies, two that wait, and eight of the epilogue.  Sixteen with half of the columns each end a tile
+// sooner, but take so much of TMEM and of the shared memory at once that the products beside them wait: 169 us for 32768 x 1024 x 4096, with
+// eight 155.
+constexpr int kPairEpi = 8;
+constexpr int kPairThreads = 128 + 32 * kPairEpi;
 constexpr int kLinChain = 64;
 
 template <int KIND, int BN>
@@ -25,8 +26,8 @@ struct PairSmem {
   static constexpr int kStage = kA + kB;
   static constexpr int NS = BN == 256 ? (KIND == kLinWeight ? 6 : 5) : 6;
   static constexpr int kEpi = NS * kStage;             // 4 KB an epilogue warp
-  static constexpr int kBars = kEpi + pair_epi(KIND) * 4096;
-  static constexpr int kMisc = kBars + (2 * NS + 5 + 2 * pair_epi(KIND)) * 8;
+  static constexpr int kBars = kEpi + kPairEpi * (KIND == kLinWeight ? 4096 : 8192);
+  static constexpr int kMisc = kBars + (2 * NS + 5 + 2 * kPairEpi) * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory");
 };
@@ -72,7 +73,7 @@ struct PairItem {
 };
 
 template <int KIND, int BN, bool BF16>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
   using SM = PairSmem<KIND, BN>;
   constexpr int NS = SM::NS;
@@ -88,7 +89,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
   uint64_t* acc_empty = acc_full + 2;                               // the even CTA's [2]: and has been read by both
   uint64_t* all_done = acc_empty + 2;
   uint64_t* beside = all_done + 1;                                  // [warp][2]: boxes beside D
-  uint32_t* slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::kMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -100,19 +101,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < 2 * NS + 2; ++i) mbar_init(&full[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&acc_empty[i], 2 * pair_epi(KIND));
+    for (int i = 0; i < 2; ++i) mbar_init(&acc_empty[i], 2 * kPairEpi);
     mbar_init(all_done, 1);
-    for (int i = 0; i < 2 * pair_epi(KIND); ++i) mbar_init(&beside[i], 1);
+    for (int i = 0; i < 2 * kPairEpi; ++i) mbar_init(&beside[i], 1);
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc_pair(slot, 2 * BN);
+    tmem_alloc_pair(tmem_slot, 2 * BN);
     tmem_relinquish_pair();
   }
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
-  const uint32_t tbase = *slot;
+  const uint32_t tbase = *tmem_slot;
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------- loads: each CTA its rows
@@ -180,11 +181,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
     }
   } else if (warp >= 4) {
     // --------------------------------------------------------------- epilogue: a warp 32 rows of its columns
-    constexpr int COLS = BN / (pair_epi(KIND) / 4);
+    constexpr int COLS = BN / (kPairEpi / 4);
     const int quarter = warp & 3, col0 = COLS * ((warp - 4) >> 2);
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-    uint8_t* const slot4k = smem + SM::kEpi + 4096 * (warp - 4);
-    LinEpi epi = {slot4k, beside + 2 * (warp - 4), 0, &maps.out, &maps.aux, &maps.pre};
+    uint8_t* const slot = smem + SM::kEpi + (CHAINS ? 4096 : 8192) * (warp - 4);
+    LinEpi epi = {slot, beside + 2 * (warp - 4), 0, &maps.out, &maps.aux, &maps.pre};
     const uint32_t empty0 = cluster_map(acc_empty, 0);
     int chain = 0;
     bool ok = true;
@@ -225,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(KIND), 
         if (!ok) break;
         void* to = a.parts ? static_cast<void*>(a.parts + static_cast<size_t>(w.piece) * a.rows * a.cols) : a.out;
         const int fmt = a.parts ? kF32 : a.out_fmt, row = row0 + (lane >> 1);
-        float4* stage = reinterpret_cast<float4*>(slot4k);
+        float4* stage = reinterpret_cast<float4*>(slot);
         #pragma unroll
         for (int c = 0; c < COLS; c += 16) {
           // through shared memory, so that two lanes have 16 columns of a row: 64 bytes a run
