@@ -93,6 +93,7 @@ __device__ __forceinline__ void store_elem(void* p, size_t i, float x, int fmt) 
 // argument is kept.)
 struct LinEpi {
   uint8_t* slot;       // [2][32 rows x 128 bytes]
+  float* row;          // [32]
   uint64_t* bars;      // [2]: a box beside D landed
   uint32_t phases;     // bit i: of the next one
   const CUtensorMap* out;
@@ -163,7 +164,7 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32
       fetch(f + 32, 1, a.aux_fmt == kF32 ? 4096 : 2048);
     }
   };
-  float bias[COLS / 32];   // a column a lane: every lane reading all 32 took 1100 cycles a piece
+  float bias[COLS / 32];   // a column a lane (every lane reading all 32 from memory took 1100 cycles a half group, shuffles 550)
   #pragma unroll
   for (int c = 0; c < COLS / 32; ++c) {
     const int f = f0 + 32 * c + lane;
@@ -211,8 +212,14 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32
       for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[half][j]);
       if (KIND == kLinForward && a.bias) {
         const float at = GROUPS > 1 && g > 0 ? bias[COLS / 32 - 2 + half] : bias[half];
+        __syncwarp();
+        e.row[lane] = at;
+        __syncwarp();
         #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, at, j);
+        for (int j = 0; j < 8; ++j) {
+          const float4 y = reinterpret_cast<const float4*>(e.row)[j];
+          v[4 * j] += y.x, v[4 * j + 1] += y.y, v[4 * j + 2] += y.z, v[4 * j + 3] += y.w;
+        }
       }
       float x[32];
       if (a.aux) {

@@ -26,7 +26,8 @@ struct PairSmem {
   static constexpr int kStage = kA + kB;
   static constexpr int NS = BN == 256 ? (KIND == kLinWeight ? 6 : 5) : 6;
   static constexpr int kEpi = NS * kStage;             // 4 KB an epilogue warp
-  static constexpr int kBars = kEpi + kPairEpi * (KIND == kLinWeight ? 4096 : 8192);
+  static constexpr int kRow = kEpi + kPairEpi * (KIND == kLinWeight ? 4096 : 8192);
+  static constexpr int kBars = kRow + kPairEpi * 128;
   static constexpr int kMisc = kBars + (2 * NS + 5 + 2 * kPairEpi) * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory");
@@ -185,7 +186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int quarter = warp & 3, col0 = COLS * ((warp - 4) >> 2);
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
     uint8_t* const slot = smem + SM::kEpi + (CHAINS ? 4096 : 8192) * (warp - 4);
-    LinEpi epi = {slot, beside + 2 * (warp - 4), 0, &maps.out, &maps.aux, &maps.pre};
+    LinEpi epi = {slot, reinterpret_cast<float*>(smem + SM::kRow) + 32 * (warp - 4), beside + 2 * (warp - 4), 0, &maps.out, &maps.aux, &maps.pre};
     const uint32_t empty0 = cluster_map(acc_empty, 0);
     int chain = 0;
     bool ok = true;
