@@ -190,15 +190,20 @@ int box_columns(dera_dtype out) { return out == DERA_F32 ? 32 : 64; }
 
 dera_status status_of(cudaError_t e) { return e == cudaSuccess ? DERA_OK : DERA_ERR_CUDA; }
 
-int sum_blocks(int sms) { return 2 * std::max(sms, 1); }
+// Partial rows of dy's column sums: four blocks an SM over all columns (256 a block), each with 32 rows or more.
+int sum_blocks(long long rows, int out, int sms) {
+  return static_cast<int>(std::min<long long>((rows + 31) / 32, std::max(1, 4 * sms / ceil_div(out, 256))));
+}
 
 // Workspace of the backward: the column sums' partial rows, then the pieces of dW.
-size_t sums_bytes(int out, int sms) { return align256(static_cast<size_t>(sum_blocks(sms)) * out * sizeof(float)); }
+size_t sums_bytes(long long rows, int out, int sms) {
+  return align256(static_cast<size_t>(sum_blocks(rows, out, sms)) * out * sizeof(float));
+}
 size_t linear_backward_workspace(int B, int N, int K, int out, int sms) {
   // whether the batches merge or not
   const long long one = (static_cast<long long>(B) * N + 63) / 64, each = static_cast<long long>(B) * ceil_div(N, 64);
   const long long most = 0x7fffffff;
-  return sums_bytes(out, sms) + std::max(weight_plan(out, K, static_cast<int>(std::min(one, most)), sms).bytes,
+  return sums_bytes(static_cast<long long>(B) * N, out, sms) + std::max(weight_plan(out, K, static_cast<int>(std::min(one, most)), sms).bytes,
                                          weight_plan(out, K, static_cast<int>(std::min(each, most)), sms).bytes);
 }
 
@@ -451,6 +456,16 @@ dera_status dera_linear_backward(const void* dy, const dera_heads* x, const void
       return DERA_ERR_CUDA;
     DERA_TRY(status_of(launch_linear_input(m, a, p, s)));
   }
+  LinJoin join = {};
+  if (dbias) {
+    const long long rows = static_cast<long long>(B) * N;
+    join.sum_rows = sum_blocks(rows, out_features, sms);
+    join.sums = static_cast<float*>(workspace);
+    join.db = dbias;
+    join.out = out_features;
+    DERA_TRY(status_of(launch_column_sums(dy, rows, out_features, fmt_of(in_dtype), static_cast<float*>(workspace),
+                                          join.sum_rows, s)));
+  }
   if (dweight) {
     int h = heads, d = head_dim;
     join_heads(xt, &h, &d);
@@ -467,22 +482,21 @@ dera_status dera_linear_backward(const void* dy, const dera_heads* x, const void
     a.out_fmt = fmt_of(weight_grad_dtype);
     const WeightPlan w = weight_plan(out_features, K, a.steps, sms);
     if (!cut(&a, w.p, 1, out_features, K)) return DERA_ERR_SHAPE;
-    if (w.p.pieces > 1) a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums_bytes(out_features, sms));
+    if (w.p.pieces > 1) a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums_bytes(static_cast<long long>(B) * N, out_features, sms));
     LinMaps m = {};
     if (!map_tokens(&m.a, tok.of(gt, N), in_dtype, tok.B, tok.N, 1, out_features, 64) ||
         !map_tokens(&m.b, tok.of(xt, N), in_dtype, tok.B, tok.N, h, d, 64))
       return DERA_ERR_CUDA;
     DERA_TRY(status_of(launch_linear_weight(m, a, w.p, s)));
-    if (w.p.pieces > 1)
-      DERA_TRY(status_of(launch_sum_pieces(a.parts, w.p.pieces, static_cast<long long>(out_features) * K, dweight, a.out_fmt, s)));
+    if (w.p.pieces > 1) {
+      join.parts = a.parts;
+      join.dw = dweight;
+      join.n = static_cast<long long>(out_features) * K;
+      join.pieces = w.p.pieces;
+      join.dw_fmt = a.out_fmt;
+    }
   }
-  if (dbias) {
-    float* parts = static_cast<float*>(workspace);
-    const long long rows = static_cast<long long>(B) * N;
-    const int blocks = static_cast<int>(std::min<long long>((rows + 7) / 8, sum_blocks(sms)));
-    DERA_TRY(status_of(launch_column_sums(dy, rows, out_features, fmt_of(in_dtype), parts, blocks, s)));
-    DERA_TRY(status_of(launch_partial_rows(parts, blocks, out_features, out_features, dbias, nullptr, s)));
-  }
+  if (join.dw || join.db) DERA_TRY(status_of(launch_linear_join(join, s)));
   return DERA_OK;
 }
 

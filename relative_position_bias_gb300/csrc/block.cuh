@@ -97,8 +97,17 @@ struct LinPlan {
   int pairs;             // pairs of CTAs that share tiles of 256 rows (0: turned)
   int pieces, piece_steps;
 };
-// out[i] = the sum of `pieces` arrays of n values, in order
-cudaError_t launch_sum_pieces(const float* parts, int pieces, long long n, void* out, int out_fmt, cudaStream_t s);
+// The end of a backward: dW from its pieces, and db from its partial rows (either may be absent).
+struct LinJoin {
+  const float* parts;    // [pieces][n]
+  void* dw;
+  long long n;           // a multiple of 8
+  int pieces, dw_fmt;
+  const float* sums;     // [sum_rows][out]
+  float* db;
+  int sum_rows, out;
+};
+cudaError_t launch_linear_join(const LinJoin& j, cudaStream_t s);
 cudaError_t launch_linear_forward(const LinMaps& m, const LinArgs& a, const LinPlan& p, cudaStream_t s);
 cudaError_t launch_linear_input(const LinMaps& m, const LinArgs& a, const LinPlan& p, cudaStream_t s);
 cudaError_t launch_linear_weight(const LinMaps& m, const LinArgs& a, const LinPlan& p, cudaStream_t s);

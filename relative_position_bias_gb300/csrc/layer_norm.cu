@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(256) act_backward_kernel(const ActArgs a) {
 template <int ACT>
 static cudaError_t act_backward(const ActArgs& a, int sms, cudaStream_t s) {
   const bool vec = a.n % 8 == 0;
-  const long long blocks = std::min(ceil_div(a.n, vec ? 2048 : 256), static_cast<long long>(std::max(sms, 1)) * 16);
+  const long long blocks = std::min(ceil_div(a.n, vec ? 2048 : 256), static_cast<long long>(std::max(sms, 1)) * 64);
   if (vec) act_backward_kernel<ACT, true><<<static_cast<int>(blocks), 256, 0, s>>>(a);
   else act_backward_kernel<ACT, false><<<static_cast<int>(blocks), 256, 0, s>>>(a);
   return cudaGetLastError();

@@ -5,7 +5,6 @@ namespace dera {
 // Partial sums of a matrix's columns: block i adds every gridDim.x-th run of 32 rows.  A warp reads 32 chunks of
 // eight columns of one row at a time.
 __global__ void __launch_bounds__(256) column_sums_kernel(const void* g, long long rows, int cols, int fmt, float* parts) {
-  grid_launch_dependents();
   const int c = (blockIdx.y * 32 + (threadIdx.x & 31)) * 8, w = threadIdx.x >> 5;
   __shared__ float red[8][256];
   float s[8] = {};
@@ -33,25 +32,46 @@ cudaError_t launch_linear_weight(const LinMaps& m, const LinArgs& a, const LinPl
   return launch_lin_all<kLinWeight>(m, a, p, s);
 }
 
-// The pieces of a split contraction, added in order.
-__global__ void __launch_bounds__(256) sum_pieces_kernel(const float* parts, int pieces, long long n, void* out, int out_fmt) {
-  grid_wait_prerequisites();   // every piece is written
-  const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (i >= n) return;
-  float v[8], x[8];
-  load8(parts, i, v, kF32);
-  #pragma unroll 4
-  for (int p = 1; p < pieces; ++p) {
-    load8(parts, static_cast<size_t>(p) * n + i, x, kF32);
-    #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += x[e];
+// Blocks of 256 threads: the first `dw_blocks` add the pieces of eight neighbouring elements a thread, in order; the others the partial
+// rows of 32 columns of dy's sums, eight runs of rows a block, in a fixed order.
+__global__ void __launch_bounds__(256) linear_join_kernel(const LinJoin j, int dw_blocks) {
+  __shared__ float red[8][33];
+  grid_wait_prerequisites();   // every piece and every partial row is written
+  if (static_cast<int>(blockIdx.x) < dw_blocks) {
+    const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 8;
+    if (i >= j.n) return;
+    float v[8], x[8];
+    load8(j.parts, i, v, kF32);
+    #pragma unroll 4
+    for (int p = 1; p < j.pieces; ++p) {
+      load8(j.parts, static_cast<size_t>(p) * j.n + i, x, kF32);
+      #pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += x[e];
+    }
+    store8(j.dw, i, v, j.dw_fmt);
+    return;
   }
-  store8(out, i, v, out_fmt);
+  const int lane = threadIdx.x & 31, run = threadIdx.x >> 5, c = (blockIdx.x - dw_blocks) * 32 + lane;
+  float v = 0.f;
+  if (c < j.out) {
+    #pragma unroll 8
+    for (int r = run; r < j.sum_rows; r += 8) v += j.sums[static_cast<size_t>(r) * j.out + c];
+  }
+  red[run][lane] = v;
+  __syncthreads();
+  if (run == 0 && c < j.out) {
+    float s = 0.f;
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) s += red[i][lane];
+    j.db[c] = s;
+  }
 }
 
-cudaError_t launch_sum_pieces(const float* parts, int pieces, long long n, void* out, int out_fmt, cudaStream_t s) {
-  return launch_early(sum_pieces_kernel, dim3(static_cast<unsigned>((n + 2047) / 2048)), dim3(256), 0, s, parts, pieces, n,
-                      out, out_fmt);
+cudaError_t launch_linear_join(const LinJoin& j, cudaStream_t s) {
+  const long long dw_blocks = j.dw ? (j.n + 2047) / 2048 : 0;
+  const int db_blocks = j.db ? (j.out + 31) / 32 : 0;
+  return launch_early(linear_join_kernel, dim3(static_cast<unsigned>(dw_blocks + db_blocks)), dim3(256), 0, s, j,
+                      static_cast<int>(dw_blocks));
 }
 
 cudaError_t launch_column_sums(const void* g, long long rows, int cols, int fmt, float* parts, int blocks, cudaStream_t s) {
