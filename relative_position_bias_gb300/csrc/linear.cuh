@@ -87,13 +87,13 @@ __device__ __forceinline__ void store_elem(void* p, size_t i, float x, int fmt) 
 }
 
 // An epilogue warp's part of a tile: 32 rows of D, COLS columns, a row a lane as TMEM gives them.  What is read and written beside D
-// goes through 8 KB of shared memory a warp by TMA, in boxes of 32 rows x 128 bytes (64 columns in 16 bits, 32 in fp32),
+// goes through shared memory by TMA, in boxes of 32 rows x 128 bytes (64 columns in 16 bits, 32 in fp32),
 // swizzled so that lanes meet different banks: whole lines of memory, asynchronously, and edges are left to TMA.  (Plain stores from
 // this layout touch 32 lines an instruction: 216 us for 32768 x 1024 x 4096; turned in shared memory first, 156, and 195 where gelu's
 // argument is kept.)
 struct LinEpi {
-  uint8_t* slot;       // [2][32 rows x 128 bytes]
-  float* row;          // [32]
+  uint8_t* slot;       // [SLOTS][32 rows x 128 bytes]
+  float* row;          // [32] (forward)
   uint64_t* bars;      // [2]: a box beside D landed
   uint32_t phases;     // bit i: of the next one
   const CUtensorMap* out;
@@ -139,30 +139,29 @@ __device__ __forceinline__ void lin_read(uint8_t* slot, float (&x)[32], int fmt,
   }
 }
 
-// wait() returns whether D is complete (of the whole warp), done() says that it has been read.
-template <int KIND, int COLS, class Wait, class Done>
+// wait() returns whether D is complete (of the whole warp), done() says that it has been read.  SLOTS: of 4 KB, one or two a warp.
+//   16-bit output            a box a group of 64 columns, with two slots each group's its own
+//   ... and an argument      a slot each (the forward has two)
+//   fp32 output              a box a half group, with two slots its own; an argument goes through the half's slot first
+template <int KIND, int COLS, int SLOTS, class Wait, class Done>
 __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32_t taddr, int b, int row0, int f0, volatile int* abort_flag,
                                              Wait&& wait, Done&& done) {
-  static_assert(COLS == 64 || COLS == 128, "one or two groups of 64 columns");
+  static_assert(COLS == 64 || (COLS == 128 && SLOTS == 2), "one or two groups of 64 columns");
+  static_assert(KIND == kLinInput || SLOTS == 2, "room for the activation's argument");
   constexpr int GROUPS = COLS / 64;
   const int lane = threadIdx.x & 31;
-  // 16-bit output: a box a group of 64 columns, each in a slot of its own, or the output's in one and the activation's argument in the
-  // other.  fp32: a box each half of a group; an argument kept goes through the half's slot first.
-  const bool out16 = a.out_fmt != kF32, own = out16 && !a.pre;
+  const bool out16 = a.out_fmt != kF32, own = out16 && !(KIND == kLinForward && a.pre);
+  const bool halves = !out16;   // a box a half group
   const bool rows_in = row0 < a.rows;
-  auto fetch = [&](int f, int i, int bytes) {   // by one lane: the box beside D from column f into slot i
+  auto fetch = [&](int f, int i) {   // by one lane: the box beside D from column f into slot i
     if (!rows_in || f >= a.cols) return;
     const int h = a.aux_at.d ? f / a.aux_at.d : 0;
-    mbar_arrive_expect_tx(&e.bars[i], bytes);
+    mbar_arrive_expect_tx(&e.bars[i], halves && a.aux_fmt != kF32 ? 2048 : 4096);
     tma_load_4d(e.slot + 4096 * i, e.aux, &e.bars[i], f - h * a.aux_at.d, row0, h, b);
   };
   auto fetch_group = [&](int f) {
-    if (out16) {
-      fetch(f, 0, 4096);
-    } else {
-      fetch(f, 0, a.aux_fmt == kF32 ? 4096 : 2048);
-      fetch(f + 32, 1, a.aux_fmt == kF32 ? 4096 : 2048);
-    }
+    fetch(f, 0);
+    if (SLOTS == 2 && halves) fetch(f + 32, 1);
   };
   float bias[COLS / 32];   // a column a lane (every lane reading all 32 from memory took 1100 cycles a half group, shuffles 550)
   #pragma unroll
@@ -170,46 +169,66 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32
     const int f = f0 + 32 * c + lane;
     bias[c] = KIND == kLinForward && a.bias && f < a.cols ? load_elem(a.bias, f, a.bias_fmt) : 0.f;
   }
-  if (lane == 0) {
-    bulk_wait_read();   // the last tile's boxes
-    if (a.aux) {
+  // boxes asked for and not waited for, should this warp give up: they land before it leaves (with a limit)
+  uint32_t pending = 0;
+  auto give_up = [&] {
+    if (lane == 0)
+      for (int i = 0; i < 2; ++i)
+        if (pending >> i & 1) mbar_wait_budget(&e.bars[i], e.phases >> i & 1, kWaitBudgetCycles);
+    return false;
+  };
+  if (lane == 0) bulk_wait_read();   // the last tile's boxes
+  if (a.aux && rows_in && f0 < a.cols) {
+    pending = 1;
+    if (SLOTS == 2 && halves && f0 + 32 < a.cols) pending = 3;
+    if (GROUPS > 1 && own && f0 + 64 < a.cols) pending = 3;
+    if (lane == 0) {
       fetch_group(f0);
-      if (own && GROUPS > 1) fetch(f0 + 64, 1, 4096);
+      if (GROUPS > 1 && own) fetch(f0 + 64, 1);
     }
   }
-  if (!wait()) {   // loads beside D land before this warp leaves (with a limit)
-    if (a.aux && lane == 0 && rows_in)
-      for (int i = 0; i < 2; ++i)
-        if (f0 + (own ? 64 : 32) * i < a.cols && (i == 0 || !out16 || (own && GROUPS > 1)))
-          mbar_wait_budget(&e.bars[i], e.phases >> i & 1, kWaitBudgetCycles);
-    return false;
-  }
+  if (!wait()) return give_up();
   #pragma unroll 1
   for (int g = 0; g < GROUPS; ++g) {
-    uint32_t u[2][32];
+    uint32_t u[SLOTS][32];
     tmem_ld32(taddr + 64 * g, u[0]);
-    tmem_ld32(taddr + 64 * g + 32, u[1]);
+    if (SLOTS == 2) tmem_ld32(taddr + 64 * g + 32, u[SLOTS - 1]);
     tmem_wait_ld();
-    if (g + 1 == GROUPS) done();
+    if (SLOTS == 2 && g + 1 == GROUPS) done();
     const int fg = f0 + 64 * g;
-    if (!rows_in || fg >= a.cols) continue;
+    const bool in = rows_in && fg < a.cols;
+    if (SLOTS == 2 && !in) continue;
     if (g > 0 && !own) {   // the last group's boxes have been read
       if (lane == 0) {
         bulk_wait_read();
         if (a.aux) fetch_group(fg);
       }
+      if (a.aux) pending = halves && fg + 32 < a.cols ? 3 : 1;
       __syncwarp();
     }
     const int h = a.out_at.d ? fg / a.out_at.d : 0, fh = fg - h * a.out_at.d;
     #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int f = fg + 32 * half;
-      if (f >= a.cols) break;
-      const int i = out16 ? (own ? g : 0) : half;   // its slot
+      if (SLOTS == 1 && half == 1) {
+        tmem_ld32(taddr + 32, u[0]);
+        tmem_wait_ld();
+        done();
+      }
+      if (!in || f >= a.cols) continue;
+      const int i = SLOTS == 1 ? 0 : (out16 ? (own ? g : 0) : half);   // its slot
       uint8_t* const slot = e.slot + 4096 * i;
+      if (SLOTS == 1 && half == 1 && halves) {   // the first half's boxes have been read
+        if (lane == 0) {
+          bulk_wait_read();
+          if (a.aux) fetch(f, 0);
+        }
+        if (a.aux) pending = 1;
+        __syncwarp();
+      }
       float v[32];
       #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[half][j]);
+      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[SLOTS == 1 ? 0 : half][j]);
       if (KIND == kLinForward && a.bias) {
         const float at = GROUPS > 1 && g > 0 ? bias[COLS / 32 - 2 + half] : bias[half];
         __syncwarp();
@@ -223,17 +242,13 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32
       }
       float x[32];
       if (a.aux) {
-        if (!out16 || half == 0) {
-          const bool ok = warp_all(mbar_wait(&e.bars[i], e.phases >> i & 1, abort_flag, a.status));
+        if (halves || half == 0) {
+          if (!warp_all(mbar_wait(&e.bars[i], e.phases >> i & 1, abort_flag, a.status))) return give_up();
           e.phases ^= 1u << i;
-          if (!ok) {
-            if (!out16 && half == 0 && lane == 0 && f + 32 < a.cols) mbar_wait_budget(&e.bars[1], e.phases >> 1 & 1, kWaitBudgetCycles);
-            if (own && g + 1 < GROUPS && lane == 0 && fg + 64 < a.cols) mbar_wait_budget(&e.bars[1], e.phases >> 1 & 1, kWaitBudgetCycles);
-            return false;
-          }
+          pending &= ~(1u << i);
         }
-        lin_read(slot, x, a.aux_fmt, half, !out16);
-        if (!out16) __syncwarp();   // rows of different types do not lie at the same bytes
+        lin_read(slot, x, a.aux_fmt, half, halves);
+        if (halves) __syncwarp();   // rows of different types do not lie at the same bytes
       }
       if (KIND == kLinForward) {
         if (a.pre) {
@@ -259,12 +274,13 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32
       }
       if (KIND == kLinInput && a.aux) with_act(a.act, [&](auto A) { slope_all<decltype(A)::value>(v, x); });
       lin_write(slot, v, a.out_fmt, half, false);
-      if (out16 && half == 0 && f + 32 < a.cols) continue;   // the other half of the box
+      if (!halves && half == 0 && f + 32 < a.cols) continue;   // the other half of the box
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        if (KIND == kLinForward && a.pre && out16) tma_store_4d(e.pre, e.slot + 4096, fh, row0, h, b);
-        tma_store_4d(e.out, slot, out16 ? fh : fh + 32 * half, row0, h, b);
+        const int at = halves ? fh + 32 * half : fh;
+        if (KIND == kLinForward && a.pre && out16) tma_store_4d(e.pre, e.slot + 4096, at, row0, h, b);
+        tma_store_4d(e.out, slot, at, row0, h, b);
         bulk_commit();
       }
     }

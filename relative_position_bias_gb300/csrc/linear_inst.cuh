@@ -26,13 +26,13 @@ static cudaError_t launch_lin_few(const LinMaps& m, const LinArgs& a, cudaStream
   return cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, a);
 }
 
-template <int KIND, int BN, bool BF16>
+template <int KIND, int BN, int EPI, bool BF16>
 static cudaError_t launch_lin_pair(const LinMaps& m, const LinArgs& a, int pairs, cudaStream_t s) {
-  auto kernel = linear_pair_kernel<KIND, BN, BF16>;
+  auto kernel = linear_pair_kernel<KIND, BN, EPI, BF16>;
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = prepare_kernel(kernel, PairSmem<KIND, BN>::kAlloc, 0, done);
+  cudaError_t e = prepare_kernel(kernel, PairSmem<KIND, BN, EPI>::kAlloc, 0, done);
   if (e != cudaSuccess) return e;
-  kernel<<<2 * pairs, kPairThreads, PairSmem<KIND, BN>::kAlloc, s>>>(m, a);
+  kernel<<<2 * pairs, pair_threads(EPI), PairSmem<KIND, BN, EPI>::kAlloc, s>>>(m, a);
   return cudaGetLastError();
 }
 
@@ -44,9 +44,11 @@ static cudaError_t launch_lin_kind(const LinMaps& m, const LinArgs& a, const Lin
       if (p.bn == 32) return launch_lin_few<KIND, 32, BF16>(m, a, s);
       return p.bn == 64 ? launch_lin_few<KIND, 64, BF16>(m, a, s) : launch_lin_few<KIND, 128, BF16>(m, a, s);
     }
-    if (p.bn == 128) return launch_lin_pair<KIND, 128, BF16>(m, a, p.pairs, s);
+    if (p.bn == 128) return launch_lin_pair<KIND, 128, 8, BF16>(m, a, p.pairs, s);
   }
-  return launch_lin_pair<KIND, 256, BF16>(m, a, p.pairs, s);
+  if constexpr (KIND == kLinInput)
+    if (p.epi == 16) return launch_lin_pair<KIND, 256, 16, BF16>(m, a, p.pairs, s);
+  return launch_lin_pair<KIND, 256, 8, BF16>(m, a, p.pairs, s);
 }
 
 template <int KIND>

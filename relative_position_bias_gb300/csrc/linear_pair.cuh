@@ -13,22 +13,22 @@
 
 namespace dera {
 
-// A warp that loads, one that multiplies, two that wait, and eight of the epilogue.  Sixteen with half of the columns each end a tile
-// sooner, but take so much of TMEM and of the shared memory at once that the products beside them wait: 169 us for 32768 x 1024 x 4096, with
-// eight 155.
-constexpr int kPairEpi = 8;
-constexpr int kPairThreads = 128 + 32 * kPairEpi;
+// A warp that loads, one that multiplies, two that wait, and eight of the epilogue; sixteen, with half of the columns each, for the
+// input's gradient through gelu.  Sixteen end a tile sooner, but take so much of TMEM and of the shared memory at once that the products
+// beside them wait: 32768 x 1024 x 4096 takes 152 us with eight and 162 with sixteen, with gelu 181 and 183; the input's gradient
+// through gelu, 32768 x 4096 x 1024, with its load and its 20 instructions a pair, 229 and 209 (through relu 184 with eight).
+constexpr int pair_threads(int epi) { return 128 + 32 * epi; }
 constexpr int kLinChain = 64;
 
-template <int KIND, int BN>
+template <int KIND, int BN, int EPI>
 struct PairSmem {
   static constexpr int kA = 128 * 128, kB = BN / 2 * 128;
   static constexpr int kStage = kA + kB;
   static constexpr int NS = BN == 256 ? (KIND == kLinWeight ? 6 : 5) : 6;
   static constexpr int kEpi = NS * kStage;             // 4 KB an epilogue warp
-  static constexpr int kRow = kEpi + kPairEpi * (KIND == kLinWeight ? 4096 : 8192);
-  static constexpr int kBars = kRow + kPairEpi * 128;
-  static constexpr int kMisc = kBars + (2 * NS + 5 + 2 * kPairEpi) * 8;
+  static constexpr int kRow = kEpi + (KIND == kLinWeight ? 32768 : 65536);
+  static constexpr int kBars = kRow + (KIND == kLinForward ? EPI * 128 : 0);
+  static constexpr int kMisc = kBars + (2 * NS + 5 + 2 * EPI) * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory");
 };
@@ -73,10 +73,10 @@ struct PairItem {
   __device__ __forceinline__ int s1(const LinArgs& a) const { return min((piece + 1) * a.piece_steps, a.steps); }
 };
 
-template <int KIND, int BN, bool BF16>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+template <int KIND, int BN, int EPI, bool BF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(EPI), 1)
     linear_pair_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
-  using SM = PairSmem<KIND, BN>;
+  using SM = PairSmem<KIND, BN, EPI>;
   constexpr int NS = SM::NS;
   constexpr bool A_MN = KIND == kLinWeight, B_MN = KIND != kLinForward;
   constexpr bool CHAINS = KIND == kLinWeight;
@@ -102,9 +102,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int i = 0; i < 2 * NS + 2; ++i) mbar_init(&full[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&acc_empty[i], 2 * kPairEpi);
+    for (int i = 0; i < 2; ++i) mbar_init(&acc_empty[i], 2 * EPI);
     mbar_init(all_done, 1);
-    for (int i = 0; i < 2 * kPairEpi; ++i) mbar_init(&beside[i], 1);
+    for (int i = 0; i < 2 * EPI; ++i) mbar_init(&beside[i], 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -182,10 +182,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp >= 4) {
     // --------------------------------------------------------------- epilogue: a warp 32 rows of its columns
-    constexpr int COLS = BN / (kPairEpi / 4);
+    constexpr int COLS = BN / (EPI / 4);
     const int quarter = warp & 3, col0 = COLS * ((warp - 4) >> 2);
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-    uint8_t* const slot = smem + SM::kEpi + (CHAINS ? 4096 : 8192) * (warp - 4);
+    constexpr int SLOTS = EPI == 8 && !CHAINS ? 2 : 1;
+    uint8_t* const slot = smem + SM::kEpi + 4096 * SLOTS * (warp - 4);
     LinEpi epi = {slot, reinterpret_cast<float*>(smem + SM::kRow) + 32 * (warp - 4), beside + 2 * (warp - 4), 0, &maps.out, &maps.aux, &maps.pre};
     const uint32_t empty0 = cluster_map(acc_empty, 0);
     int chain = 0;
@@ -203,7 +204,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     for (; ok && w.any; w.next(a)) {
       const int row0 = w.r0() + 128 * static_cast<int>(rank) + 32 * quarter, f0 = w.c0() + col0;
       if constexpr (!CHAINS) {
-        ok = lin_epilogue<KIND, COLS>(a, epi, tbase + BN * (chain & 1) + lanes + col0, w.b, row0, f0, abort_flag, wait, done);
+        ok = lin_epilogue<KIND, COLS, SLOTS>(a, epi, tbase + BN * (chain & 1) + lanes + col0, w.b, row0, f0, abort_flag, wait, done);
         ++chain;
       } else {
         float acc[COLS];

@@ -91,6 +91,9 @@ SIZES = {
     "pairs_heads": (3, 700, 384, 2000, 64, HF, HF),
     "pairs_narrow": (2, 4900, 320, 136, 0, BF, F32),
     "pairs_many_tiles": (1, 10000, 264, 1032, 0, HF, HF),
+    "pairs_wide_f32": (1, 10000, 200, 1032, 0, BF, F32),
+    "pairs_wide_heads": (3, 3000, 384, 1096, 64, BF, BF),
+    "pairs_wide_heads_f32": (2, 5000, 320, 1064, 64, HF, F32),
 }
 
 
@@ -106,6 +109,9 @@ def test_sizes(name):
     assert y.dtype == od and pre.dtype == dt
     check_forward(x, w, y, b, "gelu", res, pre)
     check_forward(x, w, rpb.linear(x, w))
+    check_forward(x, w, rpb.linear(x, w, b.float(), residual=res, out_dtype=od), b, None, res)
+    y, pre = rpb.linear(x, w, b, activation="silu", keep_pre=True, out_dtype=od)
+    check_forward(x, w, y, b, "silu", None, pre)
     dy = torch.randn(B, N, out, generator=g).to(dt).cuda()
     got = rpb.linear_backward(dy, x, w, grad_dtype=od)
     assert got[0].dtype == od and got[1].dtype == got[2].dtype == F32
@@ -116,6 +122,10 @@ def test_sizes(name):
     got2 = rpb.linear_backward(dy, x, w, input_pre=ipre, input_activation="gelu", weight_grad_dtype=dt)
     assert got2[0].dtype == F32 and got2[1].dtype == dt
     check_backward(dy, x, w, got2, ipre, "gelu")
+    got3 = rpb.linear_backward(dy, x, w, input_pre=ipre, input_activation="relu", grad_dtype=od, weight_grad=False)
+    check_backward(dy, x, w, got3, ipre, "relu")
+    got4 = rpb.linear_backward(dy, x, w, input_pre=ipre, input_activation="gelu", grad_dtype=dt, weight_grad=False)
+    check_backward(dy, x, w, got4, ipre, "gelu")
     again = rpb.linear_backward(dy, x, w, grad_dtype=od)
     assert all(torch.equal(p, q) for p, q in zip(got, again))
     assert rpb.device_status() == 0
