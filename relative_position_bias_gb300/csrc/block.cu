@@ -132,7 +132,7 @@ bool cut(LinArgs* a, const LinPlan& p, int batches, int rows, int cols) {
 }
 
 // How D of tokens (rows) by features is cut, `steps` steps long.
-LinPlan token_plan(const Tokens& tok, int features, int steps, bool gelu_slope, int sms) {
+LinPlan token_plan(const Tokens& tok, int features, int steps, bool f32, bool gelu_slope, int sms) {
   LinPlan p = {};
   p.pieces = 1;
   p.piece_steps = steps;
@@ -153,7 +153,8 @@ LinPlan token_plan(const Tokens& tok, int features, int steps, bool gelu_slope, 
   const double t_wide = 7 + std::ceil(wide / pairs) * std::max(0.27 * steps, 3.0);
   const double t_narrow = 5.3 + std::ceil(narrow / pairs) * std::max(0.23 * steps, 2.4);
   p.bn = t_wide <= t_narrow ? 256 : 128;
-  p.epi = p.bn == 256 && gelu_slope ? 16 : 8;   // linear_pair.cuh
+  p.fine = f32 && steps > 8;   // a chain of linear_pair.cuh
+  p.epi = p.bn == 256 && gelu_slope && !p.fine ? 16 : 8;
   p.pairs = static_cast<int>(std::min<double>(pairs, p.bn == 256 ? wide : narrow));
   return p;
 }
@@ -353,7 +354,7 @@ dera_status dera_linear(const dera_heads* x, const void* weight, const void* bia
   a.fmt = fmt_of(in_dtype);
   a.bias_fmt = fmt_of(bias_dtype);
   a.aux_fmt = a.out_fmt = fmt_of(out_dtype);
-  const LinPlan p = token_plan(tok, out_features, a.steps, false, sm_count(dev));
+  const LinPlan p = token_plan(tok, out_features, a.steps, out_dtype == DERA_F32, false, sm_count(dev));
   if (!(p.turned ? cut(&a, p, 1, out_features, tok.N) : cut(&a, p, tok.B, tok.N, out_features))) return DERA_ERR_SHAPE;
   LinMaps m = {};
   const HeadsPtr xm = tok.of(xt, N), wm = rows_of(weight, out_features, K);
@@ -444,7 +445,7 @@ dera_status dera_linear_backward(const void* dy, const dera_heads* x, const void
     a.act = input_activation;
     a.fmt = a.aux_fmt = fmt_of(in_dtype);
     a.out_fmt = fmt_of(grad_dtype);
-    const LinPlan p = token_plan(tok, K, a.steps, input_activation == DERA_ACT_GELU, sms);
+    const LinPlan p = token_plan(tok, K, a.steps, grad_dtype == DERA_F32, input_activation == DERA_ACT_GELU, sms);
     LinMaps m = {};
     CUtensorMap *mg = p.turned ? &m.b : &m.a, *mw = p.turned ? &m.a : &m.b;
     if (!(p.turned ? cut(&a, p, 1, K, tok.N) : cut(&a, p, tok.B, tok.N, K))) return DERA_ERR_SHAPE;

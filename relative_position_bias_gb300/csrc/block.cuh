@@ -96,6 +96,7 @@ struct LinPlan {
   bool turned;
   int pairs;             // pairs of CTAs that share tiles of 256 rows (0: turned)
   int epi;               // epilogue warps of a CTA of a pair
+  bool fine;             // long sums in chains (an fp32 output)
   int pieces, piece_steps;
 };
 // The end of a backward: dW from its pieces, and db from its partial rows (either may be absent).

@@ -143,11 +143,13 @@ __device__ __forceinline__ void lin_read(uint8_t* slot, float (&x)[32], int fmt,
 //   16-bit output            a box a group of 64 columns, with two slots each group's its own
 //   ... and an argument      a slot each (the forward has two)
 //   fp32 output              a box a half group, with two slots its own; an argument goes through the half's slot first
-template <int KIND, int COLS, int SLOTS, class Wait, class Done>
-__device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32_t taddr, int b, int row0, int f0, volatile int* abort_flag,
-                                             Wait&& wait, Done&& done) {
+// FINE: D is not in TMEM, but after wait() in acc.
+template <int KIND, int COLS, int SLOTS, bool FINE, class Wait, class Done>
+__device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32_t taddr, float (&acc)[FINE ? COLS : 1], int b, int row0,
+                                             int f0, volatile int* abort_flag, Wait&& wait, Done&& done) {
   static_assert(COLS == 64 || (COLS == 128 && SLOTS == 2), "one or two groups of 64 columns");
   static_assert(KIND == kLinInput || SLOTS == 2, "room for the activation's argument");
+  static_assert(!FINE || SLOTS == 2, "registers for D");
   constexpr int GROUPS = COLS / 64;
   const int lane = threadIdx.x & 31;
   const bool out16 = a.out_fmt != kF32, own = out16 && !(KIND == kLinForward && a.pre);
@@ -188,13 +190,18 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32
     }
   }
   if (!wait()) return give_up();
-  #pragma unroll 1
+  #pragma unroll(FINE ? GROUPS : 1)
   for (int g = 0; g < GROUPS; ++g) {
     uint32_t u[SLOTS][32];
-    tmem_ld32(taddr + 64 * g, u[0]);
-    if (SLOTS == 2) tmem_ld32(taddr + 64 * g + 32, u[SLOTS - 1]);
-    tmem_wait_ld();
-    if (SLOTS == 2 && g + 1 == GROUPS) done();
+    if (FINE) {
+      #pragma unroll
+      for (int j = 0; j < 64; ++j) u[SLOTS == 2 ? j / 32 : 0][j & 31] = __float_as_uint(acc[FINE ? 64 * g + j : 0]);
+    } else {
+      tmem_ld32(taddr + 64 * g, u[0]);
+      if (SLOTS == 2) tmem_ld32(taddr + 64 * g + 32, u[SLOTS - 1]);
+      tmem_wait_ld();
+      if (SLOTS == 2 && g + 1 == GROUPS) done();
+    }
     const int fg = f0 + 64 * g;
     const bool in = rows_in && fg < a.cols;
     if (SLOTS == 2 && !in) continue;
@@ -320,6 +327,19 @@ __device__ __forceinline__ void lin_finish_turned(const LinArgs& a, float (&v)[T
     if (j < count) store_elem(a.out, out + j * a.out_at.sn, v[j], a.out_fmt);
 }
 
+// Sixteen columns of `accs` sums in TMEM, `apart` columns from one to the next.
+__device__ __forceinline__ void lin_sum_of(uint32_t taddr, int apart, int accs, float (&v)[16]) {
+  #pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = 0.f;
+  for (int i = 0; i < accs; ++i) {
+    uint32_t u[16];
+    tmem_ld16(taddr + i * apart, u);
+    tmem_wait_ld();
+    #pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(u[j]);
+  }
+}
+
 // Up to 128 tokens: 128 features by BN tokens a tile, the features as rows, so that a product of few tokens still fills the tensor
 // core's 128 rows.  What counts then is how many SMs read the weight: a cluster of CTAs shares a tile, each with a piece of the
 // contraction, and each adds up all of their parts for its share of the tokens, through distributed shared memory and in order.
@@ -330,6 +350,9 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
   using SM = LinSmem<BN>;
   constexpr int NS = SM::NS;
   constexpr bool A_MN = KIND == kLinInput;   // W's columns in the input's gradient
+  // A piece's steps go to four sums in turn, which are added at the end: the tensor core cuts towards zero when it adds, and a long
+  // chain drifts (linear_pair.cuh).
+  constexpr int ACCS = 4;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -353,7 +376,7 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
     fence_mbar_init();
   }
   if (warp == 5) {
-    tmem_alloc(slot, BN);
+    tmem_alloc(slot, ACCS * BN);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -393,8 +416,8 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
       tc_fence_after();
       #pragma unroll
       for (int k = 0; k < 4; ++k)
-        umma_ss_w(tbase, da + st * (SM::kStage >> 4) + ka * k, db + st * (SM::kStage >> 4) + 2 * k, id,
-                  (n > 0 || k > 0) ? 1u : 0u);
+        umma_ss_w(tbase + BN * (n % ACCS), da + st * (SM::kStage >> 4) + ka * k, db + st * (SM::kStage >> 4) + 2 * k, id,
+                  (n >= ACCS || k > 0) ? 1u : 0u);
       umma_commit_w(&empty[st]);
     }
     umma_commit_w(done);
@@ -404,16 +427,16 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
   const bool ok = warp < 4 && warp_all(mbar_wait(done, 0, abort_flag, a.status));
   const uint32_t taddr = tbase + (static_cast<uint32_t>(32 * warp) << 16);
   const int f = r0 + threadIdx.x;   // this thread's feature
+  const int accs = min(ACCS, s1 - s0);
   tc_fence_after();
   if (pieces > 1) {
     if (ok) {
       #pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
-        uint32_t u[32];
-        tmem_ld32(taddr + c, u);
-        tmem_wait_ld();
+      for (int c = 0; c < BN; c += 16) {
+        float v[16];
+        lin_sum_of(taddr + c, BN, accs, v);
         #pragma unroll
-        for (int j = 0; j < 32; ++j) part[(c + j) * 128 + threadIdx.x] = __uint_as_float(u[j]);
+        for (int j = 0; j < 16; ++j) part[(c + j) * 128 + threadIdx.x] = v[j];
       }
     }
     __syncwarp();
@@ -437,19 +460,15 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
   } else if (ok) {
     #pragma unroll 1
     for (int c = 0; c < BN && c < a.cols; c += 16) {
-      uint32_t u[16];
-      tmem_ld16(taddr + c, u);
-      tmem_wait_ld();
       float v[16];
-      #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(u[j]);
+      lin_sum_of(taddr + c, BN, accs, v);
       if (f < a.rows) lin_finish_turned<KIND>(a, v, c, f, min(16, a.cols - c));
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) tmem_dealloc(tbase, BN);
+  if (warp == 5) tmem_dealloc(tbase, ACCS * BN);
 }
 
 }  // namespace dera

@@ -26,9 +26,9 @@ static cudaError_t launch_lin_few(const LinMaps& m, const LinArgs& a, cudaStream
   return cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, a);
 }
 
-template <int KIND, int BN, int EPI, bool BF16>
+template <int KIND, int BN, int EPI, bool FINE, bool BF16>
 static cudaError_t launch_lin_pair(const LinMaps& m, const LinArgs& a, int pairs, cudaStream_t s) {
-  auto kernel = linear_pair_kernel<KIND, BN, EPI, BF16>;
+  auto kernel = linear_pair_kernel<KIND, BN, EPI, FINE, BF16>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = prepare_kernel(kernel, PairSmem<KIND, BN, EPI>::kAlloc, 0, done);
   if (e != cudaSuccess) return e;
@@ -44,11 +44,14 @@ static cudaError_t launch_lin_kind(const LinMaps& m, const LinArgs& a, const Lin
       if (p.bn == 32) return launch_lin_few<KIND, 32, BF16>(m, a, s);
       return p.bn == 64 ? launch_lin_few<KIND, 64, BF16>(m, a, s) : launch_lin_few<KIND, 128, BF16>(m, a, s);
     }
-    if (p.bn == 128) return launch_lin_pair<KIND, 128, 8, BF16>(m, a, p.pairs, s);
+    if (p.fine)
+      return p.bn == 128 ? launch_lin_pair<KIND, 128, 8, true, BF16>(m, a, p.pairs, s)
+                         : launch_lin_pair<KIND, 256, 8, true, BF16>(m, a, p.pairs, s);
+    if (p.bn == 128) return launch_lin_pair<KIND, 128, 8, false, BF16>(m, a, p.pairs, s);
   }
   if constexpr (KIND == kLinInput)
-    if (p.epi == 16) return launch_lin_pair<KIND, 256, 16, BF16>(m, a, p.pairs, s);
-  return launch_lin_pair<KIND, 256, 8, BF16>(m, a, p.pairs, s);
+    if (p.epi == 16) return launch_lin_pair<KIND, 256, 16, false, BF16>(m, a, p.pairs, s);
+  return launch_lin_pair<KIND, 256, 8, false, BF16>(m, a, p.pairs, s);
 }
 
 template <int KIND>

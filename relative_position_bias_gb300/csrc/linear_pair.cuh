@@ -6,8 +6,9 @@
 // products do.
 //
 // The tensor core cuts towards zero what it adds to its fp32 sum, so a long chain drifts: 3.4e-5 of the sum after
-// 30 000 terms.  The weight's gradient sums over tokens, without limit: its chains end after kLinChain steps (4096 tokens,
-// 5e-6), and the epilogue adds them in registers while the next chain runs in the other buffer.
+// 30 000 terms, 5e-6 after 4096.  Where the result is fp32 (FINE), and for the weight's gradient, whose sums over tokens have no limit,
+// chains end after kLinChain steps (512 terms, 6e-7), and the epilogue adds them in registers while the next chain runs in the
+// other buffer; it takes a quarter of the time that a chain's products do.
 #pragma once
 #include "linear.cuh"
 
@@ -18,7 +19,7 @@ namespace dera {
 // beside them wait: 32768 x 1024 x 4096 takes 152 us with eight and 162 with sixteen, with gelu 181 and 183; the input's gradient
 // through gelu, 32768 x 4096 x 1024, with its load and its 20 instructions a pair, 229 and 209 (through relu 184 with eight).
 constexpr int pair_threads(int epi) { return 128 + 32 * epi; }
-constexpr int kLinChain = 64;
+constexpr int kLinChain = 8;
 
 template <int KIND, int BN, int EPI>
 struct PairSmem {
@@ -73,14 +74,13 @@ struct PairItem {
   __device__ __forceinline__ int s1(const LinArgs& a) const { return min((piece + 1) * a.piece_steps, a.steps); }
 };
 
-template <int KIND, int BN, int EPI, bool BF16>
+template <int KIND, int BN, int EPI, bool FINE, bool BF16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(EPI), 1)
     linear_pair_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs a) {
   using SM = PairSmem<KIND, BN, EPI>;
   constexpr int NS = SM::NS;
   constexpr bool A_MN = KIND == kLinWeight, B_MN = KIND != kLinForward;
-  constexpr bool CHAINS = KIND == kLinWeight;
-  constexpr int CHAIN = CHAINS ? kLinChain : 1 << 30;
+  constexpr bool WEIGHT = KIND == kLinWeight, CHAINS = WEIGHT || FINE;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -157,7 +157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(EPI), 1
       for (; ok && w.any; w.next(a)) {
         const int s1 = w.s1(a);
         for (int s = w.s0(a); ok && s < s1; ++chain) {
-          const int end = min(s1, CHAINS ? s + CHAIN : s1), buf = chain & 1;
+          const int end = min(s1, CHAINS ? s + kLinChain : s1), buf = chain & 1;
           ok = warp_all(mbar_wait(&acc_empty[buf], ((chain >> 1) & 1) ^ 1, abort_flag, a.status));
           if (!ok) break;
           tc_fence_after();
@@ -185,7 +185,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(EPI), 1
     constexpr int COLS = BN / (EPI / 4);
     const int quarter = warp & 3, col0 = COLS * ((warp - 4) >> 2);
     const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
-    constexpr int SLOTS = EPI == 8 && !CHAINS ? 2 : 1;
+    constexpr int SLOTS = EPI == 8 && !WEIGHT ? 2 : 1;
     uint8_t* const slot = smem + SM::kEpi + 4096 * SLOTS * (warp - 4);
     LinEpi epi = {slot, reinterpret_cast<float*>(smem + SM::kRow) + 32 * (warp - 4), beside + 2 * (warp - 4), 0, &maps.out, &maps.aux, &maps.pre};
     const uint32_t empty0 = cluster_map(acc_empty, 0);
@@ -203,15 +203,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(EPI), 1
     };
     for (; ok && w.any; w.next(a)) {
       const int row0 = w.r0() + 128 * static_cast<int>(rank) + 32 * quarter, f0 = w.c0() + col0;
-      if constexpr (!CHAINS) {
-        ok = lin_epilogue<KIND, COLS, SLOTS>(a, epi, tbase + BN * (chain & 1) + lanes + col0, w.b, row0, f0, abort_flag, wait, done);
-        ++chain;
-      } else {
-        float acc[COLS];
+      // every chain of the tile, added up
+      auto gather = [&](float (&acc)[COLS]) {
         #pragma unroll
         for (int c = 0; c < COLS; ++c) acc[c] = 0.f;
         const int s0 = w.s0(a), s1 = w.s1(a);
-        for (int s = s0; ok && s < s1; s += CHAIN, ++chain) {
+        for (int s = s0; ok && s < s1; s += kLinChain, ++chain) {
           if (!wait()) break;
           const uint32_t at = tbase + BN * (chain & 1) + lanes + col0;
           #pragma unroll
@@ -220,12 +217,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(EPI), 1
             tmem_ld16(at + c, u);
             tmem_wait_ld();
             #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              acc[c + j] += __uint_as_float(u[j]);
+            for (int j = 0; j < 16; ++j) acc[c + j] += __uint_as_float(u[j]);
           }
           done();
         }
-        if (!ok) break;
+        return ok;
+      };
+      if constexpr (!WEIGHT) {
+        const uint32_t at = tbase + BN * (chain & 1) + lanes + col0;
+        if constexpr (FINE) {
+          float acc[COLS];
+          ok = lin_epilogue<KIND, COLS, SLOTS, true>(a, epi, at, acc, w.b, row0, f0, abort_flag, [&] { return gather(acc); }, [] {});
+        } else {
+          float acc[1] = {0.f};
+          ok = lin_epilogue<KIND, COLS, SLOTS, false>(a, epi, at, acc, w.b, row0, f0, abort_flag, wait, done);
+          ++chain;
+        }
+      } else {
+        float acc[COLS];
+        if (!gather(acc)) break;
         void* to = a.parts ? static_cast<void*>(a.parts + static_cast<size_t>(w.piece) * a.rows * a.cols) : a.out;
         const int fmt = a.parts ? kF32 : a.out_fmt, row = row0 + (lane >> 1);
         float4* stage = reinterpret_cast<float4*>(slot);
