@@ -76,9 +76,6 @@ typedef enum dera_activation {
   DERA_ACT_SILU = 5         /* u / (1 + exp(-u)) */
 } dera_activation;
 
-/* Scratch of dera_linear on the current device (0 where it needs none). */
-DERA_API dera_status dera_linear_workspace_size(int B, int N, int heads, int head_dim, int out_features, size_t* bytes);
-
 /*
  * A linear layer over B * N tokens of K = heads * head_dim features:
  *     u = x weight^T + bias,   y = act(u) + residual.
@@ -89,17 +86,20 @@ DERA_API dera_status dera_linear_workspace_size(int B, int N, int heads, int hea
  *      in_dtype), or NULL.  residual [B, N, out_features] in out_dtype, or NULL.
  * out: y [B, N, out_features] in out_dtype (DERA_F32 or in_dtype); pre, if not NULL, u in in_dtype (what the backward of
  *      the activation needs).
- * K and out_features are multiples of 8, head_dim of 64 where heads > 1.  Sums are fp32 (the tensor core's, which cut
- * towards zero when they add: at most 2^-23 of a partial sum for every 16 terms); bias, activation and residual are applied to them in
- * fp32, and y (and pre) rounded once.  x and weight must be finite.
+ * K and out_features are multiples of 8, head_dim of 64 where heads > 1.  Sums are fp32.  The tensor core cuts towards zero
+ * when it adds, at most 2^-23 of a partial sum for every 16 terms: where y is fp32 it does so for no more than 512 terms at a
+ * time (with up to 128 tokens K / 4), and these sums are added with rounding (5e-7 of y); where y has 16 bits, over all K
+ * (1.2e-9 K, below its rounding).  Bias,
+ * activation and residual are applied in fp32, and y (and pre) rounded once.  x and weight must be finite.  Gelu's Phi is off by 2^-19
+ * of its distance to 0 or 1; an element's last bit may depend on its neighbour's.
  * Errors: DERA_ERR_SHAPE for sizes below one (B = 0 or N = 0 is a no-op), B * N beyond 2^31 - 1, features beyond 2^20,
  *      features or strides that break the rules above; DERA_ERR_ALIGN for strides that are not multiples of 8;
- *      DERA_ERR_DTYPE also for an unknown activation; DERA_ERR_SCRATCH for a missing or too small workspace.
+ *      DERA_ERR_DTYPE also for an unknown activation.
  */
 DERA_API dera_status dera_linear(const dera_heads* x, const void* weight, const void* bias, const void* residual, void* y,
                               void* pre, int B, int N, int heads, int head_dim, int out_features,
                               dera_activation activation, dera_dtype in_dtype, dera_dtype bias_dtype,
-                              dera_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+                              dera_dtype out_dtype, void* stream);
 
 /* Scratch of dera_linear_backward on the current device. */
 DERA_API dera_status dera_linear_backward_workspace_size(int B, int N, int heads, int head_dim, int out_features,
@@ -114,8 +114,9 @@ DERA_API dera_status dera_linear_backward_workspace_size(int B, int N, int heads
  * out: dx with the strides given, in grad_dtype, dweight [out_features, K] in weight_grad_dtype (DERA_F32 or in_dtype each),
  *      dbias [out_features] fp32.  Any of the three may be NULL: it is not computed (x is needed for dweight,
  *      weight for dx only).
- * Precision as for dera_linear; no more than 4096 tokens are summed in one chain of the tensor core's sums for dweight
- *      in fp32.  Errors as for dera_linear; B = 0 or N = 0 writes zero dweight and dbias.
+ * workspace: at least the size above if dweight or dbias is given (else it may be NULL).
+ * Precision as for dera_linear.  Errors as for dera_linear, DERA_ERR_SCRATCH for a missing or too small workspace; B = 0 or
+ *      N = 0 writes zero dweight and dbias.
  */
 DERA_API dera_status dera_linear_backward(const void* dy, const dera_heads* x, const void* weight,
                               const dera_heads* input_pre, const dera_heads* dx, void* dweight, float* dbias, int B, int N,

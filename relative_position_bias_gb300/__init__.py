@@ -13,7 +13,7 @@ from .api import (DERA_BF16, DERA_F16, DERA_F32, DeraError, attention, backward_
                   device_status, fused, fused_backward, fused_lse, load_library, project, selftest_wait_timeout,
                   workspace_size)
 from .block import (activation_backward, layer_norm, layer_norm_backward, layer_norm_backward_workspace_size, linear,
-                    linear_backward, linear_backward_workspace_size, linear_workspace_size)
+                    linear_backward, linear_backward_workspace_size)
 from .train import (attention_backward, attention_backward_workspace_size, attention_lse, project_backward,
                     project_backward_workspace_size, qk_norm_rope, qk_norm_rope_backward,
                     qk_norm_rope_backward_workspace_size)
@@ -22,6 +22,6 @@ __all__ = ["DERA_BF16", "DERA_F16", "DERA_F32", "DeraError", "activation_backwar
            "attention_backward_workspace_size", "attention_lse", "backward_workspace_size", "declared_entry_points",
            "device_status", "fused", "fused_backward", "fused_lse", "layer_norm",
            "layer_norm_backward", "layer_norm_backward_workspace_size", "linear", "linear_backward",
-           "linear_backward_workspace_size", "linear_workspace_size", "load_library", "project", "project_backward",
+           "linear_backward_workspace_size", "load_library", "project", "project_backward",
            "project_backward_workspace_size", "qk_norm_rope", "qk_norm_rope_backward",
            "qk_norm_rope_backward_workspace_size", "selftest_wait_timeout", "workspace_size"]

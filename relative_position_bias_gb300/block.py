@@ -30,8 +30,7 @@ def declare(lib: ctypes.CDLL) -> None:
         "dera_layer_norm": [vp] * 6 + [i, i, ll, f, i, i, i, vp],
         "dera_layer_norm_backward_workspace_size": [i, i, szp],
         "dera_layer_norm_backward": [vp] * 9 + [i, i, ll, i, i, i, i, vp, sz, vp],
-        "dera_linear_workspace_size": [i] * 5 + [szp],
-        "dera_linear": [vp] * 6 + [i] * 9 + [vp, sz, vp],
+        "dera_linear": [vp] * 6 + [i] * 9 + [vp],
         "dera_linear_backward_workspace_size": [i] * 5 + [szp],
         "dera_linear_backward": [vp] * 7 + [i] * 9 + [vp, sz, vp],
         "dera_activation_backward": [vp] * 3 + [ll, i, i, i, i, vp],
@@ -159,14 +158,8 @@ def _token_heads(x: torch.Tensor, name: str) -> bytes:
     return _pack_heads(x.data_ptr(), sb, sn, sh)
 
 
-def linear_workspace_size(B: int, N: int, heads: int, head_dim: int, out_features: int) -> int:
-    """Scratch bytes of :func:`linear` on the current device (0 where it needs none)."""
-    return _size("dera_linear_workspace_size", B, N, heads, head_dim, out_features)
-
-
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None, *, activation: str | None = None,
-           residual: torch.Tensor | None = None, keep_pre: bool = False, out_dtype: torch.dtype | None = None,
-           stream=None, workspace: torch.Tensor | None = None):
+           residual: torch.Tensor | None = None, keep_pre: bool = False, out_dtype: torch.dtype | None = None, stream=None):
     """``act(x weight^T + bias) + residual`` via ``dera_linear``.
 
     x ``[K]``, ``[N, K]`` or ``[B, N, K]`` with any strides that are multiples of 8, or ``[B, N, heads, d]`` with
@@ -191,12 +184,10 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
     _same(residual, size, od, "residual")
     y = torch.empty(size, dtype=od, device=dev)
     pre = torch.empty(size, dtype=dt, device=dev) if keep_pre else None
-    st = _launch_stream(dev, stream)
-    keep, ws, ws_bytes = _scratch(dev, stream, st, workspace, "dera_linear_workspace_size", B, N, heads, d, out)
     _check(api.load_library().dera_linear(
-        _token_heads(x, "x"), weight.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(pre), B, N, heads, d,
-        out, _activation(activation), _dtype(dt), DERA_F32 if bias is None else _dtype(bias.dtype), _dtype(od), ws,
-        ws_bytes, st))
+        _token_heads(x, "x"), weight.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(), _ptr(pre), B, N, heads, d, out,
+        _activation(activation), _dtype(dt), DERA_F32 if bias is None else _dtype(bias.dtype), _dtype(od),
+        _launch_stream(dev, stream)))
     return (y, pre) if keep_pre else y
 
 
@@ -229,6 +220,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *, 
     if input_pre is not None and (input_pre.shape != x.shape or input_pre.dtype != dt):
         raise ValueError(f"input_pre must have x's shape and dtype, got {tuple(input_pre.shape)} {input_pre.dtype}")
     dx = dw = db = keep = ws = None
+    ws_bytes = 0
     if input_grad:
         dx = torch.empty_like(x, dtype=gd)
     if weight_grad:
@@ -236,7 +228,8 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *, 
     if bias_grad:
         db = torch.empty(out, dtype=torch.float32, device=dev)
     st = _launch_stream(dev, stream)
-    keep, ws, ws_bytes = _scratch(dev, stream, st, workspace, "dera_linear_backward_workspace_size", B, N, heads, d, out)
+    if weight_grad or bias_grad:
+        keep, ws, ws_bytes = _scratch(dev, stream, st, workspace, "dera_linear_backward_workspace_size", B, N, heads, d, out)
     _check(api.load_library().dera_linear_backward(
         dy.data_ptr(), _token_heads(x, "x"), weight.data_ptr(),
         None if input_pre is None else _token_heads(input_pre, "input_pre"),

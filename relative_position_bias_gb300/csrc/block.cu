@@ -310,19 +310,9 @@ dera_status dera_layer_norm_backward(const void* dy, const void* x, const float*
   return status_of(launch_ln_backward(a, ln_plan(rows, cols, true, vec, sms), vec, dweight, dbias, s));
 }
 
-dera_status dera_linear_workspace_size(int B, int N, int heads, int head_dim, int out_features, size_t* bytes) {
-  if (!bytes) return DERA_ERR_NULL;
-  DERA_TRY(check_linear(B, N, heads, head_dim, out_features));
-  *bytes = 0;
-  return DERA_OK;
-}
-
 dera_status dera_linear(const dera_heads* x, const void* weight, const void* bias, const void* residual, void* y,
                         void* pre, int B, int N, int heads, int head_dim, int out_features, dera_activation activation,
-                        dera_dtype in_dtype, dera_dtype bias_dtype, dera_dtype out_dtype, void* workspace,
-                        size_t workspace_bytes, void* stream) {
-  (void)workspace;
-  (void)workspace_bytes;
+                        dera_dtype in_dtype, dera_dtype bias_dtype, dera_dtype out_dtype, void* stream) {
   DERA_TRY(check_linear(B, N, heads, head_dim, out_features));
   if (!is16(in_dtype) || !(out_dtype == DERA_F32 || out_dtype == in_dtype) || activation < 0 || activation >= kActs ||
       (bias && !(bias_dtype == DERA_F32 || bias_dtype == in_dtype)))

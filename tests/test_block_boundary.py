@@ -38,7 +38,7 @@ def _at(h):
 def test_header_and_exports(lib):
     names = set(rpb.declared_entry_points(block.HEADER))
     assert names == {"dera_layer_norm", "dera_layer_norm_backward", "dera_layer_norm_backward_workspace_size",
-                     "dera_linear", "dera_linear_workspace_size", "dera_linear_backward",
+                     "dera_linear", "dera_linear_backward",
                      "dera_linear_backward_workspace_size", "dera_activation_backward"}
     out = subprocess.run(["nm", "-D", "--defined-only", rbuild.LIB], capture_output=True, text=True, check=True)
     exported = {line.split()[-1] for line in out.stdout.splitlines() if " T " in line}
@@ -122,8 +122,7 @@ def _x(p=FAKE, sb=64 * 12, st=64, sh=64):
 
 def _lin(lib, *, x=None, w=FAKE, b=FAKE, res=FAKE, y=FAKE, pre=FAKE, B=2, N=3, heads=1, d=64, out=72, act=2, in_dt=BF16,
          b_dt=F32, out_dt=BF16):
-    return lib.dera_linear(_at(x or _x()), w, b, res, y, pre, B, N, heads, d, out, act, in_dt, b_dt, out_dt, FAKE, 1 << 30,
-                           None)
+    return lib.dera_linear(_at(x or _x()), w, b, res, y, pre, B, N, heads, d, out, act, in_dt, b_dt, out_dt, None)
 
 
 def _lin_bwd(lib, *, dy=FAKE, x=None, w=FAKE, ip=None, dx=None, dw=FAKE, db=FAKE, B=2, N=3, heads=1, d=64, out=72, act=0,
@@ -175,10 +174,10 @@ def test_linear_refuses_the_rest(lib):
 
 def test_linear_sizes(lib):
     n = ctypes.c_size_t(7)
-    for size in (lib.dera_linear_workspace_size, lib.dera_linear_backward_workspace_size):
-        assert size(1, 1, 1, 8, 8, None) == CODES["DERA_ERR_NULL"]
-        assert size(1, 1, 1, 8, 7, ctypes.byref(n)) == CODES["DERA_ERR_SHAPE"]
-        assert size(0, 5, 1, 8, 8, ctypes.byref(n)) == 0 and n.value == 0
+    size = lib.dera_linear_backward_workspace_size
+    assert size(1, 1, 1, 8, 8, None) == CODES["DERA_ERR_NULL"]
+    assert size(1, 1, 1, 8, 7, ctypes.byref(n)) == CODES["DERA_ERR_SHAPE"]
+    assert size(0, 5, 1, 8, 8, ctypes.byref(n)) == 0 and n.value == 0
 
 
 def test_linear_binding_checks():

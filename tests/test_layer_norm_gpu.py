@@ -209,6 +209,21 @@ def test_streams_and_graphs():
         assert all(torch.equal(p, q) for p, q in zip((*want, *wantg), o))
 
 
+def test_workspaces():
+    x, w, b, dy, _ = make(900, 264, BF, BF)
+    _, mean, rstd = rpb.layer_norm(x, w, b)
+    need = rpb.layer_norm_backward_workspace_size(900, 264)
+    ws = torch.full((need + 16,), 0xff, dtype=torch.uint8, device="cuda")
+    want = rpb.layer_norm_backward(dy, x, mean, rstd, w)
+    got = rpb.layer_norm_backward(dy, x, mean, rstd, w, workspace=ws[:need])
+    assert all(torch.equal(p, q) for p, q in zip(want, got)) and (ws[need:] == 0xff).all()
+    for bad, status in ((ws[:need - 256], 9), (ws[16:], 5)):
+        with pytest.raises(rpb.DeraError) as e:
+            rpb.layer_norm_backward(dy, x, mean, rstd, w, workspace=bad)
+        assert e.value.status == status
+    assert rpb.device_status() == 0
+
+
 def test_more_than_two_to_the_31_elements():
     rows, C = (1 << 31) // 2048 + 5, 2048
     x = torch.empty(rows, C, device="cuda", dtype=BF)

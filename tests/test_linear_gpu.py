@@ -284,6 +284,54 @@ def test_streams_and_graphs(N):
     assert rpb.device_status() == 0
 
 
+def test_workspaces():
+    """A caller's own, of exactly the size, with anything in it; too small, off its alignment and none at all are refused."""
+    g = torch.Generator().manual_seed(12)
+    x, w = tokens(2, 3000, 128, 64, BF, g), torch.randn(264, 128, generator=g).to(BF).cuda()
+    dy = torch.randn(2, 3000, 264, generator=g).to(BF).cuda()
+    need = rpb.linear_backward_workspace_size(2, 3000, 2, 64, 264)
+    ws = torch.full((need + 16,), 0xff, dtype=torch.uint8, device="cuda")
+    want = rpb.linear_backward(dy, x, w)
+    got = rpb.linear_backward(dy, x, w, workspace=ws[:need])
+    assert all(torch.equal(p, q) for p, q in zip(want, got)) and (ws[need:] == 0xff).all()
+    for bad, status in ((ws[:need - 1], 9), (ws[16:], 5)):
+        with pytest.raises(rpb.DeraError) as e:
+            rpb.linear_backward(dy, x, w, workspace=bad)
+        assert e.value.status == status
+    assert torch.equal(rpb.linear_backward(dy, x, w, weight_grad=False, bias_grad=False, workspace=ws[:1])[0], want[0])
+
+
+def test_two_streams_at_once():
+    """Calls on two streams that overlap, and a third that reads what the first wrote."""
+    g = torch.Generator().manual_seed(13)
+    x, w = tokens(1, 4000, 256, 0, BF, g), torch.randn(1032, 256, generator=g).to(BF).cuda()
+    dy = torch.randn(1, 4000, 1032, generator=g).to(BF).cuda()
+    want = (rpb.linear(x, w, activation="gelu"), *rpb.linear_backward(dy, x, w))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for _ in range(5):
+        for s in streams:
+            outs.append((rpb.linear(x, w, activation="gelu", stream=s), *rpb.linear_backward(dy, x, w, stream=s)))
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(p, q) for p, q in zip(want, o))
+
+
+def test_fp32_results_are_summed_finely():
+    """y, dx and dW in fp32 over long contractions, with few tokens and many: of one size, so that cutting towards zero would add up."""
+    g = torch.Generator().manual_seed(14)
+    for N in (9, 300, 3000):
+        x = (1 + 0.1 * torch.rand(1, N, 4096, generator=g)).to(BF).cuda()
+        w = (1 + 0.1 * torch.rand(264, 4096, generator=g)).to(BF).cuda()
+        dy = (1 + 0.1 * torch.rand(1, N, 264, generator=g)).to(BF).cuda()
+        y, (dx, dw, _) = rpb.linear(x, w, out_dtype=F32)[0], rpb.linear_backward(dy, x, w)
+        x64, w64, d64 = x[0].double(), w.double(), dy[0].double()
+        for got, want in ((y, x64 @ w64.T), (dx[0], d64 @ w64), (dw, d64.T @ x64)):
+            # 32 cuts of a chain, at most 2^-22 each, and as many roundings of 2^-24 for the chains
+            assert float(((got.double() - want) / want).abs().max()) <= 32 * 2.0 ** -22 + 64 * 2.0 ** -24
+
+
 def test_many_tokens_sum_as_finely():
     """dweight in fp32 over more tokens than one chain of the tensor core's sums takes: of ones, every bit."""
     for N in (4096, 20000):
