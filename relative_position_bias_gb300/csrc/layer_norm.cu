@@ -46,10 +46,10 @@ template <int XF, int NV>
 cudaError_t fwd_warp(LnArgs& a, int sms, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   const int row = a.C * size_of(XF), params = a.w ? (a.b ? 8 : 4) * a.C : 0;
-  a.sets = std::max(1, std::min(8, (kRingMost / 2 - 2048 - 640 - params) / 8 / row));
+  a.sets = std::max(1, std::min(8, (kRingMost / ln_warp_blocks(NV) - 2048 - 640 - params) / 8 / row));
   LnPlan p;
   p.threads = 256;
-  p.grid = static_cast<int>(std::min(ceil_div(a.rows, 8), 2ll * std::max(sms, 1)));
+  p.grid = static_cast<int>(std::min(ceil_div(a.rows, 8), static_cast<long long>(ln_warp_blocks(NV)) * std::max(sms, 1)));
   return launch(layer_norm_warp_kernel<XF, NV>, a, p, 640 + params + 8 * a.sets * row, done, s);
 }
 
@@ -132,32 +132,30 @@ cudaError_t launch_partial_rows(const float* parts, int rows, int n, int n1, flo
   return launch_early(partial_rows_kernel, dim3((n + 31) / 32), dim3(32, 32), 0, s, parts, rows, n, n1, d1, d2);
 }
 
-// dpre = dy act'(pre): bound by memory; eight elements a thread where n and the addresses allow.
-template <int ACT, bool VEC>
+// dpre = dy act'(pre): bound by memory; eight elements a thread, what is left at the end one each.  8 x 4096 x 2048, fp16 to fp32,
+// 537 MB: 93 us, 5.8 TB/s.
+template <int ACT>
 __global__ void __launch_bounds__(256) act_backward_kernel(const ActArgs a) {
-  constexpr int E = VEC ? 8 : 1;
-  const long long step = static_cast<long long>(gridDim.x) * 256 * E;
-  for (long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * E; i < a.n; i += step) {
-    if (VEC) {
-      float u[8], z[8];
-      load8(a.pre, i, u, a.fmt);
-      load8(a.dy, i, z, a.z_fmt);
-      slope_all<ACT>(z, u);
-      store8(a.dpre, i, z, a.out_fmt);
-    } else {
-      const float z = load_elem(a.dy, i, a.z_fmt) * act_slope<ACT>(pair_of(load_elem(a.pre, i, a.fmt))).x;
-      if (a.out_fmt == kF32) static_cast<float*>(a.dpre)[i] = z;
-      else static_cast<uint16_t*>(a.dpre)[i] = static_cast<uint16_t>(pack_in(z, 0.f, a.out_fmt));
-    }
+  const long long n8 = a.n & ~7ll, step = static_cast<long long>(gridDim.x) * 2048;
+  for (long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 8; i < n8; i += step) {
+    float u[8], z[8];
+    load8(a.pre, i, u, a.fmt);
+    load8(a.dy, i, z, a.z_fmt);
+    slope_all<ACT>(z, u);
+    store8(a.dpre, i, z, a.out_fmt);
+  }
+  const long long i = n8 + threadIdx.x;
+  if (blockIdx.x == 0 && i < a.n) {
+    const float z = load_elem(a.dy, i, a.z_fmt) * act_slope<ACT>(pair_of(load_elem(a.pre, i, a.fmt))).x;
+    if (a.out_fmt == kF32) static_cast<float*>(a.dpre)[i] = z;
+    else static_cast<uint16_t*>(a.dpre)[i] = static_cast<uint16_t>(pack_in(z, 0.f, a.out_fmt));
   }
 }
 
 template <int ACT>
 static cudaError_t act_backward(const ActArgs& a, int sms, cudaStream_t s) {
-  const bool vec = a.n % 8 == 0;
-  const long long blocks = std::min(ceil_div(a.n, vec ? 2048 : 256), static_cast<long long>(std::max(sms, 1)) * 64);
-  if (vec) act_backward_kernel<ACT, true><<<static_cast<int>(blocks), 256, 0, s>>>(a);
-  else act_backward_kernel<ACT, false><<<static_cast<int>(blocks), 256, 0, s>>>(a);
+  const long long blocks = std::min(ceil_div(a.n, 2048), static_cast<long long>(std::max(sms, 1)) * 64);
+  act_backward_kernel<ACT><<<static_cast<int>(blocks), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 

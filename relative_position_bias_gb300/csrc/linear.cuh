@@ -343,6 +343,8 @@ __device__ __forceinline__ void lin_sum_of(uint32_t taddr, int apart, int accs, 
 // Up to 128 tokens: 128 features by BN tokens a tile, the features as rows, so that a product of few tokens still fills the tensor
 // core's 128 rows.  What counts then is how many SMs read the weight: a cluster of CTAs shares a tile, each with a piece of the
 // contraction, and each adds up all of their parts for its share of the tokens, through distributed shared memory and in order.
+// 32 tokens x 1024 x 4096: 6 us (9.6 without clusters; the weight's 8 MB take 1.2 at 6.8 TB/s), 32 x 4096 x 1024 7 (19 without); the
+// rest is the kernel's start, two trips to memory and the exchange.
 template <int KIND, int BN, bool BF16>
 __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_constant__ CUtensorMap map_a,
                                                                  const __grid_constant__ CUtensorMap map_b,

@@ -5,6 +5,11 @@
 // with one pipeline of loads, and the accumulators have two buffers in TMEM, so that a tile's epilogue runs while the next tile's
 // products do.
 //
+// Measured (bf16): 32768 x 1024 x 4096 152 us, 1.8 PFLOP/s (a library product 143; without its stores 143, without its epilogue 131),
+// with gelu 174, and its argument kept 200; 32768 x 2048 x 2048 from the attention's heads onto a residual 162; the input's gradient through
+// gelu, 32768 x 4096 x 1024, 205; dW of the same 163 to 178 (64 tiles for 76 pairs: 84 % of them have work); 4900 x 768 x 2304 18
+// (three waves for 2.4; a library product 11.6).
+//
 // The tensor core cuts towards zero what it adds to its fp32 sum, so a long chain drifts: 3.4e-5 of the sum after
 // 30 000 terms, 5e-6 after 4096.  Where the result is fp32 (FINE), and for the weight's gradient, whose sums over tokens have no limit,
 // chains end after kLinChain steps (512 terms, 6e-7), and the epilogue adds them in registers while the next chain runs in the

@@ -284,6 +284,31 @@ def test_streams_and_graphs(N):
     assert rpb.device_status() == 0
 
 
+@pytest.mark.parametrize("N", [5, 140, 1000])
+@pytest.mark.parametrize("gd", [BF, F32])
+@pytest.mark.parametrize("heads,d", [(1, 136), (3, 64)])
+def test_a_gradient_into_a_larger_buffer(N, gd, heads, d):
+    """dx by strides of the caller's: the rows, heads and columns beside it are left as they were."""
+    B, K, out = 2, heads * d, 264
+    g = torch.Generator().manual_seed(15)
+    x = tokens(B, N, K, 0, BF, g)
+    w, dy = torch.randn(out, K, generator=g).to(BF).cuda(), torch.randn(B, N, out, generator=g).to(BF).cuda()
+    want = rpb.linear_backward(dy, x, w, weight_grad=False, bias_grad=False, grad_dtype=gd)[0]
+    buf = torch.full((B, N + 3, heads + 1, d + 16), 7.0, dtype=gd, device="cuda")
+    sb, sn, sh, _ = buf.stride()
+    at = torch.tensor([buf.data_ptr(), sb, sn, sh], dtype=torch.int64).numpy().tobytes()
+    code = {BF: rpb.DERA_BF16, F32: rpb.DERA_F32}[gd]
+    assert rpb.load_library().dera_linear_backward(dy.data_ptr(), None, w.data_ptr(), None, at, None, None, B, N, heads, d, out, 0,
+                                                   rpb.DERA_BF16, code, rpb.DERA_F32, None, 0,
+                                                   torch.cuda.current_stream().cuda_stream) == 0
+    got = buf[:, :N, :heads, :d].reshape(B, N, K)
+    # tiles may lie otherwise, and sums be taken in another order
+    near(got, f64(want), 2 * rounding(f64(want), gd) + 2 * tol.product(flat(dy, out), f64(w).T).reshape(B, N, K), "dx")
+    keep = torch.ones_like(buf, dtype=torch.bool)
+    keep[:, :N, :heads, :d] = False
+    assert (buf[keep] == 7.0).all()
+
+
 def test_workspaces():
     """A caller's own, of exactly the size, with anything in it; too small, off its alignment and none at all are refused."""
     g = torch.Generator().manual_seed(12)
