@@ -88,7 +88,7 @@ typedef enum dera_activation {
  *      the activation needs).
  * K and out_features are multiples of 8, head_dim of 64 where heads > 1.  Sums are fp32.  The tensor core cuts towards zero
  * when it adds, at most 2^-23 of a partial sum for every 16 terms: where y is fp32 it does so for no more than 512 terms at a
- * time (with up to 128 tokens K / 4), and these sums are added with rounding (5e-7 of y); where y has 16 bits, over all K
+ * time (with few tokens K / 4), and these sums are added with rounding (5e-7 of y); where y has 16 bits, over all K
  * (1.2e-9 K, below its rounding).  Bias,
  * activation and residual are applied in fp32, and y (and pre) rounded once.  x and weight must be finite.  Gelu's Phi is off by 2^-19
  * of its distance to 0 or 1; an element's last bit may depend on its neighbour's.

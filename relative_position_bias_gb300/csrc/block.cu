@@ -111,7 +111,7 @@ void join_heads(const HeadsPtr& t, int* heads, int* d) {
 int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
 // Columns of a tile for `tokens` of them in a turned product.
-int turned_columns(int tokens) { return tokens <= 32 ? 32 : (tokens <= 64 ? 64 : 128); }
+int turned_columns(int tokens) { return tokens <= 32 ? 32 : (tokens <= 64 ? 64 : (tokens <= 128 ? 128 : 256)); }
 
 // Cuts rows x cols of D into tiles; false if there are more than a grid holds.
 bool cut(LinArgs* a, const LinPlan& p, int batches, int rows, int cols) {
@@ -136,13 +136,24 @@ LinPlan token_plan(const Tokens& tok, int features, int steps, bool f32, bool ge
   LinPlan p = {};
   p.pieces = 1;
   p.piece_steps = steps;
-  if (tok.merged && tok.N <= 128) {
-    p.turned = true;
-    p.bn = turned_columns(tok.N);
-    // the largest cluster that leaves every CTA two steps or more, and no more CTAs than there are SMs
-    const int tiles = ceil_div(features, 128);
-    while (p.pieces < 8 && 4 * p.pieces <= steps && 2 * p.pieces * tiles <= sms) p.pieces *= 2;
-    return p;
+  // Few tokens take linear_few_kernel: up to 128 always.  More, 256 to a tile, only where a contraction is long and the tiles so
+  // few that each has a whole cluster of 8: the pairs' kernel has one CTA pair a tile and takes 5.3 us + 0.23 a step, this one
+  // 12 + 0.27 for an eighth of the steps.  256 tokens x 4096 x 1024: 13.4 us against 19.6, 300 x 8192 x 512 15.7 against 33.9; but
+  // 256 x 1024 x 1024 11.9 against 8.8 and, with a cluster of 4, 512 x 4096 x 1024 25.3 against 19.7.
+  if (tok.merged && (tok.N <= 128 || steps >= 48)) {
+    const int bn = turned_columns(tok.N);
+    const long long tiles = static_cast<long long>(ceil_div(features, 128)) * ceil_div(tok.N, bn);
+    // The largest cluster that leaves every CTA two steps or more and that all tiles can have at the same time.  A cluster lies
+    // within a group of SMs that share their way to memory, so that 152 SMs hold 15 of 8, not 19: 256 x 4096 x 1920 (15 tiles)
+    // takes 14.3 us, x 2048 in two rounds 25.4.
+    int pieces = 8;
+    while (pieces > 1 && (2 * pieces > steps || tiles > few_clusters(pieces))) pieces /= 2;
+    if (tok.N <= 128 || pieces == 8) {
+      p.turned = true;
+      p.bn = bn;
+      p.pieces = pieces;
+      return p;
+    }
   }
   const int pairs = std::max(1, sms / 2);
   const double m = static_cast<double>(tok.B) * ceil_div(tok.N, 256);

@@ -110,6 +110,8 @@ struct LinJoin {
   int sum_rows, out;
 };
 cudaError_t launch_linear_join(const LinJoin& j, cudaStream_t s);
+// Clusters of 2, 4 or 8 CTAs of linear_few_kernel that run at the same time on the current device, one CTA an SM.
+int few_clusters(int size);
 cudaError_t launch_linear_forward(const LinMaps& m, const LinArgs& a, const LinPlan& p, cudaStream_t s);
 cudaError_t launch_linear_input(const LinMaps& m, const LinArgs& a, const LinPlan& p, cudaStream_t s);
 cudaError_t launch_linear_weight(const LinMaps& m, const LinArgs& a, const LinPlan& p, cudaStream_t s);

@@ -20,7 +20,7 @@ template <int BN>
 struct LinSmem {
   static constexpr int kA = 128 * 128, kB = BN * 128;
   static constexpr int kStage = kA + kB;
-  static constexpr int NS = BN == 128 ? 6 : 8;
+  static constexpr int NS = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
   static constexpr int kBars = NS * kStage;
   static constexpr int kMisc = kBars + (2 * NS + 1) * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
@@ -340,10 +340,10 @@ __device__ __forceinline__ void lin_sum_of(uint32_t taddr, int apart, int accs, 
   }
 }
 
-// Up to 128 tokens: 128 features by BN tokens a tile, the features as rows, so that a product of few tokens still fills the tensor
+// Few tokens: 128 features by BN tokens a tile, the features as rows, so that a product of few tokens still fills the tensor
 // core's 128 rows.  What counts then is how many SMs read the weight: a cluster of CTAs shares a tile, each with a piece of the
 // contraction, and each adds up all of their parts for its share of the tokens, through distributed shared memory and in order.
-// 32 tokens x 1024 x 4096: 6 us (9.6 without clusters; the weight's 8 MB take 1.2 at 6.8 TB/s), 32 x 4096 x 1024 7 (19 without); the
+// 32 tokens x 1024 x 4096: 6.5 us (9.6 without clusters; the weight's 8 MB take 1.2 at 6.8 TB/s), 32 x 4096 x 1024 7 (19 without); the
 // rest is the kernel's start, two trips to memory and the exchange.
 template <int KIND, int BN, bool BF16>
 __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_constant__ CUtensorMap map_a,
@@ -352,9 +352,9 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
   using SM = LinSmem<BN>;
   constexpr int NS = SM::NS;
   constexpr bool A_MN = KIND == kLinInput;   // W's columns in the input's gradient
-  // A piece's steps go to four sums in turn, which are added at the end: the tensor core cuts towards zero when it adds, and a long
-  // chain drifts (linear_pair.cuh).
-  constexpr int ACCS = 4;
+  // A piece's steps go to four sums (two of 256 tokens) in turn, which are added at the end: the tensor core cuts towards zero when
+  // it adds, and a long chain drifts (linear_pair.cuh).
+  constexpr int ACCS = BN == 256 ? 2 : 4;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -363,10 +363,10 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
   uint64_t* done = empty + NS;
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::kMisc + 4);
-  float* part = reinterpret_cast<float*>(smem);   // [BN][128] once the products are done
+  float4* part = reinterpret_cast<float4*>(smem);   // [BN / 4][128 features] four tokens, once the products are done
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank()), pieces = a.pieces;
-  const int r0 = blockIdx.x / pieces * 128;
+  const int r0 = blockIdx.x / pieces * 128, c0 = blockIdx.y * BN;   // first feature and token
   const int s0 = rank * a.steps / pieces, s1 = (rank + 1) * a.steps / pieces;
   if (threadIdx.x == 128) {
     tma_prefetch_desc(&map_a);
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
   if (warp == 4) {
     if (lane == 0) {
       LinCursor<A_MN, 128> at_a(a.a_d, r0, 0, s0, a.steps);
-      LinCursor<false, BN> at_b(a.b_d, 0, 0, s0, a.steps);
+      LinCursor<false, BN> at_b(a.b_d, c0, 0, s0, a.steps);
       int n = 0;
       for (int s = s0; s < s1; ++s, ++n) {
         const int st = n % NS;
@@ -438,33 +438,47 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
         float v[16];
         lin_sum_of(taddr + c, BN, accs, v);
         #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c + j) * 128 + threadIdx.x] = v[j];
+        for (int j = 0; j < 4; ++j)
+          part[(c / 4 + j) * 128 + threadIdx.x] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
       }
     }
     __syncwarp();
     cluster_sync_all();
-    // this CTA's share of the tokens, four at a time; every CTA's part of them, one after another
+    // this CTA's share of the tokens, T at a time; every CTA's part of them, added in order (their loads are all on their way before
+    // the first is needed)
     const int share = BN / pieces;
-    if (warp < 4 && f < a.rows) {
+    auto join = [&](auto tokens) {
+      constexpr int T = decltype(tokens)::value;
       #pragma unroll 1
-      for (int t = rank * share; t < (rank + 1) * share && t < a.cols; t += 4) {
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int t = rank * share; t < (rank + 1) * share && c0 + t < a.cols; t += T) {
+        float v[T];
+        #pragma unroll
+        for (int j = 0; j < T; ++j) v[j] = 0.f;
+        const float4* from = part + t / 4 * 128 + threadIdx.x;
+        #pragma unroll 4
         for (int p = 0; p < pieces; ++p) {
-          const uint32_t from = cluster_map(part + t * 128 + threadIdx.x, p);
+          const uint32_t at = cluster_map(from, p);
           #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] += ld_cluster(from + j * 512);
+          for (int j = 0; j < T / 4; ++j) {
+            const float4 x = ld_cluster4(at + j * 2048);
+            v[4 * j] += x.x, v[4 * j + 1] += x.y, v[4 * j + 2] += x.z, v[4 * j + 3] += x.w;
+          }
         }
-        lin_finish_turned<KIND>(a, v, t, f, min(4, a.cols - t));
+        lin_finish_turned<KIND>(a, v, c0 + t, f, min(T, a.cols - c0 - t));
       }
+    };
+    if (warp < 4 && f < a.rows) {
+      if (share >= 8) join(std::integral_constant<int, 8>());
+      else join(std::integral_constant<int, 4>());
     }
     __syncwarp();
     cluster_sync_all_relaxed();   // no CTA leaves while its part is read
   } else if (ok) {
     #pragma unroll 1
-    for (int c = 0; c < BN && c < a.cols; c += 16) {
+    for (int c = 0; c < BN && c0 + c < a.cols; c += 16) {
       float v[16];
       lin_sum_of(taddr + c, BN, accs, v);
-      if (f < a.rows) lin_finish_turned<KIND>(a, v, c, f, min(16, a.cols - c));
+      if (f < a.rows) lin_finish_turned<KIND>(a, v, c0 + c, f, min(16, a.cols - c0 - c));
     }
   }
   __syncwarp();

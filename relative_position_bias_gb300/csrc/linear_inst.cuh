@@ -6,23 +6,29 @@
 
 namespace dera {
 
+static void cluster_launch(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int size, int smem) {
+  *attr = {};
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = size;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  *cfg = {};
+  cfg->blockDim = dim3(kLinThreads);
+  cfg->dynamicSmemBytes = smem;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
+
 template <int KIND, int BN, bool BF16>
 static cudaError_t launch_lin_few(const LinMaps& m, const LinArgs& a, cudaStream_t s) {
   auto kernel = linear_few_kernel<KIND, BN, BF16>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = prepare_kernel(kernel, LinSmem<BN>::kAlloc, 0, done);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = a.pieces;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.m_tiles * a.pieces);
-  cfg.blockDim = dim3(kLinThreads);
-  cfg.dynamicSmemBytes = LinSmem<BN>::kAlloc;
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg;
+  cluster_launch(&cfg, &attr, a.pieces, LinSmem<BN>::kAlloc);
+  cfg.gridDim = dim3(a.m_tiles * a.pieces, a.n_tiles);
   cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, m.a, m.b, a);
 }
 
@@ -42,7 +48,8 @@ static cudaError_t launch_lin_kind(const LinMaps& m, const LinArgs& a, const Lin
   if constexpr (KIND != kLinWeight) {
     if (p.turned) {
       if (p.bn == 32) return launch_lin_few<KIND, 32, BF16>(m, a, s);
-      return p.bn == 64 ? launch_lin_few<KIND, 64, BF16>(m, a, s) : launch_lin_few<KIND, 128, BF16>(m, a, s);
+      if (p.bn == 64) return launch_lin_few<KIND, 64, BF16>(m, a, s);
+      return p.bn == 128 ? launch_lin_few<KIND, 128, BF16>(m, a, s) : launch_lin_few<KIND, 256, BF16>(m, a, s);
     }
     if (p.fine)
       return p.bn == 128 ? launch_lin_pair<KIND, 128, 8, true, BF16>(m, a, p.pairs, s)

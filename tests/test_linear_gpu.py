@@ -85,6 +85,10 @@ SIZES = {
     "heads_few": (2, 5, 128, 40, 64, HF, HF),
     "heads_one": (2, 300, 64, 64, 64, BF, BF),
     "long": (1, 200, 4104, 328, 0, BF, F32),
+    "many_features": (1, 32, 768, 2088, 0, HF, F32),
+    "long_tiles": (1, 600, 3144, 456, 0, HF, HF),
+    "long_heads": (1, 257, 4096, 264, 64, BF, F32),
+    "long_gradient": (2, 150, 264, 4104, 0, BF, F32),
     "wide": (1, 260, 136, 2304, 0, HF, HF),
     "image": (1, 1369, 256, 520, 0, BF, F32),
     "pairs": (1, 2500, 200, 2056, 0, BF, BF),
