@@ -131,8 +131,8 @@ bool cut(LinArgs* a, const LinPlan& p, int batches, int rows, int cols) {
   return true;
 }
 
-// How D of tokens (rows) by features is cut, `steps` steps long.
-LinPlan token_plan(const Tokens& tok, int features, int steps, bool f32, bool gelu_slope, int sms) {
+// How D of tokens (rows) by features is cut, `steps` steps long.  `long_epilogue`: one that outlasts a tile's products.
+LinPlan token_plan(const Tokens& tok, int features, int steps, bool f32, bool long_epilogue, int sms) {
   LinPlan p = {};
   p.pieces = 1;
   p.piece_steps = steps;
@@ -165,7 +165,7 @@ LinPlan token_plan(const Tokens& tok, int features, int steps, bool f32, bool ge
   const double t_narrow = 5.3 + std::ceil(narrow / pairs) * std::max(0.23 * steps, 2.4);
   p.bn = t_wide <= t_narrow ? 256 : 128;
   p.fine = f32 && steps > 8;   // a chain of linear_pair.cuh
-  p.epi = p.bn == 256 && gelu_slope && !p.fine ? 16 : 8;
+  p.epi = p.bn == 256 && long_epilogue && !p.fine ? 16 : 8;
   p.pairs = static_cast<int>(std::min<double>(pairs, p.bn == 256 ? wide : narrow));
   return p;
 }
@@ -355,7 +355,10 @@ dera_status dera_linear(const dera_heads* x, const void* weight, const void* bia
   a.fmt = fmt_of(in_dtype);
   a.bias_fmt = fmt_of(bias_dtype);
   a.aux_fmt = a.out_fmt = fmt_of(out_dtype);
-  const LinPlan p = token_plan(tok, out_features, a.steps, out_dtype == DERA_F32, false, sm_count(dev));
+  // (linear_pair.cuh has both sides measured; with one slot a warp there is no room for a residual and an argument)
+  const bool long_epilogue = activation > DERA_ACT_RELU && a.steps <= (activation == DERA_ACT_GELU ? 16 : 12) && !residual &&
+                             out_dtype != DERA_F32;
+  const LinPlan p = token_plan(tok, out_features, a.steps, out_dtype == DERA_F32, long_epilogue, sm_count(dev));
   if (!(p.turned ? cut(&a, p, 1, out_features, tok.N) : cut(&a, p, tok.B, tok.N, out_features))) return DERA_ERR_SHAPE;
   LinMaps m = {};
   const HeadsPtr xm = tok.of(xt, N), wm = rows_of(weight, out_features, K);
@@ -367,7 +370,7 @@ dera_status dera_linear(const dera_heads* x, const void* weight, const void* bia
   if (!p.turned) {
     const HeadsPtr ym = tok.of(rows_of(y, N, out_features), N), rm = {const_cast<char*>(static_cast<const char*>(residual)), ym.sb, ym.st, 0},
                    pm = {static_cast<char*>(pre), ym.sb, ym.st, 0};
-    const int box = box_columns(out_dtype);
+    const int box = p.epi == 16 && pre ? 32 : box_columns(out_dtype);   // as the kernel's `narrow`
     if (!map_boxes(&m.out, ym, out_dtype, tok.B, tok.N, 1, out_features, box) ||
         (residual && !map_boxes(&m.aux, rm, out_dtype, tok.B, tok.N, 1, out_features, box)) ||
         (pre && !map_boxes(&m.pre, pm, in_dtype, tok.B, tok.N, 1, out_features, box)))
@@ -446,7 +449,8 @@ dera_status dera_linear_backward(const void* dy, const dera_heads* x, const void
     a.act = input_activation;
     a.fmt = a.aux_fmt = fmt_of(in_dtype);
     a.out_fmt = fmt_of(grad_dtype);
-    const LinPlan p = token_plan(tok, K, a.steps, grad_dtype == DERA_F32, input_activation == DERA_ACT_GELU, sms);
+    const bool long_epilogue = input_activation == DERA_ACT_GELU || (input_activation > DERA_ACT_RELU && a.steps <= 12);
+    const LinPlan p = token_plan(tok, K, a.steps, grad_dtype == DERA_F32, long_epilogue, sms);
     LinMaps m = {};
     CUtensorMap *mg = p.turned ? &m.b : &m.a, *mw = p.turned ? &m.a : &m.b;
     if (!(p.turned ? cut(&a, p, 1, K, tok.N) : cut(&a, p, tok.B, tok.N, K))) return DERA_ERR_SHAPE;

@@ -141,19 +141,19 @@ __device__ __forceinline__ void lin_read(uint8_t* slot, float (&x)[32], int fmt,
 
 // wait() returns whether D is complete (of the whole warp), done() says that it has been read.  SLOTS: of 4 KB, one or two a warp.
 //   16-bit output            a box a group of 64 columns, with two slots each group's its own
-//   ... and an argument      a slot each (the forward has two)
+//   ... and an argument      a slot each; with one slot (then nothing is read beside D) half a slot each, a box a half group
 //   fp32 output              a box a half group, with two slots its own; an argument goes through the half's slot first
 // FINE: D is not in TMEM, but after wait() in acc.
 template <int KIND, int COLS, int SLOTS, bool FINE, class Wait, class Done>
 __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32_t taddr, float (&acc)[FINE ? COLS : 1], int b, int row0,
                                              int f0, volatile int* abort_flag, Wait&& wait, Done&& done) {
   static_assert(COLS == 64 || (COLS == 128 && SLOTS == 2), "one or two groups of 64 columns");
-  static_assert(KIND == kLinInput || SLOTS == 2, "room for the activation's argument");
   static_assert(!FINE || SLOTS == 2, "registers for D");
   constexpr int GROUPS = COLS / 64;
   const int lane = threadIdx.x & 31;
   const bool out16 = a.out_fmt != kF32, own = out16 && !(KIND == kLinForward && a.pre);
-  const bool halves = !out16;   // a box a half group
+  const bool narrow = SLOTS == 1 && KIND == kLinForward && a.pre;   // boxes of 64-byte rows
+  const bool halves = !out16 || narrow;   // a box a half group
   const bool rows_in = row0 < a.rows;
   auto fetch = [&](int f, int i) {   // by one lane: the box beside D from column f into slot i
     if (!rows_in || f >= a.cols) return;
@@ -260,7 +260,7 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32
       if (KIND == kLinForward) {
         if (a.pre) {
           if (out16) {
-            lin_write(e.slot + 4096, v, a.fmt, half, false);
+            lin_write(e.slot + (narrow ? 2048 : 4096), v, a.fmt, half, narrow);
           } else {
             lin_write(slot, v, a.fmt, 0, true);
             fence_proxy_async_smem();
@@ -280,13 +280,13 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32
         }
       }
       if (KIND == kLinInput && a.aux) with_act(a.act, [&](auto A) { slope_all<decltype(A)::value>(v, x); });
-      lin_write(slot, v, a.out_fmt, half, false);
+      lin_write(slot, v, a.out_fmt, half, narrow);
       if (!halves && half == 0 && f + 32 < a.cols) continue;   // the other half of the box
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         const int at = halves ? fh + 32 * half : fh;
-        if (KIND == kLinForward && a.pre && out16) tma_store_4d(e.pre, e.slot + 4096, at, row0, h, b);
+        if (KIND == kLinForward && a.pre && out16) tma_store_4d(e.pre, e.slot + (narrow ? 2048 : 4096), at, row0, h, b);
         tma_store_4d(e.out, slot, at, row0, h, b);
         bulk_commit();
       }

@@ -56,7 +56,7 @@ static cudaError_t launch_lin_kind(const LinMaps& m, const LinArgs& a, const Lin
                          : launch_lin_pair<KIND, 256, 8, true, BF16>(m, a, p.pairs, s);
     if (p.bn == 128) return launch_lin_pair<KIND, 128, 8, false, BF16>(m, a, p.pairs, s);
   }
-  if constexpr (KIND == kLinInput)
+  if constexpr (KIND != kLinWeight)
     if (p.epi == 16) return launch_lin_pair<KIND, 256, 16, false, BF16>(m, a, p.pairs, s);
   return launch_lin_pair<KIND, 256, 8, false, BF16>(m, a, p.pairs, s);
 }

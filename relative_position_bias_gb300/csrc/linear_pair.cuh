@@ -6,8 +6,8 @@
 // products do.
 //
 // Measured (bf16): 32768 x 1024 x 4096 152 us, 1.8 PFLOP/s (a library product 143; without its stores 143, without its epilogue 131),
-// with gelu 174, and its argument kept 200; 32768 x 2048 x 2048 from the attention's heads onto a residual 162; the input's gradient through
-// gelu, 32768 x 4096 x 1024, 205; dW of the same 163 to 178 (64 tiles for 76 pairs: 84 % of them have work); 4900 x 768 x 2304 18
+// with gelu 171, and its argument kept 198; 32768 x 2048 x 2048 from the attention's heads onto a residual 162; the input's gradient through
+// gelu, 32768 x 4096 x 1024, 200; dW of the same 163 to 178 (64 tiles for 76 pairs: 84 % of them have work); 4900 x 768 x 2304 18
 // (three waves for 2.4; a library product 11.6).
 //
 // The tensor core cuts towards zero what it adds to its fp32 sum, so a long chain drifts: 3.4e-5 of the sum after
@@ -19,10 +19,12 @@
 
 namespace dera {
 
-// A warp that loads, one that multiplies, two that wait, and eight of the epilogue; sixteen, with half of the columns each, for the
-// input's gradient through gelu.  Sixteen end a tile sooner, but take so much of TMEM and of the shared memory at once that the products
-// beside them wait: 32768 x 1024 x 4096 takes 152 us with eight and 162 with sixteen, with gelu 181 and 183; the input's gradient
-// through gelu, 32768 x 4096 x 1024, with its load and its 20 instructions a pair, 229 and 209 (through relu 184 with eight).
+// A warp that loads, one that multiplies, two that wait, and eight of the epilogue; sixteen, with half of the columns each, where the
+// epilogue outlasts a tile's products.  Sixteen end a tile sooner, but take so much of TMEM and of the shared memory at once that products
+// beside them wait: 32768 x 1024 x 4096 takes 152 us with eight and 162 with sixteen, with gelu 182 and 172; 32768 x 768 x 2304 with
+// gelu 108 and 87 (its argument kept, 121 and 110), with silu 92 and 78, with relu 82 and 88; 32768 x 2048 x 2048 with gelu 160 and
+// 164.  The input's gradient through gelu, 32768 x 4096 x 1024, with its load and its 20 instructions a pair, 229 and 199 (through relu
+// 181 with eight), through silu 193 and 210, but 32768 x 2304 x 768 113 and 97.
 constexpr int pair_threads(int epi) { return 128 + 32 * epi; }
 constexpr int kLinChain = 8;
 
@@ -35,7 +37,7 @@ struct PairSmem {
   static constexpr int kRow = kEpi + (KIND == kLinWeight ? 32768 : 65536);
   static constexpr int kBars = kRow + (KIND == kLinForward ? EPI * 128 : 0);
   static constexpr int kMisc = kBars + (2 * NS + 5 + 2 * EPI) * 8;
-  static constexpr int kAlloc = kMisc + 16 + 1024;
+  static constexpr int kAlloc = kMisc + 16;
   static_assert(kAlloc <= 232448, "shared memory");
 };
 
@@ -86,9 +88,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(EPI), 1
   constexpr int NS = SM::NS;
   constexpr bool A_MN = KIND == kLinWeight, B_MN = KIND != kLinForward;
   constexpr bool WEIGHT = KIND == kLinWeight, CHAINS = WEIGHT || FINE;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  extern __shared__ __align__(1024) uint8_t smem[];   // there is no room to align it here
+  if (smem_u32(smem) & 1023u) {
+    if (threadIdx.x == 0) atomicCAS(a.status, 0, 8 /* DERA_ERR_CUDA */);
+    return;
+  }
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBars);   // the even CTA's: both CTAs' loads of a step landed
   uint64_t* empty = full + NS;                                      // each CTA's: the step's products are complete
   uint64_t* acc_full = empty + NS;                                  // each CTA's [2]: a chain is complete

@@ -150,6 +150,26 @@ def test_activations(act, N):
         check_backward(dy, x, w, rpb.linear_backward(dy, x, w, input_pre=ipre, input_activation=act), ipre, act)
 
 
+@pytest.mark.parametrize("act", ACTS[2:])
+@pytest.mark.parametrize("B,N,K,out,d,dt", [(1, 2500, 200, 2056, 0, BF), (3, 700, 384, 2088, 64, HF), (1, 5001, 768, 2128, 0, HF),
+                                            (2, 4900, 1024, 1024, 64, BF)])
+def test_long_epilogues(act, B, N, K, out, d, dt):
+    """Short contractions of many tiles, whose epilogue takes longer than their products."""
+    g = torch.Generator().manual_seed(12)
+    x = tokens(B, N, K, d, dt, g)
+    w = (torch.randn(out, K, generator=g) * K ** -0.5).to(dt).cuda()
+    b = torch.randn(out, generator=g).cuda()
+    y, pre = rpb.linear(x, w, b, activation=act, keep_pre=True)
+    check_forward(x, w, y, b, act, None, pre)
+    assert torch.equal(rpb.linear(x, w, b, activation=act), y)
+    dy = torch.randn(B, N, K, generator=g).to(dt).cuda()            # and back through a layer after it
+    ipre = tokens(B, N, out // 64 * 64, d, dt, g)
+    wb = (torch.randn(K, out // 64 * 64, generator=g) * K ** -0.5).to(dt).cuda()
+    for gd in (dt, F32):
+        got = rpb.linear_backward(dy, ipre, wb, input_pre=ipre, input_activation=act, weight_grad=False, bias_grad=False, grad_dtype=gd)
+        check_backward(dy, ipre, wb, got, ipre, act)
+
+
 @pytest.mark.parametrize("act", ACTS[1:])
 @pytest.mark.parametrize("n", [1, 8, 1000, 1003, 40960])
 @pytest.mark.parametrize("dt,zd,od", [(BF, BF, BF), (HF, HF, F32), (F32, F32, F32), (BF, F32, BF)])
