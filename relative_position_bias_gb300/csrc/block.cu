@@ -464,15 +464,6 @@ dera_status dera_linear_backward(const void* dy, const dera_heads* x, const void
     DERA_TRY(status_of(launch_linear_input(m, a, p, s)));
   }
   LinJoin join = {};
-  if (dbias) {
-    const long long rows = static_cast<long long>(B) * N;
-    join.sum_rows = sum_blocks(rows, out_features, sms);
-    join.sums = static_cast<float*>(workspace);
-    join.db = dbias;
-    join.out = out_features;
-    DERA_TRY(status_of(launch_column_sums(dy, rows, out_features, fmt_of(in_dtype), static_cast<float*>(workspace),
-                                          join.sum_rows, s)));
-  }
   if (dweight) {
     int h = heads, d = head_dim;
     join_heads(xt, &h, &d);
@@ -487,7 +478,8 @@ dera_status dera_linear_backward(const void* dy, const dera_heads* x, const void
     a.steps = tok.B * a.steps_batch;
     a.fmt = fmt_of(in_dtype);
     a.out_fmt = fmt_of(weight_grad_dtype);
-    const WeightPlan w = weight_plan(out_features, K, a.steps, sms);
+    WeightPlan w = weight_plan(out_features, K, a.steps, sms);
+    w.p.beside = dx != nullptr;
     if (!cut(&a, w.p, 1, out_features, K)) return DERA_ERR_SHAPE;
     if (w.p.pieces > 1) a.parts = reinterpret_cast<float*>(static_cast<char*>(workspace) + sums_bytes(static_cast<long long>(B) * N, out_features, sms));
     LinMaps m = {};
@@ -502,6 +494,15 @@ dera_status dera_linear_backward(const void* dy, const dera_heads* x, const void
       join.pieces = w.p.pieces;
       join.dw_fmt = a.out_fmt;
     }
+  }
+  if (dbias) {
+    const long long rows = static_cast<long long>(B) * N;
+    join.sum_rows = sum_blocks(rows, out_features, sms);
+    join.sums = static_cast<float*>(workspace);
+    join.db = dbias;
+    join.out = out_features;
+    DERA_TRY(status_of(launch_column_sums(dy, rows, out_features, fmt_of(in_dtype), static_cast<float*>(workspace),
+                                          join.sum_rows, dx || dweight, s)));
   }
   if (join.dw || join.db) DERA_TRY(status_of(launch_linear_join(join, s)));
   return DERA_OK;

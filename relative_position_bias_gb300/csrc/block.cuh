@@ -98,6 +98,7 @@ struct LinPlan {
   int epi;               // epilogue warps of a CTA of a pair
   bool fine;             // long sums in chains (an fp32 output)
   int pieces, piece_steps;
+  bool beside;           // kLinWeight: launched early, with the kernel before it on the stream, which is of the same call
 };
 // The end of a backward: dW from its pieces, and db from its partial rows (either may be absent).
 struct LinJoin {
@@ -116,6 +117,7 @@ cudaError_t launch_linear_forward(const LinMaps& m, const LinArgs& a, const LinP
 cudaError_t launch_linear_input(const LinMaps& m, const LinArgs& a, const LinPlan& p, cudaStream_t s);
 cudaError_t launch_linear_weight(const LinMaps& m, const LinArgs& a, const LinPlan& p, cudaStream_t s);
 // partial rows of g's column sums: [blocks][cols]
-cudaError_t launch_column_sums(const void* g, long long rows, int cols, int fmt, float* parts, int blocks, cudaStream_t s);
+// beside: early, with the kernel before it on the stream, which is of the same call
+cudaError_t launch_column_sums(const void* g, long long rows, int cols, int fmt, float* parts, int blocks, bool beside, cudaStream_t s);
 
 }  // namespace dera

@@ -368,6 +368,7 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
   const int rank = static_cast<int>(cluster_rank()), pieces = a.pieces;
   const int r0 = blockIdx.x / pieces * 128, c0 = blockIdx.y * BN;   // first feature and token
   const int s0 = rank * a.steps / pieces, s1 = (rank + 1) * a.steps / pieces;
+  if (KIND == kLinInput) grid_launch_dependents();   // as in linear_pair.cuh
   if (threadIdx.x == 128) {
     tma_prefetch_desc(&map_a);
     tma_prefetch_desc(&map_b);

@@ -33,11 +33,12 @@ static cudaError_t launch_lin_few(const LinMaps& m, const LinArgs& a, cudaStream
 }
 
 template <int KIND, int BN, int EPI, bool FINE, bool BF16>
-static cudaError_t launch_lin_pair(const LinMaps& m, const LinArgs& a, int pairs, cudaStream_t s) {
+static cudaError_t launch_lin_pair(const LinMaps& m, const LinArgs& a, int pairs, bool beside, cudaStream_t s) {
   auto kernel = linear_pair_kernel<KIND, BN, EPI, FINE, BF16>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = prepare_kernel(kernel, PairSmem<KIND, BN, EPI>::kAlloc, 0, done);
   if (e != cudaSuccess) return e;
+  if (beside) return launch_early(kernel, dim3(2 * pairs), dim3(pair_threads(EPI)), PairSmem<KIND, BN, EPI>::kAlloc, s, m, a);
   kernel<<<2 * pairs, pair_threads(EPI), PairSmem<KIND, BN, EPI>::kAlloc, s>>>(m, a);
   return cudaGetLastError();
 }
@@ -52,13 +53,13 @@ static cudaError_t launch_lin_kind(const LinMaps& m, const LinArgs& a, const Lin
       return p.bn == 128 ? launch_lin_few<KIND, 128, BF16>(m, a, s) : launch_lin_few<KIND, 256, BF16>(m, a, s);
     }
     if (p.fine)
-      return p.bn == 128 ? launch_lin_pair<KIND, 128, 8, true, BF16>(m, a, p.pairs, s)
-                         : launch_lin_pair<KIND, 256, 8, true, BF16>(m, a, p.pairs, s);
-    if (p.bn == 128) return launch_lin_pair<KIND, 128, 8, false, BF16>(m, a, p.pairs, s);
+      return p.bn == 128 ? launch_lin_pair<KIND, 128, 8, true, BF16>(m, a, p.pairs, p.beside, s)
+                         : launch_lin_pair<KIND, 256, 8, true, BF16>(m, a, p.pairs, p.beside, s);
+    if (p.bn == 128) return launch_lin_pair<KIND, 128, 8, false, BF16>(m, a, p.pairs, p.beside, s);
   }
   if constexpr (KIND != kLinWeight)
-    if (p.epi == 16) return launch_lin_pair<KIND, 256, 16, false, BF16>(m, a, p.pairs, s);
-  return launch_lin_pair<KIND, 256, 8, false, BF16>(m, a, p.pairs, s);
+    if (p.epi == 16) return launch_lin_pair<KIND, 256, 16, false, BF16>(m, a, p.pairs, p.beside, s);
+  return launch_lin_pair<KIND, 256, 8, false, BF16>(m, a, p.pairs, p.beside, s);
 }
 
 template <int KIND>

@@ -20,6 +20,7 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const void* g, long lo
   #pragma unroll
   for (int e = 0; e < 8; ++e) red[w][(threadIdx.x & 31) * 8 + e] = s[e];
   __syncthreads();
+  grid_wait_prerequisites();   // as in linear_pair.cuh
   const int col = blockIdx.y * 256 + threadIdx.x;
   if (col >= cols) return;
   float v = 0.f;
@@ -74,8 +75,10 @@ cudaError_t launch_linear_join(const LinJoin& j, cudaStream_t s) {
                       static_cast<int>(dw_blocks));
 }
 
-cudaError_t launch_column_sums(const void* g, long long rows, int cols, int fmt, float* parts, int blocks, cudaStream_t s) {
-  column_sums_kernel<<<dim3(blocks, (cols + 255) / 256), 256, 0, s>>>(g, rows, cols, fmt, parts);
+cudaError_t launch_column_sums(const void* g, long long rows, int cols, int fmt, float* parts, int blocks, bool beside, cudaStream_t s) {
+  const dim3 grid(blocks, (cols + 255) / 256);
+  if (beside) return launch_early(column_sums_kernel, grid, dim3(256), 0, s, g, rows, cols, fmt, parts);
+  column_sums_kernel<<<grid, 256, 0, s>>>(g, rows, cols, fmt, parts);
   return cudaGetLastError();
 }
 }  // namespace dera
