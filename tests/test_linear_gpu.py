@@ -408,3 +408,32 @@ def test_offsets_past_two_to_the_31():
     dx2, dw2, db2 = rpb.linear_backward(y[-140:].contiguous(), tail, w, grad_dtype=BF)
     assert torch.allclose(dx[-140:].float(), dx2.float(), rtol=2 ** -7, atol=1e-2) and not dx[:-140].any()
     assert torch.allclose(dw, dw2, rtol=1e-4, atol=1e-3) and torch.allclose(db, db2, rtol=1e-4, atol=1e-3)
+
+
+@pytest.mark.parametrize("N,K,out", [(20, 512, 768), (196, 768, 768), (1369, 768, 1000), (4900, 1024, 512)])
+def test_gradients_end_before_what_follows(N, K, out):
+    """The kernels of a backward run into one another: what is enqueued after the call may overwrite all that it read, and read all that
+    it wrote, with or without each gradient."""
+    g = torch.Generator().manual_seed(13)
+    dy0, x0 = torch.randn(N, out, generator=g).to(BF).cuda(), torch.randn(N, K, generator=g).to(BF).cuda()
+    w0 = (torch.randn(out, K, generator=g) / 30).to(BF).cuda()
+    ws = torch.empty(rpb.linear_backward_workspace_size(1, N, 1, K, out), dtype=torch.uint8, device="cuda")
+    which = [dict(input_grad=i, weight_grad=j, bias_grad=k) for i in (True, False) for j in (True, False) for k in (True, False) if i or j or k]
+    want = []
+    for kw in which:
+        want.append(rpb.linear_backward(dy0, x0, w0, **kw))
+        torch.cuda.synchronize()
+    bad = torch.zeros((), dtype=torch.int64, device="cuda")
+    dy, x, w = dy0.clone(), x0.clone(), w0.clone()
+    for _ in range(30):
+        for kw, ref in zip(which, want):
+            got = rpb.linear_backward(dy, x, w, workspace=ws, **kw)
+            for t in (dy, x, w):
+                t.fill_(float("nan"))
+            ws.fill_(255)
+            for a, b in zip(got, ref):
+                if a is not None:
+                    bad += (a != b).sum()
+            for t, t0 in ((dy, dy0), (x, x0), (w, w0)):
+                t.copy_(t0)
+    assert bad.item() == 0
