@@ -92,6 +92,12 @@ def _check(status: int) -> None:
         raise DeraError(status, msg)
 
 
+def _fits(sizes: int) -> None:
+    """Refuses sizes, given or'ed together, that a C int does not hold: ctypes would cut them to 32 bits and say nothing."""
+    if sizes >> 31:
+        _check(2)   # DERA_ERR_SHAPE
+
+
 def _code(t: torch.dtype) -> int:
     if t not in _DTYPE_CODE:
         raise TypeError(f"unsupported dtype {t}")

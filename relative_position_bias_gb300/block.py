@@ -13,7 +13,7 @@ import os
 import torch
 
 from . import api
-from .api import DERA_F32, _check, _ptr
+from .api import DERA_F32, _check, _fits, _ptr
 from .train import _dtype, _launch_stream, _pack_heads, _same, _scratch, _size, _want
 
 HEADER = os.path.join(os.path.dirname(api.HEADER), "dera_block.h")
@@ -54,6 +54,7 @@ def _norm_rows(x: torch.Tensor) -> tuple[int, int, int]:
         raise ValueError("x must be [..., C]")
     C = x.shape[-1]
     rows = x.numel() // C if C else 0
+    _fits(rows | C)
     if x.is_contiguous() or rows == 0:
         return rows, C, C
     if x.stride(-1) != 1 and C > 1:
@@ -173,6 +174,7 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = No
         raise ValueError("weight must be [out_features, K]")
     out, K = weight.shape
     B, N, heads, d = _tokens(x, K, "x")
+    _fits(B | N | heads | d | out)
     dt, dev = x.dtype, x.device
     od = out_dtype or dt
     _same(weight, (out, K), dt, "weight")
@@ -211,6 +213,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *, 
         raise ValueError("weight must be [out_features, K]")
     out, K = weight.shape
     B, N, heads, d = _tokens(x, K, "x")
+    _fits(B | N | heads | d | out)
     dt, dev = x.dtype, x.device
     gd, wd = grad_dtype or torch.float32, weight_grad_dtype or torch.float32
     _same(weight, (out, K), dt, "weight")

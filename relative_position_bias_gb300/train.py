@@ -11,13 +11,14 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import struct
 
 import torch
 
 from . import api
-from .api import DERA_F32, _check, _expect, _ptr
+from .api import DERA_F32, _check, _expect, _fits, _ptr
 
 HEADER = os.path.join(os.path.dirname(api.HEADER), "dera_train.h")
 _CODE = api._DTYPE_CODE
@@ -84,6 +85,7 @@ def _size_on(device_index: int, entry: str, *sizes: int) -> int:
 
 def _size(entry: str, *sizes: int) -> int:
     """The same on the current device, if there is one."""
+    _fits(functools.reduce(operator.or_, sizes))
     n = ctypes.c_size_t(0)
     _check(getattr(api.load_library(), entry)(*sizes, ctypes.byref(n)))
     return n.value
