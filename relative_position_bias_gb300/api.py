@@ -118,6 +118,7 @@ def _stream(device: torch.device, stream) -> int | None:
 
 def workspace_size(BH: int, H: int, W: int, head_dim: int = 64) -> int:
     """Scratch bytes the attention entries use for this size on the current device (0 if none)."""
+    _fits(BH | H | W | head_dim)
     n = ctypes.c_size_t(0)
     _check(load_library().dera_relpos_workspace_size(BH, H, W, head_dim, ctypes.byref(n)))
     return n.value
@@ -180,6 +181,7 @@ def project(q: torch.Tensor, rel_pos_h: torch.Tensor, rel_pos_w: torch.Tensor, H
             rel_w: torch.Tensor | None = None, stream=None):
     """``rel_h [BH,N,H]``, ``rel_w [BH,N,W]`` via ``dera_relpos_project``."""
     BH, N, d = q.shape
+    _fits(BH | H | W | d)
     if rel_h is None:
         rel_h = torch.empty((BH, N, H), dtype=bias_dtype, device=q.device)
     if rel_w is None:
@@ -206,6 +208,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h: torch.Te
     captured into a graph, False = no scratch (one CTA per unit), or a caller-owned uint8 tensor, which no other
     call in flight may use."""
     BH, N, d = q.shape
+    _fits(BH | H | W | d)
     scale = d ** -0.5 if scale is None else scale
     if out is None:
         out = torch.empty((BH, N, d), dtype=out_dtype or q.dtype, device=q.device)
@@ -231,6 +234,7 @@ def fused(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_pos_h: torch.Te
           out: torch.Tensor | None = None, stream=None, workspace=None) -> torch.Tensor:
     """Projection + attention in one kernel via ``dera_relpos_fused`` (``workspace`` as in :func:`attention`)."""
     BH, N, d = q.shape
+    _fits(BH | H | W | d)
     scale = d ** -0.5 if scale is None else scale
     if out is None:
         out = torch.empty((BH, N, d), dtype=out_dtype or q.dtype, device=q.device)
@@ -254,6 +258,7 @@ def fused_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_pos_h: torc
               workspace=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Training forward via ``dera_relpos_fused_lse``: ``(out, lse)``, lse [BH, N] fp32 (base 2)."""
     BH, N, d = q.shape
+    _fits(BH | H | W | d)
     scale = d ** -0.5 if scale is None else scale
     out = torch.empty((BH, N, d), dtype=out_dtype or q.dtype, device=q.device)
     lse = torch.empty((BH, N), dtype=torch.float32, device=q.device)
@@ -274,6 +279,7 @@ def fused_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_pos_h: torc
 
 def backward_workspace_size(BH: int, H: int, W: int, head_dim: int = 64) -> int:
     """Scratch bytes of :func:`fused_backward` for this size."""
+    _fits(BH | H | W | head_dim)
     n = ctypes.c_size_t(0)
     _check(load_library().dera_relpos_backward_workspace_size(BH, H, W, head_dim, ctypes.byref(n)))
     return n.value
@@ -287,6 +293,7 @@ def fused_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_pos_h:
     ``(dq, dk, dv, drel_pos_h, drel_pos_w)``; dq, dk, dv in ``grad_dtype`` (default fp32), the
     table gradients fp32.  ``out`` and ``lse`` come from :func:`fused_lse`."""
     BH, N, d = q.shape
+    _fits(BH | H | W | d)
     scale = d ** -0.5 if scale is None else scale
     gd = grad_dtype or torch.float32
     for t, name in ((q, "q"), (k, "k"), (v, "v"), (out, "out"), (dout, "dout")):

@@ -157,6 +157,7 @@ def _qk_common(q, k, v, q_weight, k_weight, cos, sin, positions):
         _same(positions, (B, N), torch.int32, "positions")
     elif positions is not None:
         raise ValueError("positions need cos and sin")
+    _fits(B | N | hq | hk | d | rot | rows)
     return B, N, hq, hk, d, rot, rows, wcode
 
 
@@ -250,6 +251,7 @@ def attention_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h: torc
     out = 0 and lse = -inf.  ``workspace``: a caller-owned uint8 tensor that no other call in flight
     uses, None for a buffer of this call, or False for none (whole units)."""
     BH, N, d = q.shape
+    _fits(BH | H | W | d)
     scale = d ** -0.5 if scale is None else scale
     size = (BH, H * W, d)
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
@@ -287,6 +289,7 @@ def attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rel_h:
     ``out`` and ``lse`` come from :func:`attention_lse`.  ``workspace``: a caller-owned uint8 tensor that
     no other call in flight uses, or None for a buffer of this call."""
     BH, N, d = q.shape
+    _fits(BH | H | W | d)
     scale = d ** -0.5 if scale is None else scale
     gd = grad_dtype or torch.float32
     size, size_h, size_w = (BH, H * W, d), (BH, N, H), (BH, N, W)
@@ -329,6 +332,7 @@ def project_backward(q: torch.Tensor, rel_pos_h: torch.Tensor, rel_pos_w: torch.
     of dq, to which the projection's is added (in a new tensor of the same dtype); else dq comes in
     ``grad_dtype`` (default fp32).  The tables' gradients are fp32."""
     BH, N, d = q.shape
+    _fits(BH | H | W | d)
     gd = grad_dtype or (torch.float32 if dq is None else dq.dtype)
     size, size_h, size_w = (BH, H * W, d), (2 * H - 1, d), (2 * W - 1, d)
     _want(q, size, "q")
