@@ -30,12 +30,12 @@ __device__ __forceinline__ int ln_col(int i, int e, int t, int tpr) {
   return VEC ? (i * tpr + t) * 8 + e : (i * 8 + e) * tpr + t;
 }
 
-// Eight elements of a row as they lie, 0 past its end.  FMT < 0: the type at run time.
+// Eight elements of a row as they lie, 0 past its end, or (`repeat`) its last ones again.  FMT < 0: the type at run time.
 template <int FMT, bool VEC>
 struct LnRaw {
   uint4 lo, hi;   // hi: the second half of fp32's
-  __device__ __forceinline__ void load(const char* row, int i, int t, int tpr, int C, bool there, int fmt) {
-    const int f = FMT >= 0 ? FMT : fmt, c = ln_col<VEC>(i, 0, t, tpr);
+  __device__ __forceinline__ void load(const char* row, int i, int t, int tpr, int C, bool there, int fmt, bool repeat = false) {
+    const int f = FMT >= 0 ? FMT : fmt, at = ln_col<VEC>(i, 0, t, tpr), c = repeat ? min(at, C - 8) : at;
     lo = hi = make_uint4(0u, 0u, 0u, 0u);
     if (!there || c >= C) return;
     const uint4* q = reinterpret_cast<const uint4*>(row + static_cast<size_t>(c) * (f == kF32 ? 4 : 2));
@@ -60,10 +60,10 @@ struct LnRaw {
 template <int FMT>
 struct LnRaw<FMT, false> {
   float x[8];
-  __device__ __forceinline__ void load(const char* row, int i, int t, int tpr, int C, bool there, int fmt) {
+  __device__ __forceinline__ void load(const char* row, int i, int t, int tpr, int C, bool there, int fmt, bool repeat = false) {
     #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = ln_col<false>(i, e, t, tpr);
+      const int at = ln_col<false>(i, e, t, tpr), c = repeat ? min(at, C - 1) : at;
       x[e] = there && c < C ? load_elem(row, c, FMT >= 0 ? FMT : fmt) : 0.f;
     }
   }
@@ -446,7 +446,9 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) layer_norm_bwd_kernel(const LnAr
     LnRaw<-1, VEC> d[NV];
     #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      x[i].load(xp, i, t, a.tpr, C, r < a.rows, a.x_fmt);
+      // past the row's end an x of the row, not 0: (0 - mean) rstd may be an infinity where no h of the row is, and 0 times it would
+      // reach the sums
+      x[i].load(xp, i, t, a.tpr, C, r < a.rows, a.x_fmt, true);
       z[i].load(zp, i, t, a.tpr, C, r < a.rows, a.y_fmt);
       d[i].load(dp, i, t, a.tpr, C, r < a.rows && dres, a.dx_fmt);
     }
@@ -470,6 +472,8 @@ __global__ void __launch_bounds__(MAXT, BLOCKS) layer_norm_bwd_kernel(const LnAr
     if (r + step < a.rows) {   // the next row's statistics are on their way
       mu = a.mean_in[r + step];
       rs = a.rstd_in[r + step];
+    } else {
+      mu = rs = 0.f;
     }
     const float t1 = s1.x + s1.y, t2 = s2.x + s2.y;
     const bool odd = j.lane & 1;
