@@ -197,6 +197,7 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32
       #pragma unroll
       for (int j = 0; j < 64; ++j) u[SLOTS == 2 ? j / 32 : 0][j & 31] = __float_as_uint(acc[FINE ? 64 * g + j : 0]);
     } else {
+      if (g > 0) __syncwarp();   // one lane stored the last group, the whole warp loads this one
       tmem_ld32(taddr + 64 * g, u[0]);
       if (SLOTS == 2) tmem_ld32(taddr + 64 * g + 32, u[SLOTS - 1]);
       tmem_wait_ld();
@@ -218,6 +219,7 @@ __device__ __forceinline__ bool lin_epilogue(const LinArgs& a, LinEpi& e, uint32
     for (int half = 0; half < 2; ++half) {
       const int f = fg + 32 * half;
       if (SLOTS == 1 && half == 1) {
+        __syncwarp();   // as above
         tmem_ld32(taddr + 32, u[0]);
         tmem_wait_ld();
         done();
@@ -480,6 +482,7 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
       float v[16];
       lin_sum_of(taddr + c, BN, accs, v);
       if (f < a.rows) lin_finish_turned<KIND>(a, v, c0 + c, f, min(16, a.cols - c0 - c));
+      __syncwarp();   // lanes without a feature left it out; the whole warp loads what follows
     }
   }
   __syncwarp();
