@@ -164,7 +164,7 @@ LinPlan token_plan(const Tokens& tok, int features, int steps, bool f32, bool lo
   const double t_wide = 7 + std::ceil(wide / pairs) * std::max(0.27 * steps, 3.0);
   const double t_narrow = 5.3 + std::ceil(narrow / pairs) * std::max(0.23 * steps, 2.4);
   p.bn = t_wide <= t_narrow ? 256 : 128;
-  p.fine = f32 && steps > 8;   // a chain of linear_pair.cuh
+  p.fine = f32 && steps > kLinChain;
   p.epi = p.bn == 256 && long_epilogue && !p.fine ? 16 : 8;
   p.pairs = static_cast<int>(std::min<double>(pairs, p.bn == 256 ? wide : narrow));
   return p;

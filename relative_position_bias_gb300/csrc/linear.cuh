@@ -22,7 +22,7 @@ struct LinSmem {
   static constexpr int kStage = kA + kB;
   static constexpr int NS = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
   static constexpr int kBars = NS * kStage;
-  static constexpr int kMisc = kBars + (2 * NS + 1) * 8;
+  static constexpr int kMisc = kBars + (2 * NS + 3) * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
   static_assert(kAlloc <= 232448, "shared memory");
 };
@@ -329,17 +329,18 @@ __device__ __forceinline__ void lin_finish_turned(const LinArgs& a, float (&v)[T
     if (j < count) store_elem(a.out, out + j * a.out_at.sn, v[j], a.out_fmt);
 }
 
-// Sixteen columns of `accs` sums in TMEM, `apart` columns from one to the next.
+// Sixteen columns of TMEM added to v, and v of `accs` sums, `apart` columns from one to the next.
+__device__ __forceinline__ void lin_add_to(uint32_t taddr, float (&v)[16]) {
+  uint32_t u[16];
+  tmem_ld16(taddr, u);
+  tmem_wait_ld();
+  #pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(u[j]);
+}
 __device__ __forceinline__ void lin_sum_of(uint32_t taddr, int apart, int accs, float (&v)[16]) {
   #pragma unroll
   for (int j = 0; j < 16; ++j) v[j] = 0.f;
-  for (int i = 0; i < accs; ++i) {
-    uint32_t u[16];
-    tmem_ld16(taddr + i * apart, u);
-    tmem_wait_ld();
-    #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(u[j]);
-  }
+  for (int i = 0; i < accs; ++i) lin_add_to(taddr + i * apart, v);
 }
 
 // Few tokens: 128 features by BN tokens a tile, the features as rows, so that a product of few tokens still fills the tensor
@@ -355,7 +356,8 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
   constexpr int NS = SM::NS;
   constexpr bool A_MN = KIND == kLinInput;   // W's columns in the input's gradient
   // A piece's steps go to four sums (two of 256 tokens) in turn, which are added at the end: the tensor core cuts towards zero when
-  // it adds, and a long chain drifts (linear_pair.cuh).
+  // it adds, and a long chain drifts (linear_pair.cuh).  Where the result is fp32 and a sum would have more than kLinChain steps, one of
+  // them is a total, to which the epilogue's warps add the others after every `round` steps; the loads run on meanwhile.
   constexpr int ACCS = BN == 256 ? 2 : 4;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -363,6 +365,8 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBars);
   uint64_t* empty = full + NS;
   uint64_t* done = empty + NS;
+  uint64_t* round_full = done + 1;
+  uint64_t* round_empty = done + 2;
   uint32_t* slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SM::kMisc + 4);
   float4* part = reinterpret_cast<float4*>(smem);   // [BN / 4][128 features] four tokens, once the products are done
@@ -370,6 +374,8 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
   const int rank = static_cast<int>(cluster_rank()), pieces = a.pieces;
   const int r0 = blockIdx.x / pieces * 128, c0 = blockIdx.y * BN;   // first feature and token
   const int s0 = rank * a.steps / pieces, s1 = (rank + 1) * a.steps / pieces;
+  const bool rounds = a.out_fmt == kF32 && s1 - s0 > kLinChain * ACCS;
+  const int live = rounds ? ACCS - 1 : ACCS, round = rounds ? kLinChain * live : s1 - s0, last = rounds ? (s1 - s0 - 1) / round : 0;
   if (KIND == kLinInput) grid_launch_dependents();   // as in linear_pair.cuh
   if (threadIdx.x == 128) {
     tma_prefetch_desc(&map_a);
@@ -377,7 +383,8 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
   }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < 2 * NS + 1; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < 2 * NS + 2; ++i) mbar_init(&full[i], 1);
+    mbar_init(round_empty, 4);
     fence_mbar_init();
   }
   if (warp == 5) {
@@ -414,25 +421,55 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
     constexpr uint32_t ka = A_MN ? 128 : 2;   // 16 contraction elements further, in 16 bytes
     const uint64_t da = sdesc_sw128(smem_u32(smem), A_MN ? 8192 : 16, 1024);
     const uint64_t db = sdesc_sw128(smem_u32(smem) + SM::kA, 16, 1024);
-    for (int n = 0; n < s1 - s0; ++n) {
+    int at = 0, sum = 0, r = 0;   // the step in its round, its sum, the round
+    for (int n = 0; n < s1 - s0; ++n, ++at) {
       const int st = n % NS;
+      if (at == round) {
+        umma_commit_w(round_full);
+        if (!warp_all(mbar_wait(round_empty, r & 1, abort_flag, a.status))) break;
+        at = sum = 0;
+        ++r;
+      }
       const bool ok = mbar_wait(&full[st], (n / NS) & 1, abort_flag, a.status);
       if (!warp_all(ok)) break;
       tc_fence_after();
       #pragma unroll
       for (int k = 0; k < 4; ++k)
-        umma_ss_w(tbase + BN * (n % ACCS), da + st * (SM::kStage >> 4) + ka * k, db + st * (SM::kStage >> 4) + 2 * k, id,
-                  (n >= ACCS || k > 0) ? 1u : 0u);
+        umma_ss_w(tbase + BN * sum, da + st * (SM::kStage >> 4) + ka * k, db + st * (SM::kStage >> 4) + 2 * k, id,
+                  (at >= live || k > 0) ? 1u : 0u);
+      if (++sum == live) sum = 0;
       umma_commit_w(&empty[st]);
     }
     umma_commit_w(done);
     mbar_wait_budget(done, 0, kWaitBudgetCycles);
     __syncwarp();
   }
+  const uint32_t taddr = tbase + (static_cast<uint32_t>(32 * warp) << 16), total = taddr + BN * (ACCS - 1);
+  if (warp < 4) {
+    for (int r = 0; r < last && warp_all(mbar_wait(round_full, r & 1, abort_flag, a.status)); ++r) {
+      tc_fence_after();
+      #pragma unroll 1
+      for (int c = 0; c < BN; c += 16) {
+        float v[16];
+        lin_sum_of(taddr + c, BN, live, v);
+        if (r > 0) lin_add_to(total + c, v);
+        #pragma unroll
+        for (int j = 0; j < 16; j += 8) {
+          uint32_t u[8];
+          #pragma unroll
+          for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(v[j + i]);
+          tmem_st8(total + c + j, u);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(round_empty);
+    }
+  }
   const bool ok = warp < 4 && warp_all(mbar_wait(done, 0, abort_flag, a.status));
-  const uint32_t taddr = tbase + (static_cast<uint32_t>(32 * warp) << 16);
   const int f = r0 + threadIdx.x;   // this thread's feature
-  const int accs = min(ACCS, s1 - s0);
+  const int accs = min(live, s1 - s0 - last * round);
   tc_fence_after();
   if (pieces > 1) {
     if (ok) {
@@ -440,6 +477,7 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
       for (int c = 0; c < BN; c += 16) {
         float v[16];
         lin_sum_of(taddr + c, BN, accs, v);
+        if (rounds) lin_add_to(total + c, v);
         #pragma unroll
         for (int j = 0; j < 4; ++j)
           part[(c / 4 + j) * 128 + threadIdx.x] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
@@ -481,6 +519,7 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
     for (int c = 0; c < BN && c0 + c < a.cols; c += 16) {
       float v[16];
       lin_sum_of(taddr + c, BN, accs, v);
+      if (rounds) lin_add_to(total + c, v);
       if (f < a.rows) lin_finish_turned<KIND>(a, v, c0 + c, f, min(16, a.cols - c0 - c));
       __syncwarp();   // lanes without a feature left it out; the whole warp loads what follows
     }

@@ -26,7 +26,6 @@ namespace dera {
 // 164.  The input's gradient through gelu, 32768 x 4096 x 1024, with its load and its 20 instructions a pair, 229 and 199 (through relu
 // 181 with eight), through silu 193 and 210, but 32768 x 2304 x 768 113 and 97.
 constexpr int pair_threads(int epi) { return 128 + 32 * epi; }
-constexpr int kLinChain = 8;
 
 template <int KIND, int BN, int EPI>
 struct PairSmem {
