@@ -90,8 +90,9 @@ typedef enum dera_activation {
  * when it adds, at most 2^-23 of a partial sum for every 16 terms: where y is fp32 it does so for no more than 512 terms at a
  * time (with few tokens K / 4), and these sums are added with rounding (5e-7 of y); where y has 16 bits, over all K
  * (1.2e-9 K, below its rounding).  Bias,
- * activation and residual are applied in fp32, and y (and pre) rounded once.  x and weight must be finite.  Gelu's Phi is off by 2^-19
- * of its distance to 0 or 1; an element's last bit may depend on its neighbour's.
+ * activation and residual are applied in fp32, and y (and pre) rounded once.  x and weight must be finite.  Gelu's Phi(u) is off by
+ * 2^-18 + u^2 2^-23 of its distance to 0 or 1 (measured: 1.2e-6 of it up to |u| = 2, 2e-6 up to 6, 4.4e-6 up to 10, 6.5e-6 up to 13); an
+ * element's last bit may depend on its neighbour's.
  * Errors: DERA_ERR_SHAPE for sizes below one (B = 0 or N = 0 is a no-op), B * N beyond 2^31 - 1, features beyond 2^20,
  *      features or strides that break the rules above; DERA_ERR_ALIGN for strides that are not multiples of 8;
  *      DERA_ERR_DTYPE also for an unknown activation.

@@ -6,11 +6,12 @@
 //   quick_gelu   u s(1.702 u)
 //   silu         u s(u)
 //
-// An epilogue of a product over K terms has about K / 2 issue slots an element (a tensor core takes 128 x 256 x 64 in
-// 512 cycles, four schedulers issue for 32 elements each), so Phi has to be had for ten instructions:
+// An epilogue of a product over K terms has K / 32 issue slots an element (a tensor core takes 128 x 256 x 64 in
+// 512 cycles, in which four schedulers issue for 32 elements each), so Phi has to be had for ten instructions:
 //   Phi(-z) = exp(-z^2 / 2) t P(t),  t = 1 / (1 + 0.36 z),  z >= 0,
 // with P of degree 6 fitted to erfcx(z / sqrt 2) / 2 over [0, 14] for the smallest largest relative error (reweighted least
-// squares): 9e-7, in the tail too.  Its exponential serves the density in the derivative.
+// squares): 9e-7.  The exponential's argument is rounded to fp32, which makes up to 6.5e-6 of it at z = 13.  The exponential serves the
+// density in the derivative.
 #pragma once
 #include <type_traits>
 
