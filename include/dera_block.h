@@ -32,8 +32,8 @@ extern "C" {
  * Layer norm.  Per row x of `cols` values:
  *     mean = sum(x) / cols,  rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps),
  *     y = (x - mean) rstd weight + bias                 (weight 1 and bias 0 where they are NULL)
- * in fp32, the variance from centred values, y rounded once.  A row's sum has to stay within fp32's range; an
- * infinity or NaN makes its own row NaN and no other.
+ * in fp32, the variance from centred values, y rounded once.  A row's sum, and the sum of its squared deviations, have to stay
+ * within fp32's range; an infinity or NaN makes its own row NaN and no other.
  * in:  x [rows, cols] in in_dtype (any of the three), its rows x_stride >= cols elements apart (not looked at for one
  *      row); weight, bias [cols] in weight_dtype (DERA_F32 or the 16-bit type of in_dtype or out_dtype).
  * out: y [rows, cols] in out_dtype (DERA_F32, in_dtype, or any type where in_dtype is DERA_F32); mean, rstd [rows] fp32.
@@ -87,9 +87,11 @@ typedef enum dera_activation {
  * out: y [B, N, out_features] in out_dtype (DERA_F32 or in_dtype); pre, if not NULL, u in in_dtype (what the backward of
  *      the activation needs).
  * K and out_features are multiples of 8, head_dim of 64 where heads > 1.  Sums are fp32.  The tensor core cuts towards zero
- * when it adds, at most 2^-23 of a partial sum for every 16 terms: where y is fp32 it does so for no more than 512 terms at a
- * time (with few tokens K / 4), and these sums are added with rounding (5e-7 of y); where y has 16 bits, over all K
- * (1.2e-9 K, below its rounding).  Bias,
+ * when it adds: 16 products a step, each at a quarter of a unit in the last place of the sum so far, and the new sum at a whole one, at
+ * most 5 2^-23 of a partial sum.  In sums of one sign this adds up, to 6.4e-9 a term for fp16 and 3.6e-9 for bf16, whose products have fewer
+ * bits (measured; relative to the sum of the terms' sizes); mixed signs cancel.  Where y is fp32 no more than 512 terms are added so
+ * (2.8e-6 off on average for fp16 terms of one sign and 9e-7 for bf16, 3.7e-6 and 1.5e-6 at most), and these sums with rounding; where y has 16
+ * bits, up to all K: below half a step of y for fp16 up to K = 75000, and for bf16.  Bias,
  * activation and residual are applied in fp32, and y (and pre) rounded once.  x and weight must be finite.  Gelu's Phi(u) is off by
  * 2^-18 + u^2 2^-23 of its distance to 0 or 1 (measured: 1.2e-6 of it up to |u| = 2, 2e-6 up to 6, 4.4e-6 up to 10, 6.5e-6 up to 13); an
  * element's last bit may depend on its neighbour's.

@@ -4,7 +4,8 @@
 //   backward  g = dy w,  dx = r (g - sum g / C - h sum(g h) / C) + dres,  dw = sum over rows of dy h,  db = of dy
 //
 // Both should be bound by memory: every element is read and written once, for about 8 and 16 operations.  At 6.8 TB/s an
-// SM has 12 issue slots for 32 elements of a 16-bit row read and written, so instructions count as much as bytes:
+// SM has 22 to 31 bytes a clock (2.07 to 1.46 GHz), so 17 to 24 issue slots for 32 elements of a 16-bit row read and written, and
+// instructions count, too:
 // arithmetic is on packed pairs, addresses advance by additions, and a row's sums are joined by few shuffles.
 //
 // A row lies over `tpr` threads (whole warps, as many as C needs), NV times eight neighbouring elements each, so that a thread
@@ -16,7 +17,7 @@
 //
 // Measured: forward, 32768 x 2048 fp16, 268 MB: 51.6 us, 5.2 TB/s (a plain copy reaches 6.8); 32768 x 1024 bf16 25 us.  Backward with
 // the residual's gradient, 32768 x 1024: fp32 stream, 470 MB, 74.7 us, 6.3 TB/s; bf16, 268 MB, 49 us, 5.4 TB/s; the weights' sums
-// are 4 to 5 us of each.  Rows of an odd number of columns, element by element: 32768 x 1001 bf16 61 us, backward 131.
+// are 4 to 5 us of each.  Rows of an odd number of columns, element by element: 32768 x 1001 bf16 61 us, backward 108.
 #pragma once
 #include "activation.cuh"
 #include "block.cuh"

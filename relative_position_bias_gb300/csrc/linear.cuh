@@ -346,7 +346,7 @@ __device__ __forceinline__ void lin_sum_of(uint32_t taddr, int apart, int accs, 
 // Few tokens: 128 features by BN tokens a tile, the features as rows, so that a product of few tokens still fills the tensor
 // core's 128 rows.  What counts then is how many SMs read the weight: a cluster of CTAs shares a tile, each with a piece of the
 // contraction, and each adds up all of their parts for its share of the tokens, through distributed shared memory and in order.
-// 32 tokens x 1024 x 4096: 6.5 us (9.6 without clusters; the weight's 8 MB take 1.2 at 6.8 TB/s), 32 x 4096 x 1024 7 (19 without); the
+// 32 tokens x 1024 x 4096: 5.8 us (9.6 without clusters; the weight's 8 MB take 1.2 at 6.8 TB/s), 32 x 4096 x 1024 6.7 (19 without); the
 // rest is the kernel's start, two trips to memory and the exchange.
 template <int KIND, int BN, bool BF16>
 __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_constant__ CUtensorMap map_a,
@@ -357,7 +357,8 @@ __global__ void __launch_bounds__(kLinThreads) linear_few_kernel(const __grid_co
   constexpr bool A_MN = KIND == kLinInput;   // W's columns in the input's gradient
   // A piece's steps go to four sums (two of 256 tokens) in turn, which are added at the end: the tensor core cuts towards zero when
   // it adds, and a long chain drifts (linear_pair.cuh).  Where the result is fp32 and a sum would have more than kLinChain steps, one of
-  // them is a total, to which the epilogue's warps add the others after every `round` steps; the loads run on meanwhile.
+  // them is a total, to which the epilogue's warps add the others after every `round` steps; the loads run on meanwhile (fp32, 32 x 4096 x
+  // 32000 50 us either way, 100 x 16384 x 9800 84 for 74, 200 x 16384 x 264, one sum and a total, 24 for 19; the pairs' chains took 87 and 63).
   constexpr int ACCS = BN == 256 ? 2 : 4;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);

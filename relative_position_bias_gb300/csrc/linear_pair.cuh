@@ -10,10 +10,11 @@
 // gelu, 32768 x 4096 x 1024, 200; dW of the same 163 to 178 (64 tiles for 76 pairs: 84 % of them have work); 4900 x 768 x 2304 18
 // (three waves for 2.4; a library product 11.6).
 //
-// The tensor core cuts towards zero what it adds to its fp32 sum, so a long chain drifts: 3.4e-5 of the sum after
-// 30 000 terms, 5e-6 after 4096.  Where the result is fp32 (FINE), and for the weight's gradient, whose sums over tokens have no limit,
-// chains end after kLinChain steps (512 terms, 6e-7), and the epilogue adds them in registers while the next chain runs in the
-// other buffer; it takes a quarter of the time that a chain's products do.
+// The tensor core cuts towards zero: each of 16 products at a quarter of a unit in the last place of the sum so far, the new sum at a whole
+// one (of 2^20 + 15 f 2^-3 in one step, f = 7/8 leaves 11/8, f = 1/8 nothing).  So a long chain of one sign drifts: 2.6e-5 of the sum after
+// 4096 terms for fp16, 1.4e-5 for bf16, whose products have fewer bits.  Where the result is fp32 (FINE), and for the weight's gradient, whose
+// sums over tokens have no limit, chains end after kLinChain steps (512 terms: 2.8e-6 and 9e-7), and the epilogue adds them in registers while
+// the next chain runs in the other buffer; it takes a quarter of the time that a chain's products do.
 #pragma once
 #include "linear.cuh"
 
@@ -24,7 +25,8 @@ namespace dera {
 // beside them wait: 32768 x 1024 x 4096 takes 152 us with eight and 162 with sixteen, with gelu 182 and 172; 32768 x 768 x 2304 with
 // gelu 108 and 87 (its argument kept, 121 and 110), with silu 92 and 78, with relu 82 and 88; 32768 x 2048 x 2048 with gelu 160 and
 // 164.  The input's gradient through gelu, 32768 x 4096 x 1024, with its load and its 20 instructions a pair, 229 and 199 (through relu
-// 181 with eight), through silu 193 and 210, but 32768 x 2304 x 768 113 and 97.
+// 181 with eight), through silu 193 and 210, but 32768 x 2304 x 768 113 and 97.  The limits in block.cu are the last lengths at which
+// sixteen won: gelu's between K = 1024 and 2048 was not measured, and dx through gelu at 1024 alone.
 constexpr int pair_threads(int epi) { return 128 + 32 * epi; }
 
 template <int KIND, int BN, int EPI>
